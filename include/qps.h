@@ -79,7 +79,7 @@
 extern "C" {
 #endif
 
-#define QPS_ABI_VERSION 7
+#define QPS_ABI_VERSION 8
 
 #if defined(__GNUC__)
 #define QPS_API __attribute__((visibility("default")))
@@ -302,6 +302,149 @@ QPS_API qps_status qps_attn_decode_window(const qps_attn_args* a, void* stream);
 QPS_API qps_status qps_lse_combine(const float* o_parts, const float* lse_parts, int32_t n_parts,
                            int64_t rows, int32_t d, float* o, float* lse, void* stream);
 
+/* ---- Paged KV cache: rotated queries, appended rows, ragged decode ------------------ */
+
+/* Element types of the activations around the cache. */
+typedef enum qps_dtype { QPS_DT_F16 = 0, QPS_DT_BF16 = 1, QPS_DT_F32 = 2 } qps_dtype;
+
+/* Activation rows [tokens][heads][D]: element (t, h, i) at t*tok_stride + h*head_stride +
+ * i.  data: device, 16-byte aligned; strides in elements, multiples of 8, so that a
+ * slice of a fused projection is passed as it lies. */
+typedef struct qps_rows {
+  void* data;
+  int32_t dtype;       /* qps_dtype */
+  int32_t heads;       /* 0: no rows (data unused) */
+  int64_t tok_stride;
+  int64_t head_stride;
+} qps_rows;
+
+/* RMS norm of one head's row x [D], all in IEEE float32 with a fixed order: squares; the
+ * 8 squares of elements 8j .. 8j+7 folded by t[i] += t[i+h], h = 4, 2, 1; the D/8 sums
+ * folded the same way, h = D/16 .. 1; inv = 1 / sqrt(ss / D + eps); y = (x * inv) *
+ * (w + offset), or x * inv when w is NULL. */
+typedef struct qps_head_norm {
+  const void* w;       /* device, [D] of w_dtype, 16-byte aligned; NULL: no weight */
+  int32_t w_dtype;     /* qps_dtype */
+  int32_t on;          /* 0: no norm (the other fields are unused) */
+  float eps;           /* finite, >= 0 */
+  float offset;        /* finite; 1 for weights stored as w - 1 */
+} qps_head_norm;
+
+/* Position rotation of the first `dim` elements of a row (after its norm), in IEEE
+ * float32 without contraction: with (a, b) the pair j and (c, s) = (cos, sin) of its
+ * angle, a' = a*c - b*s, b' = b*c + a*s.  Pair j is (j, j + dim/2), or (2j, 2j + 1) when
+ * `pairs` is 1.  Row p of the table holds dim/2 cosines, then dim/2 sines: the angles
+ * (base, scaling, length extension) are the caller's. */
+typedef struct qps_rotation {
+  const float* table;  /* device, [len][dim] f32, 16-byte aligned */
+  int64_t len;         /* positions the table holds */
+  int32_t dim;         /* 0: no rotation; else a multiple of 16, <= D */
+  int32_t pairs;       /* 0: halves, 1: neighbours */
+} qps_rotation;
+
+/* Indexes that a call reads on the device (positions, slots, pages, lengths) cannot be
+ * checked by the host.  The kernels check each before using it: one out of range is
+ * never followed, its row is left out (below), and qps_device_status then returns
+ * INVALID_ARG until reset. */
+
+typedef struct qps_qk_rope_args {
+  int64_t tokens;
+  int32_t d;
+  int32_t reserved0;   /* must be 0 */
+  qps_rows q, k;             /* input rows; either may have heads == 0 */
+  qps_rows q_out, k_out;     /* F16 or BF16 (heads as the input's); may be the input itself,
+                                element for element and of its type, else must not overlap it */
+  qps_head_norm q_norm, k_norm;
+  qps_rotation rot;
+  const int64_t* positions;  /* device, [tokens]; unused without a rotation */
+} qps_qk_rope_args;
+
+/* Norm each head's query and key row and rotate it by its token's position, in one pass
+ * (the rows a decode step hands to qps_attn_* and to the cache; no counterpart on the
+ * pages, which start at stored keys).  Each value is rounded once, to the output type.
+ * A token whose position is outside the table is left as it was.  D in {32, 64, 128,
+ * 256, 512}; tokens == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED (D, output type), CUDA. */
+QPS_API qps_status qps_qk_norm_rope(const qps_qk_rope_args* a, void* stream);
+
+/* A paged cache: every plane of its format is [n_pages][hkv][page_size][bytes per row],
+ * contiguous.  A slot is page * page_size + offset.  Planes (device): data 16-byte
+ * aligned and every other one too; aux / aux2 as in qps_kv_view. */
+typedef struct qps_paged_kv {
+  int32_t k_fmt, v_fmt;      /* the pairings of qps_attn_decode_window */
+  int32_t hkv, d;            /* D in {64, 128, 256, 512} */
+  int32_t page_size;         /* positions per page: 16, 32, 64, 128, 256, 512 or 1024 */
+  int32_t reserved0;         /* must be 0 */
+  int64_t n_pages;           /* > 0; n_pages * page_size < 2^31 */
+  void *k_data, *k_aux, *k_aux2;
+  void *v_data, *v_aux, *v_aux2;
+  const uint32_t* signs1;    /* host, D/32 words: the TurboQuant rotation (any such plane) */
+  const uint32_t* signs2;    /* host, D/32 words or NULL */
+  int32_t tq_block;          /* G, or 0 = D */
+  int32_t reserved1;         /* must be 0 */
+} qps_paged_kv;
+
+typedef struct qps_paged_append_args {
+  qps_paged_kv kv;
+  int64_t tokens;
+  qps_rows k, v;             /* heads == kv.hkv */
+  qps_head_norm k_norm;
+  qps_rotation rot;          /* of K */
+  const int64_t* positions;  /* device, [tokens]; unused without a rotation */
+  const int64_t* slots;      /* device, [tokens]; a negative slot is padding: its token is
+                                skipped.  No two tokens share a slot (such a slot would hold
+                                a mix of their rows; the others are right) */
+} qps_paged_append_args;
+
+/* Append key and value rows to a paged cache: K is normed and rotated as by
+ * qps_qk_norm_rope and rounded to fp16, V is rounded to fp16, then both are encoded as
+ * by qps_kv_quant_* (bit for bit) into their slots (no counterpart on the pages, whose
+ * caches are encoded whole).  A token whose slot or position is out of range is skipped.
+ * tokens == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED (D, formats), CUDA. */
+QPS_API qps_status qps_kv_append_paged(const qps_paged_append_args* a, void* stream);
+
+typedef struct qps_paged_attn_args {
+  const void* q;             /* device, fp16 [batch][n_q][hq][D], 16-byte aligned */
+  int64_t q_batch_stride;    /* elements, >= n_q*hq*D, multiple of 8 */
+  int32_t batch, n_q, hq;    /* n_q in [1, 64]; n_q * hq / hkv <= 1024 */
+  int32_t causal;            /* query token i of sequence b sees the positions
+                                < kv_lens[b] - n_q + i + 1 (the n_q newest positions are the
+                                queries' own); 0: all of [0, kv_lens[b]) */
+  qps_paged_kv kv;
+  const int32_t* page_table; /* device: entry (b, j) at b*table_stride + j is the page of the
+                                positions [j*page_size, (j+1)*page_size) of sequence b; entries
+                                behind the last position are not read */
+  int64_t table_stride;
+  int32_t table_width;       /* entries per sequence, >= 1; table_width * page_size < 2^31 - 64 */
+  int32_t o_dtype;           /* qps_dtype of o */
+  const int32_t* kv_lens;    /* device, [batch]: positions of each sequence, the new ones
+                                included; 0 gives O = 0, lse = -inf.  A length outside
+                                [0, table_width * page_size] is cut to that range */
+  int64_t shared_len;        /* the first shared_len positions (a multiple of page_size) lie in
+                                the same pages for every sequence and are read once, through
+                                sequence 0's entries; 0: none */
+  float scale, softcap;      /* as in qps_attn_args */
+  void* o;                   /* device, [batch*n_q*hq][D] of o_dtype, rows as in qps_attn_args */
+  float* lse;                /* device, f32 [batch*n_q*hq] */
+  void* workspace;           /* device, 256-byte aligned, as large as qps_attn_paged_plan says;
+                                calls that overlap on the GPU need one each */
+  size_t workspace_bytes;
+} qps_paged_attn_args;
+
+/* Workspace bytes of qps_attn_decode_paged for these args (host only, no launch; o, lse
+ * and workspace are not looked at).  Depends on the batch, the heads and the formats,
+ * not on the lengths.  Library utility, no counterpart on the pages.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA (the SM count). */
+QPS_API qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* workspace_bytes);
+
+/* Decode attention of a ragged batch over a paged cache, the split-KV attention of
+ * [RKV] with its LSE merge: every sequence's positions are cut into chunks on the
+ * device from kv_lens, so a captured graph replays with new lengths, tables and rows.
+ * With shared_len the prefix's chunks are attended once for the rows of the whole batch
+ * ([POLY, "S1 — SharedKVPool"]).  A table entry outside [0, n_pages) reads as zero rows.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+QPS_API qps_status qps_attn_decode_paged(const qps_paged_attn_args* a, void* stream);
+
 /* ---- Pinned host storage of the tail ------------------------------------------- */
 
 /* Page-locked host memory for the tail ("F5 M7 — Rolling KV: position-windowed KV
@@ -520,13 +663,14 @@ QPS_API qps_status qps_attn_decode_window_noalloc(const qps_attn_args* a, void* 
  * invalid outputs.  This call reads that word synchronously (it waits for the
  * device's pending work to reach it on the legacy stream) and clears it if `reset`.
  * Errors: INTERNAL (a bounds check of the checked build failed since the last reset;
- * see qps_build_checked), TIMEOUT (some wait gave up since the last reset), CUDA. */
+ * see qps_build_checked), TIMEOUT (some wait gave up since the last reset), INVALID_ARG
+ * (a paged call met a position, slot, page or length out of range), CUDA. */
 QPS_API qps_status qps_device_status(int32_t reset);
 
 /* The device error word and the record of the first bounded wait that gave up since
  * the last reset (failure detection; no counterpart on the pages), copied synchronously
  * into `words` (host, n words; words past the record are zeroed):
- *   [0] status bits (1: a wait gave up, 2: a bounds check failed), [1] number of waits
+ *   [0] status bits (1: a wait gave up, 2: a bounds check failed, 4: an index out of range), [1] number of waits
  *   that gave up, [2..4] that CTA's block index x / y / z, [5] its warp, [6] the warp's
  *   tile whose wait ran out, [7] tiles the warp had issued, [8] tiles the warp owns,
  *   [9] positions in the CTA's chunk, [10] ns the drain wait of that tile took,

@@ -7,7 +7,9 @@ is no CPU or eager-PyTorch fallback, and a missing library raises at first use.
 
 Names follow the ABI without its ``qps_`` prefix (``kv_quant_q8_0``,
 ``kv_quant_tq3``, ``attn_decode_window``, ``attn_decode_tail``, ``lse_combine``,
-``Ring`` for ``qps_ring_*``, ``StepPlan`` for ``qps_decode_step``).
+``Ring`` for ``qps_ring_*``, ``StepPlan`` for ``qps_decode_step``).  The calls around a
+paged cache (``qk_norm_rope``, ``kv_append_paged``, ``attn_decode_paged``) are in
+``paged.py``.
 """
 
 from __future__ import annotations
@@ -45,6 +47,15 @@ __all__ = [
     "StepPlan",
     "launch_count",
     "lib",
+    "Rope",
+    "rope_table",
+    "qk_rope_args",
+    "qk_norm_rope",
+    "PagedKV",
+    "paged_append_args",
+    "kv_append_paged",
+    "paged_attn_args",
+    "attn_decode_paged",
 ]
 
 
@@ -661,3 +672,7 @@ def choose_tier(kv_bytes_per_tier, budget_bytes: float, t_star_bytes: float) -> 
     out = ctypes.c_int32()
     N.check(lib().qps_choose_tier(arr, len(kv_bytes_per_tier), budget_bytes, t_star_bytes, ctypes.byref(out)))
     return out.value
+
+
+from .paged import (PagedKV, Rope, attn_decode_paged, kv_append_paged, paged_append_args,  # noqa: E402
+                    paged_attn_args, qk_norm_rope, qk_rope_args, rope_table)

@@ -123,6 +123,110 @@ class LayerStep(ctypes.Structure):
     ]
 
 
+class Rows(ctypes.Structure):
+    _fields_ = [
+        ("data", c_void_p),
+        ("dtype", c_int32),
+        ("heads", c_int32),
+        ("tok_stride", c_int64),
+        ("head_stride", c_int64),
+    ]
+
+
+class HeadNorm(ctypes.Structure):
+    _fields_ = [
+        ("w", c_void_p),
+        ("w_dtype", c_int32),
+        ("on", c_int32),
+        ("eps", c_float),
+        ("offset", c_float),
+    ]
+
+
+class RotationArgs(ctypes.Structure):
+    _fields_ = [
+        ("table", c_void_p),
+        ("len", c_int64),
+        ("dim", c_int32),
+        ("pairs", c_int32),
+    ]
+
+
+class QkRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("tokens", c_int64),
+        ("d", c_int32),
+        ("reserved0", c_int32),
+        ("q", Rows),
+        ("k", Rows),
+        ("q_out", Rows),
+        ("k_out", Rows),
+        ("q_norm", HeadNorm),
+        ("k_norm", HeadNorm),
+        ("rot", RotationArgs),
+        ("positions", c_void_p),
+    ]
+
+
+class PagedKvStruct(ctypes.Structure):
+    _fields_ = [
+        ("k_fmt", c_int32),
+        ("v_fmt", c_int32),
+        ("hkv", c_int32),
+        ("d", c_int32),
+        ("page_size", c_int32),
+        ("reserved0", c_int32),
+        ("n_pages", c_int64),
+        ("k_data", c_void_p),
+        ("k_aux", c_void_p),
+        ("k_aux2", c_void_p),
+        ("v_data", c_void_p),
+        ("v_aux", c_void_p),
+        ("v_aux2", c_void_p),
+        ("signs1", POINTER(c_uint32)),
+        ("signs2", POINTER(c_uint32)),
+        ("tq_block", c_int32),
+        ("reserved1", c_int32),
+    ]
+
+
+class PagedAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("kv", PagedKvStruct),
+        ("tokens", c_int64),
+        ("k", Rows),
+        ("v", Rows),
+        ("k_norm", HeadNorm),
+        ("rot", RotationArgs),
+        ("positions", c_void_p),
+        ("slots", c_void_p),
+    ]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", c_void_p),
+        ("q_batch_stride", c_int64),
+        ("batch", c_int32),
+        ("n_q", c_int32),
+        ("hq", c_int32),
+        ("causal", c_int32),
+        ("kv", PagedKvStruct),
+        ("page_table", c_void_p),
+        ("table_stride", c_int64),
+        ("table_width", c_int32),
+        ("o_dtype", c_int32),
+        ("kv_lens", c_void_p),
+        ("shared_len", c_int64),
+        ("scale", c_float),
+        ("softcap", c_float),
+        ("o", c_void_p),
+        ("lse", c_void_p),
+        ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t),
+    ]
+
+
 # (name, restype, argtypes) of every exported function, in header order.
 SIGNATURES = [
     ("qps_abi_version", c_int32, []),
@@ -144,6 +248,10 @@ SIGNATURES = [
     ("qps_attn_path", c_int32, [POINTER(AttnArgs)]),
     ("qps_attn_decode_window", c_int32, [POINTER(AttnArgs), c_void_p]),
     ("qps_lse_combine", c_int32, [c_void_p, c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_void_p]),
+    ("qps_qk_norm_rope", c_int32, [POINTER(QkRopeArgs), c_void_p]),
+    ("qps_kv_append_paged", c_int32, [POINTER(PagedAppendArgs), c_void_p]),
+    ("qps_attn_paged_plan", c_int32, [POINTER(PagedAttnArgs), POINTER(c_size_t)]),
+    ("qps_attn_decode_paged", c_int32, [POINTER(PagedAttnArgs), c_void_p]),
     ("qps_host_alloc", c_int32, [c_size_t, c_int32, POINTER(c_void_p)]),
     ("qps_host_free", c_int32, [c_void_p]),
     ("qps_copy_host", c_int32, [c_void_p, c_void_p, c_size_t, c_void_p]),

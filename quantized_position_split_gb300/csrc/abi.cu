@@ -99,9 +99,14 @@ unsigned int* device_error_word() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lk(mu);
   if (!words[dev]) {
+    // (relaxed: the first call on a device may come while a stream is being captured)
     unsigned int* w = nullptr;
-    if (cudaMalloc(&w, kErrWords * sizeof(unsigned int)) != cudaSuccess) return nullptr;
-    if (cudaMemset(w, 0, kErrWords * sizeof(unsigned int)) != cudaSuccess) return nullptr;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+    const bool ok = cudaMalloc(&w, kErrWords * sizeof(unsigned int)) == cudaSuccess &&
+                    cudaMemset(w, 0, kErrWords * sizeof(unsigned int)) == cudaSuccess;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!ok) return nullptr;
     words[dev] = w;
   }
   return words[dev];
@@ -426,7 +431,9 @@ qps_status qps_device_status(int32_t reset) {
     return fail(QPS_ERR_INTERNAL, std::string("device_status: a bounds check of the checked build failed (the access "
                                               "was skipped; outputs are not valid)") +
                                       ((v & kErrTimeout) ? "; a bounded wait also gave up" : ""));
-  if (v) return fail(QPS_ERR_TIMEOUT, "device_status: a kernel's bounded wait for its tile copies gave up");
+  if (v & kErrTimeout) return fail(QPS_ERR_TIMEOUT, "device_status: a kernel's bounded wait for its tile copies gave up");
+  if (v & kErrIndex)
+    return fail(QPS_ERR_INVALID_ARG, "device_status: a paged call met a position, slot, page or length out of range");
   return QPS_OK;
 }
 

@@ -28,9 +28,12 @@
 // arrive as zeros; tokens outside [t0, t1) are masked in the softmax.
 #pragma once
 
-#include <cstring>
+#include <cuda_bf16.h>
 
-#include "internal.h"
+#include <cstring>
+#include <type_traits>
+
+#include "paged.h"
 
 namespace qps {
 namespace mma {
@@ -347,10 +350,16 @@ __host__ __device__ constexpr int ow_col(int col) { return col + col / (D / 8); 
 // ---- the kernel -------------------------------------------------------------------
 // CAUSAL: the verify batch's causal limit (a separate instance, so that single-token
 // decode compiles without it).
-template <int D, int KF, int VF, int NTW, bool CAUSAL>
+// P = PagedAttnParams: the paged cache's instances.  Positions come through a page table
+// (a tensor map's batch coordinate is the page, its token coordinate the offset in it),
+// a sequence's chunks from its length on the device, and every row has its own limit
+// (length and causal limit in one comparison).  With p.shared the chunks are of the
+// prefix, cut by the host, and the rows those of the whole batch.
+template <int D, int KF, int VF, int NTW, bool CAUSAL, class P>
 __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, NTW>::CTAS)
-    attn_mma_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ TmaSet maps) {
+    attn_mma_kernel(const __grid_constant__ P p, const __grid_constant__ TmaSet maps) {
   using G = Geo<D, KF, VF, NTW>;
+  constexpr bool PAGED = std::is_same<P, PagedAttnParams>::value;
   constexpr int kWarps = G::NW;
   constexpr int ROWS = 8 * NTW;  // query rows per CTA
   constexpr int MT = D / 16;     // m-tiles of O^T, k-steps of S^T
@@ -378,12 +387,45 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   // KV rows at about the same time and all but the first read come from L2
   const int rgroups = (p.rows_per_cta + ROWS - 1) / ROWS;
   const int split = blockIdx.x / rgroups, rg = blockIdx.x % rgroups;
-  const int head = blockIdx.y, bz = blockIdx.z;
+  const int head = blockIdx.y;
+  int bz = blockIdx.z;
   const int row0 = rg * ROWS;
   const int nrows = min(ROWS, p.rows_per_cta - row0);
-  const int64_t t0 = p.begin + (int64_t)split * p.chunk;
-  const int64_t t1 = min(p.end, t0 + p.chunk);
+  int64_t t0 = p.begin + (int64_t)split * p.chunk;
+  int64_t t1 = min(p.end, t0 + p.chunk);
   const int part = p.part_offset + split;
+  bool whole = false;  // (paged) the chunk is all its rows attend: the output itself is written
+  if constexpr (PAGED) {
+    if (!p.shared) {  // chunk number `split` of the batch: find its sequence and positions
+      const int cu = paged_chunk_units(p, lane);
+      int before = 0, found = -1, at = 0, len = 0, n = 0;
+      for (int b0 = 0; b0 < p.batch && found < 0; b0 += 32) {
+        const int b = b0 + lane;
+        const int bl = b < p.batch ? paged_len(p, b) : 0;
+        const int cnt = (paged_units(bl, p.prefix_len) + cu - 1) / cu;
+        int sum = cnt;  // inclusive scan over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > split);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          found = b0 + src;
+          n = __shfl_sync(0xffffffffu, cnt, src);
+          at = split - (before + __shfl_sync(0xffffffffu, sum, src) - n);
+          len = __shfl_sync(0xffffffffu, bl, src);
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+      }
+      if (found < 0) return;  // more CTAs than chunks (every warp finds the same)
+      bz = found;
+      whole = n == 1 && p.prefix_len == 0;
+      t0 = p.prefix_len + (int64_t)at * cu * kPagedUnit;
+      t1 = min((int64_t)len, t0 + (int64_t)cu * kPagedUnit);
+    }
+  }
 
   // CTA row rr: (batch entry, head) in a shared tile; (query token rr / group, head)
   // of batch entry bz otherwise
@@ -391,6 +433,15 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     const int h = head * p.group + rr % p.group;
     if (p.shared) return (int64_t)(rr / p.group) * p.hq + h;
     return ((int64_t)bz * p.n_q + rr / p.group) * p.hq + h;
+  };
+  auto q_row = [&](int rr) -> const __half* {
+    const int h = head * p.group + rr % p.group, e = rr / p.group;
+    if constexpr (PAGED) {
+      if (p.shared) return p.q + (int64_t)(e / p.n_q) * p.q_bstride + ((int64_t)(e % p.n_q) * p.hq + h) * D;
+    } else {
+      if (p.shared) return p.q + (int64_t)e * p.q_bstride + (int64_t)h * D;
+    }
+    return p.q + (int64_t)bz * p.q_bstride + ((int64_t)e * p.hq + h) * D;
   };
 
   if (t0 >= t1) {  // an empty chunk: O = 0, lse = -inf
@@ -439,9 +490,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     const __half* qrow = nullptr;
     bool valid_q = valid;
     if (valid) {
-      const int h = head * p.group + rr % p.group;
-      qrow = p.shared ? p.q + (int64_t)(rr / p.group) * p.q_bstride + (int64_t)h * D
-                      : p.q + (int64_t)bz * p.q_bstride + ((int64_t)(rr / p.group) * p.hq + h) * D;
+      qrow = q_row(rr);
       valid_q = in_bounds((int64_t)(qrow - p.q) + D <= p.q_elems, p.err);
     }
 #pragma unroll
@@ -482,9 +531,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       const int r = idx / D, dd = idx % D, rr = row0 + r;
       float v = 0.f;
       if (rr < p.rows_per_cta) {
-        const int h = head * p.group + rr % p.group;
-        const __half* qrow = p.shared ? p.q + (int64_t)(rr / p.group) * p.q_bstride + (int64_t)h * D
-                                      : p.q + (int64_t)bz * p.q_bstride + ((int64_t)(rr / p.group) * p.hq + h) * D;
+        const __half* qrow = q_row(rr);
         if (in_bounds((int64_t)(qrow - p.q) + dd < p.q_elems, p.err)) v = __half2float(qrow[dd]);
         if ((p.vsigns[dd >> 5] >> (dd & 31)) & 1u) v = -v;
       }
@@ -548,6 +595,37 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   // CTA issues another tile copy.  Read by lane 0 and broadcast, so warp-uniform.
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + ABORT_OFF);
   int n_issued = 0;  // this warp's tiles whose copies were issued (warp-uniform)
+  // (paged) The pages of the warp's next tiles, lane L holding those of tile 32 j + L and
+  // of tile 32 (j + 1) + L, loaded a block ahead.  A tile of 32 positions on pages of 16
+  // takes two pages.  A page behind the last position, or out of range, is page n_pages:
+  // its boxes arrive as zeros.
+  struct Pages {
+    int a, b;
+  };
+  auto page_of = [&](int64_t t) -> int {
+    if constexpr (PAGED) {
+      if (t >= t1) return (int)p.n_pages;
+      const int pg = p.table[(p.shared ? 0 : (int64_t)bz * p.table_stride) + (t >> p.page_shift)];
+      if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
+      atomicOr(p.err, kErrIndex);
+      return (int)p.n_pages;
+    }
+    return 0;
+  };
+  auto load_pages = [&](int j) -> Pages {
+    const int64_t t = tile0 + (int64_t)(warp + (32 * j + lane) * kWarps) * TT;
+    Pages r;
+    r.a = page_of(t);
+    r.b = 0;
+    if constexpr (PAGED && TT == 32)
+      if (p.page_shift == 4) r.b = page_of(t + 16);
+    return r;
+  };
+  Pages pages_now = {0, 0}, pages_next = {0, 0};
+  if constexpr (PAGED) {
+    pages_now = load_pages(0);
+    pages_next = load_pages(1);
+  }
 
   // The warp's k-th tile -> stage k % STAGES.  Lane 0 announces the tensor-map bytes; lanes issue one box each; small planes go by
   // zero-filling cp.async from every lane, each lane then arriving on the same mbarrier
@@ -557,6 +635,15 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     if (tile >= ntiles) return;
     if (__shfl_sync(0xffffffffu, lane == 0 ? *abort_flag : 0, 0)) return;  // a warp gave up: no new copies
     n_issued = k + 1;  // (tiles are issued in order, so every earlier one was too)
+    Pages pg = {0, 0};
+    if constexpr (PAGED) {
+      if (k > 0 && (k & 31) == 0) {
+        pages_now = pages_next;
+        pages_next = load_pages((k >> 5) + 1);
+      }
+      pg.a = __shfl_sync(0xffffffffu, pages_now.a, k & 31);
+      if constexpr (TT == 32) pg.b = __shfl_sync(0xffffffffu, pages_now.b, k & 31);
+    }
     uint8_t* st = wpipe + (k % G::STAGES) * G::STAGE;
     const int64_t tb = tile0 + (int64_t)tile * TT;
     const int tok = (int)tb;
@@ -569,6 +656,61 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     constexpr int NKB = G::PK::NB, NVB = G::PV::NB;
     constexpr int NBOX = NKB + NVB + (G::PKA::TMA ? 1 : 0) + (G::PVA::TMA ? 1 : 0);
     static_assert(NBOX <= 32, "one tensor-map box per lane");
+    if constexpr (PAGED) {
+      // the same boxes, of min(page size, TT) positions: a tile on pages of 16 takes each
+      // as two halves
+      static_assert(TT == 16 || 2 * NBOX <= 32, "one tensor-map box per lane");
+      const bool halves = TT == 32 && p.page_shift == 4;
+      const int half = lane / NBOX, box = lane % NBOX;
+      if (half == 0 || (half == 1 && halves)) {
+        const TensorMap* mp = &maps.k;
+        int dst = G::K_OFF + box * (TT * G::PK::IB), x = box * G::PK::IB, ib = G::PK::IB;
+        if (box >= NKB && box < NKB + NVB) {
+          mp = &maps.v;
+          dst = G::V_OFF + (box - NKB) * (TT * G::PV::IB);
+          x = (box - NKB) * G::PV::IB;
+          ib = G::PV::IB;
+        } else if (box >= NKB + NVB) {
+          const bool ka = G::PKA::TMA && box == NKB + NVB;
+          mp = ka ? &maps.ka : &maps.va;
+          dst = ka ? G::KA_OFF : G::VA_OFF;
+          x = 0;
+          ib = ka ? G::PKA::IB : G::PVA::IB;
+        }
+        const int rows = halves ? 16 : TT;
+        if (in_bounds(dst + half * 16 * ib + rows * ib <= G::STAGE && head < p.hkv, p.err))
+          tma_load_4d(sbase + dst + half * 16 * ib, mp, x, halves ? 0 : tok & ((1 << p.page_shift) - 1), head,
+                      half ? pg.b : pg.a, bar);
+      }
+      if constexpr (G::SMALL) {
+        // first bytes of the halves' rows in a plane of rb bytes per row; rows at or behind
+        // t1 are not read
+        const int valid = (int)max((int64_t)0, min((int64_t)TT, t1 - tb));
+        const int split_at = halves ? 16 : TT;
+        auto row_of = [&](int page) {
+          return (((int64_t)page * p.hkv + head) << p.page_shift) + (halves ? 0 : tok & ((1 << p.page_shift) - 1));
+        };
+        const int64_t ra = row_of(pg.a), rb2 = row_of(pg.b);
+        const bool ina = (int64_t)pg.a < p.n_pages, inb = (int64_t)pg.b < p.n_pages;
+        auto stage_small = [&](int off, int bytes, const void* plane, int rb) {
+          for (int ch = lane; ch < bytes / 16; ch += 32) {
+            const int row = ch * 16 / rb;  // (16 divides 16 rows: a chunk is of one half)
+            const bool second = row >= split_at;
+            int nb = valid * rb - ch * 16;
+            nb = nb < 0 || !(second ? inb : ina) ? 0 : (nb > 16 ? 16 : nb);
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(plane) + (second ? rb2 : ra) * rb + ch * 16 -
+                                 (second ? split_at * rb : 0);
+            cp_async16(smem_addr(st + off) + ch * 16, nb > 0 ? src : safe, nb);
+          }
+        };
+        if constexpr (G::K_ARB > 0 && !G::PKA::TMA) stage_small(G::KA_OFF, G::PKA::BYTES, p.k.aux, G::K_ARB);
+        if constexpr (G::V_ARB > 0 && !G::PVA::TMA) stage_small(G::VA_OFF, G::PVA::BYTES, p.v.aux, G::V_ARB);
+        if constexpr (G::K_A2RB > 0) stage_small(G::KA2_OFF, G::PKA2::BYTES, p.k.aux2, G::K_A2RB);
+        if constexpr (G::V_A2RB > 0) stage_small(G::VA2_OFF, G::PVA2::BYTES, p.v.aux2, G::V_A2RB);
+        cp_async_arrive_noinc(bar);
+      }
+      return;
+    }
     if (lane < NBOX) {
       const TensorMap* mp = &maps.k;
       int dst = G::K_OFF + lane * (TT * G::PK::IB), x = lane * G::PK::IB;
@@ -648,6 +790,25 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   __syncthreads();  // the barriers and the flag are ready
 
   // ---- per-tile work ------------------------------------------------------------------
+
+  // (paged) positions below lim are visible to rows 2c, 2c + 1 of each n-tile
+  int lim[NTW][2];
+  if constexpr (PAGED) {
+#pragma unroll
+    for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int e = (row0 + nt * 8 + 2 * c + u) / p.group;
+        const int i = p.shared ? e % p.n_q : e, b = p.shared ? e / p.n_q : bz;
+        int n = (int)t1;
+        if (p.shared || p.causal) {
+          n = b < p.batch ? paged_len(p, b) : 0;
+          if (p.causal) n += i + 1 - p.n_q;
+          n = min(n, (int)t1);
+        }
+        lim[nt][u] = n;
+      }
+  }
 
   // per-lane stage offsets that do not change from tile to tile
   const int ks_lane = g * (D / 32);                        // K scale of (row g, block 0)
@@ -952,8 +1113,16 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
           if (cap > 0.f) v = softcap_tanh(v, cap, cap_k);
           x[sb][e] = v * LOG2E;
         }
+        if constexpr (PAGED) {
+          const int t = (int)tb + 16 * sb + g;
+          if (t >= lim[nt][0]) x[sb][0] = -INFINITY;
+          if (t >= lim[nt][1]) x[sb][1] = -INFINITY;
+          if (t + 8 >= lim[nt][0]) x[sb][2] = -INFINITY;
+          if (t + 8 >= lim[nt][1]) x[sb][3] = -INFINITY;
+        } else {
         if (!in_g[sb]) x[sb][0] = x[sb][1] = -INFINITY;
         if (!in_g8[sb]) x[sb][2] = x[sb][3] = -INFINITY;
+        }
         if constexpr (CAUSAL) {
           // position t is visible to CTA row r (query token r / group) iff
           // t - q_pos <= r / group, i.e. (t - q_pos) * group <= r; t - q_pos is clamped
@@ -1238,6 +1407,25 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     }
     __syncwarp();
     const uint8_t* st = wpipe + (k % G::STAGES) * G::STAGE;
+    if constexpr (PAGED) {
+      // Rows of the last page behind the sequence's end hold whatever was there: their
+      // logits are masked, but 0 x NaN is NaN, so what V multiplies P with is zeroed (the
+      // fp16 values, or the q8_0 scales that came by a box; the other planes' rows were
+      // not read).
+      const int64_t left = t1 - (tile0 + (int64_t)(warp + k * kWarps) * TT);
+      if (left < TT) {
+        constexpr int OFF = VF == QPS_FMT_F16 ? G::V_OFF : G::VA_OFF;
+        constexpr int IB = VF == QPS_FMT_F16 ? G::PV::IB : G::PVA::IB;
+        constexpr int NB = VF == QPS_FMT_F16 ? G::PV::NB : (VF == QPS_FMT_Q8_0 && G::PVA::TMA) ? 1 : 0;
+        const int first = (int)left * (IB / 16), last = TT * (IB / 16);
+        for (int idx = first + lane; NB > 0 && idx < last; idx += 32)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            *reinterpret_cast<uint4*>(wpipe + (k % G::STAGES) * G::STAGE + OFF + b * (TT * IB) + idx * 16) =
+                make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
+    }
     float sacc[SUB][NTW][4];
     k_part(st, sacc);
     attend_tile(st, tile0 + (int64_t)(warp + k * kWarps) * TT, sacc);
@@ -1381,7 +1569,25 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       if ((p.vsigns[dd >> 5] >> (dd & 31)) & 1u) val = -val;
     }
     const int64_t row = orow[r];
-    const bool empty = !(den > 0.f);
+    const bool empty = PAGED ? den == 0.f : !(den > 0.f);  // (paged: a NaN logit stays one)
+    if constexpr (PAGED) {
+      if (!in_bounds(part < (p.shared ? p.n_prefix : p.target + p.batch) && row >= 0 && row < p.rows_total, p.err)) continue;
+      const float ov = empty ? 0.f : val / den;
+      const float lv = empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
+      if (whole) {  // nothing to merge: the one rounding to the output type
+        if (p.out_dtype == QPS_DT_F16) reinterpret_cast<__half*>(p.out)[row * D + dd] = __float2half_rn(ov);
+        else if (p.out_dtype == QPS_DT_BF16) reinterpret_cast<__nv_bfloat16*>(p.out)[row * D + dd] = __float2bfloat16_rn(ov);
+        else reinterpret_cast<float*>(p.out)[row * D + dd] = ov;
+        if (dd == 0) p.out_lse[row] = lv;
+      } else {
+        // the prefix's parts hold every row of the batch, a sequence's chunk its own
+        const int64_t at = p.shared ? (int64_t)part * p.rows_total + row
+                                    : (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
+        (p.shared ? p.pre_o : p.own_o)[at * D + dd] = ov;
+        if (dd == 0) (p.shared ? p.pre_lse : p.own_lse)[at] = lv;
+      }
+      continue;
+    }
     if (!in_bounds(part < p.parts_cap && row >= 0 && row < p.rows_total, p.err)) continue;
     p.o_parts[((int64_t)part * p.rows_total + row) * D + dd] = empty ? 0.f : val / den;
     if (dd == 0)
@@ -1401,8 +1607,8 @@ constexpr size_t smem_bytes() {
   return (pipe > merge ? pipe : merge) + 1024;  // + slack for the 1024-byte base alignment
 }
 
-template <int D, int KF, int VF, int NTW, bool CAUSAL>
-qps_status launch_mma_t(const AttnParams& p, cudaStream_t s) {
+template <int D, int KF, int VF, int NTW, bool CAUSAL, class P>
+qps_status launch_mma_t(const P& p, cudaStream_t s) {
   using G = Geo<D, KF, VF, NTW>;
   constexpr size_t smem = smem_bytes<D, KF, VF, NTW>();
   static_assert(smem <= 227 * 1024, "tile staging exceeds the 227 KB shared memory of one CTA");
@@ -1417,6 +1623,19 @@ qps_status launch_mma_t(const AttnParams& p, cudaStream_t s) {
   TmaSet maps;
   std::memset(&maps, 0, sizeof(maps));
   const int nb = p.shared ? 1 : p.batch;
+  constexpr bool PAGED = std::is_same<P, PagedAttnParams>::value;
+  if constexpr (PAGED) {  // [row bytes][positions of a page][KV heads][pages]
+    const int page = 1 << p.page_shift, rows = page < G::TT ? page : G::TT;
+    auto map = [&](TensorMap* m, const void* base, int rb, int ib, int sw) {
+      return encode_plane_map(m, base, rb, page, p.hkv, page, (int)p.n_pages, (int64_t)p.hkv * page, ib, sw, rows);
+    };
+    if (!map(&maps.k, p.k.data, G::K_RB, G::PK::IB, G::PK::SW) || !map(&maps.v, p.v.data, G::V_RB, G::PV::IB, G::PV::SW))
+      return QPS_ERR_CUDA;
+    if constexpr (G::PKA::TMA)
+      if (!map(&maps.ka, p.k.aux, G::K_ARB, G::PKA::IB, G::PKA::SW)) return QPS_ERR_CUDA;
+    if constexpr (G::PVA::TMA)
+      if (!map(&maps.va, p.v.aux, G::V_ARB, G::PVA::IB, G::PVA::SW)) return QPS_ERR_CUDA;
+  } else {
   if (!encode_plane_map(&maps.k, p.k.data, G::K_RB, p.end, p.hkv, p.k.head, nb, p.k.batch, G::PK::IB, G::PK::SW, G::TT) ||
       !encode_plane_map(&maps.v, p.v.data, G::V_RB, p.end, p.hkv, p.v.head, nb, p.v.batch, G::PV::IB, G::PV::SW, G::TT))
     return QPS_ERR_CUDA;
@@ -1426,7 +1645,8 @@ qps_status launch_mma_t(const AttnParams& p, cudaStream_t s) {
   if constexpr (G::PVA::TMA)
     if (!encode_plane_map(&maps.va, p.v.aux, G::V_ARB, p.end, p.hkv, p.v.head, nb, p.v.batch, G::PVA::IB, G::PVA::SW, G::TT))
       return QPS_ERR_CUDA;
-  auto kern = attn_mma_kernel<D, KF, VF, NTW, CAUSAL>;
+  }
+  auto kern = attn_mma_kernel<D, KF, VF, NTW, CAUSAL, P>;
   // Ask for enough shared memory that no more than G::CTAS CTAs fit on an SM: under
   // programmatic launch the next grid's CTAs would otherwise take a spare slot early
   // and pile three of them onto some SMs (the q8_0 Qwen-like window: 39.5 -> 45 us).
@@ -1438,7 +1658,8 @@ qps_status launch_mma_t(const AttnParams& p, cudaStream_t s) {
   QPS_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_launch));
   constexpr int ROWS = 8 * NTW;
   const int rgroups = (p.rows_per_cta + ROWS - 1) / ROWS;
-  const dim3 grid(p.n_split * rgroups, p.hkv, p.shared ? 1 : p.batch);
+  dim3 grid(p.n_split * rgroups, p.hkv, p.shared ? 1 : p.batch);
+  if constexpr (PAGED) grid = dim3((p.shared ? p.n_split : p.target + p.batch) * rgroups, p.hkv, 1);
   // launched with programmatic stream serialization: overlaps this grid's launch with
   // the end of the previous kernel on the stream (the kernel waits before any global
   // memory access)
@@ -1462,8 +1683,8 @@ qps_status launch_mma_t(const AttnParams& p, cudaStream_t s) {
 // limit; SET selects the pairings: 0 K F16 / Q8_0 with V F16 / Q8_0 / TQ3, 1 the same K
 // with V TQ2 / TQ4, 2 a TurboQuant K with V of the same tier.  The sets live in
 // separate translation units.
-template <int D, bool CAUSAL, int SET>
-qps_status launch_mma_d(const AttnParams& p, cudaStream_t s) {
+template <int D, bool CAUSAL, int SET, class P>
+qps_status launch_mma_d(const P& p, cudaStream_t s) {
   // 8-row n-tiles per warp: more only where the accumulators still fit in registers
   const int ntw = mma_tile_rows(D, p.rows_per_cta, p.shared != 0) / 8;
 #define QPS_MMA_CASE(KF, VF)                                                       \

@@ -1,0 +1,333 @@
+// Decode attention over a paged cache: argument checks, the split into chunks, and the
+// merge of the chunks' parts.  The attention itself is attn_mma.cuh's tensor-core kernel
+// over page tables.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <string>
+
+#include "paged.h"
+
+namespace qps {
+namespace {
+
+// ---- merge --------------------------------------------------------------------------------
+// One CTA per output row: M = max lse, w = exp(lse - M), o = sum w o / sum w over the
+// prefix's parts and the row's own chunks.  D / 4 threads read one part's row (16 bytes
+// each), 1024 / D parts side by side and kU of each in flight; every thread keeps its
+// maximum online and the groups meet in shared memory.  A row whose only part was written
+// by the attention is skipped, a row without any gets O = 0, lse = -inf.
+constexpr int kMergeThreads = 256;
+constexpr int kU = 4;
+
+__device__ __forceinline__ void store_out(void* o, int dtype, int64_t at, float4 v) {
+  if (dtype == QPS_DT_F32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(o) + at) = v;
+  } else {
+    uint2 w;
+    if (dtype == QPS_DT_F16) {
+      const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(o) + at) = w;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
+  constexpr int COLS = D / 4, GROUPS = kMergeThreads / COLS;
+  __shared__ float wm[GROUPS], wd[GROUPS];
+  __shared__ float4 wacc[GROUPS][COLS];
+  const int lane = threadIdx.x & 31;
+  const int rows = p.n_q * p.hq;
+  const int64_t row = blockIdx.x;
+  const int b = (int)(row / rows);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the sequence's chunks, as the attention counted them
+  const int cu = paged_chunk_units(p, lane);
+  int first = 0;
+  for (int i = lane; i < b; i += 32) first += (paged_units(paged_len(p, i), p.prefix_len) + cu - 1) / cu;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+  const int count = (paged_units(paged_len(p, b), p.prefix_len) + cu - 1) / cu;
+  if (count == 1 && p.n_prefix == 0) return;  // written by the attention
+  const int total = p.n_prefix + count;
+  const int grp = threadIdx.x / COLS, col = (threadIdx.x % COLS) * 4;
+  float m = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int t0 = grp; t0 < total; t0 += GROUPS * kU) {
+    float l[kU];
+    float4 v[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int t = t0 + u * GROUPS;
+      l[u] = -INFINITY;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < total) {
+        const bool pre = t < p.n_prefix;
+        const int64_t at = pre ? (int64_t)t * p.rows_total + row : (int64_t)(first + t - p.n_prefix) * rows + (row - (int64_t)b * rows);
+        l[u] = (pre ? p.pre_lse : p.own_lse)[at];
+        v[u] = *reinterpret_cast<const float4*>((pre ? p.pre_o : p.own_o) + at * D + col);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (l[u] == -INFINITY) continue;
+      if (l[u] > m) {
+        const float cr = __expf(m - l[u]);  // 0 when m == -inf
+        den *= cr;
+        acc = make_float4(acc.x * cr, acc.y * cr, acc.z * cr, acc.w * cr);
+        m = l[u];
+      }
+      const float w = __expf(l[u] - m);
+      den += w;
+      acc.x = fmaf(w, v[u].x, acc.x);
+      acc.y = fmaf(w, v[u].y, acc.y);
+      acc.z = fmaf(w, v[u].z, acc.z);
+      acc.w = fmaf(w, v[u].w, acc.w);
+    }
+  }
+  if (threadIdx.x % COLS == 0) {
+    wm[grp] = m;
+    wd[grp] = den;
+  }
+  wacc[grp][threadIdx.x % COLS] = acc;
+  __syncthreads();
+  if (grp != 0) return;
+  float mx = -INFINITY, dt = 0.f;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) mx = fmaxf(mx, wm[g]);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    const float f = wm[g] == -INFINITY ? 0.f : __expf(wm[g] - mx);
+    dt += wd[g] * f;
+    const float4 a = wacc[g][col / 4];
+    s.x = fmaf(a.x, f, s.x);
+    s.y = fmaf(a.y, f, s.y);
+    s.z = fmaf(a.z, f, s.z);
+    s.w = fmaf(a.w, f, s.w);
+  }
+  // (a NaN logit makes its row's sums NaN: it stays one)
+  const bool empty = mx == -INFINITY && dt == 0.f;
+  const float inv = empty ? 0.f : 1.f / dt;
+  store_out(p.out, p.out_dtype, row * D + col, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
+  if (col == 0) p.out_lse[row] = empty ? -INFINITY : mx + logf(dt);
+}
+
+template <int D>
+qps_status launch_merge(const PagedAttnParams& p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.rows_total);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p));
+  count_launch();
+  QPS_CUDA_TRY(cudaGetLastError());
+  return QPS_OK;
+}
+
+// ---- plan -----------------------------------------------------------------------------------
+struct Plan {
+  PagedAttnParams p;
+  size_t off_pre_lse, off_own_o, off_own_lse, bytes;
+};
+
+// Chunks of the sequences' own positions: enough for kWaves rounds of the CTAs the GPU
+// holds, so that ragged lengths level out, each at least kMinPositions long, so that a
+// part is worth its merge.
+constexpr int kWaves = 2;
+constexpr int kMinPositions = 128;
+
+qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
+  const std::string n("attn_decode_paged");
+  if (!a) return fail(QPS_ERR_INVALID_ARG, n + ": args is NULL");
+  PagedKv kv;
+  qps_status st = check_paged_kv(a->kv, "attn_decode_paged", &kv);
+  if (st != QPS_OK) return st;
+  if (!a->q || !aligned_to(a->q, 16)) return fail(QPS_ERR_INVALID_ARG, n + ": q is NULL or not 16-byte aligned");
+  if (a->batch < 1 || a->batch > 65535) return fail(QPS_ERR_INVALID_ARG, n + ": batch must be in [1, 65535]");
+  if (a->n_q < 1 || a->n_q > 64) return fail(QPS_ERR_INVALID_ARG, n + ": n_q must be in [1, 64]");
+  if (a->hq < 1 || a->hq % kv.hkv) return fail(QPS_ERR_INVALID_ARG, n + ": hq must be a multiple of hkv");
+  const int group = a->hq / kv.hkv, rows = a->n_q * group;
+  if (group > 1024 || rows > 1024) return fail(QPS_ERR_UNSUPPORTED, n + ": more than 1024 query rows per KV head and sequence");
+  if (a->q_batch_stride % 8 || (a->batch > 1 && a->q_batch_stride < (int64_t)a->n_q * a->hq * kv.d))
+    return fail(QPS_ERR_INVALID_ARG, n + ": q_batch_stride must be >= n_q*hq*d and a multiple of 8");
+  if (!a->page_table || !aligned_to(a->page_table, 4) || !a->kv_lens || !aligned_to(a->kv_lens, 4))
+    return fail(QPS_ERR_INVALID_ARG, n + ": page_table / kv_lens are NULL or misaligned");
+  if (a->table_width < 1 || ((int64_t)a->table_width << kv.page_shift) >= ((int64_t)1 << 31) - 64)
+    return fail(QPS_ERR_INVALID_ARG, n + ": need table_width >= 1 and table_width * page_size < 2^31 - 64");
+  if (a->batch > 1 && a->table_stride < a->table_width)
+    return fail(QPS_ERR_INVALID_ARG, n + ": table_stride must be >= table_width");
+  if (a->shared_len < 0 || a->shared_len & ((1 << kv.page_shift) - 1) ||
+      a->shared_len > ((int64_t)a->table_width << kv.page_shift))
+    return fail(QPS_ERR_INVALID_ARG, n + ": shared_len must be a multiple of page_size within the table");
+  if (a->o_dtype != QPS_DT_F16 && a->o_dtype != QPS_DT_BF16 && a->o_dtype != QPS_DT_F32)
+    return fail(QPS_ERR_INVALID_ARG, n + ": unknown o_dtype");
+  if (!std::isfinite(a->scale) || !std::isfinite(a->softcap))
+    return fail(QPS_ERR_INVALID_ARG, n + ": scale and softcap must be finite");
+  const int64_t rows_total = (int64_t)a->batch * a->n_q * a->hq;
+  if (rows_total > 0x7fffffffLL) return fail(QPS_ERR_UNSUPPORTED, n + ": too many rows");
+  const int sms = sm_count_current();
+  if (sms <= 0) return fail(QPS_ERR_CUDA, n + ": cannot query the current device's SM count");
+
+  PagedAttnParams& p = out->p;
+  p = PagedAttnParams{};
+  p.q = reinterpret_cast<const __half*>(a->q);
+  p.q_bstride = a->batch > 1 ? a->q_batch_stride : (int64_t)a->n_q * a->hq * kv.d;
+  p.batch = a->batch;
+  p.hq = a->hq;
+  p.hkv = kv.hkv;
+  p.d = kv.d;
+  p.group = group;
+  p.kfmt = kv.kfmt;
+  p.vfmt = kv.vfmt;
+  const int64_t page = (int64_t)1 << kv.page_shift;
+  p.k = KvSide{kv.k[0], kv.k[1], kv.k[2], 1, page, kv.hkv * page};
+  p.v = KvSide{kv.v[0], kv.v[1], kv.v[2], 1, page, kv.hkv * page};
+  p.scale = a->scale;
+  p.softcap = a->softcap > 0.f ? a->softcap : 0.f;
+  p.n_q = a->n_q;
+  p.causal = a->causal ? 1 : 0;
+  p.rows_total = rows_total;
+  p.q_elems = (int64_t)(a->batch - 1) * p.q_bstride + (int64_t)a->n_q * a->hq * kv.d;
+  p.k_rows = p.v_rows = kv.n_pages * page * kv.hkv;
+  const int g = a->kv.tq_block == 0 ? kv.d : a->kv.tq_block;
+  p.vblock = g;
+  p.v_out_scale = (float)(1.0 / std::sqrt((double)kv.d * g));
+  p.k_rot_scale = (float)(1.0 / std::sqrt((double)g));
+  p.k_norm_scale = (float)(1.0 / std::sqrt((double)kv.d));
+  if (is_tq(kv.vfmt)) {
+    for (int i = 0; i < kv.d / 32; ++i) {
+      p.vsigns[i] = a->kv.signs1[i];
+      p.vsigns2[i] = a->kv.signs2 ? a->kv.signs2[i] : 0u;
+    }
+    const Codebook* cb = tq_codebook(tq_bits(kv.vfmt));
+    for (int i = 0; i < cb->n; ++i) p.tq_levels[i] = cb->levels[i];
+  }
+  p.table = a->page_table;
+  p.table_stride = a->batch > 1 ? a->table_stride : a->table_width;
+  p.lens = a->kv_lens;
+  p.n_pages = kv.n_pages;
+  p.page_shift = kv.page_shift;
+  p.table_width = a->table_width;
+  p.out_dtype = a->o_dtype;
+
+  // the prefix: whole tiles of the shared positions (what is left of them is read through
+  // each sequence's own entries, which name the same pages)
+  p.prefix_len = a->batch > 1 ? (int)(a->shared_len & ~(int64_t)31) : 0;
+  if (p.prefix_len > 0) {
+    const int all = a->batch * rows, tile_rows = mma_tile_rows(kv.d, all, true);
+    const int ctas = kv.hkv * ((all + tile_rows - 1) / tile_rows);
+    const int slots = mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
+    const int want = std::max(1, std::min((slots + ctas - 1) / ctas, (p.prefix_len + 511) / 512));
+    const int64_t chunk = ((p.prefix_len + want - 1) / want + 31) / 32 * 32;
+    p.n_prefix = (int)((p.prefix_len + chunk - 1) / chunk);
+    p.chunk = chunk;
+  }
+  {
+    const int tile_rows = mma_tile_rows(kv.d, rows, false);
+    const int ctas = kv.hkv * ((rows + tile_rows - 1) / tile_rows);
+    const int slots = mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
+    p.target = std::max(1, (kWaves * slots + ctas - 1) / ctas);
+    p.min_units = kMinPositions / kPagedUnit;
+  }
+  const size_t own = (size_t)(p.target + p.batch) * a->n_q * a->hq, pre = (size_t)p.n_prefix * rows_total;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  out->off_pre_lse = up(pre * kv.d * sizeof(float));
+  out->off_own_o = out->off_pre_lse + up(pre * sizeof(float));
+  out->off_own_lse = out->off_own_o + up(own * kv.d * sizeof(float));
+  out->bytes = out->off_own_lse + up(own * sizeof(float));
+  return QPS_OK;
+}
+
+qps_status launch_paged(const PagedAttnParams& p, cudaStream_t s) {
+  switch (p.d) {
+    case 64: return launch_paged_mma_d64(p, s);
+    case 128: return launch_paged_mma_d128(p, s);
+    case 256: return launch_paged_mma_d256(p, s);
+    default: return launch_paged_mma_d512(p, s);
+  }
+}
+
+qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
+  Plan pl;
+  qps_status st = plan_paged(a, &pl);
+  if (st != QPS_OK) return st;
+  const std::string n("attn_decode_paged");
+  if (!a->o || !aligned_to(a->o, 16) || !a->lse || !aligned_to(a->lse, 4))
+    return fail(QPS_ERR_INVALID_ARG, n + ": o / lse are NULL or misaligned (o: 16 bytes)");
+  if (!a->workspace || a->workspace_bytes < pl.bytes)
+    return fail(QPS_ERR_INVALID_ARG, n + ": workspace missing or smaller than qps_attn_paged_plan reports");
+  if (!aligned_to(a->workspace, 256)) return fail(QPS_ERR_INVALID_ARG, n + ": workspace must be 256-byte aligned");
+  PagedAttnParams& p = pl.p;
+  p.err = device_error_word();
+  if (!p.err) return fail(QPS_ERR_CUDA, n + ": cannot allocate the device error word");
+  char* ws = reinterpret_cast<char*>(a->workspace);
+  p.pre_o = reinterpret_cast<float*>(ws);
+  p.pre_lse = reinterpret_cast<float*>(ws + pl.off_pre_lse);
+  p.own_o = reinterpret_cast<float*>(ws + pl.off_own_o);
+  p.own_lse = reinterpret_cast<float*>(ws + pl.off_own_lse);
+  p.out = a->o;
+  p.out_lse = a->lse;
+  const int rows = p.n_q * p.group;
+  if (p.n_prefix > 0) {
+    PagedAttnParams f = p;
+    f.shared = 1;
+    f.rows_per_cta = p.batch * rows;
+    f.n_split = p.n_prefix;
+    f.begin = 0;
+    f.end = p.prefix_len;
+    st = launch_paged(f, s);
+    if (st != QPS_OK) return st;
+  }
+  p.shared = 0;
+  p.rows_per_cta = rows;
+  p.chunk = 0;
+  st = launch_paged(p, s);
+  if (st != QPS_OK) return st;
+  switch (p.d) {
+    case 64: return launch_merge<64>(p, s);
+    case 128: return launch_merge<128>(p, s);
+    case 256: return launch_merge<256>(p, s);
+    default: return launch_merge<512>(p, s);
+  }
+}
+
+}  // namespace
+}  // namespace qps
+
+using namespace qps;
+
+extern "C" {
+
+qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* workspace_bytes) {
+  try {
+    Plan pl;
+    const qps_status st = plan_paged(a, &pl);
+    if (st == QPS_OK && workspace_bytes) *workspace_bytes = pl.bytes;
+    return st;
+  } catch (const std::exception&) {
+    return QPS_ERR_INTERNAL;
+  }
+}
+
+qps_status qps_attn_decode_paged(const qps_paged_attn_args* a, void* stream) {
+  try {
+    return attn_decode_paged(a, reinterpret_cast<cudaStream_t>(stream));
+  } catch (const std::exception&) {
+    return QPS_ERR_INTERNAL;
+  }
+}
+
+}  // extern "C"

@@ -37,13 +37,14 @@ bool encode_plane_map(TensorMap* map, const void* base, int row_bytes, int64_t t
 int sm_count_current();
 // The current device's error word (library-owned, allocated on first use, zeroed).
 // Bits: kErrTimeout, a bounded in-kernel wait gave up; kErrBounds, a bounds check of the
-// checked build failed and its access was skipped.
+// checked build failed and its access was skipped; kErrIndex, a position, slot, page or
+// length that a kernel read was out of range and was not followed.
 // The word is the first of kErrWords: [1] counts bounded waits that gave up, [2..11]
 // record the first of them (block x / y / z, warp, the tile k whose wait ran out, tiles
 // issued, the warp's tiles, the chunk's positions, the ns the drain wait of that tile
 // took, 1 if it then completed), [12] the ns of the self-test's full bounded wait.
 unsigned int* device_error_word();
-constexpr unsigned int kErrTimeout = 1u, kErrBounds = 2u;
+constexpr unsigned int kErrTimeout = 1u, kErrBounds = 2u, kErrIndex = 4u;
 constexpr int kErrWords = 16;
 
 // ---- the checked build ----------------------------------------------------------------

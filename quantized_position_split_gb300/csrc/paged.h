@@ -1,0 +1,72 @@
+// Shared by the calls around the paged KV cache: argument checks, the resolved cache and
+// the attention's parameters.
+#pragma once
+
+#include "internal.h"
+
+namespace qps {
+
+// Sizes of a checked qps_paged_kv (page_size is a power of two).
+struct PagedKv {
+  int kfmt, vfmt, hkv, d, page_shift;
+  int64_t n_pages;
+  uint8_t *k[3], *v[3];  // data, aux, aux2
+};
+
+inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+inline int dtype_bytes(int dt) { return dt == QPS_DT_F32 ? 4 : 2; }
+
+qps_status check_paged_kv(const qps_paged_kv& kv, const char* call, PagedKv* out);
+
+// Parameters of the paged attention kernels: the tensor-core kernel's own (q, heads,
+// scales, rotation; n_split, chunk and part_offset are the prefix's) and the page tables.
+struct PagedAttnParams : AttnParams {
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  int64_t n_pages;
+  int page_shift, table_width;
+  int prefix_len;     // positions attended by the prefix launch (a multiple of 32)
+  int target;         // chunks per (KV head, row group) the sequences are cut into, about
+  int min_units;      // smallest chunk, in units
+  int n_prefix;       // parts of the prefix
+  float* pre_o;       // f32 [n_prefix][rows_total][D], [n_prefix][rows_total]
+  float* pre_lse;
+  float* own_o;       // f32 [chunk][n_q*hq][D], [chunk][n_q*hq]
+  float* own_lse;
+  void* out;          // the call's o (out_dtype) and lse
+  float* out_lse;
+  int out_dtype;
+};
+
+// The chunking of the sequences' own positions [prefix_len, len), the same in the
+// attention and in the merge: units of 32 positions, C units a chunk, sequence b's
+// chunks first[b] .. first[b] + count - 1.  C is such that all chunks together number at
+// most `target` + batch.
+__device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
+  const int n = p.lens[b];
+  const int most = p.table_width << p.page_shift;
+  const int cut = min(max(n, 0), most);
+  if (cut != n) atomicOr(p.err, kErrIndex);
+  return cut;
+}
+constexpr int kPagedUnit = 32;  // a whole number of any instance's tiles
+__device__ __forceinline__ int paged_units(int len, int prefix) {
+  return len > prefix ? (len - prefix + kPagedUnit - 1) / kPagedUnit : 0;
+}
+
+// Chunk length in units; every lane of the warp takes part.
+__device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int lane) {
+  int total = 0;
+  for (int b = lane; b < p.batch; b += 32) total += paged_units(paged_len(p, b), p.prefix_len);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  return max(p.min_units, (total + p.target - 1) / p.target);
+}
+
+qps_status launch_paged_mma_d64(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_mma_d128(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_mma_d256(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_mma_d512(const PagedAttnParams& p, cudaStream_t s);
+
+}  // namespace qps
