@@ -1,0 +1,6 @@
+// qk_norm_rope instances for float16 rows (see head_rows.cuh).
+#include "head_rows.cuh"
+
+namespace qps {
+qps_status rope_f16(int d, const RopeP& p, cudaStream_t s) { return rows::rope_by_d<__half>(d, p, s); }
+}  // namespace qps

@@ -89,24 +89,28 @@ def _rotation(rope: Optional[Rope], positions, tokens: int, device) -> tuple:
     return N.RotationArgs(t.data_ptr(), t.shape[0], t.shape[1], 1 if rope.interleaved else 0), positions.data_ptr()
 
 
-def _call(fn, a, stream):
-    """Run a library call for a block's device, on ``stream`` (default: that device's
-    current stream)."""
-    dev = a._device
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(fn, a, stream)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(a, stream):
+    """Run a block's call on its device, on ``stream`` (default: that device's current
+    stream)."""
+    if a._index != torch.cuda.current_device():
+        with torch.cuda.device(a._index):
+            return _call(a, stream)
     if stream is None:
-        s = torch.cuda.current_stream().cuda_stream
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-    st = fn(a._ref, s)
+        stream = _raw_stream(a._index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    st = a._fn(a._ref, stream)
     if st:
         N.check(st)
 
 
-def _block(a, device, keep):
-    a._device = device
+def _block(a, fn, device, keep):
+    a._fn = getattr(N.load(), fn)
+    a._index = device.index
     a._ref = ctypes.byref(a)
     a._tensors = keep
     return a
@@ -155,12 +159,12 @@ def qk_rope_args(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, positions
     a.k_norm = _norm(on_k, k_norm if on_k else None, d, eps, norm_offset, "k_norm", dev)
     a.rot, a.positions = _rotation(rope, positions, tokens, dev)
     a._out = (q_out, k_out)
-    return _block(a, dev, (q, k, q_out, k_out, q_norm, k_norm, rope, positions))
+    return _block(a, "qps_qk_norm_rope", dev, (q, k, q_out, k_out, q_norm, k_norm, rope, positions))
 
 
 def qk_norm_rope(a: N.QkRopeArgs, stream=None):
     """Norm and rotate the rows of ``qk_rope_args``; returns (q_out, k_out)."""
-    _call(N.load().qps_qk_norm_rope, a, stream)
+    _call(a, stream)
     return a._out
 
 
@@ -246,12 +250,12 @@ def paged_append_args(cache: PagedKV, k: torch.Tensor, v: torch.Tensor, slots: t
     a.k_norm = _norm(on, k_norm if on else None, cache.d, eps, norm_offset, "k_norm", dev)
     a.rot, a.positions = _rotation(rope, positions, tokens, dev)
     a.slots = _tensor(slots, "slots", dev, torch.int64, (tokens,)).data_ptr()
-    return _block(a, dev, (cache, k, v, slots, positions, rope, k_norm))
+    return _block(a, "qps_kv_append_paged", dev, (cache, k, v, slots, positions, rope, k_norm))
 
 
 def kv_append_paged(a: N.PagedAppendArgs, stream=None) -> None:
     """Encode the rows of ``paged_append_args`` into their slots."""
-    _call(N.load().qps_kv_append_paged, a, stream)
+    _call(a, stream)
 
 
 def paged_attn_args(q: torch.Tensor, cache: PagedKV, page_table: torch.Tensor, kv_lens: torch.Tensor, *, scale: float,
@@ -304,10 +308,10 @@ def paged_attn_args(q: torch.Tensor, cache: PagedKV, page_table: torch.Tensor, k
     _tensor(workspace, "workspace", dev, torch.uint8)
     a.o, a.lse, a.workspace, a.workspace_bytes = o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel()
     a._out = (o, lse)
-    return _block(a, dev, (q, cache, page_table, kv_lens, o, lse, workspace))
+    return _block(a, "qps_attn_decode_paged", dev, (q, cache, page_table, kv_lens, o, lse, workspace))
 
 
 def attn_decode_paged(a: N.PagedAttnArgs, stream=None):
     """Decode attention of ``paged_attn_args``; returns (o, lse)."""
-    _call(N.load().qps_attn_decode_paged, a, stream)
+    _call(a, stream)
     return a._out
