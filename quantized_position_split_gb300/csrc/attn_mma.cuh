@@ -30,6 +30,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstring>
 #include <type_traits>
 
@@ -397,33 +398,12 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   bool whole = false;  // (paged) the chunk is all its rows attend: the output itself is written
   if constexpr (PAGED) {
     if (!p.shared) {  // chunk number `split` of the batch: find its sequence and positions
-      const int cu = paged_chunk_units(p, lane);
-      int before = 0, found = -1, at = 0, len = 0, n = 0;
-      for (int b0 = 0; b0 < p.batch && found < 0; b0 += 32) {
-        const int b = b0 + lane;
-        const int bl = b < p.batch ? paged_len(p, b) : 0;
-        const int cnt = (paged_units(bl, p.prefix_len) + cu - 1) / cu;
-        int sum = cnt;  // inclusive scan over the lanes
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += v;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > split);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          found = b0 + src;
-          n = __shfl_sync(0xffffffffu, cnt, src);
-          at = split - (before + __shfl_sync(0xffffffffu, sum, src) - n);
-          len = __shfl_sync(0xffffffffu, bl, src);
-        }
-        before += __shfl_sync(0xffffffffu, sum, 31);
-      }
-      if (found < 0) return;  // more CTAs than chunks (every warp finds the same)
-      bz = found;
-      whole = n == 1 && p.prefix_len == 0;
-      t0 = p.prefix_len + (int64_t)at * cu * kPagedUnit;
-      t1 = min((int64_t)len, t0 + (int64_t)cu * kPagedUnit);
+      const PagedChunk ch = paged_find(p, split, lane);
+      if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
+      bz = ch.b;
+      whole = ch.whole;
+      t0 = ch.t0;
+      t1 = ch.t1;
     }
   }
 
@@ -448,6 +428,12 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     for (int idx = threadIdx.x; idx < nrows * D; idx += G::NW * 32) {
       const int r = idx / D, dd = idx % D;
       const int64_t row = out_row(row0 + r);
+      if constexpr (PAGED) {  // (an empty sequence: `whole`)
+        if (p.out_dtype == QPS_DT_F32) reinterpret_cast<float*>(p.out)[row * D + dd] = 0.f;
+        else reinterpret_cast<uint16_t*>(p.out)[row * D + dd] = 0;
+        if (dd == 0) p.out_lse[row] = -INFINITY;
+        continue;
+      }
       if (!in_bounds(part < p.parts_cap && row >= 0 && row < p.rows_total, p.err)) continue;
       p.o_parts[((int64_t)part * p.rows_total + row) * D + dd] = 0.f;
       if (dd == 0) p.lse_parts[(int64_t)part * p.rows_total + row] = -INFINITY;
@@ -1571,7 +1557,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     const int64_t row = orow[r];
     const bool empty = PAGED ? den == 0.f : !(den > 0.f);  // (paged: a NaN logit stays one)
     if constexpr (PAGED) {
-      if (!in_bounds(part < (p.shared ? p.n_prefix : p.target + p.batch) && row >= 0 && row < p.rows_total, p.err)) continue;
+      if (!in_bounds(part < (p.shared ? p.n_prefix : p.max_chunks) && row >= 0 && row < p.rows_total, p.err)) continue;
       const float ov = empty ? 0.f : val / den;
       const float lv = empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
       if (whole) {  // nothing to merge: the one rounding to the output type
@@ -1655,11 +1641,19 @@ qps_status launch_mma_t(const P& p, cudaStream_t s) {
   constexpr size_t smem_launch = smem > smem_floor ? smem : smem_floor;
   static_assert(G::CTAS * (smem_launch + kReserved) <= kSmPerSm || smem_launch == smem,
                 "the padding must not cost a CTA per SM");
-  QPS_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_launch));
+  // (once for each device: the call costs about as much as a launch's own bookkeeping)
+  static std::atomic<uint64_t> sized{0};
+  int dev = 0;
+  QPS_CUDA_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(sized.load(std::memory_order_relaxed) & bit) || !bit) {
+    QPS_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_launch));
+    sized.fetch_or(bit, std::memory_order_relaxed);
+  }
   constexpr int ROWS = 8 * NTW;
   const int rgroups = (p.rows_per_cta + ROWS - 1) / ROWS;
   dim3 grid(p.n_split * rgroups, p.hkv, p.shared ? 1 : p.batch);
-  if constexpr (PAGED) grid = dim3((p.shared ? p.n_split : p.target + p.batch) * rgroups, p.hkv, 1);
+  if constexpr (PAGED) grid = dim3((p.shared ? p.n_split : p.max_chunks) * rgroups, p.hkv, 1);
   // launched with programmatic stream serialization: overlaps this grid's launch with
   // the end of the previous kernel on the stream (the kernel waits before any global
   // memory access)

@@ -51,10 +51,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
   // the sequence's chunks, as the attention counted them
   const int cu = paged_chunk_units(p, lane);
   int first = 0;
-  for (int i = lane; i < b; i += 32) first += (paged_units(paged_len(p, i), p.prefix_len) + cu - 1) / cu;
+  for (int i = lane; i < b; i += 32) first += paged_chunks(p, paged_len(p, i), cu);
 #pragma unroll
   for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  const int count = (paged_units(paged_len(p, b), p.prefix_len) + cu - 1) / cu;
+  const int count = paged_chunks(p, paged_len(p, b), cu);
   if (count == 1 && p.n_prefix == 0) return;  // written by the attention
   const int total = p.n_prefix + count;
   const int grp = threadIdx.x / COLS, col = (threadIdx.x % COLS) * 4;
@@ -140,46 +140,55 @@ qps_status launch_merge(const PagedAttnParams& p, cudaStream_t s) {
 // ---- plan -----------------------------------------------------------------------------------
 struct Plan {
   PagedAttnParams p;
+  bool prefix_tm, own_tm;  // which kernel the launches are
+  bool merge;  // some row can have several parts
   size_t off_pre_lse, off_own_o, off_own_lse, bytes;
 };
 
-// Chunks of the sequences' own positions: enough for kWaves rounds of the CTAs the GPU
-// holds, so that ragged lengths level out, each at least kMinPositions long, so that a
-// part is worth its merge.
+// Chunks of the sequences' own positions: as many as the CTAs the GPU holds for one
+// sequence, kWaves times that for several, so that ragged lengths level out; each at least
+// kMinPositions long, so that a part is worth its merge.
 constexpr int kWaves = 2;
 constexpr int kMinPositions = 128;
 
+// Rows of a KV head from which attn_tm.cuh's kernel is taken: it works on 128 rows at a
+// time whatever their number, the other on 8 to 24 and reads the positions again for each.
+constexpr int kManyRows = 32;
+bool takes_tm(const PagedKv& kv, int rows) {
+  return kv.kfmt == QPS_FMT_F16 && kv.vfmt == QPS_FMT_F16 && (kv.d == 64 || kv.d == 128) && rows > kManyRows;
+}
+constexpr int kTmRows = 128, kTmTile = 128;  // of attn_tm.cuh
+
 qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
-  const std::string n("attn_decode_paged");
-  if (!a) return fail(QPS_ERR_INVALID_ARG, n + ": args is NULL");
+  if (!a) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: args is NULL");
   PagedKv kv;
   qps_status st = check_paged_kv(a->kv, "attn_decode_paged", &kv);
   if (st != QPS_OK) return st;
-  if (!a->q || !aligned_to(a->q, 16)) return fail(QPS_ERR_INVALID_ARG, n + ": q is NULL or not 16-byte aligned");
-  if (a->batch < 1 || a->batch > 65535) return fail(QPS_ERR_INVALID_ARG, n + ": batch must be in [1, 65535]");
-  if (a->n_q < 1 || a->n_q > 64) return fail(QPS_ERR_INVALID_ARG, n + ": n_q must be in [1, 64]");
-  if (a->hq < 1 || a->hq % kv.hkv) return fail(QPS_ERR_INVALID_ARG, n + ": hq must be a multiple of hkv");
+  if (!a->q || !aligned_to(a->q, 16)) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: q is NULL or not 16-byte aligned");
+  if (a->batch < 1 || a->batch > 65535) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: batch must be in [1, 65535]");
+  if (a->n_q < 1 || a->n_q > 64) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: n_q must be in [1, 64]");
+  if (a->hq < 1 || a->hq % kv.hkv) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: hq must be a multiple of hkv");
   const int group = a->hq / kv.hkv, rows = a->n_q * group;
-  if (group > 1024 || rows > 1024) return fail(QPS_ERR_UNSUPPORTED, n + ": more than 1024 query rows per KV head and sequence");
+  if (group > 1024 || rows > 1024) return fail(QPS_ERR_UNSUPPORTED, "attn_decode_paged: more than 1024 query rows per KV head and sequence");
   if (a->q_batch_stride % 8 || (a->batch > 1 && a->q_batch_stride < (int64_t)a->n_q * a->hq * kv.d))
-    return fail(QPS_ERR_INVALID_ARG, n + ": q_batch_stride must be >= n_q*hq*d and a multiple of 8");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: q_batch_stride must be >= n_q*hq*d and a multiple of 8");
   if (!a->page_table || !aligned_to(a->page_table, 4) || !a->kv_lens || !aligned_to(a->kv_lens, 4))
-    return fail(QPS_ERR_INVALID_ARG, n + ": page_table / kv_lens are NULL or misaligned");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: page_table / kv_lens are NULL or misaligned");
   if (a->table_width < 1 || ((int64_t)a->table_width << kv.page_shift) >= ((int64_t)1 << 31) - 64)
-    return fail(QPS_ERR_INVALID_ARG, n + ": need table_width >= 1 and table_width * page_size < 2^31 - 64");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: need table_width >= 1 and table_width * page_size < 2^31 - 64");
   if (a->batch > 1 && a->table_stride < a->table_width)
-    return fail(QPS_ERR_INVALID_ARG, n + ": table_stride must be >= table_width");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: table_stride must be >= table_width");
   if (a->shared_len < 0 || a->shared_len & ((1 << kv.page_shift) - 1) ||
       a->shared_len > ((int64_t)a->table_width << kv.page_shift))
-    return fail(QPS_ERR_INVALID_ARG, n + ": shared_len must be a multiple of page_size within the table");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: shared_len must be a multiple of page_size within the table");
   if (a->o_dtype != QPS_DT_F16 && a->o_dtype != QPS_DT_BF16 && a->o_dtype != QPS_DT_F32)
-    return fail(QPS_ERR_INVALID_ARG, n + ": unknown o_dtype");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: unknown o_dtype");
   if (!std::isfinite(a->scale) || !std::isfinite(a->softcap))
-    return fail(QPS_ERR_INVALID_ARG, n + ": scale and softcap must be finite");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: scale and softcap must be finite");
   const int64_t rows_total = (int64_t)a->batch * a->n_q * a->hq;
-  if (rows_total > 0x7fffffffLL) return fail(QPS_ERR_UNSUPPORTED, n + ": too many rows");
+  if (rows_total > 0x7fffffffLL) return fail(QPS_ERR_UNSUPPORTED, "attn_decode_paged: too many rows");
   const int sms = sm_count_current();
-  if (sms <= 0) return fail(QPS_ERR_CUDA, n + ": cannot query the current device's SM count");
+  if (sms <= 0) return fail(QPS_ERR_CUDA, "attn_decode_paged: cannot query the current device's SM count");
 
   PagedAttnParams& p = out->p;
   p = PagedAttnParams{};
@@ -227,22 +236,33 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
   // each sequence's own entries, which name the same pages)
   p.prefix_len = a->batch > 1 ? (int)(a->shared_len & ~(int64_t)31) : 0;
   if (p.prefix_len > 0) {
-    const int all = a->batch * rows, tile_rows = mma_tile_rows(kv.d, all, true);
+    const int all = a->batch * rows;
+    out->prefix_tm = takes_tm(kv, all);
+    const int tile_rows = out->prefix_tm ? kTmRows : mma_tile_rows(kv.d, all, true);
     const int ctas = kv.hkv * ((all + tile_rows - 1) / tile_rows);
-    const int slots = mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
-    const int want = std::max(1, std::min((slots + ctas - 1) / ctas, (p.prefix_len + 511) / 512));
-    const int64_t chunk = ((p.prefix_len + want - 1) / want + 31) / 32 * 32;
+    const int slots = out->prefix_tm ? sms : mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
+    const int64_t tile = out->prefix_tm ? kTmTile : 32, least = out->prefix_tm ? kTmTile : 512;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(out->prefix_tm ? slots / ctas : (slots + ctas - 1) / ctas,
+                                                                (p.prefix_len + least - 1) / least));
+    const int64_t chunk = ((p.prefix_len + want - 1) / want + tile - 1) / tile * tile;
     p.n_prefix = (int)((p.prefix_len + chunk - 1) / chunk);
     p.chunk = chunk;
   }
   {
-    const int tile_rows = mma_tile_rows(kv.d, rows, false);
+    out->own_tm = takes_tm(kv, rows);
+    const int tile_rows = out->own_tm ? kTmRows : mma_tile_rows(kv.d, rows, false);
     const int ctas = kv.hkv * ((rows + tile_rows - 1) / tile_rows);
-    const int slots = mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
-    p.target = std::max(1, (kWaves * slots + ctas - 1) / ctas);
+    const int slots = out->own_tm ? sms : mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
+    p.target = std::max(1, (a->batch > 1 ? kWaves : 1) * slots / ctas);
     p.min_units = kMinPositions / kPagedUnit;
+    p.unit_round = out->own_tm ? kTmTile / kPagedUnit : 1;
+    // chunks of a sequence that fills its table, and of all of them
+    const int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
+    const int64_t each = std::max<int64_t>(1, (most + kMinPositions - 1) / kMinPositions);
+    p.max_chunks = (int)std::min<int64_t>((int64_t)p.target + a->batch, each * a->batch);
+    out->merge = p.n_prefix > 0 || each > 1;
   }
-  const size_t own = (size_t)(p.target + p.batch) * a->n_q * a->hq, pre = (size_t)p.n_prefix * rows_total;
+  const size_t own = (size_t)p.max_chunks * a->n_q * a->hq, pre = (size_t)p.n_prefix * rows_total;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   out->off_pre_lse = up(pre * kv.d * sizeof(float));
   out->off_own_o = out->off_pre_lse + up(pre * sizeof(float));
@@ -252,6 +272,7 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
 }
 
 qps_status launch_paged(const PagedAttnParams& p, cudaStream_t s) {
+  if (p.tm) return p.d == 64 ? launch_paged_tm_d64(p, s) : launch_paged_tm_d128(p, s);
   switch (p.d) {
     case 64: return launch_paged_mma_d64(p, s);
     case 128: return launch_paged_mma_d128(p, s);
@@ -264,15 +285,14 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   Plan pl;
   qps_status st = plan_paged(a, &pl);
   if (st != QPS_OK) return st;
-  const std::string n("attn_decode_paged");
   if (!a->o || !aligned_to(a->o, 16) || !a->lse || !aligned_to(a->lse, 4))
-    return fail(QPS_ERR_INVALID_ARG, n + ": o / lse are NULL or misaligned (o: 16 bytes)");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: o / lse are NULL or misaligned (o: 16 bytes)");
   if (!a->workspace || a->workspace_bytes < pl.bytes)
-    return fail(QPS_ERR_INVALID_ARG, n + ": workspace missing or smaller than qps_attn_paged_plan reports");
-  if (!aligned_to(a->workspace, 256)) return fail(QPS_ERR_INVALID_ARG, n + ": workspace must be 256-byte aligned");
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: workspace missing or smaller than qps_attn_paged_plan reports");
+  if (!aligned_to(a->workspace, 256)) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: workspace must be 256-byte aligned");
   PagedAttnParams& p = pl.p;
   p.err = device_error_word();
-  if (!p.err) return fail(QPS_ERR_CUDA, n + ": cannot allocate the device error word");
+  if (!p.err) return fail(QPS_ERR_CUDA, "attn_decode_paged: cannot allocate the device error word");
   char* ws = reinterpret_cast<char*>(a->workspace);
   p.pre_o = reinterpret_cast<float*>(ws);
   p.pre_lse = reinterpret_cast<float*>(ws + pl.off_pre_lse);
@@ -284,6 +304,7 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   if (p.n_prefix > 0) {
     PagedAttnParams f = p;
     f.shared = 1;
+    f.tm = pl.prefix_tm;
     f.rows_per_cta = p.batch * rows;
     f.n_split = p.n_prefix;
     f.begin = 0;
@@ -292,10 +313,11 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
     if (st != QPS_OK) return st;
   }
   p.shared = 0;
+  p.tm = pl.own_tm;
   p.rows_per_cta = rows;
   p.chunk = 0;
   st = launch_paged(p, s);
-  if (st != QPS_OK) return st;
+  if (st != QPS_OK || !pl.merge) return st;
   switch (p.d) {
     case 64: return launch_merge<64>(p, s);
     case 128: return launch_merge<128>(p, s);

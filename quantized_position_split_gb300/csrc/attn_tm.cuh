@@ -1,0 +1,542 @@
+// Decode attention of many query rows per KV head on the fifth-generation tensor cores:
+// a shared prefix (the rows of a whole batch) or a verify batch, over fp16 pages.
+//
+// A CTA holds 128 query rows of one KV head (M of the products) and walks its chunk in
+// tiles of 128 positions:
+//     S = Q K^T          tcgen05.mma, Q and K in shared memory (K-major), S in TMEM (f32)
+//     P = 2^(S' - m)     4 warps, one query row a thread: no reduction crosses lanes
+//     O += P V           tcgen05.mma, P (fp16) in TMEM over the S it came from, V in shared
+//                        memory as it lies in the page (MN-major), O in TMEM (f32)
+// Even and odd tiles are two streams with an S, an O and softmax state of their own (TMEM:
+// 128 + 128 + 2 D <= 512 columns), so that one stream's exponentials run beside the other's
+// products; the two states are merged once at the end, as two parts would be.
+//
+// The running reference m of a row is raised only when a tile's maximum exceeds it by more
+// than 8 (log2): P stays <= 2^8 in fp16 and the rescale of O is rare.  P is rounded once to
+// fp16 (the operand type); sums, m and O are float32.
+//
+// Roles: warp 0 brings the tiles (tensor-map boxes of one page each, kStages ahead), warp 1
+// issues the products, warps 4-7 and 8-11 are the streams' softmax.  Every wait is bounded
+// (see mma::mbar_wait); one that gives up stops the CTA's roles, the copies and products in
+// flight are waited for, the TMEM is freed, and the error word is set.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "attn_mma.cuh"
+
+namespace qps {
+namespace tm {
+
+using mma::global_ns;
+using mma::mbar_expect_tx;
+using mma::mbar_init;
+using mma::mbar_try_wait;
+using mma::smem_addr;
+using mma::tma_load_4d;
+using mma::TmaSet;
+
+constexpr int kRows = 128, kTok = 128, kThreads = 384;
+
+template <int D>
+struct Geo {
+  static constexpr int CG = D / 64;                // 128-byte column groups of a row
+  static constexpr int TILE = kTok * D * 2;        // bytes of a K or V tile (and of Q)
+  static constexpr int STAGES = D == 64 ? 5 : 3;
+  static constexpr int K_OFF = TILE;               // Q first
+  static constexpr int V_OFF = K_OFF + STAGES * TILE;
+  static constexpr int BAR = V_OFF + STAGES * TILE;
+  static constexpr int SMEM = BAR + 256 + 1024;    // + slack for the 1024-byte base alignment
+  // TMEM columns
+  static constexpr int S_COL = 0, O_COL = 256;
+};
+
+// ---- tcgen05 -------------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, int cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, int cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
+}
+// 32 columns of the warp's 32 lanes
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle: rows (K-major) or k steps (MN-major)
+// of 128 bytes in groups of 8 (1024 bytes apart); `lead` is the distance of the next 64
+// columns of an MN-major operand (K-major: unused).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// f16 x f16 -> f32, M = 128; b_mn: B is MN-major
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---- the kernel ------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tm_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ TmaSet maps) {
+  using G = Geo<D>;
+  constexpr int ST = G::STAGES;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // ---- this CTA's rows and positions ------------------------------------------------------
+  const int rtiles = (p.rows_per_cta + kRows - 1) / kRows;
+  const int split = blockIdx.x / rtiles, row0 = (blockIdx.x % rtiles) * kRows;
+  const int head = blockIdx.y;
+  int bz = 0, t0, t1;
+  bool whole = false;
+  if (p.shared) {
+    t0 = split * (int)p.chunk;
+    t1 = min((int)p.end, t0 + (int)p.chunk);
+  } else {
+    const PagedChunk ch = paged_find(p, split, lane);
+    if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
+    bz = ch.b;
+    t0 = ch.t0;
+    t1 = ch.t1;
+    whole = ch.whole;
+  }
+  const int ntiles = t1 > t0 ? (t1 - t0 + kTok - 1) / kTok : 0;  // 0: an empty sequence
+
+  // ---- barriers, TMEM, queries ---------------------------------------------------------------
+  const uint32_t bars = sbase + G::BAR;
+  auto k_full = [&](int s) { return bars + 8 * s; };
+  auto k_empty = [&](int s) { return bars + 8 * (ST + s); };
+  auto v_full = [&](int s) { return bars + 8 * (2 * ST + s); };
+  auto v_empty = [&](int s) { return bars + 8 * (3 * ST + s); };
+  auto s_full = [&](int w) { return bars + 8 * (4 * ST + w); };
+  auto p_ready = [&](int w) { return bars + 8 * (4 * ST + 2 + w); };
+  const uint32_t all_done = bars + 8 * (4 * ST + 4);
+  static_assert(8 * (4 * ST + 5) <= 240, "barriers fit their region");
+  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + G::BAR + 240);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::BAR + 244);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4 * ST + 5; ++i) mbar_init(bars + 8 * i, i >= 4 * ST + 2 && i < 4 * ST + 4 ? 4 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    *abort_flag = 0;
+  }
+  if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
+  // Q [128][D], K-major: row r's 16-byte chunk c of a column group at r * 128 + (c ^ r % 8) * 16
+  for (int i = threadIdx.x; i < kRows * D / 8; i += kThreads) {
+    const int r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (rr < p.rows_per_cta) {
+      const int e = rr / p.group, h = head * p.group + rr % p.group;
+      const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
+      v = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+    }
+    *reinterpret_cast<uint4*>(smem + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+  }
+  mma::fence_proxy_async();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_word;
+
+  // Bounded wait of a whole warp, with one answer for all of its lanes; gives up at once
+  // when another role has.
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t since = global_ns();
+    for (;;) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      int over = 0;
+      if (lane == 0) {
+        over = *abort_flag;
+        if (!over && global_ns() - since >= mma::kWaitLimitNs) {
+          atomicOr(p.err, kErrTimeout);
+          atomicAdd(p.err + 1, 1u);
+          *abort_flag = over = 1;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, over, 0)) return false;
+    }
+  };
+  int issued_k = 0, issued_v = 0;  // (warp 0) tiles under way or landed
+
+  if (warp == 0) {
+    // ---- tiles: each box is min(page, 128) positions of one page and 64 columns ----------------
+    const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
+    const int32_t* row = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
+    auto load = [&](const TensorMap* map, uint32_t dst, uint32_t bar, int t) {
+      if (lane == 0) mbar_expect_tx(bar, G::TILE);
+      __syncwarp();
+      for (int i = lane; i < G::CG * nb; i += 32) {
+        const int cg = i % G::CG, r = i / G::CG, at = t + r * br;
+        int page = (int)p.n_pages;  // behind the last position, or out of range: zeros
+        if (at < t1) {
+          const int pg = row[at >> p.page_shift];
+          if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) page = pg;
+          else atomicOr(p.err, kErrIndex);
+        }
+        tma_load_4d(dst + cg * (kTok * 128) + r * br * 128, map, cg * 128, at & ((1 << p.page_shift) - 1), head, page, bar);
+      }
+    };
+    for (int j = 0; j < ntiles; ++j) {
+      const int s = j % ST;
+      const uint32_t par = ((j / ST) & 1) ^ 1;
+      if (j >= ST && !wait(k_empty(s), par)) break;
+      __syncwarp();
+      load(&maps.k, sbase + G::K_OFF + s * G::TILE, k_full(s), t0 + j * kTok);
+      issued_k = j + 1;
+      if (j >= ST && !wait(v_empty(s), par)) break;
+      __syncwarp();
+      load(&maps.v, sbase + G::V_OFF + s * G::TILE, v_full(s), t0 + j * kTok);
+      issued_v = j + 1;
+    }
+  } else if (warp == 1) {
+    // ---- products --------------------------------------------------------------------------------
+    constexpr uint32_t ID_S = instr_desc(kTok, 0), ID_O = instr_desc(D, 1);
+    auto s_product = [&](int j) -> bool {  // S of tile j
+      const int s = j % ST;
+      if (!wait(k_full(s), (j / ST) & 1)) return false;
+      fence_after();
+      if (lane == 0) {
+        const uint32_t d = tmem + G::S_COL + (j & 1) * kTok, kb = sbase + G::K_OFF + s * G::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
+          mma_ss(d, smem_desc(sbase + off, 16), smem_desc(kb + off, 16), ID_S, kk > 0);
+        }
+        commit(k_empty(s));
+        commit(s_full(j & 1));
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    for (int j = 0; j < min(2, ntiles) && ok; ++j) ok = s_product(j);
+    for (int j = 0; j < ntiles && ok; ++j) {
+      const int s = j % ST, w = j & 1;
+      if (!(ok = wait(v_full(s), (j / ST) & 1))) break;
+      const int left = t1 - (t0 + j * kTok);
+      const uint32_t vb = G::V_OFF + s * G::TILE;
+      if (left < kTok) {
+        // rows of the last page behind the end hold whatever was there, and 0 x NaN is NaN
+        for (int i = left * 8 + lane; i < kTok * 8; i += 32)
+#pragma unroll
+          for (int cg = 0; cg < G::CG; ++cg)
+            *reinterpret_cast<uint4*>(smem + vb + cg * (kTok * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        mma::fence_proxy_async();
+        __syncwarp();
+      }
+      if (!(ok = wait(p_ready(w), (j >> 1) & 1))) break;
+      fence_after();
+      if (lane == 0) {
+        const uint32_t d = tmem + G::O_COL + w * D, a = tmem + G::S_COL + w * kTok;
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk)
+          mma_ts(d, a + kk * 8, smem_desc(sbase + vb + kk * 2048, kTok * 128), ID_O, j >= 2 || kk > 0);
+        commit(v_empty(s));
+      }
+      __syncwarp();
+      if (j + 2 < ntiles) ok = s_product(j + 2);
+    }
+    if (lane == 0) commit(all_done);  // completes when everything issued above has
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- softmax: stream w, one row a thread --------------------------------------------------
+    const int w = (warp - 4) >> 2, r = (warp & 3) * 32 + lane, rr = row0 + r;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
+    const uint32_t s_at = tmem + lanes + G::S_COL + w * kTok, o_at = tmem + lanes + G::O_COL + w * D;
+    int lim = 0;  // positions below it are visible to the row
+    if (rr < p.rows_per_cta) {
+      const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
+      lim = paged_len(p, b);
+      if (p.causal) lim += qi + 1 - p.n_q;
+      lim = min(lim, t1);
+    }
+    constexpr float LOG2E = 1.4426950408889634f;
+    const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap : 0.f;
+    // plain: maxima and exponentials straight from S (a positive scale keeps the order)
+    const bool plain = cap <= 0.f && qs >= 0.f;
+    auto logit = [&](uint32_t v) -> float {
+      const float s = __uint_as_float(v);
+      return cap > 0.f ? mma::softcap_tanh(s * p.scale, cap, cap_k) * LOG2E : s * qs;
+    };
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = w; j < ntiles; j += 2) {
+      if (!(ok = wait(s_full(w), (j >> 1) & 1))) break;
+      fence_after();
+      const int first = t0 + j * kTok;
+      const bool cut = first + kTok > lim;  // some of the tile is masked for this row
+      uint32_t v[32];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kTok / 32; ++c) {
+        __syncwarp();
+        tmem_ld32(v, s_at + 32 * c);
+        tmem_wait_ld();
+        if (plain && !cut) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (first + 32 * c + i < lim) mx = fmaxf(mx, plain ? __uint_as_float(v[i]) : logit(v[i]));
+        }
+      }
+      if (plain && mx != -INFINITY) mx *= qs;
+      const bool raise = mx - m > 8.f;  // (false when both are -inf)
+      const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
+      if (raise) {
+        m = mx;
+        l *= cr;
+      }
+      // S of this tile is complete, so every product before it is: this stream's O is at rest
+      if (j >= 2 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          __syncwarp();
+          tmem_ld32(v, o_at + 32 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * cr);
+          tmem_st32(o_at + 32 * c, v);
+        }
+      }
+      const float ms = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kTok / 32; ++c) {
+        __syncwarp();
+        tmem_ld32(v, s_at + 32 * c);
+        tmem_wait_ld();
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float a, b;
+          if (plain) {
+            a = ex2(fmaf(__uint_as_float(v[2 * i]), qs, -ms));
+            b = ex2(fmaf(__uint_as_float(v[2 * i + 1]), qs, -ms));
+          } else {
+            a = ex2(logit(v[2 * i]) - ms);
+            b = ex2(logit(v[2 * i + 1]) - ms);
+          }
+          if (cut) {
+            if (first + 32 * c + 2 * i >= lim) a = 0.f;
+            if (first + 32 * c + 2 * i + 1 >= lim) b = 0.f;
+          }
+          sum += a + b;
+          pk[i] = mma::pack_h2(a, b);
+        }
+        __syncwarp();
+        tmem_st16(s_at + 16 * c, pk);  // (over columns of S that are already read)
+      }
+      l += sum;
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(w)) : "memory");
+    }
+    // ---- merge the streams, write the chunk's part --------------------------------------------
+    if (ok) ok = wait(all_done, 0);
+    fence_after();
+    // stream 1 hands over its state and O through the stages (every tile has been consumed):
+    // column-major, so that a warp's rows are neighbours
+    float* hand = reinterpret_cast<float*>(smem + G::K_OFF);   // [D][128]
+    float* state = reinterpret_cast<float*>(smem);              // [2][128] (over Q)
+    uint32_t v[32];
+    if (ok && w == 1 && ntiles > 1) {
+      state[r] = m;
+      state[kRows + r] = l;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        __syncwarp();
+        tmem_ld32(v, o_at + 32 * c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) hand[(32 * c + i) * kRows + r] = __uint_as_float(v[i]);
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (ok && w == 0 && !__any_sync(0xffffffffu, *abort_flag)) {
+      const bool two = ntiles > 1;
+      const float m1 = two ? state[r] : -INFINITY, l1 = two ? state[kRows + r] : 0.f;
+      const float mx = fmaxf(m, m1);
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - mx), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mx);
+      const float den = l * f0 + l1 * f1;
+      const bool empty = den == 0.f;
+      const float inv = empty ? 0.f : 1.f / den;
+      const float w0 = f0 * inv, w1 = f1 * inv;
+      int64_t at = 0;
+      if (rr < p.rows_per_cta) {
+        const int h = head * p.group + rr % p.group;
+        const int64_t local = (int64_t)(rr / p.group) * p.hq + h;  // of the batch, or of the sequence
+        at = p.shared ? (int64_t)split * p.rows_total + local
+             : whole  ? (int64_t)bz * (p.n_q * p.hq) + local
+                      : (int64_t)split * (p.n_q * p.hq) + local;
+        const float lv = empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
+        (whole ? p.out_lse : p.shared ? p.pre_lse : p.own_lse)[at] = lv;
+      }
+      float* parts = p.shared ? p.pre_o : p.own_o;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        __syncwarp();
+        if (ntiles > 0) {
+          tmem_ld32(v, o_at + 32 * c);
+          tmem_wait_ld();
+        }
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          o[i] = ntiles > 0 && w0 != 0.f ? __uint_as_float(v[i]) * w0 : 0.f;
+          if (two && w1 != 0.f) o[i] = fmaf(hand[(32 * c + i) * kRows + r], w1, o[i]);
+        }
+        if (rr >= p.rows_per_cta) {
+          // (no row: nothing to store)
+        } else if (!whole || p.out_dtype == QPS_DT_F32) {
+          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : parts) + at * D + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at * D + 32 * c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float a = o[8 * i + 2 * q], b = o[8 * i + 2 * q + 1];
+              if (p.out_dtype == QPS_DT_F16) {
+                x[q] = mma::pack_h2(a, b);
+              } else {
+                const __nv_bfloat162 hb = __floats2bfloat162_rn(a, b);
+                x[q] = *reinterpret_cast<const uint32_t*>(&hb);
+              }
+            }
+            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+    }
+    fence_before();
+  }
+
+  // ---- end: nothing may be in flight when the CTA leaves -----------------------------------------
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  if (*abort_flag) {  // (uniform: the flag is only set before the barrier above)
+    auto drain = [&](uint32_t bar, uint32_t parity) {
+      const uint64_t since = global_ns();
+      while (!mbar_try_wait(bar, parity) && global_ns() - since < mma::kWaitLimitNs) {
+      }
+    };
+    if (warp == 0) {
+      for (int j = max(0, issued_k - ST); j < issued_k; ++j) drain(k_full(j % ST), (j / ST) & 1);
+      for (int j = max(0, issued_v - ST); j < issued_v; ++j) drain(v_full(j % ST), (j / ST) & 1);
+    } else if (warp == 1) {
+      drain(all_done, 0);
+    }
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 2) tmem_free(tmem, 512);
+}
+
+template <int D>
+qps_status launch_tm(const PagedAttnParams& p, cudaStream_t s) {
+  using G = Geo<D>;
+  static_assert(G::SMEM <= 227 * 1024, "the stages exceed the shared memory of one CTA");
+  static_assert(G::O_COL + 2 * D <= 512, "S and O exceed TMEM");
+  TmaSet maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int page = 1 << p.page_shift, rows = page < kTok ? page : kTok;
+  for (int i = 0; i < 2; ++i)
+    if (!encode_plane_map(i ? &maps.v : &maps.k, i ? p.v.data : p.k.data, 2 * D, page, p.hkv, page, (int)p.n_pages,
+                          (int64_t)p.hkv * page, 128, 128, rows))
+      return QPS_ERR_CUDA;
+  auto kern = attn_tm_kernel<D>;
+  static std::atomic<uint64_t> sized{0};
+  int dev = 0;
+  QPS_CUDA_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(sized.load(std::memory_order_relaxed) & bit) || !bit) {
+    QPS_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
+    sized.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.shared ? p.n_split : p.max_chunks) * ((p.rows_per_cta + kRows - 1) / kRows), p.hkv, 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = G::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, maps));
+  count_launch();
+  QPS_CUDA_TRY(cudaGetLastError());
+  return QPS_OK;
+}
+
+}  // namespace tm
+}  // namespace qps

@@ -29,6 +29,9 @@ struct PagedAttnParams : AttnParams {
   int prefix_len;     // positions attended by the prefix launch (a multiple of 32)
   int target;         // chunks per (KV head, row group) the sequences are cut into, about
   int min_units;      // smallest chunk, in units
+  int unit_round;     // chunks are multiples of this many units
+  int max_chunks;     // chunks there can be, by the tables' width
+  int tm;             // this launch is attn_tm.cuh's kernel
   int n_prefix;       // parts of the prefix
   float* pre_o;       // f32 [n_prefix][rows_total][D], [n_prefix][rows_total]
   float* pre_lse;
@@ -40,9 +43,10 @@ struct PagedAttnParams : AttnParams {
 };
 
 // The chunking of the sequences' own positions [prefix_len, len), the same in the
-// attention and in the merge: units of 32 positions, C units a chunk, sequence b's
-// chunks first[b] .. first[b] + count - 1.  C is such that all chunks together number at
-// most `target` + batch.
+// attention and in the merge: units of 32 positions, C units a chunk (a multiple of
+// unit_round), sequence b's chunks numbered behind those of the sequences before it.  C is
+// such that all chunks together number at most `target` + batch.  Without a prefix an
+// empty sequence has one chunk, which writes its empty output.
 __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
   const int n = p.lens[b];
   const int most = p.table_width << p.page_shift;
@@ -54,6 +58,10 @@ constexpr int kPagedUnit = 32;  // a whole number of any instance's tiles
 __device__ __forceinline__ int paged_units(int len, int prefix) {
   return len > prefix ? (len - prefix + kPagedUnit - 1) / kPagedUnit : 0;
 }
+__device__ __forceinline__ int paged_chunks(const PagedAttnParams& p, int len, int cu) {
+  const int n = (paged_units(len, p.prefix_len) + cu - 1) / cu;
+  return n == 0 && p.prefix_len == 0 ? 1 : n;
+}
 
 // Chunk length in units; every lane of the warp takes part.
 __device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int lane) {
@@ -61,12 +69,51 @@ __device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int l
   for (int b = lane; b < p.batch; b += 32) total += paged_units(paged_len(p, b), p.prefix_len);
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return max(p.min_units, (total + p.target - 1) / p.target);
+  const int c = max(p.min_units, (total + p.target - 1) / p.target);
+  return (c + p.unit_round - 1) / p.unit_round * p.unit_round;
+}
+
+// Chunk number `index` of the batch: its sequence (-1: there are fewer chunks), positions
+// [t0, t1) and whether it is its sequence's only part; the same in every lane.
+struct PagedChunk {
+  int b, t0, t1;
+  bool whole;
+};
+__device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int index, int lane) {
+  const int cu = paged_chunk_units(p, lane);
+  PagedChunk r = {-1, 0, 0, false};
+  int before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    const int len = b < p.batch ? paged_len(p, b) : 0;
+    const int cnt = b < p.batch ? paged_chunks(p, len, cu) : 0;
+    int sum = cnt;  // inclusive scan over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + sum > index);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int n = __shfl_sync(0xffffffffu, cnt, src);
+      const int at = index - (before + __shfl_sync(0xffffffffu, sum, src) - n);
+      r.b = b0 + src;
+      r.t0 = p.prefix_len + at * cu * kPagedUnit;
+      r.t1 = min(__shfl_sync(0xffffffffu, len, src), r.t0 + cu * kPagedUnit);
+      r.whole = n == 1 && p.prefix_len == 0;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return r;
 }
 
 qps_status launch_paged_mma_d64(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_mma_d128(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_mma_d256(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_mma_d512(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_tm_d64(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_tm_d128(const PagedAttnParams& p, cudaStream_t s);
 
 }  // namespace qps
