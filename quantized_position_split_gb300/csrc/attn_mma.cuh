@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   bool whole = false;  // (paged) the chunk is all its rows attend: the output itself is written
   if constexpr (PAGED) {
     if (!p.shared) {  // chunk number `split` of the batch: find its sequence and positions
+      if (blockIdx.x == 0 && head == 0 && warp == 0) paged_publish(p, lane);
       const PagedChunk ch = paged_find(p, split, lane);
       if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
       bz = ch.b;

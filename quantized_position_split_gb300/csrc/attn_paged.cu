@@ -14,13 +14,13 @@ namespace qps {
 namespace {
 
 // ---- merge --------------------------------------------------------------------------------
-// One CTA per output row: M = max lse, w = exp(lse - M), o = sum w o / sum w over the
-// prefix's parts and the row's own chunks.  D / 4 threads read one part's row (16 bytes
-// each), 1024 / D parts side by side and kU of each in flight; every thread keeps its
-// maximum online and the groups meet in shared memory.  A row whose only part was written
-// by the attention is skipped, a row without any gets O = 0, lse = -inf.
+// M = max lse, w = exp(lse - M), o = sum w o / sum w over the prefix's parts and the row's
+// own chunks.  D / 4 threads read one part's row (16 bytes each); `groups` such sets share
+// a row, kU parts of each in flight, so that a row takes about one round of loads; every
+// thread keeps its maximum online and the sets meet in shared memory.  A row whose only
+// part was written by the attention is skipped.
 constexpr int kMergeThreads = 256;
-constexpr int kU = 4;
+constexpr int kU = 8;
 
 __device__ __forceinline__ void store_out(void* o, int dtype, int64_t at, float4 v) {
   if (dtype == QPS_DT_F32) {
@@ -39,33 +39,28 @@ __device__ __forceinline__ void store_out(void* o, int dtype, int64_t at, float4
 }
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int COLS = D / 4, GROUPS = kMergeThreads / COLS;
-  __shared__ float wm[GROUPS], wd[GROUPS];
-  __shared__ float4 wacc[GROUPS][COLS];
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kMergeThreads)
+    paged_merge_kernel(const __grid_constant__ PagedAttnParams p, int groups) {
+  constexpr int COLS = D / 4, SETS = kMergeThreads / COLS;
+  __shared__ float wm[SETS], wd[SETS];
+  __shared__ float4 wacc[SETS][COLS];
   const int rows = p.n_q * p.hq;
-  const int64_t row = blockIdx.x;
-  const int b = (int)(row / rows);
+  const int set = threadIdx.x / COLS, grp = set % groups, col = (threadIdx.x % COLS) * 4;
+  const int64_t row = (int64_t)blockIdx.x * (SETS / groups) + set / groups;
+  const bool real = row < p.rows_total;
+  const int b = real ? (int)(row / rows) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // the sequence's chunks, as the attention counted them
-  const int cu = paged_chunk_units(p, lane);
-  int first = 0;
-  for (int i = lane; i < b; i += 32) first += paged_chunks(p, paged_len(p, i), cu);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
-  const int count = paged_chunks(p, paged_len(p, b), cu);
-  if (count == 1 && p.n_prefix == 0) return;  // written by the attention
-  const int total = p.n_prefix + count;
-  const int grp = threadIdx.x / COLS, col = (threadIdx.x % COLS) * 4;
+  const int first = p.first[b], count = p.first[b + 1] - first;
+  const bool mine = real && !(count == 1 && p.n_prefix == 0);  // (else written by the attention)
+  const int total = mine ? p.n_prefix + count : 0;
   float m = -INFINITY, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int t0 = grp; t0 < total; t0 += GROUPS * kU) {
+  for (int t0 = grp; t0 < total; t0 += groups * kU) {
     float l[kU];
     float4 v[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int t = t0 + u * GROUPS;
+      const int t = t0 + u * groups;
       l[u] = -INFINITY;
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < total) {
@@ -92,27 +87,30 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
       acc.w = fmaf(w, v[u].w, acc.w);
     }
   }
-  if (threadIdx.x % COLS == 0) {
-    wm[grp] = m;
-    wd[grp] = den;
+  float mx = m, dt = den;
+  float4 s = acc;
+  if (groups > 1) {
+    if (col == 0) {
+      wm[set] = m;
+      wd[set] = den;
+    }
+    wacc[set][col / 4] = acc;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int g = 1; g < groups; ++g) mx = fmaxf(mx, wm[set + g]);
+    dt = 0.f;
+    s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < groups; ++g) {
+      const float f = wm[set + g] == -INFINITY ? 0.f : __expf(wm[set + g] - mx);
+      dt += wd[set + g] * f;
+      const float4 a = wacc[set + g][col / 4];
+      s.x = fmaf(a.x, f, s.x);
+      s.y = fmaf(a.y, f, s.y);
+      s.z = fmaf(a.z, f, s.z);
+      s.w = fmaf(a.w, f, s.w);
+    }
   }
-  wacc[grp][threadIdx.x % COLS] = acc;
-  __syncthreads();
-  if (grp != 0) return;
-  float mx = -INFINITY, dt = 0.f;
-#pragma unroll
-  for (int g = 0; g < GROUPS; ++g) mx = fmaxf(mx, wm[g]);
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    const float f = wm[g] == -INFINITY ? 0.f : __expf(wm[g] - mx);
-    dt += wd[g] * f;
-    const float4 a = wacc[g][col / 4];
-    s.x = fmaf(a.x, f, s.x);
-    s.y = fmaf(a.y, f, s.y);
-    s.z = fmaf(a.z, f, s.z);
-    s.w = fmaf(a.w, f, s.w);
-  }
+  if (!mine) return;
   // (a NaN logit makes its row's sums NaN: it stays one)
   const bool empty = mx == -INFINITY && dt == 0.f;
   const float inv = empty ? 0.f : 1.f / dt;
@@ -121,9 +119,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const __grid
 }
 
 template <int D>
-qps_status launch_merge(const PagedAttnParams& p, cudaStream_t s) {
+qps_status launch_merge(const PagedAttnParams& p, int parts, cudaStream_t s) {
+  constexpr int SETS = kMergeThreads / (D / 4);
+  int groups = 1;
+  while (groups < SETS && groups * kU < parts) groups *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.rows_total);
+  cfg.gridDim = dim3((unsigned)((p.rows_total + SETS / groups - 1) / (SETS / groups)));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -131,7 +132,7 @@ qps_status launch_merge(const PagedAttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p));
+  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p, groups));
   count_launch();
   QPS_CUDA_TRY(cudaGetLastError());
   return QPS_OK;
@@ -141,8 +142,8 @@ qps_status launch_merge(const PagedAttnParams& p, cudaStream_t s) {
 struct Plan {
   PagedAttnParams p;
   bool prefix_tm, own_tm;  // which kernel the launches are
-  bool merge;  // some row can have several parts
-  size_t off_pre_lse, off_own_o, off_own_lse, bytes;
+  int parts;   // most parts a row can have; one: no merge
+  size_t off_pre_lse, off_own_o, off_own_lse, off_first, bytes;
 };
 
 // Chunks of the sequences' own positions: as many as the CTAs the GPU holds for one
@@ -260,14 +261,15 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
     const int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
     const int64_t each = std::max<int64_t>(1, (most + kMinPositions - 1) / kMinPositions);
     p.max_chunks = (int)std::min<int64_t>((int64_t)p.target + a->batch, each * a->batch);
-    out->merge = p.n_prefix > 0 || each > 1;
+    out->parts = p.n_prefix + (int)std::min<int64_t>(each, p.target + 1);
   }
   const size_t own = (size_t)p.max_chunks * a->n_q * a->hq, pre = (size_t)p.n_prefix * rows_total;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   out->off_pre_lse = up(pre * kv.d * sizeof(float));
   out->off_own_o = out->off_pre_lse + up(pre * sizeof(float));
   out->off_own_lse = out->off_own_o + up(own * kv.d * sizeof(float));
-  out->bytes = out->off_own_lse + up(own * sizeof(float));
+  out->off_first = out->off_own_lse + up(own * sizeof(float));
+  out->bytes = out->off_first + up((size_t)(a->batch + 1) * sizeof(int32_t));
   return QPS_OK;
 }
 
@@ -298,6 +300,7 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   p.pre_lse = reinterpret_cast<float*>(ws + pl.off_pre_lse);
   p.own_o = reinterpret_cast<float*>(ws + pl.off_own_o);
   p.own_lse = reinterpret_cast<float*>(ws + pl.off_own_lse);
+  p.first = pl.parts > 1 ? reinterpret_cast<int32_t*>(ws + pl.off_first) : nullptr;
   p.out = a->o;
   p.out_lse = a->lse;
   const int rows = p.n_q * p.group;
@@ -317,12 +320,12 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   p.rows_per_cta = rows;
   p.chunk = 0;
   st = launch_paged(p, s);
-  if (st != QPS_OK || !pl.merge) return st;
+  if (st != QPS_OK || pl.parts <= 1) return st;
   switch (p.d) {
-    case 64: return launch_merge<64>(p, s);
-    case 128: return launch_merge<128>(p, s);
-    case 256: return launch_merge<256>(p, s);
-    default: return launch_merge<512>(p, s);
+    case 64: return launch_merge<64>(p, pl.parts, s);
+    case 128: return launch_merge<128>(p, pl.parts, s);
+    case 256: return launch_merge<256>(p, pl.parts, s);
+    default: return launch_merge<512>(p, pl.parts, s);
   }
 }
 

@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     t0 = split * (int)p.chunk;
     t1 = min((int)p.end, t0 + (int)p.chunk);
   } else {
+    if (blockIdx.x == 0 && head == 0 && warp == 2) paged_publish(p, lane);
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
     bz = ch.b;
@@ -315,8 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     constexpr float LOG2E = 1.4426950408889634f;
     const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap : 0.f;
-    // plain: maxima and exponentials straight from S (a positive scale keeps the order)
-    const bool plain = cap <= 0.f && qs >= 0.f;
     auto logit = [&](uint32_t v) -> float {
       const float s = __uint_as_float(v);
       return cap > 0.f ? mma::softcap_tanh(s * p.scale, cap, cap_k) * LOG2E : s * qs;
@@ -327,24 +326,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(s_full(w), (j >> 1) & 1))) break;
       fence_after();
       const int first = t0 + j * kTok;
-      const bool cut = first + kTok > lim;  // some of the tile is masked for this row
-      uint32_t v[32];
+      // Whole tiles of plain logits, the common case, have a body of their own: maxima and
+      // exponentials straight from S (a positive scale keeps the order), four chains each,
+      // the next 32 columns read beside the present ones' arithmetic.
+      const bool fast = __all_sync(0xffffffffu, first + kTok <= lim || rr >= p.rows_per_cta) && cap <= 0.f && qs >= 0.f;
+      uint32_t va[32], vb[32];
       float mx = -INFINITY;
+      if (fast) {
+        float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto most = [&](const uint32_t (&v)[32]) {
 #pragma unroll
-      for (int c = 0; c < kTok / 32; ++c) {
-        __syncwarp();
-        tmem_ld32(v, s_at + 32 * c);
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mm[k] = fmaxf(fmaxf(mm[k], __uint_as_float(v[i + k])), __uint_as_float(v[i + 4 + k]));
+        };
+        tmem_ld32(va, s_at);
         tmem_wait_ld();
-        if (plain && !cut) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
-        } else {
+        for (int c = 0; c < kTok / 32; c += 2) {
+          tmem_ld32(vb, s_at + 32 * (c + 1));
+          most(va);
+          tmem_wait_ld();
+          if (c + 2 < kTok / 32) tmem_ld32(va, s_at + 32 * (c + 2));
+          most(vb);
+          if (c + 2 < kTok / 32) tmem_wait_ld();
+        }
+        mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * qs;
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+          __syncwarp();
+          tmem_ld32(va, s_at + 32 * c);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (first + 32 * c + i < lim) mx = fmaxf(mx, plain ? __uint_as_float(v[i]) : logit(v[i]));
+            if (first + 32 * c + i < lim) mx = fmaxf(mx, logit(va[i]));
         }
+        __syncwarp();
       }
-      if (plain && mx != -INFINITY) mx *= qs;
       const bool raise = mx - m > 8.f;  // (false when both are -inf)
       const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
       if (raise) {
@@ -353,43 +373,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // S of this tile is complete, so every product before it is: this stream's O is at rest
       if (j >= 2 && __any_sync(0xffffffffu, raise)) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           __syncwarp();
-          tmem_ld32(v, o_at + 32 * c);
+          tmem_ld32(va, o_at + 32 * c);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * cr);
-          tmem_st32(o_at + 32 * c, v);
+          for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * cr);
+          tmem_st32(o_at + 32 * c, va);
         }
       }
       const float ms = m == -INFINITY ? 0.f : m;
       float sum = 0.f;
+      if (fast) {
+        float ss[4] = {0.f, 0.f, 0.f, 0.f};
+        auto weigh = [&](const uint32_t (&v)[32], int c) {
+          uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < kTok / 32; ++c) {
-        __syncwarp();
-        tmem_ld32(v, s_at + 32 * c);
-        tmem_wait_ld();
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a, b;
-          if (plain) {
-            a = ex2(fmaf(__uint_as_float(v[2 * i]), qs, -ms));
-            b = ex2(fmaf(__uint_as_float(v[2 * i + 1]), qs, -ms));
-          } else {
-            a = ex2(logit(v[2 * i]) - ms);
-            b = ex2(logit(v[2 * i + 1]) - ms);
+          for (int i = 0; i < 16; ++i) {
+            const float a = ex2(fmaf(__uint_as_float(v[2 * i]), qs, -ms));
+            const float b = ex2(fmaf(__uint_as_float(v[2 * i + 1]), qs, -ms));
+            ss[(2 * i) & 3] += a;
+            ss[(2 * i + 1) & 3] += b;
+            pk[i] = mma::pack_h2(a, b);
           }
-          if (cut) {
+          tmem_st16(s_at + 16 * c, pk);  // (over columns of S that are already read, none under way)
+        };
+        tmem_ld32(va, s_at);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kTok / 32; c += 2) {
+          tmem_ld32(vb, s_at + 32 * (c + 1));
+          weigh(va, c);
+          tmem_wait_ld();
+          if (c + 2 < kTok / 32) tmem_ld32(va, s_at + 32 * (c + 2));
+          weigh(vb, c + 1);
+          if (c + 2 < kTok / 32) tmem_wait_ld();
+        }
+        sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+          __syncwarp();
+          tmem_ld32(va, s_at + 32 * c);
+          tmem_wait_ld();
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a = ex2(logit(va[2 * i]) - ms), b = ex2(logit(va[2 * i + 1]) - ms);
             if (first + 32 * c + 2 * i >= lim) a = 0.f;
             if (first + 32 * c + 2 * i + 1 >= lim) b = 0.f;
+            sum += a + b;
+            pk[i] = mma::pack_h2(a, b);
           }
-          sum += a + b;
-          pk[i] = mma::pack_h2(a, b);
+          __syncwarp();
+          tmem_st16(s_at + 16 * c, pk);
         }
         __syncwarp();
-        tmem_st16(s_at + 16 * c, pk);  // (over columns of S that are already read)
       }
       l += sum;
       tmem_wait_st();

@@ -37,6 +37,7 @@ struct PagedAttnParams : AttnParams {
   float* pre_lse;
   float* own_o;       // f32 [chunk][n_q*hq][D], [chunk][n_q*hq]
   float* own_lse;
+  int32_t* first;     // [batch + 1] (see paged_publish), NULL when there is no merge
   void* out;          // the call's o (out_dtype) and lse
   float* out_lse;
   int out_dtype;
@@ -71,6 +72,26 @@ __device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int l
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int c = max(p.min_units, (total + p.target - 1) / p.target);
   return (c + p.unit_round - 1) / p.unit_round * p.unit_round;
+}
+
+// The number of every sequence's first chunk, for the merge: p.first[b], p.first[batch].
+__device__ __forceinline__ void paged_publish(const PagedAttnParams& p, int lane) {
+  if (!p.first) return;
+  const int cu = paged_chunk_units(p, lane);
+  int before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int sum = b < p.batch ? paged_chunks(p, paged_len(p, b), cu) : 0;
+    const int own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (b < p.batch) p.first[b] = before + sum - own;
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) p.first[p.batch] = before;
 }
 
 // Chunk number `index` of the batch: its sequence (-1: there are fewer chunks), positions
