@@ -141,24 +141,33 @@ qps_status launch_merge(const PagedAttnParams& p, int parts, cudaStream_t s) {
 // ---- plan -----------------------------------------------------------------------------------
 struct Plan {
   PagedAttnParams p;
-  bool prefix_tm, own_tm;  // which kernel the launches are
+  PagedKernel prefix_kernel, own_kernel;
   int parts;   // most parts a row can have; one: no merge
   size_t off_pre_lse, off_own_o, off_own_lse, off_first, bytes;
 };
 
-// Chunks of the sequences' own positions: as many as the CTAs the GPU holds for one
-// sequence, kWaves times that for several, so that ragged lengths level out; each at least
-// kMinPositions long, so that a part is worth its merge.
+// Chunks of the sequences' own positions.  Few sequences: one round of the CTAs the GPU
+// holds, less one for each sequence's short last chunk (a second round of a few CTAs costs
+// as much as a full one).  More sequences than half a round: kWaves rounds, so that ragged
+// lengths level out.  Each at least kMinPositions long, so that a part is worth its merge.
 constexpr int kWaves = 2;
 constexpr int kMinPositions = 128;
 
-// Rows of a KV head from which attn_tm.cuh's kernel is taken: it works on 128 rows at a
-// time whatever their number, the other on 8 to 24 and reads the positions again for each.
-constexpr int kManyRows = 32;
-bool takes_tm(const PagedKv& kv, int rows) {
-  return kv.kfmt == QPS_FMT_F16 && kv.vfmt == QPS_FMT_F16 && (kv.d == 64 || kv.d == 128) && rows > kManyRows;
+// The kernel for `rows` query rows per KV head, and the rows, positions and CTAs per SM
+// that it works with.
+struct Shape {
+  PagedKernel kernel;
+  int rows, tile, ctas_per_sm;
+};
+Shape shape_for(const PagedKv& kv, int rows, bool shared) {
+  if (kv.kfmt == QPS_FMT_F16 && kv.vfmt == QPS_FMT_F16 && kv.d <= 128) {
+    if (rows > 32) return {kTm, 128, 128, 1};
+  } else if (kv.d >= 128 && !is_tq(kv.kfmt) && kv.vfmt != QPS_FMT_TQ4) {
+    if (rows > (kv.d == 128 ? 24 : 8)) return {kTt, 64, 128, 1};
+  }
+  const int n = mma_tile_rows(kv.d, rows, shared);
+  return {kMma, n, 32, mma_ctas_per_sm(kv.d, n / 8, kv.vfmt)};
 }
-constexpr int kTmRows = 128, kTmTile = 128;  // of attn_tm.cuh
 
 qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
   if (!a) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: args is NULL");
@@ -238,25 +247,25 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
   p.prefix_len = a->batch > 1 ? (int)(a->shared_len & ~(int64_t)31) : 0;
   if (p.prefix_len > 0) {
     const int all = a->batch * rows;
-    out->prefix_tm = takes_tm(kv, all);
-    const int tile_rows = out->prefix_tm ? kTmRows : mma_tile_rows(kv.d, all, true);
-    const int ctas = kv.hkv * ((all + tile_rows - 1) / tile_rows);
-    const int slots = out->prefix_tm ? sms : mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
-    const int64_t tile = out->prefix_tm ? kTmTile : 32, least = out->prefix_tm ? kTmTile : 512;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(out->prefix_tm ? slots / ctas : (slots + ctas - 1) / ctas,
+    const Shape sh = shape_for(kv, all, true);
+    out->prefix_kernel = sh.kernel;
+    const int ctas = kv.hkv * ((all + sh.rows - 1) / sh.rows), slots = sh.ctas_per_sm * sms;
+    // one round of CTAs
+    const int least = sh.kernel == kMma ? 512 : sh.tile;
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(sh.kernel == kMma ? (slots + ctas - 1) / ctas : slots / ctas,
                                                                 (p.prefix_len + least - 1) / least));
-    const int64_t chunk = ((p.prefix_len + want - 1) / want + tile - 1) / tile * tile;
+    const int64_t chunk = ((p.prefix_len + want - 1) / want + sh.tile - 1) / sh.tile * sh.tile;
     p.n_prefix = (int)((p.prefix_len + chunk - 1) / chunk);
     p.chunk = chunk;
   }
   {
-    out->own_tm = takes_tm(kv, rows);
-    const int tile_rows = out->own_tm ? kTmRows : mma_tile_rows(kv.d, rows, false);
-    const int ctas = kv.hkv * ((rows + tile_rows - 1) / tile_rows);
-    const int slots = out->own_tm ? sms : mma_ctas_per_sm(kv.d, tile_rows / 8, kv.vfmt) * sms;
-    p.target = std::max(1, (a->batch > 1 ? kWaves : 1) * slots / ctas);
+    const Shape sh = shape_for(kv, rows, false);
+    out->own_kernel = sh.kernel;
+    const int ctas = kv.hkv * ((rows + sh.rows - 1) / sh.rows), slots = sh.ctas_per_sm * sms;
+    const int round = slots / ctas;
+    p.target = std::max(1, 2 * a->batch <= round ? round - a->batch + 1 : kWaves * slots / ctas);
     p.min_units = kMinPositions / kPagedUnit;
-    p.unit_round = out->own_tm ? kTmTile / kPagedUnit : 1;
+    p.unit_round = sh.tile / kPagedUnit;
     // chunks of a sequence that fills its table, and of all of them
     const int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
     const int64_t each = std::max<int64_t>(1, (most + kMinPositions - 1) / kMinPositions);
@@ -274,7 +283,9 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
 }
 
 qps_status launch_paged(const PagedAttnParams& p, cudaStream_t s) {
-  if (p.tm) return p.d == 64 ? launch_paged_tm_d64(p, s) : launch_paged_tm_d128(p, s);
+  if (p.kernel == kTm) return p.d == 64 ? launch_paged_tm_d64(p, s) : launch_paged_tm_d128(p, s);
+  if (p.kernel == kTt)
+    return p.d == 128 ? launch_paged_tt_d128(p, s) : p.d == 256 ? launch_paged_tt_d256(p, s) : launch_paged_tt_d512(p, s);
   switch (p.d) {
     case 64: return launch_paged_mma_d64(p, s);
     case 128: return launch_paged_mma_d128(p, s);
@@ -307,7 +318,7 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   if (p.n_prefix > 0) {
     PagedAttnParams f = p;
     f.shared = 1;
-    f.tm = pl.prefix_tm;
+    f.kernel = pl.prefix_kernel;
     f.rows_per_cta = p.batch * rows;
     f.n_split = p.n_prefix;
     f.begin = 0;
@@ -316,7 +327,7 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
     if (st != QPS_OK) return st;
   }
   p.shared = 0;
-  p.tm = pl.own_tm;
+  p.kernel = pl.own_kernel;
   p.rows_per_cta = rows;
   p.chunk = 0;
   st = launch_paged(p, s);

@@ -31,7 +31,7 @@ struct PagedAttnParams : AttnParams {
   int min_units;      // smallest chunk, in units
   int unit_round;     // chunks are multiples of this many units
   int max_chunks;     // chunks there can be, by the tables' width
-  int tm;             // this launch is attn_tm.cuh's kernel
+  int kernel;         // PagedKernel of this launch
   int n_prefix;       // parts of the prefix
   float* pre_o;       // f32 [n_prefix][rows_total][D], [n_prefix][rows_total]
   float* pre_lse;
@@ -136,5 +136,11 @@ qps_status launch_paged_mma_d256(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_mma_d512(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tm_d64(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tm_d128(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_tt_d128(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_tt_d256(const PagedAttnParams& p, cudaStream_t s);
+qps_status launch_paged_tt_d512(const PagedAttnParams& p, cudaStream_t s);
+
+// The kernels of a paged launch: attn_mma.cuh's, attn_tm.cuh's, attn_tt.cuh's.
+enum PagedKernel { kMma, kTm, kTt };
 
 }  // namespace qps
