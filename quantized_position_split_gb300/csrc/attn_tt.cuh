@@ -6,24 +6,28 @@
 // The products run with the positions and the head dimension on the wide side (M = 128)
 // and the query rows on the narrow one (N = 16 .. 64), so their time follows the number of
 // rows:
-//     S^T [128 positions][N] = K Q^T      A = K (K-major), B = Q (K-major), per 64 dims
+//     S^T [128 positions][N] = K Q^T      A = K (TMEM), B = Q (shared, K-major), per 64 dims
 //     P   = 2^(S' - m)                    one position a thread, all rows in its registers
-//     O^T [128 dims][N]     += V^T P^T    A = V (MN-major, as stored), B = P (MN-major)
-// S^T (two buffers) and O^T (D / 128 blocks) live in TMEM: 128 + D / 2 columns.
+//     O^T [128 dims][N]     += V^T P^T    A = V (shared, MN-major, as stored), B = P (MN-major)
+// S^T (two buffers), O^T (D / 128 blocks) and two slots of K live in TMEM: 256 + D / 2
+// columns.
 //
-// K and V are decoded once per tile by eight warps into 32 KB slots of fp16 operands (64
-// dims of K, 128 of V), a ring that the products empty.  Numerics: a q8_0 key (code x
-// scale) is stored as hi + lo fp16 parts, two products, so logits keep float32 accuracy; a
-// TurboQuant V is its exact fp16 levels in the rotated domain with the norm folded into P
-// before P's one rounding, the output being rotated back once; a q8_0 V is rounded once to
-// fp16; sums, maxima and O are float32.
+// The stored rows arrive by tensor-map boxes in small raw stages; four warps decode K, one
+// position a thread, from there into TMEM (64 dims a slot), four more V into 32 KB slots of
+// fp16 operands (128 dims; fp16 values are boxed there as they are).  K by way of shared
+// memory slots too, a tile took 17000 cycles at head_dim 512: 8600 of shared-memory traffic
+// and most of the rest in the decoding warps' waits.  Numerics: a q8_0 key (code x scale)
+// is its hi + lo fp16 parts, two products, so logits keep float32 accuracy; a TurboQuant V
+// is its exact fp16 levels in the rotated domain with the norm folded into P before P's one
+// rounding, the output being rotated back once; a q8_0 V is rounded once to fp16; sums,
+// maxima and O are float32.
 //
 // A row's maximum over the positions would cross all threads, so the running reference m
 // (in shared memory) is raised only when some position exceeds it by more than 8 (log2):
 // one vote a tile, and on a raise the maxima are taken, O and the sums rescaled.
 //
-// Roles: warp 0 issues the products, warps 4-7 are the softmax, warps 8-15 decode.  Waits
-// are bounded as in attn_tm.cuh.
+// Roles: warp 0 issues the products, warps 2 and 3 the boxes of K and V, warps 4-7 are the
+// softmax, 8-11 decode K and 12-15 V.  Waits are bounded as in attn_tm.cuh.
 #pragma once
 
 #include "attn_tm.cuh"
@@ -36,27 +40,27 @@ using namespace tm;
 constexpr int kN = 64;             // query rows per CTA
 constexpr int kTile = 128;         // positions per tile
 constexpr int kThreadsTt = 512;
-constexpr int kSlot = 32 * 1024, kSlots = 4;
+constexpr int kSlot = 32 * 1024, kSlots = 3;  // V's fp16 slots
 
-template <int D>
+template <int D, int KF, int VF>
 struct GeoTt {
   static constexpr int KC = D / 64, VC = D / 128;   // slots of a tile: K's and V's
   static constexpr int Q_BYTES = kN * D * 2;
   static constexpr int P_OFF = Q_BYTES;             // two buffers [128][64] fp16
   static constexpr int RING = P_OFF + 2 * kTile * kN * 2;
-  static constexpr int MISC = RING + kSlots * kSlot;
-  static constexpr int SMEM = MISC + 2048 + 1024;   // + slack for the 1024-byte base alignment
-  static constexpr int S_COL = 0, O_COL = 128;
-  static constexpr int COLS = O_COL + VC * kN <= 256 ? 256 : 512;
+  // raw stages: [128 positions] of 64 dims of K (codes, or fp16), of 128 of V (codes, or the
+  // 2-bit plane and behind it the signs)
+  static constexpr int RAW_BYTES = (D == 128 ? 32 : 16) * 1024;  // of each side
+  static constexpr int KSTAGE = (KF == QPS_FMT_F16 ? 16 : 8) * 1024, KN = RAW_BYTES / KSTAGE;
+  static constexpr int VSTAGE = (VF == QPS_FMT_Q8_0 ? 16 : 8) * 1024, VN = RAW_BYTES / VSTAGE;
+  static constexpr int KRAW = RING + kSlots * kSlot, VRAW = KRAW + RAW_BYTES;
+  static constexpr int MISC = VRAW + RAW_BYTES;
+  static constexpr int MISC_BYTES = D == 128 ? 2304 : 2048;
+  static constexpr int SMEM = MISC + MISC_BYTES + 1024;  // + slack for the 1024-byte base alignment
+  // TMEM columns: S (two buffers), K (two slots of hi and lo), O
+  static constexpr int S_COL = 0, K_COL = 128, O_COL = 256;
+  static constexpr int COLS = 512;
 };
-
-// Floats as integers of the same order, for integer maxima (-inf below all others; a NaN
-// does not occur: it is not compared).
-__device__ __forceinline__ int ordered(float f) {
-  const int i = __float_as_int(f);
-  return i >= 0 ? i : i ^ 0x7fffffff;
-}
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
 
 // Position in a 16-column word of a TurboQuant V -> column: the decode yields the columns
 // j, j + 4, j + 8, j + 12 of step j.
@@ -64,8 +68,9 @@ __device__ __forceinline__ int tq_unswap(int pos) { return (pos >> 2) + 4 * (pos
 
 template <int D, int KF, int VF>
 __global__ void __launch_bounds__(kThreadsTt, 1)
-    attn_tt_kernel(const __grid_constant__ PagedAttnParams p) {
-  using G = GeoTt<D>;
+    attn_tt_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ TmaSet maps) {
+  using G = GeoTt<D, KF, VF>;
+  constexpr bool VDEC = VF != QPS_FMT_F16;  // V is decoded, or boxed into the slots
   constexpr float LOG2E = 1.4426950408889634f;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -103,31 +108,49 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   int* red = reinterpret_cast<int*>(misc + 768);          // [4][64] maxima, then sums
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(misc + 1792);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1796);
-  const uint32_t bars = sbase + G::MISC + 1808;
-  auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (kSlots + s); };
-  auto s_full = [&](int w) { return bars + 8 * (2 * kSlots + w); };
-  auto p_ready = [&](int w) { return bars + 8 * (2 * kSlots + 2 + w); };
-  auto p_free = [&](int w) { return bars + 8 * (2 * kSlots + 4 + w); };
-  const uint32_t all_done = bars + 8 * (2 * kSlots + 6);
-  static_assert(1808 + 8 * (2 * kSlots + 7) <= 2048, "the row state and barriers fit their region");
+  const uint32_t bars = sbase + G::MISC + 1800;
+  constexpr int KN = G::KN, VN = G::VN;
+  auto bar_at = [&](int i) { return bars + 8 * i; };
+  auto s_full = [&](int w) { return bar_at(w); };
+  auto p_free = [&](int w) { return bar_at(2 + w); };
+  const uint32_t all_done = bar_at(4);
+  auto k_empty = [&](int s) { return bar_at(5 + s); };           // TMEM slots of K
+  auto v_empty = [&](int s) { return bar_at(7 + s); };           // slots of V
+  auto kraw_full = [&](int s) { return bar_at(7 + kSlots + s); };
+  auto vraw_full = [&](int s) { return bar_at(7 + kSlots + KN + s); };
+  constexpr int ONES = 7 + kSlots + KN + VN;                      // the barriers above count one, those below four
+  auto p_ready = [&](int w) { return bar_at(ONES + w); };
+  auto k_full = [&](int s) { return bar_at(ONES + 2 + s); };
+  auto v_full = [&](int s) { return bar_at(ONES + 4 + s); };
+  auto kraw_empty = [&](int s) { return bar_at(ONES + 4 + kSlots + s); };
+  auto vraw_empty = [&](int s) { return bar_at(ONES + 4 + kSlots + KN + s); };
+  constexpr int NBARS = ONES + 4 + kSlots + KN + VN;
+  static_assert(1800 + 8 * NBARS <= G::MISC_BYTES, "the row state and barriers fit their region");
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kSlots + 7; ++i)
-      mbar_init(bars + 8 * i, i < kSlots ? 8 : (i == 2 * kSlots + 2 || i == 2 * kSlots + 3) ? 4 : 1);
+    for (int i = 0; i < NBARS; ++i) mbar_init(bar_at(i), i < ONES ? 1 : 4);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *abort_flag = 0;
   }
   if (warp == 1) tmem_alloc(smem_addr(tmem_word), G::COLS);
-  // Q [64][D], K-major, 128-byte swizzle, column groups of 64 dims
-  for (int i = threadIdx.x; i < kN * D / 8; i += kThreadsTt) {
-    const int r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (rr < p.rows_per_cta) {
-      const int e = rr / p.group, h = head * p.group + rr % p.group;
-      const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
-      v = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+  // Q [64][D], K-major, 128-byte swizzle, column groups of 64 dims: every load first
+  {
+    constexpr int N = kN * D / 8 / kThreadsTt;
+    uint4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * kThreadsTt, r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (rr < p.rows_per_cta) {
+        const int e = rr / p.group, h = head * p.group + rr % p.group;
+        const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
+        v[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+      }
     }
-    *reinterpret_cast<uint4*>(smem + (c >> 3) * (kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * kThreadsTt, r = i / (D / 8), c = i % (D / 8);
+      *reinterpret_cast<uint4*>(smem + (c >> 3) * (kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
+    }
   }
   if (threadIdx.x < kN) {
     const int rr = row0 + threadIdx.x;
@@ -165,31 +188,30 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       if (__shfl_sync(0xffffffffu, over, 0)) return false;
     }
   };
+  int issued = 0;  // (warps 2, 3) stages or slots boxed
   auto arrive = [&](uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
   };
 
   if (warp == 0) {
-    // ---- products: K(0), then K(j + 1), V(j) for every tile, in the ring's order ----------------
-    const uint32_t id_s = instr_desc(n16, 0), id_o = instr_desc(n16, 1) | (1u << 15);
-    int f = 0;  // slots emptied
+    // ---- products: S(0), then S(j + 1) and O(j) for every tile -----------------------------------
+    const uint32_t id_s = instr_desc(n16, 0), id_o = instr_desc(n16, 1) | (1u << 15), one = elect_lane();
+    int fk = 0, fv = 0;  // slots used
     auto s_product = [&](int j) -> bool {
-      for (int c = 0; c < G::KC; ++c, ++f) {
-        const int s = f % kSlots;
-        if (!wait(full(s), (f / kSlots) & 1)) return false;
+#pragma unroll 1
+      for (int c = 0; c < G::KC; ++c, ++fk) {
+        const int s = fk & 1;
+        if (!wait(k_full(s), (fk >> 1) & 1)) return false;
         fence_after();
-        if (lane == 0) {
-          const uint32_t d = tmem + G::S_COL + (j & 1) * kN, a = sbase + G::RING + s * kSlot, b = sbase + c * (kN * 128);
+        const uint32_t d = tmem + G::S_COL + (j & 1) * kN, a = tmem + G::K_COL + s * 64;
+        const uint64_t b = smem_desc(sbase + c * (kN * 128), 16);
 #pragma unroll
-          for (int part = 0; part < (KF == QPS_FMT_Q8_0 ? 2 : 1); ++part)
+        for (int part = 0; part < (KF == QPS_FMT_Q8_0 ? 2 : 1); ++part)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss(d, smem_desc(a + part * (kSlot / 2) + kk * 32, 16), smem_desc(b + kk * 32, 16), id_s,
-                     c > 0 || part > 0 || kk > 0);
-          commit(empty(s));
-          if (c == G::KC - 1) commit(s_full(j & 1));
-        }
-        __syncwarp();
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(d, a + part * 32 + kk * 8, b + (uint64_t)(kk * 2), id_s, c > 0 || part > 0 || kk > 0, one);
+        commit(k_empty(s), one);
+        if (c == G::KC - 1) commit(s_full(j & 1), one);
       }
       return true;
     };
@@ -197,215 +219,255 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     for (int j = 0; j < ntiles && ok; ++j) {
       if (j + 1 < ntiles && !(ok = s_product(j + 1))) break;
       if (!(ok = wait(p_ready(j & 1), (j >> 1) & 1))) break;
-      for (int c = 0; c < G::VC && ok; ++c, ++f) {
-        const int s = f % kSlots;
-        if (!(ok = wait(full(s), (f / kSlots) & 1))) break;
+#pragma unroll 1
+      for (int c = 0; c < G::VC && ok; ++c, ++fv) {
+        const int s = fv % kSlots;
+        if (!(ok = wait(v_full(s), (fv / kSlots) & 1))) break;
+        if constexpr (!VDEC) {
+          // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
+          const int left = t1 - (t0 + j * kTile);
+          if (left < kTile) {
+            for (int i = left * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+            mma::fence_proxy_async();
+            __syncwarp();
+          }
+        }
         fence_after();
-        if (lane == 0) {
-          const uint32_t d = tmem + G::O_COL + c * kN, a = sbase + G::RING + s * kSlot;
-          const uint32_t b = sbase + G::P_OFF + (j & 1) * (kTile * kN * 2);
+        const uint32_t d = tmem + G::O_COL + c * kN;
+        const uint64_t a = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
+        const uint64_t b = smem_desc(sbase + G::P_OFF + (j & 1) * (kTile * kN * 2), 16);
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_ss(d, smem_desc(a + kk * 2048, kSlot / 2), smem_desc(b + kk * 2048, 16), id_o, j > 0 || kk > 0);
-          commit(empty(s));
-          if (c == G::VC - 1) commit(p_free(j & 1));
-        }
-        __syncwarp();
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ss(d, a + (uint64_t)((kk * 2048) >> 4), b + (uint64_t)((kk * 2048) >> 4), id_o, j > 0 || kk > 0, one);
+        commit(v_empty(s), one);
+        if (c == G::VC - 1) commit(p_free(j & 1), one);
       }
     }
-    if (lane == 0) commit(all_done);
-    __syncwarp();
+    commit(all_done, one);
     wait(all_done, 0);
-  } else if (warp >= 8) {
-    // ---- decode: one position and half a slot's columns a thread ------------------------------
-    const int tid = threadIdx.x - 256, tok = tid >> 1, half = tid & 1;
-    // levels as fp16 (see attn_mma.cuh): TQ3 magnitudes m in bytes 2m, 2m + 1; TQ2 fields
-    uint32_t tq_lo = 0u, tq_hi = 0u;
-    if constexpr (VF == QPS_FMT_TQ3) {
-      tq_lo = mma::pack_h2(p.tq_levels[4], p.tq_levels[5]);
-      tq_hi = mma::pack_h2(p.tq_levels[6], p.tq_levels[7]);
-    } else if constexpr (VF == QPS_FMT_TQ2) {
-      tq_lo = mma::pack_h2(p.tq_levels[1], p.tq_levels[0]);
-      tq_hi = mma::pack_h2(p.tq_levels[2], p.tq_levels[3]);
-    }
+  } else if (warp == 2 || warp == 3) {
+    // ---- boxes of min(page, 128) positions, K's (warp 2) and V's (warp 3) -------------------------
+    const bool v = warp == 3;
+    const int br = min(1 << p.page_shift, kTile), nb = kTile / br;
     const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
-    // A slot of the sequence K(0), K(1), V(0), K(2), V(1), ...: phase 0 is K(0), phase
-    // 2i + 1 K(i + 1), phase 2i + 2 V(i).
-    struct Task {
-      int ph, c;
-    };
-    auto is_v = [](const Task& t) { return t.ph > 0 && !(t.ph & 1); };
-    auto tile_of = [](const Task& t) { return t.ph == 0 ? 0 : (t.ph & 1) ? (t.ph + 1) >> 1 : (t.ph >> 1) - 1; };
-    auto done = [&](const Task& t) { return t.ph > 0 && (t.ph >> 1) - ((t.ph & 1) ^ 1) >= ntiles; };
-    auto advance = [&](Task& t) {
-      if (++t.c < (is_v(t) ? G::VC : G::KC)) return;
-      t.c = 0;
-      ++t.ph;
-      if ((t.ph & 1) && (t.ph + 1) >> 1 >= ntiles) ++t.ph;
-    };
-    constexpr int RAW = VF == QPS_FMT_F16 ? 8 : 4;
-    struct Raw {
-      uint4 d[RAW];
-      uint32_t x[2];  // scales or signs
-    };
-    int64_t rows[2] = {-1, -1};  // this thread's row of tile j in rows[j & 1] (-1: none)
-    auto load = [&](const Task& t, Raw& r) {
-      const int j = tile_of(t);
-#pragma unroll
-      for (int i = 0; i < RAW; ++i) r.d[i] = make_uint4(0, 0, 0, 0);
-      r.x[0] = r.x[1] = 0u;
-      if (!is_v(t)) {
-        if (t.c == 0) {
-          const int at = t0 + j * kTile + tok;
-          int64_t row = -1;
-          if (at < t1) {
-            const int pg = table[at >> p.page_shift];
-            if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages)
-              row = (((int64_t)pg * p.hkv + head) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
-            else
-              atomicOr(p.err, kErrIndex);
-          }
-          if (j & 1) rows[1] = row;
-          else rows[0] = row;
-        }
-        const int64_t row = (j & 1) ? rows[1] : rows[0];
-        if (row < 0) return;
-        const int e = t.c * 64 + half * 32;  // 32 dims
-        if constexpr (KF == QPS_FMT_Q8_0) {
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p.k.data) + row * D + e);
-          r.d[0] = src[0];
-          r.d[1] = src[1];
-          r.x[0] = reinterpret_cast<const uint16_t*>(p.k.aux)[row * (D / 32) + e / 32];
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.k.data) + row * D + e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r.d[i] = src[i];
-        }
-      } else {
-        const int64_t row = (j & 1) ? rows[1] : rows[0];
-        if (row < 0) return;
-        const int e = t.c * 128 + half * 64;  // 64 dims
-        if constexpr (VF == QPS_FMT_Q8_0) {
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p.v.data) + row * D + e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) r.d[i] = src[i];
-          r.x[0] = reinterpret_cast<const uint32_t*>(p.v.aux)[(row * (D / 32) + e / 32) / 2];
-        } else if constexpr (VF == QPS_FMT_F16) {
-          const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.v.data) + row * D + e);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) r.d[i] = src[i];
-        } else {
-          r.d[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p.v.data) + row * (D / 4) + e / 4);
-          if constexpr (VF == QPS_FMT_TQ3) {
-            const uint2 s = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.v.aux) + row * (D / 8) + e / 8);
-            r.x[0] = s.x;
-            r.x[1] = s.y;
-          }
-        }
+    // bytes of a position's row in a box; V: column groups of a slot, signs behind the codes
+    const int rb = v ? (VF == QPS_FMT_F16 || VF == QPS_FMT_Q8_0 ? 128 : 32) : (KF == QPS_FMT_F16 ? 128 : 64);
+    const int groups = v && !VDEC ? 2 : 1;
+    const bool signs = v && VF == QPS_FMT_TQ3;
+    const int ring = !v ? KN : VDEC ? VN : kSlots, count = ntiles * (v ? G::VC : G::KC);
+    for (int f = 0; f < count; ++f) {
+      const int s = f % ring, round = f / ring, j = f / (v ? G::VC : G::KC), c = f % (v ? G::VC : G::KC);
+      if (round > 0 && !wait(!v ? kraw_empty(s) : VDEC ? vraw_empty(s) : v_empty(s), (round & 1) ^ 1)) break;
+      const uint32_t bar = !v ? kraw_full(s) : VDEC ? vraw_full(s) : v_full(s);
+      const uint32_t dst = sbase + (!v ? G::KRAW + s * G::KSTAGE : VDEC ? G::VRAW + s * G::VSTAGE : G::RING + s * kSlot);
+      if (lane == 0) {
+        mbar_expect_tx(bar, kTile * (groups * rb + (signs ? 16 : 0)));
+        if (v && !VDEC)
+          for (int i = 1; i < 4; ++i) arrive(bar);  // (a slot's barrier counts four)
       }
-    };
-    // 16-byte chunk c of the thread's row in a column group at `base`
-    auto put = [&](uint8_t* base, int c, uint4 v) {
-      *reinterpret_cast<uint4*>(base + tok * 128 + ((c ^ (tok & 7)) << 4)) = v;
-    };
-    auto convert = [&](const Task& t, const Raw& r, uint8_t* slot) {
-      if (!is_v(t)) {
-        if constexpr (KF == QPS_FMT_Q8_0) {
-          const __half2 sc = __half2half2(__ushort_as_half((unsigned short)r.x[0]));
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {  // 8 dims
-            const uint32_t w[2] = {c & 1 ? r.d[c >> 1].z : r.d[c >> 1].x, c & 1 ? r.d[c >> 1].w : r.d[c >> 1].y};
-            uint32_t code[4], hi[4], lo[4];
-            mma::i8x4_to_h2x2(w[0], code[0], code[1]);
-            mma::i8x4_to_h2x2(w[1], code[2], code[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __half2 x = *reinterpret_cast<const __half2*>(&code[i]);
-              const __half2 h = __hmul2(x, sc), l = __hfma2(x, sc, __hneg2(h));  // the product's rounding error
-              hi[i] = *reinterpret_cast<const uint32_t*>(&h);
-              lo[i] = *reinterpret_cast<const uint32_t*>(&l);
-            }
-            put(slot, half * 4 + c, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-            put(slot + kSlot / 2, half * 4 + c, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) put(slot, half * 4 + c, r.d[c]);
-        }
-      } else {
-        uint8_t* base = slot + half * (kSlot / 2);  // the half's column group of 64 dims
-        if constexpr (VF == QPS_FMT_Q8_0) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint4 q = r.d[c >> 1];
-            const uint32_t w[2] = {c & 1 ? q.z : q.x, c & 1 ? q.w : q.y};
-            const __half2 sc = __half2half2(__ushort_as_half((unsigned short)(c < 4 ? r.x[0] : r.x[0] >> 16)));
-            uint32_t o[4];
-            mma::i8x4_to_h2x2(w[0], o[0], o[1]);
-            mma::i8x4_to_h2x2(w[1], o[2], o[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = mma::hmul2_u(o[i], sc);
-            put(base, c, make_uint4(o[0], o[1], o[2], o[3]));
-          }
-        } else if constexpr (VF == QPS_FMT_F16) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) put(base, c, r.d[c]);
-        } else {
-          const uint32_t w[4] = {r.d[0].x, r.d[0].y, r.d[0].z, r.d[0].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 16 dims: two chunks
-            uint32_t s1 = 0u, s2 = 0u;
-            if constexpr (VF == QPS_FMT_TQ3) {  // columns j, j + 4 | j + 8, j + 12 at bits j, 16 + j
-              const uint32_t sg = k & 1 ? r.x[k >> 1] >> 16 : r.x[k >> 1] & 0xffffu;
-              s1 = (sg & 0xfu) | ((sg & 0xf0u) << 12);
-              s2 = ((sg >> 8) & 0xfu) | ((sg & 0xf000u) << 4);
-            }
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t sel = ((w[k] >> (2 * j)) & 0x03030303u) * 0x22u + 0x10101010u;
-              uint32_t m0 = __byte_perm(tq_lo, tq_hi, sel), m1 = __byte_perm(tq_lo, tq_hi, sel >> 16);
-              if constexpr (VF == QPS_FMT_TQ3) {  // a clear sign bit stores a negative level
-                m0 |= ~(s1 << (15 - j)) & 0x80008000u;
-                m1 |= ~(s2 << (15 - j)) & 0x80008000u;
-              }
-              o[2 * j] = m0;
-              o[2 * j + 1] = m1;
-            }
-            put(base, 2 * k, make_uint4(o[0], o[1], o[2], o[3]));
-            put(base, 2 * k + 1, make_uint4(o[4], o[5], o[6], o[7]));
-          }
-        }
-      }
-    };
-    Task next = {0, 0}, now = {0, 0};
-    Raw ring[2];
-    if (ntiles > 0) {
-      load(next, ring[0]);
-      advance(next);
-      if (!done(next)) load(next, ring[1]);
-      advance(next);
-    }
-    bool ok = true;
-    auto turn = [&](int f, Raw& r) {  // fill slot f from r, then load two slots ahead into r
-      const int s = f % kSlots;
-      if (f >= kSlots && !wait(empty(s), ((f / kSlots) & 1) ^ 1)) {
-        ok = false;
-        return;
-      }
-      convert(now, r, smem + G::RING + s * kSlot);
-      mma::fence_proxy_async();
       __syncwarp();
-      if (lane == 0) arrive(full(s));
-      advance(now);
-      if (!done(next)) {
-        load(next, r);
-        advance(next);
+      for (int i = lane; i < nb * groups; i += 32) {
+        const int grp = i / nb, r = i % nb, at = t0 + j * kTile + r * br;
+        int page = (int)p.n_pages;  // behind the last position, or out of range: zeros
+        if (at < t1) {
+          const int pg = table[at >> p.page_shift];
+          if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) page = pg;
+          else atomicOr(p.err, kErrIndex);
+        }
+        const int y = at & ((1 << p.page_shift) - 1);
+        tma_load_4d(dst + grp * (kSlot / 2) + r * br * rb, v ? &maps.v : &maps.k, (c * groups + grp) * rb, y, head, page, bar);
+        if (signs) tma_load_4d(dst + kTile * 32 + r * br * 16, &maps.va, c * 16, y, head, page, bar);
+      }
+      issued = f + 1;
+    }
+  } else if (warp >= 8) {
+    // ---- decode: one position a thread, K by warps 8-11, V by warps 12-15 ------------------------
+    const bool v = warp >= 12;
+    const int tok = threadIdx.x & 127;
+    const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
+    // the position's q8_0 scales (0: no position, or no page), loaded a tile ahead
+    constexpr int W = D / 64;  // words of two
+    auto load_scales = [&](int j, const void* aux, uint32_t (&w)[W]) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = 0u;
+      const int at = t0 + j * kTile + tok;
+      if (j >= ntiles || at >= t1) return;
+      const int pg = table[at >> p.page_shift];
+      if ((uint64_t)(int64_t)pg >= (uint64_t)p.n_pages) return;  // (reported by the boxes' warps)
+      const int64_t row = (((int64_t)pg * p.hkv + head) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+      const uint2* src = reinterpret_cast<const uint2*>(reinterpret_cast<const __half*>(aux) + row * (D / 32));
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const uint2 x = src[i];
+        w[2 * i] = x.x;
+        w[2 * i + 1] = x.y;
       }
     };
-    for (int f = 0; ntiles > 0 && ok && !done(now); f += 2) {
-      turn(f, ring[0]);
-      if (ok && !done(now)) turn(f + 1, ring[1]);
+    auto scale_of = [](uint32_t w, int hi) { return __half2half2(__ushort_as_half((unsigned short)(hi ? w >> 16 : w))); };
+    uint32_t next[W], w[W];
+    if (!v) {
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+      if constexpr (KF == QPS_FMT_Q8_0) load_scales(0, p.k.aux, next);
+      int f = 0;
+      bool ok = true;
+      for (int j = 0; j < ntiles && ok; ++j) {
+        if constexpr (KF == QPS_FMT_Q8_0) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) w[i] = next[i];
+          load_scales(j + 1, p.k.aux, next);
+        }
+#pragma unroll 1
+        for (int c = 0; c < G::KC; ++c, ++f) {
+          const int rs = f % KN, s = f & 1;
+          if (!(ok = wait(kraw_full(rs), (f / KN) & 1))) break;
+          const uint8_t* raw = smem + G::KRAW + rs * G::KSTAGE;
+          const uint32_t dst = tmem + lanes + G::K_COL + s * 64;
+          if constexpr (KF == QPS_FMT_Q8_0) {
+            uint4 q[4];  // 64 codes, chunk i of the 64-byte row at i ^ (row / 2) % 4
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              q[i] = *reinterpret_cast<const uint4*>(raw + tok * 64 + ((i ^ ((tok >> 1) & 3)) << 4));
+            __syncwarp();
+            if (lane == 0) arrive(kraw_empty(rs));
+            if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
+            fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {  // a block of 32
+              const __half2 sc = scale_of(w[0], b);
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 qq = q[2 * b + (i >> 2)];
+                const uint32_t word = (i & 3) == 0 ? qq.x : (i & 3) == 1 ? qq.y : (i & 3) == 2 ? qq.z : qq.w;
+                uint32_t code[2];
+                mma::i8x4_to_h2x2(word, code[0], code[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const __half2 c2 = *reinterpret_cast<const __half2*>(&code[k]);
+                  const __half2 h = __hmul2(c2, sc), l = __hfma2(c2, sc, __hneg2(h));  // the product's rounding error
+                  hi[2 * i + k] = *reinterpret_cast<const uint32_t*>(&h);
+                  lo[2 * i + k] = *reinterpret_cast<const uint32_t*>(&l);
+                }
+              }
+              tmem_st16(dst + 16 * b, hi);
+              tmem_st16(dst + 32 + 16 * b, lo);
+            }
+#pragma unroll
+            for (int i = 0; i + 1 < W; ++i) w[i] = w[i + 1];  // the next slot's scales
+          } else {
+            uint32_t x[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint4 q = *reinterpret_cast<const uint4*>(raw + tok * 128 + ((i ^ (tok & 7)) << 4));
+              x[4 * i] = q.x;
+              x[4 * i + 1] = q.y;
+              x[4 * i + 2] = q.z;
+              x[4 * i + 3] = q.w;
+            }
+            __syncwarp();
+            if (lane == 0) arrive(kraw_empty(rs));
+            if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
+            fence_after();
+            tmem_st32(dst, x);
+          }
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive(k_full(s));
+        }
+      }
+    } else if constexpr (VDEC) {
+      // levels as fp16 (see attn_mma.cuh): TQ3 magnitudes m in bytes 2m, 2m + 1; TQ2 fields
+      uint32_t tq_lo = 0u, tq_hi = 0u;
+      if constexpr (VF == QPS_FMT_TQ3) {
+        tq_lo = mma::pack_h2(p.tq_levels[4], p.tq_levels[5]);
+        tq_hi = mma::pack_h2(p.tq_levels[6], p.tq_levels[7]);
+      } else if constexpr (VF == QPS_FMT_TQ2) {
+        tq_lo = mma::pack_h2(p.tq_levels[1], p.tq_levels[0]);
+        tq_hi = mma::pack_h2(p.tq_levels[2], p.tq_levels[3]);
+      }
+      if constexpr (VF == QPS_FMT_Q8_0) load_scales(0, p.v.aux, next);
+      // 16-byte chunk c of the position's row in a slot's column group g
+      auto put = [&](uint8_t* slot, int g, int c, const uint32_t* o) {
+        *reinterpret_cast<uint4*>(slot + g * (kSlot / 2) + tok * 128 + ((c ^ (tok & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      };
+      int f = 0;
+      bool ok = true;
+      for (int j = 0; j < ntiles && ok; ++j) {
+        if constexpr (VF == QPS_FMT_Q8_0) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) w[i] = next[i];
+          load_scales(j + 1, p.v.aux, next);
+        }
+#pragma unroll 1
+        for (int c = 0; c < G::VC; ++c, ++f) {
+          const int rs = f % VN, s = f % kSlots;
+          if (!(ok = wait(vraw_full(rs), (f / VN) & 1))) break;
+          const uint8_t* raw = smem + G::VRAW + rs * G::VSTAGE;
+          uint8_t* slot = smem + G::RING + s * kSlot;
+          if constexpr (VF == QPS_FMT_Q8_0) {
+            uint4 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = *reinterpret_cast<const uint4*>(raw + tok * 128 + ((i ^ (tok & 7)) << 4));
+            __syncwarp();
+            if (lane == 0) arrive(vraw_empty(rs));
+            if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1))) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // 16 dims
+              const __half2 sc = scale_of(w[i >> 2], (i >> 1) & 1);
+              const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                mma::i8x4_to_h2x2(word[k], o[2 * k], o[2 * k + 1]);
+                o[2 * k] = mma::hmul2_u(o[2 * k], sc);
+                o[2 * k + 1] = mma::hmul2_u(o[2 * k + 1], sc);
+              }
+              put(slot, i >> 2, (2 * i) & 7, o);
+              put(slot, i >> 2, (2 * i + 1) & 7, o + 4);
+            }
+#pragma unroll
+            for (int i = 0; i + 2 < W; ++i) w[i] = w[i + 2];  // the next slot's scales
+          } else {
+            uint4 q[2], sg = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) q[i] = *reinterpret_cast<const uint4*>(raw + tok * 32 + ((i ^ ((tok >> 2) & 1)) << 4));
+            if constexpr (VF == QPS_FMT_TQ3) sg = *reinterpret_cast<const uint4*>(raw + kTile * 32 + tok * 16);
+            __syncwarp();
+            if (lane == 0) arrive(vraw_empty(rs));
+            if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1))) break;
+            const uint32_t words[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+            const uint32_t sgw[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {  // a word: 16 dims, two chunks
+              const uint32_t word = words[k], g16 = k & 1 ? sgw[k >> 1] >> 16 : sgw[k >> 1] & 0xffffu;
+              // signs of columns j, j + 4 | j + 8, j + 12 at bits j, 16 + j
+              const uint32_t s1 = g16 | (g16 << 12), s2 = (g16 >> 8) | (g16 << 4);
+              uint32_t o[8];
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) {
+                const uint32_t sel = ((word >> (2 * jj)) & 0x03030303u) * 0x22u + 0x10101010u;
+                uint32_t m0 = __byte_perm(tq_lo, tq_hi, sel), m1 = __byte_perm(tq_lo, tq_hi, sel >> 16);
+                if constexpr (VF == QPS_FMT_TQ3) {  // a clear sign bit stores a negative level
+                  m0 |= ~(s1 << (15 - jj)) & 0x80008000u;
+                  m1 |= ~(s2 << (15 - jj)) & 0x80008000u;
+                }
+                o[2 * jj] = m0;
+                o[2 * jj + 1] = m1;
+              }
+              put(slot, k >> 2, (2 * k) & 7, o);
+              put(slot, k >> 2, (2 * k + 1) & 7, o + 4);
+            }
+          }
+          mma::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) arrive(v_full(s));
+        }
+      }
     }
   } else if (warp >= 4) {
     // ---- softmax: one position a thread ----------------------------------------------------------
@@ -492,19 +554,27 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         for (int c = 0; c < nch; ++c) {
           float x[16];
           logits(s_at, c, at, cut, x);
+          // halving exchange: after the steps 16, 8, 4, 2 a lane holds the maximum of one row
+          // over 16 lanes, the last step joins the pairs (fmaxf drops a NaN)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int m = __reduce_max_sync(0xffffffffu, ordered(x[i] == x[i] ? x[i] : -INFINITY));
-            if (lane == 0) red[(warp & 3) * kN + 16 * c + i] = m;
+          for (int h = 8; h >= 1; h /= 2) {
+            const bool up = (lane & (2 * h)) != 0;
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+              const float give = up ? x[i] : x[i + h], keep = up ? x[i + h] : x[i];
+              x[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 2 * h));
+            }
           }
+          x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
+          if (!(lane & 1)) red[(warp & 3) * kN + 16 * c + (lane >> 1)] = __float_as_int(x[0]);
         }
         asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
         float cr = 1.f;
         if (tl < 16 * nch) {
-          int m = red[tl];
+          float top = __int_as_float(red[tl]);
 #pragma unroll
-          for (int w = 1; w < 4; ++w) m = max(m, red[w * kN + tl]);
-          const float top = unordered(m), old = thr[tl] - 8.f;
+          for (int w = 1; w < 4; ++w) top = fmaxf(top, __int_as_float(red[w * kN + tl]));
+          const float old = thr[tl] - 8.f;
           if (top > old) {
             cr = old == -INFINITY ? 0.f : ex2(old - top);
             thr[tl] = top + 8.f;
@@ -671,9 +741,19 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         else reinterpret_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(v);
       }
     }
-  } else if (warp == 0) {  // the products under way, before their operands and TMEM go
-    const uint64_t since = global_ns();
-    while (!mbar_try_wait(all_done, 0) && global_ns() - since < mma::kWaitLimitNs) {
+  } else {  // the products and boxes under way, before their operands and TMEM go
+    auto drain = [&](uint32_t bar, uint32_t parity) {
+      const uint64_t since = global_ns();
+      while (!mbar_try_wait(bar, parity) && global_ns() - since < mma::kWaitLimitNs) {
+      }
+    };
+    if (warp == 0) drain(all_done, 0);
+    if (warp == 2)
+      for (int i = max(0, issued - KN); i < issued; ++i) drain(kraw_full(i % KN), (i / KN) & 1);
+    if (warp == 3) {
+      const int ring = VDEC ? VN : kSlots;
+      for (int i = max(0, issued - ring); i < issued; ++i)
+        drain(VDEC ? vraw_full(i % ring) : v_full(i % ring), (i / ring) & 1);
     }
   }
   fence_before();
@@ -684,10 +764,22 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 
 template <int D, int KF, int VF>
 qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
-  using G = GeoTt<D>;
+  using G = GeoTt<D, KF, VF>;
   static_assert(G::SMEM <= 227 * 1024, "the slots exceed the shared memory of one CTA");
   static_assert(G::O_COL + G::VC * kN <= G::COLS, "S and O exceed TMEM");
-  static_assert(kN * D * 4 <= kSlots * kSlot, "the output rows fit the slots");
+  static_assert(kN * D * 4 <= kSlots * kSlot + 2 * G::RAW_BYTES, "the output rows fit the slots and raw stages");
+  TmaSet maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int page = 1 << p.page_shift, rows = page < kTile ? page : kTile;
+  auto map = [&](TensorMap* m, const void* plane, int row_bytes, int box, int swizzle) {
+    return encode_plane_map(m, plane, row_bytes, page, p.hkv, page, (int)p.n_pages, (int64_t)p.hkv * page, box, swizzle, rows);
+  };
+  if (!(KF == QPS_FMT_F16 ? map(&maps.k, p.k.data, 2 * D, 128, 128) : map(&maps.k, p.k.data, D, 64, 64)) ||
+      !(VF == QPS_FMT_F16    ? map(&maps.v, p.v.data, 2 * D, 128, 128)
+        : VF == QPS_FMT_Q8_0 ? map(&maps.v, p.v.data, D, 128, 128)
+                             : map(&maps.v, p.v.data, D / 4, 32, 32)) ||
+      (VF == QPS_FMT_TQ3 && !map(&maps.va, p.v.aux, D / 8, 16, 0)))
+    return QPS_ERR_CUDA;
   auto kern = attn_tt_kernel<D, KF, VF>;
   static std::atomic<uint64_t> sized{0};
   int dev = 0;
@@ -707,7 +799,7 @@ qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p));
+  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, maps));
   count_launch();
   QPS_CUDA_TRY(cudaGetLastError());
   return QPS_OK;
