@@ -102,12 +102,12 @@ qps_status append_f32(int d, const AppendP& p, cudaStream_t s);
 namespace rows {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kAhead = 2;  // groups of rows under way per warp
 // Blocks per SM the registers are sized for: element-by-element angles (neighbours, a part
 // of the row) take 32 registers, the halves' 16.
 template <int D, typename T, int MODE>
-constexpr int kBlocksPerSm = MODE == 1 || MODE == 3 ? 2 : 3;
+constexpr int kBlocksPerSm = MODE == 1 || MODE == 3 ? 4 : 6;
 
 template <int D>
 struct Row {
@@ -480,12 +480,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, T, MODE>)
 
 // q8_0: blocks of 32 are 4 neighbouring lanes' groups.  A code is the quotient x / d16,
 // rounded to float32 and then to the nearest whole number, halves away from zero.  As
-// |x / d16| <= 128, x times the correctly rounded reciprocal is within 2^-16 of it and
-// the rounded quotient within 2^-17: unless the product is within 2^-15 of a half, both
-// give the same code.  Only near a half (or for a NaN) is the division made.
+// |x / d16| <= 128, z = x times the correctly rounded reciprocal is within 2^-16 of it and
+// the rounded quotient within 2^-17: unless z is within 2^-15 of a half, both give the same
+// code, which z + 1.5 * 2^23 holds in its low byte.  Only near a half, and where the scale
+// is not a normal number (a code could leave +-127) or a value is NaN, is the division made.
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 template <int D>
 __device__ __forceinline__ void store_q8(const float (&x)[2][8], uint8_t* data, uint8_t* aux, int64_t row, int sub,
-                                         bool on) {
+                                         bool on, f2 one) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  const f2 magic = pack2(kMagic, kMagic), unmagic = pack2(-kMagic, -kMagic), minus = pack2(-1.f, -1.f);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     float amax = 0.f;
@@ -496,21 +504,24 @@ __device__ __forceinline__ void store_q8(const float (&x)[2][8], uint8_t* data, 
     const __half d16 = __float2half_rn(__fdiv_rn(amax, 127.0f));
     const float dd = __half2float(d16);
     const float rcp = __frcp_rn(dd);
-    int q[8];
-    bool near = false;
+    const f2 r2 = pack2(rcp, rcp);
+    float off = 0.f;  // the largest distance of a z from its code
+    uint32_t q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float z = __fmul_rn(x[c][i], rcp);
-      const float t = rintf(z);
-      near |= !(fabsf(z - t) < 0.5f - 0x1p-15f);
-      q[i] = min(max((int)t, -127), 127);
+    for (int i = 0; i < 4; ++i) {
+      const f2 z = mul2(pack2(x[c][2 * i], x[c][2 * i + 1]), r2);
+      const f2 m = add2(z, magic, one);
+      float a, b, u, v;
+      unpack2(m, a, b);
+      q[2 * i] = __float_as_uint(a);
+      q[2 * i + 1] = __float_as_uint(b);
+      unpack2(add2(z, add2(m, unmagic, one), minus), u, v);  // code - z (the product with -1 is exact)
+      off = max_nan(max_nan(off, fabsf(u)), fabsf(v));
     }
-    if (near) {
+    if (!(off < 0.5f - 0x1p-15f && dd >= 0x1p-14f && dd < 65536.f)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        q[i] = 0;
-        if (dd != 0.f) q[i] = (int)fminf(fmaxf(roundf(__fdiv_rn(x[c][i], dd)), -127.f), 127.f);
-      }
+      for (int i = 0; i < 8; ++i)
+        q[i] = dd != 0.f ? (uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x[c][i], dd)), -127.f), 127.f) : 0u;
     }
     if (!on) continue;
     uint32_t packed[2];
@@ -682,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, T, MODE>)
       float x[2][8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) unpack8<__half>(h16[c], x[c]);
-      if (s.fmt == QPS_FMT_Q8_0) store_q8<D>(x, s.data, s.aux, row, sub, on);
+      if (s.fmt == QPS_FMT_Q8_0) store_q8<D>(x, s.data, s.aux, row, sub, on, one);
       else store_tq<D>(x, p.tq, s.data, s.aux, s.aux2, row, sub, on);
     }
   }
