@@ -398,9 +398,9 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   bool whole = false;  // (paged) the chunk is all its rows attend: the output itself is written
   if constexpr (PAGED) {
     if (!p.shared) {  // chunk number `split` of the batch: find its sequence and positions
-      if (blockIdx.x == 0 && head == 0 && warp == 0) paged_publish(p, lane);
       const PagedChunk ch = paged_find(p, split, lane);
       if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
+      if (ch.first && head == 0 && rg == 0 && threadIdx.x == 0) p.chunks[ch.b] = make_int2(split, ch.count);
       bz = ch.b;
       whole = ch.whole;
       t0 = ch.t0;
@@ -429,10 +429,12 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     for (int idx = threadIdx.x; idx < nrows * D; idx += G::NW * 32) {
       const int r = idx / D, dd = idx % D;
       const int64_t row = out_row(row0 + r);
-      if constexpr (PAGED) {  // (an empty sequence: `whole`)
-        if (p.out_dtype == QPS_DT_F32) reinterpret_cast<float*>(p.out)[row * D + dd] = 0.f;
+      if constexpr (PAGED) {  // (a sequence without own positions: its output, or an empty part)
+        const int64_t at = (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
+        if (!whole) p.own_o[at * D + dd] = 0.f;
+        else if (p.out_dtype == QPS_DT_F32) reinterpret_cast<float*>(p.out)[row * D + dd] = 0.f;
         else reinterpret_cast<uint16_t*>(p.out)[row * D + dd] = 0;
-        if (dd == 0) p.out_lse[row] = -INFINITY;
+        if (dd == 0) (whole ? p.out_lse[row] : p.own_lse[at]) = -INFINITY;
         continue;
       }
       if (!in_bounds(part < p.parts_cap && row >= 0 && row < p.rows_total, p.err)) continue;

@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   const bool real = row < p.rows_total;
   const int b = real ? (int)(row / rows) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int first = p.first[b], count = p.first[b + 1] - first;
+  const int2 own = p.chunks[b];
+  const int first = own.x, count = own.y;
   const bool mine = real && !(count == 1 && p.n_prefix == 0);  // (else written by the attention)
   const int total = mine ? p.n_prefix + count : 0;
   float m = -INFINITY, den = 0.f;
@@ -143,15 +144,17 @@ struct Plan {
   PagedAttnParams p;
   PagedKernel prefix_kernel, own_kernel;
   int parts;   // most parts a row can have; one: no merge
-  size_t off_pre_lse, off_own_o, off_own_lse, off_first, bytes;
+  size_t off_pre_lse, off_own_o, off_own_lse, off_chunks, bytes;
 };
 
 // Chunks of the sequences' own positions.  Few sequences: one round of the CTAs the GPU
 // holds, less one for each sequence's short last chunk (a second round of a few CTAs costs
 // as much as a full one).  More sequences than half a round: kWaves rounds, so that ragged
-// lengths level out.  Each at least kMinPositions long, so that a part is worth its merge.
+// lengths level out.  Each at least kMinPositions long, so that a part is worth its merge,
+// or kMinMany where the sequences alone fill a round (64 suffixes of 1 to 512 positions
+// behind a prefix, 8 KV heads: 23 us in chunks of 128).
 constexpr int kWaves = 2;
-constexpr int kMinPositions = 128;
+constexpr int kMinPositions = 128, kMinMany = 512;
 
 // The kernel for `rows` query rows per KV head, and the rows, positions and CTAs per SM
 // that it works with.
@@ -264,11 +267,12 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
     const int ctas = kv.hkv * ((rows + sh.rows - 1) / sh.rows), slots = sh.ctas_per_sm * sms;
     const int round = slots / ctas;
     p.target = std::max(1, 2 * a->batch <= round ? round - a->batch + 1 : kWaves * slots / ctas);
-    p.min_units = kMinPositions / kPagedUnit;
+    const int least = a->batch >= round ? kMinMany : kMinPositions;
+    p.min_units = least / kPagedUnit;
     p.unit_round = sh.tile / kPagedUnit;
     // chunks of a sequence that fills its table, and of all of them
     const int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
-    const int64_t each = std::max<int64_t>(1, (most + kMinPositions - 1) / kMinPositions);
+    const int64_t each = std::max<int64_t>(1, (most + least - 1) / least);
     p.max_chunks = (int)std::min<int64_t>((int64_t)p.target + a->batch, each * a->batch);
     out->parts = p.n_prefix + (int)std::min<int64_t>(each, p.target + 1);
   }
@@ -277,8 +281,8 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
   out->off_pre_lse = up(pre * kv.d * sizeof(float));
   out->off_own_o = out->off_pre_lse + up(pre * sizeof(float));
   out->off_own_lse = out->off_own_o + up(own * kv.d * sizeof(float));
-  out->off_first = out->off_own_lse + up(own * sizeof(float));
-  out->bytes = out->off_first + up((size_t)(a->batch + 1) * sizeof(int32_t));
+  out->off_chunks = out->off_own_lse + up(own * sizeof(float));
+  out->bytes = out->off_chunks + up((size_t)a->batch * sizeof(int2));
   return QPS_OK;
 }
 
@@ -311,7 +315,7 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   p.pre_lse = reinterpret_cast<float*>(ws + pl.off_pre_lse);
   p.own_o = reinterpret_cast<float*>(ws + pl.off_own_o);
   p.own_lse = reinterpret_cast<float*>(ws + pl.off_own_lse);
-  p.first = pl.parts > 1 ? reinterpret_cast<int32_t*>(ws + pl.off_first) : nullptr;
+  p.chunks = reinterpret_cast<int2*>(ws + pl.off_chunks);
   p.out = a->o;
   p.out_lse = a->lse;
   const int rows = p.n_q * p.group;

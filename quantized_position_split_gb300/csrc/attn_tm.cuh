@@ -169,15 +169,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     t0 = split * (int)p.chunk;
     t1 = min((int)p.end, t0 + (int)p.chunk);
   } else {
-    if (blockIdx.x == 0 && head == 0 && warp == 2) paged_publish(p, lane);
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
+    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0) p.chunks[ch.b] = make_int2(split, ch.count);
     bz = ch.b;
     t0 = ch.t0;
     t1 = ch.t1;
     whole = ch.whole;
   }
-  const int ntiles = t1 > t0 ? (t1 - t0 + kTok - 1) / kTok : 0;  // 0: an empty sequence
+  const int ntiles = t1 > t0 ? (t1 - t0 + kTok - 1) / kTok : 0;  // 0: no own positions
 
   // ---- barriers, TMEM, queries ---------------------------------------------------------------
   const uint32_t bars = sbase + G::BAR;
@@ -187,28 +187,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_empty = [&](int s) { return bars + 8 * (3 * ST + s); };
   auto s_full = [&](int w) { return bars + 8 * (4 * ST + w); };
   auto p_ready = [&](int w) { return bars + 8 * (4 * ST + 2 + w); };
-  const uint32_t all_done = bars + 8 * (4 * ST + 4);
-  static_assert(8 * (4 * ST + 5) <= 240, "barriers fit their region");
+  const uint32_t all_done = bars + 8 * (4 * ST + 4), q_full = bars + 8 * (4 * ST + 5);
+  static_assert(8 * (4 * ST + 6) <= 240, "barriers fit their region");
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + G::BAR + 240);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::BAR + 244);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * ST + 5; ++i) mbar_init(bars + 8 * i, i >= 4 * ST + 2 && i < 4 * ST + 4 ? 4 : 1);
+    for (int i = 0; i < 4 * ST + 6; ++i)
+      mbar_init(bars + 8 * i, i == 4 * ST + 5 ? 8 : i >= 4 * ST + 2 && i < 4 * ST + 4 ? 4 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *abort_flag = 0;
   }
   if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
-  // Q [128][D], K-major: row r's 16-byte chunk c of a column group at r * 128 + (c ^ r % 8) * 16
-  for (int i = threadIdx.x; i < kRows * D / 8; i += kThreads) {
-    const int r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (rr < p.rows_per_cta) {
-      const int e = rr / p.group, h = head * p.group + rr % p.group;
-      const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
-      v = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
-    }
-    *reinterpret_cast<uint4*>(smem + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-  }
-  mma::fence_proxy_async();
   fence_before();
   __syncthreads();
   fence_after();
@@ -232,6 +221,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (__shfl_sync(0xffffffffu, over, 0)) return false;
     }
+  };
+  // Q [128][D], K-major: row r's 16-byte chunk c of a column group at r * 128 + (c ^ r % 8) *
+  // 16; by the softmax warps, every load first, while the first tiles are under way.
+  auto load_q = [&]() {
+    constexpr int N = kRows * D / 8 / 256;
+    uint4 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x - 128 + k * 256, r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (rr < p.rows_per_cta) {
+        const int e = rr / p.group, h = head * p.group + rr % p.group;
+        const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
+        v[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x - 128 + k * 256, r = i / (D / 8), c = i % (D / 8);
+      *reinterpret_cast<uint4*>(smem + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
+    }
+    mma::fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(q_full) : "memory");
   };
   int issued_k = 0, issued_v = 0;  // (warp 0) tiles under way or landed
 
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(s_full(j & 1), one);
       return true;
     };
-    bool ok = true;
+    bool ok = ntiles == 0 || wait(q_full, 0);
     for (int j = 0; j < min(2, ntiles) && ok; ++j) ok = s_product(j);
     for (int j = 0; j < ntiles && ok; ++j) {
       const int s = j % ST, w = j & 1;
@@ -316,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = (warp - 4) >> 2, r = (warp & 3) * 32 + lane, rr = row0 + r;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_at = tmem + lanes + G::S_COL + w * kTok, o_at = tmem + lanes + G::O_COL + w * D;
+    load_q();
     int lim = 0;  // positions below it are visible to the row
     if (rr < p.rows_per_cta) {
       const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
@@ -449,33 +463,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- merge the streams, write the chunk's part --------------------------------------------
     if (ok) ok = wait(all_done, 0);
     fence_after();
-    // stream 1 hands over its state and O through the stages (every tile has been consumed):
-    // column-major, so that a warp's rows are neighbours
-    float* hand = reinterpret_cast<float*>(smem + G::K_OFF);   // [D][128]
-    float* state = reinterpret_cast<float*>(smem);              // [2][128] (over Q)
-    uint32_t v[32];
-    if (ok && w == 1 && ntiles > 1) {
-      state[r] = m;
-      state[kRows + r] = l;
+    // The streams exchange halves of O through the stages (every tile has been consumed), and
+    // their states: stream w finishes the columns [w D/2, (w + 1) D/2).  Column-major, so that
+    // a warp's rows are neighbours.
+    constexpr int H = D / 2;
+    float* hand = reinterpret_cast<float*>(smem + G::K_OFF);   // [2][D / 2][128]
+    float* state = reinterpret_cast<float*>(smem);              // [2][2][128] (over Q)
+    const bool two = ntiles > 1;
+    if (ok) {
+      state[w * 2 * kRows + r] = m;
+      state[w * 2 * kRows + kRows + r] = l;
+      if (two) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        __syncwarp();
-        tmem_ld32(v, o_at + 32 * c);
-        tmem_wait_ld();
+        for (int c = 0; c < H / 32; ++c) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(v, o_at + (1 - w) * H + 32 * c);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) hand[(32 * c + i) * kRows + r] = __uint_as_float(v[i]);
+          for (int i = 0; i < 32; ++i) hand[w * H * kRows + (32 * c + i) * kRows + r] = __uint_as_float(v[i]);
+        }
       }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (ok && w == 0 && !__any_sync(0xffffffffu, *abort_flag)) {
-      const bool two = ntiles > 1;
-      const float m1 = two ? state[r] : -INFINITY, l1 = two ? state[kRows + r] : 0.f;
-      const float mx = fmaxf(m, m1);
-      const float f0 = m == -INFINITY ? 0.f : ex2(m - mx), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mx);
-      const float den = l * f0 + l1 * f1;
+    if (ok && !__any_sync(0xffffffffu, *abort_flag)) {
+      const float m0 = m, l0 = l, m1 = state[(1 - w) * 2 * kRows + r], l1 = state[(1 - w) * 2 * kRows + kRows + r];
+      const float mx = fmaxf(m0, m1);
+      const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - mx), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mx);
+      const float den = l0 * f0 + l1 * f1;
       const bool empty = den == 0.f;
       const float inv = empty ? 0.f : 1.f / den;
-      const float w0 = f0 * inv, w1 = f1 * inv;
+      const float w0 = f0 * inv, w1 = f1 * inv;  // of this stream's columns, and of the other's
+      const bool has0 = ntiles > w, has1 = ntiles > 1 - w;
       int64_t at = 0;
       if (rr < p.rows_per_cta) {
         const int h = head * p.group + rr % p.group;
@@ -483,31 +502,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         at = p.shared ? (int64_t)split * p.rows_total + local
              : whole  ? (int64_t)bz * (p.n_q * p.hq) + local
                       : (int64_t)split * (p.n_q * p.hq) + local;
-        const float lv = empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
-        (whole ? p.out_lse : p.shared ? p.pre_lse : p.own_lse)[at] = lv;
+        if (w == 0)
+          (whole ? p.out_lse : p.shared ? p.pre_lse : p.own_lse)[at] =
+              empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
       }
       float* parts = p.shared ? p.pre_o : p.own_o;
+      // stream 1 wrote nothing where there is one tile: stream 0's half is then read from TMEM
+      const uint32_t o_own = (two || w == 0) ? o_at + w * H : tmem + lanes + G::O_COL + H;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < H / 32; ++c) {
+        uint32_t v[32];
         __syncwarp();
-        if (ntiles > 0) {
-          tmem_ld32(v, o_at + 32 * c);
-          tmem_wait_ld();
-        }
+        tmem_ld32(v, o_own + 32 * c);
+        tmem_wait_ld();
+        const float wv = two || w == 0 ? w0 : w1;  // the weight of what was read
+        const bool hv = two || w == 0 ? has0 : has1;
         float o[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          o[i] = ntiles > 0 && w0 != 0.f ? __uint_as_float(v[i]) * w0 : 0.f;
-          if (two && w1 != 0.f) o[i] = fmaf(hand[(32 * c + i) * kRows + r], w1, o[i]);
+          o[i] = hv && wv != 0.f ? __uint_as_float(v[i]) * wv : 0.f;
+          if (two && w1 != 0.f) o[i] = fmaf(hand[(1 - w) * H * kRows + (32 * c + i) * kRows + r], w1, o[i]);
         }
+        const int64_t to = at * D + w * H + 32 * c;
         if (rr >= p.rows_per_cta) {
           // (no row: nothing to store)
         } else if (!whole || p.out_dtype == QPS_DT_F32) {
-          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : parts) + at * D + 32 * c);
+          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : parts) + to);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at * D + 32 * c);
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + to);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t x[4];

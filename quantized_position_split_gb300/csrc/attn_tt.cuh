@@ -88,15 +88,15 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     t0 = split * (int)p.chunk;
     t1 = min((int)p.end, t0 + (int)p.chunk);
   } else {
-    if (blockIdx.x == 0 && head == 0 && warp == 2) paged_publish(p, lane);
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
+    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0) p.chunks[ch.b] = make_int2(split, ch.count);
     bz = ch.b;
     t0 = ch.t0;
     t1 = ch.t1;
     whole = ch.whole;
   }
-  const int ntiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;  // 0: an empty sequence
+  const int ntiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;  // 0: no own positions
   const int nrows = min(kN, p.rows_per_cta - row0);
   const int n16 = (nrows + 15) & ~15;  // N of the products
 

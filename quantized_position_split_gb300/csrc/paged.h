@@ -37,7 +37,7 @@ struct PagedAttnParams : AttnParams {
   float* pre_lse;
   float* own_o;       // f32 [chunk][n_q*hq][D], [chunk][n_q*hq]
   float* own_lse;
-  int32_t* first;     // [batch + 1] (see paged_publish), NULL when there is no merge
+  int2* chunks;       // [batch] first chunk and count, for the merge; written by first chunks
   void* out;          // the call's o (out_dtype) and lse
   float* out_lse;
   int out_dtype;
@@ -46,8 +46,8 @@ struct PagedAttnParams : AttnParams {
 // The chunking of the sequences' own positions [prefix_len, len), the same in the
 // attention and in the merge: units of 32 positions, C units a chunk (a multiple of
 // unit_round), sequence b's chunks numbered behind those of the sequences before it.  C is
-// such that all chunks together number at most `target` + batch.  Without a prefix an
-// empty sequence has one chunk, which writes its empty output.
+// such that all chunks together number at most `target` + batch.  A sequence without own
+// positions has one chunk, which writes an empty part.
 __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
   const int n = p.lens[b];
   const int most = p.table_width << p.page_shift;
@@ -60,13 +60,13 @@ __device__ __forceinline__ int paged_units(int len, int prefix) {
   return len > prefix ? (len - prefix + kPagedUnit - 1) / kPagedUnit : 0;
 }
 __device__ __forceinline__ int paged_chunks(const PagedAttnParams& p, int len, int cu) {
-  const int n = (paged_units(len, p.prefix_len) + cu - 1) / cu;
-  return n == 0 && p.prefix_len == 0 ? 1 : n;
+  return max(1, (paged_units(len, p.prefix_len) + cu - 1) / cu);
 }
 
 // Chunk length in units; every lane of the warp takes part.
 __device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int lane) {
   int total = 0;
+#pragma unroll 4  // (the loads together: one latency for 128 sequences)
   for (int b = lane; b < p.batch; b += 32) total += paged_units(paged_len(p, b), p.prefix_len);
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -74,35 +74,16 @@ __device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int l
   return (c + p.unit_round - 1) / p.unit_round * p.unit_round;
 }
 
-// The number of every sequence's first chunk, for the merge: p.first[b], p.first[batch].
-__device__ __forceinline__ void paged_publish(const PagedAttnParams& p, int lane) {
-  if (!p.first) return;
-  const int cu = paged_chunk_units(p, lane);
-  int before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    int sum = b < p.batch ? paged_chunks(p, paged_len(p, b), cu) : 0;
-    const int own = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (b < p.batch) p.first[b] = before + sum - own;
-    before += __shfl_sync(0xffffffffu, sum, 31);
-  }
-  if (lane == 0) p.first[p.batch] = before;
-}
-
 // Chunk number `index` of the batch: its sequence (-1: there are fewer chunks), positions
-// [t0, t1) and whether it is its sequence's only part; the same in every lane.
+// [t0, t1), whether it is its sequence's first (of `count`) and its only part; the same in
+// every lane.
 struct PagedChunk {
-  int b, t0, t1;
-  bool whole;
+  int b, t0, t1, count;
+  bool first, whole;
 };
 __device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int index, int lane) {
   const int cu = paged_chunk_units(p, lane);
-  PagedChunk r = {-1, 0, 0, false};
+  PagedChunk r = {-1, 0, 0, 0, false, false};
   int before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
@@ -122,6 +103,8 @@ __device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int i
       r.b = b0 + src;
       r.t0 = p.prefix_len + at * cu * kPagedUnit;
       r.t1 = min(__shfl_sync(0xffffffffu, len, src), r.t0 + cu * kPagedUnit);
+      r.count = n;
+      r.first = at == 0;
       r.whole = n == 1 && p.prefix_len == 0;
       break;
     }
