@@ -1504,6 +1504,87 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     }
   }
   __syncthreads();
+  if constexpr (PAGED) {
+    // A row a warp, element lane + 32 e in register e: weights, sum over the warps, the
+    // rotation's inverse by shuffles, the output, without another barrier.  (Elements spread
+    // over the CTA and a barrier for each step, as below, took 3500 of the 11400 cycles of a
+    // short chunk.)
+    constexpr int E = D / 32;
+#pragma unroll 1
+    for (int r = warp; r < nrows; r += kWarps) {
+      const int64_t row = out_row(row0 + r);
+      if (!in_bounds(part < (p.shared ? p.n_prefix : p.max_chunks) && row >= 0 && row < p.rows_total, p.err)) continue;
+      float f[kWarps], mx = -INFINITY, den = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = mw[w * ROWS + r];
+        mx = fmaxf(mx, f[w]);
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = mx != -INFINITY && f[w] != -INFINITY ? exp2f(f[w] - mx) : 0.f;
+        den += lw[w * ROWS + r] * f[w];
+      }
+      const bool empty = den == 0.f;  // (a NaN logit stays one)
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v[e] += ow[(w * ROWS + r) * OWS + ow_col<D>(lane + 32 * e)] * f[w];
+      }
+      if constexpr (is_tq(VF)) {  // x = s1 .* blockdiag(H_G)(s2 .* y) / sqrt(D G)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((p.vsigns2[e] >> lane) & 1u) v[e] = -v[e];
+#pragma unroll
+        for (int h = 1; h < 32; h *= 2) {  // (every block is at least 32 wide)
+          const bool upper = (lane & h) != 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float other = __shfl_xor_sync(0xffffffffu, v[e], h);
+            v[e] = upper ? other - v[e] : v[e] + other;
+          }
+        }
+#pragma unroll
+        for (int H = 1; H < E; H *= 2) {
+          if (32 * H >= p.vblock) break;
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (!(e & H)) {
+              const float a = v[e], b = v[e + H];
+              v[e] = a + b;
+              v[e + H] = a - b;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if ((p.vsigns[e] >> lane) & 1u) v[e] = -v[e];
+      }
+      const float inv = empty ? 0.f : (is_tq(VF) ? p.v_out_scale : 1.f) / den;
+      const float lv = empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
+      if (whole) {  // nothing to merge: the one rounding to the output type
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int64_t i = row * D + lane + 32 * e;
+          const float ov = empty ? 0.f : v[e] * inv;
+          if (p.out_dtype == QPS_DT_F16) reinterpret_cast<__half*>(p.out)[i] = __float2half_rn(ov);
+          else if (p.out_dtype == QPS_DT_BF16) reinterpret_cast<__nv_bfloat16*>(p.out)[i] = __float2bfloat16_rn(ov);
+          else reinterpret_cast<float*>(p.out)[i] = ov;
+        }
+        if (lane == 0) p.out_lse[row] = lv;
+      } else {
+        // the prefix's parts hold every row of the batch, a sequence's chunk its own
+        const int64_t at = p.shared ? (int64_t)part * p.rows_total + row
+                                    : (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
+        float* dst = (p.shared ? p.pre_o : p.own_o) + at * D + lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) dst[32 * e] = empty ? 0.f : v[e] * inv;
+        if (lane == 0) (p.shared ? p.pre_lse : p.own_lse)[at] = lv;
+      }
+    }
+    return;
+  }
   // per row: the maximum over the warps, each warp's weight 2^(m_w - max) (0 for a warp
   // that saw nothing of the row) and the merged denominator
   if (threadIdx.x < ROWS) {
@@ -1558,25 +1639,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       if ((p.vsigns[dd >> 5] >> (dd & 31)) & 1u) val = -val;
     }
     const int64_t row = orow[r];
-    const bool empty = PAGED ? den == 0.f : !(den > 0.f);  // (paged: a NaN logit stays one)
-    if constexpr (PAGED) {
-      if (!in_bounds(part < (p.shared ? p.n_prefix : p.max_chunks) && row >= 0 && row < p.rows_total, p.err)) continue;
-      const float ov = empty ? 0.f : val / den;
-      const float lv = empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
-      if (whole) {  // nothing to merge: the one rounding to the output type
-        if (p.out_dtype == QPS_DT_F16) reinterpret_cast<__half*>(p.out)[row * D + dd] = __float2half_rn(ov);
-        else if (p.out_dtype == QPS_DT_BF16) reinterpret_cast<__nv_bfloat16*>(p.out)[row * D + dd] = __float2bfloat16_rn(ov);
-        else reinterpret_cast<float*>(p.out)[row * D + dd] = ov;
-        if (dd == 0) p.out_lse[row] = lv;
-      } else {
-        // the prefix's parts hold every row of the batch, a sequence's chunk its own
-        const int64_t at = p.shared ? (int64_t)part * p.rows_total + row
-                                    : (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
-        (p.shared ? p.pre_o : p.own_o)[at * D + dd] = ov;
-        if (dd == 0) (p.shared ? p.pre_lse : p.own_lse)[at] = lv;
-      }
-      continue;
-    }
+    const bool empty = !(den > 0.f);
     if (!in_bounds(part < p.parts_cap && row >= 0 && row < p.rows_total, p.err)) continue;
     p.o_parts[((int64_t)part * p.rows_total + row) * D + dd] = empty ? 0.f : val / den;
     if (dd == 0)

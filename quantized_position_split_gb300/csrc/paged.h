@@ -29,7 +29,7 @@ struct PagedAttnParams : AttnParams {
   int prefix_len;     // positions attended by the prefix launch (a multiple of 32)
   int target;         // chunks per (KV head, row group) the sequences are cut into, about
   int min_units;      // smallest chunk, in units
-  int unit_round;     // chunks are multiples of this many units
+  int unit_round;     // chunks are multiples of this many units (a power of two)
   int max_chunks;     // chunks there can be, by the tables' width
   int kernel;         // PagedKernel of this launch
   int n_prefix;       // parts of the prefix
@@ -60,18 +60,8 @@ __device__ __forceinline__ int paged_units(int len, int prefix) {
   return len > prefix ? (len - prefix + kPagedUnit - 1) / kPagedUnit : 0;
 }
 __device__ __forceinline__ int paged_chunks(const PagedAttnParams& p, int len, int cu) {
-  return max(1, (paged_units(len, p.prefix_len) + cu - 1) / cu);
-}
-
-// Chunk length in units; every lane of the warp takes part.
-__device__ __forceinline__ int paged_chunk_units(const PagedAttnParams& p, int lane) {
-  int total = 0;
-#pragma unroll 4  // (the loads together: one latency for 128 sequences)
-  for (int b = lane; b < p.batch; b += 32) total += paged_units(paged_len(p, b), p.prefix_len);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int c = max(p.min_units, (total + p.target - 1) / p.target);
-  return (c + p.unit_round - 1) / p.unit_round * p.unit_round;
+  const int units = paged_units(len, p.prefix_len);
+  return units <= cu ? 1 : (units + cu - 1) / cu;
 }
 
 // Chunk number `index` of the batch: its sequence (-1: there are fewer chunks), positions
@@ -82,13 +72,25 @@ struct PagedChunk {
   bool first, whole;
 };
 __device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int index, int lane) {
-  const int cu = paged_chunk_units(p, lane);
+  // every CTA goes this way before its first load of a position: the first 128 lengths are
+  // read together, once
+  constexpr int R = 4;
+  int len[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) len[i] = lane + 32 * i < p.batch ? paged_len(p, lane + 32 * i) : 0;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) total += paged_units(len[i], p.prefix_len);
+#pragma unroll 4
+  for (int b = lane + 32 * R; b < p.batch; b += 32) total += paged_units(paged_len(p, b), p.prefix_len);
+  total = __reduce_add_sync(0xffffffffu, total);
+  int cu = p.min_units;  // chunk length in units
+  if (total > cu * p.target) cu = (total + p.target - 1) / p.target;
+  cu = (cu + p.unit_round - 1) & ~(p.unit_round - 1);
   PagedChunk r = {-1, 0, 0, 0, false, false};
   int before = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += 32) {
-    const int b = b0 + lane;
-    const int len = b < p.batch ? paged_len(p, b) : 0;
-    const int cnt = b < p.batch ? paged_chunks(p, len, cu) : 0;
+  auto look = [&](int b0, int bl) -> bool {
+    const int cnt = b0 + lane < p.batch ? paged_chunks(p, bl, cu) : 0;
     int sum = cnt;  // inclusive scan over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -102,14 +104,22 @@ __device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int i
       const int at = index - (before + __shfl_sync(0xffffffffu, sum, src) - n);
       r.b = b0 + src;
       r.t0 = p.prefix_len + at * cu * kPagedUnit;
-      r.t1 = min(__shfl_sync(0xffffffffu, len, src), r.t0 + cu * kPagedUnit);
+      r.t1 = min(__shfl_sync(0xffffffffu, bl, src), r.t0 + cu * kPagedUnit);
       r.count = n;
       r.first = at == 0;
       r.whole = n == 1 && p.prefix_len == 0;
-      break;
+      return true;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
+    return false;
+  };
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (32 * i >= p.batch) return r;
+    if (look(32 * i, len[i])) return r;
   }
+  for (int b0 = 32 * R; b0 < p.batch; b0 += 32)
+    if (look(b0, b0 + lane < p.batch ? paged_len(p, b0 + lane) : 0)) break;
   return r;
 }
 
