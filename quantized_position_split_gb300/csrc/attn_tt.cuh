@@ -7,10 +7,12 @@
 // and the query rows on the narrow one (N = 16 .. 64), so their time follows the number of
 // rows:
 //     S^T [128 positions][N] = K Q^T      A = K (TMEM), B = Q (shared, K-major), per 64 dims
-//     P   = 2^(S' - m)                    one position a thread, all rows in its registers
+//     P   = 2^(S' - m)                    one position and 32 rows a thread
 //     O^T [128 dims][N]     += V^T P^T    A = V (shared, MN-major, as stored), B = P (MN-major)
-// S^T (two buffers), O^T (D / 128 blocks) and two slots of K live in TMEM: 256 + D / 2
-// columns.
+// S^T (two buffers), O^T (D / 128 blocks) and two slots of K live in TMEM.  Products that
+// add to one accumulator follow each other at 75 to 100 cycles, whatever N: so S^T has two
+// accumulators a buffer where TMEM has the columns (hi and lo parts, or odd and even steps),
+// and O^T takes two blocks in turn.
 //
 // The stored rows arrive by tensor-map boxes in small raw stages; four warps decode K, one
 // position a thread, from there into TMEM (64 dims a slot), four more V into 32 KB slots of
@@ -26,8 +28,9 @@
 // (in shared memory) is raised only when some position exceeds it by more than 8 (log2):
 // one vote a tile, and on a raise the maxima are taken, O and the sums rescaled.
 //
-// Roles: warp 0 issues the products, warps 2 and 3 the boxes of K and V, warps 4-7 are the
-// softmax, 8-11 decode K and 12-15 V.  Waits are bounded as in attn_tm.cuh.
+// Roles: warp 0 issues the products, warps 2 and 3 the boxes of K and V, warps 4-11 are the
+// softmax (two groups of rows), 12-15 decode K and 16-19 V.  Waits are bounded as in
+// attn_tm.cuh.
 #pragma once
 
 #include "attn_tm.cuh"
@@ -39,7 +42,7 @@ using namespace tm;
 
 constexpr int kN = 64;             // query rows per CTA
 constexpr int kTile = 128;         // positions per tile
-constexpr int kThreadsTt = 512;
+constexpr int kThreadsTt = 640;
 constexpr int kSlot = 32 * 1024, kSlots = 3;  // V's fp16 slots
 
 template <int D, int KF, int VF>
@@ -57,9 +60,6 @@ struct GeoTt {
   static constexpr int MISC = VRAW + RAW_BYTES;
   static constexpr int MISC_BYTES = D == 128 ? 2304 : 2048;
   static constexpr int SMEM = MISC + MISC_BYTES + 1024;  // + slack for the 1024-byte base alignment
-  // TMEM columns: S (two buffers), K (two slots of hi and lo), O
-  static constexpr int S_COL = 0, K_COL = 128, O_COL = 256;
-  static constexpr int COLS = 512;
 };
 
 // Position in a 16-column word of a TurboQuant V -> column: the decode yields the columns
@@ -99,6 +99,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   const int ntiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;  // 0: no own positions
   const int nrows = min(kN, p.rows_per_cta - row0);
   const int n16 = (nrows + 15) & ~15;  // N of the products
+  // TMEM columns: S (two buffers of one or two accumulators), K (two slots of 32 hi and 32
+  // lo), O
+  const int accs = (4 + G::VC) * n16 + 128 <= 512 ? 2 : 1;
+  const int k_col = 2 * accs * n16, o_col = k_col + 128;
 
   // ---- barriers, TMEM, queries, row state ----------------------------------------------------
   uint8_t* misc = smem + G::MISC;
@@ -119,53 +123,20 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   auto kraw_full = [&](int s) { return bar_at(7 + kSlots + s); };
   auto vraw_full = [&](int s) { return bar_at(7 + kSlots + KN + s); };
   constexpr int ONES = 7 + kSlots + KN + VN;                      // the barriers above count one, those below four
-  auto p_ready = [&](int w) { return bar_at(ONES + w); };
-  auto k_full = [&](int s) { return bar_at(ONES + 2 + s); };
-  auto v_full = [&](int s) { return bar_at(ONES + 4 + s); };
-  auto kraw_empty = [&](int s) { return bar_at(ONES + 4 + kSlots + s); };
-  auto vraw_empty = [&](int s) { return bar_at(ONES + 4 + kSlots + KN + s); };
-  constexpr int NBARS = ONES + 4 + kSlots + KN + VN;
+  auto p_ready = [&](int w) { return bar_at(ONES + w); };         // (p_ready, q_full: eight)
+  const uint32_t q_full = bar_at(ONES + 2);
+  auto k_full = [&](int s) { return bar_at(ONES + 3 + s); };
+  auto v_full = [&](int s) { return bar_at(ONES + 5 + s); };
+  auto kraw_empty = [&](int s) { return bar_at(ONES + 5 + kSlots + s); };
+  auto vraw_empty = [&](int s) { return bar_at(ONES + 5 + kSlots + KN + s); };
+  constexpr int NBARS = ONES + 5 + kSlots + KN + VN;
   static_assert(1800 + 8 * NBARS <= G::MISC_BYTES, "the row state and barriers fit their region");
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NBARS; ++i) mbar_init(bar_at(i), i < ONES ? 1 : 4);
+    for (int i = 0; i < NBARS; ++i) mbar_init(bar_at(i), i < ONES ? 1 : i < ONES + 3 ? 8 : 4);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *abort_flag = 0;
   }
-  if (warp == 1) tmem_alloc(smem_addr(tmem_word), G::COLS);
-  // Q [64][D], K-major, 128-byte swizzle, column groups of 64 dims: every load first
-  {
-    constexpr int N = kN * D / 8 / kThreadsTt;
-    uint4 v[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = threadIdx.x + k * kThreadsTt, r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
-      v[k] = make_uint4(0, 0, 0, 0);
-      if (rr < p.rows_per_cta) {
-        const int e = rr / p.group, h = head * p.group + rr % p.group;
-        const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
-        v[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = threadIdx.x + k * kThreadsTt, r = i / (D / 8), c = i % (D / 8);
-      *reinterpret_cast<uint4*>(smem + (c >> 3) * (kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
-    }
-  }
-  if (threadIdx.x < kN) {
-    const int rr = row0 + threadIdx.x;
-    int n = 0;
-    if (rr < p.rows_per_cta) {
-      const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
-      n = paged_len(p, b);
-      if (p.causal) n += qi + 1 - p.n_q;
-      n = min(n, t1);
-    }
-    lim[threadIdx.x] = n;
-    thr[threadIdx.x] = -INFINITY;
-    mneg[threadIdx.x] = 0.f;
-  }
-  mma::fence_proxy_async();
+  if (warp == 1) tmem_alloc(smem_addr(tmem_word), 512);
   fence_before();
   __syncthreads();
   fence_after();
@@ -203,47 +174,62 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         const int s = fk & 1;
         if (!wait(k_full(s), (fk >> 1) & 1)) return false;
         fence_after();
-        const uint32_t d = tmem + G::S_COL + (j & 1) * kN, a = tmem + G::K_COL + s * 64;
+        const uint32_t d = tmem + (j & 1) * accs * n16, d1 = d + (accs - 1) * n16, a = tmem + k_col + s * 64;
         const uint64_t b = smem_desc(sbase + c * (kN * 128), 16);
+        const uint32_t fresh = c > 0;  // (0: a tile's first products start their accumulators)
 #pragma unroll
-        for (int part = 0; part < (KF == QPS_FMT_Q8_0 ? 2 : 1); ++part)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(d, a + part * 32 + kk * 8, b + (uint64_t)(kk * 2), id_s, c > 0 || part > 0 || kk > 0, one);
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t bk = b + (uint64_t)(kk * 2);
+          if constexpr (KF == QPS_FMT_Q8_0) {
+            mma_ts(d, a + kk * 8, bk, id_s, fresh | (kk > 0), one);
+            mma_ts(d1, a + 32 + kk * 8, bk, id_s, fresh | (kk > 0) | (accs == 1), one);
+          } else {
+            mma_ts(kk & 1 ? d1 : d, a + kk * 8, bk, id_s, fresh | (kk > 1) | (kk == 1 && accs == 1), one);
+          }
+        }
         commit(k_empty(s), one);
         if (c == G::KC - 1) commit(s_full(j & 1), one);
       }
       return true;
     };
-    bool ok = ntiles == 0 || s_product(0);
+    bool ok = ntiles == 0 || (wait(q_full, 0) && s_product(0));
     for (int j = 0; j < ntiles && ok; ++j) {
       if (j + 1 < ntiles && !(ok = s_product(j + 1))) break;
       if (!(ok = wait(p_ready(j & 1), (j >> 1) & 1))) break;
+      constexpr int PAIR = G::VC > 1 ? 2 : 1;  // blocks in turn
 #pragma unroll 1
-      for (int c = 0; c < G::VC && ok; ++c, ++fv) {
-        const int s = fv % kSlots;
-        if (!(ok = wait(v_full(s), (fv / kSlots) & 1))) break;
-        if constexpr (!VDEC) {
-          // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
-          const int left = t1 - (t0 + j * kTile);
-          if (left < kTile) {
-            for (int i = left * 8 + lane; i < kTile * 8; i += 32)
+      for (int c = 0; c < G::VC && ok; c += PAIR, fv += PAIR) {
+        uint64_t a[PAIR];
 #pragma unroll
-              for (int g = 0; g < 2; ++g)
-                *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
-            mma::fence_proxy_async();
-            __syncwarp();
+        for (int u = 0; u < PAIR; ++u) {
+          const int s = (fv + u) % kSlots;
+          if (!(ok = wait(v_full(s), ((fv + u) / kSlots) & 1))) break;
+          if constexpr (!VDEC) {
+            // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
+            const int left = t1 - (t0 + j * kTile);
+            if (left < kTile) {
+              for (int i = left * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                  *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+              mma::fence_proxy_async();
+              __syncwarp();
+            }
           }
+          a[u] = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
         }
+        if (!ok) break;
         fence_after();
-        const uint32_t d = tmem + G::O_COL + c * kN;
-        const uint64_t a = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
         const uint64_t b = smem_desc(sbase + G::P_OFF + (j & 1) * (kTile * kN * 2), 16);
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ss(d, a + (uint64_t)((kk * 2048) >> 4), b + (uint64_t)((kk * 2048) >> 4), id_o, j > 0 || kk > 0, one);
-        commit(v_empty(s), one);
-        if (c == G::VC - 1) commit(p_free(j & 1), one);
+#pragma unroll
+          for (int u = 0; u < PAIR; ++u)
+            mma_ss(tmem + o_col + (c + u) * n16, a[u] + (uint64_t)((kk * 2048) >> 4), b + (uint64_t)((kk * 2048) >> 4), id_o,
+                   j > 0 || kk > 0, one);
+#pragma unroll
+        for (int u = 0; u < PAIR; ++u) commit(v_empty((fv + u) % kSlots), one);
+        if (c + PAIR >= G::VC) commit(p_free(j & 1), one);
       }
     }
     commit(all_done, one);
@@ -283,9 +269,9 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       }
       issued = f + 1;
     }
-  } else if (warp >= 8) {
-    // ---- decode: one position a thread, K by warps 8-11, V by warps 12-15 ------------------------
-    const bool v = warp >= 12;
+  } else if (warp >= 12) {
+    // ---- decode: one position a thread, K by warps 12-15, V by warps 16-19 ------------------------
+    const bool v = warp >= 16;
     const int tok = threadIdx.x & 127;
     const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
     // the position's q8_0 scales (0: no position, or no page), loaded a tile ahead
@@ -324,7 +310,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           const int rs = f % KN, s = f & 1;
           if (!(ok = wait(kraw_full(rs), (f / KN) & 1))) break;
           const uint8_t* raw = smem + G::KRAW + rs * G::KSTAGE;
-          const uint32_t dst = tmem + lanes + G::K_COL + s * 64;
+          const uint32_t dst = tmem + lanes + k_col + s * 64;
           if constexpr (KF == QPS_FMT_Q8_0) {
             uint4 q[4];  // 64 codes, chunk i of the 64-byte row at i ^ (row / 2) % 4
 #pragma unroll
@@ -470,45 +456,86 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       }
     }
   } else if (warp >= 4) {
-    // ---- softmax: one position a thread ----------------------------------------------------------
-    const int tl = (warp & 3) * 32 + lane;
+    // ---- softmax: one position a thread, rows [0, 32) by warps 4-7, [32, 64) by warps 8-11 ---------
+    const int tl = (warp & 3) * 32 + lane, half = (warp - 4) >> 2, tid = threadIdx.x - 128;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    // Q [64][D], K-major, 128-byte swizzle, column groups of 64 dims: every load first, while
+    // the first boxes are under way
+    {
+      constexpr int N = kN * D / 8 / 256;
+      uint4 v[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int i = tid + k * 256, r = i / (D / 8), c = i % (D / 8), rr = row0 + r;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (rr < p.rows_per_cta) {
+          const int e = rr / p.group, h = head * p.group + rr % p.group;
+          const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
+          v[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int i = tid + k * 256, r = i / (D / 8), c = i % (D / 8);
+        *reinterpret_cast<uint4*>(smem + (c >> 3) * (kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
+      }
+      mma::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive(q_full);
+    }
+    if (tid < kN) {
+      const int rr = row0 + tid;
+      int n = 0;
+      if (rr < p.rows_per_cta) {
+        const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
+        n = paged_len(p, b);
+        if (p.causal) n += qi + 1 - p.n_q;
+        n = min(n, t1);
+      }
+      lim[tid] = n;
+      thr[tid] = -INFINITY;
+      mneg[tid] = 0.f;
+    }
+    auto meet = [&]() { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); };
+    meet();
     const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap : 0.f;
-    const int nch = n16 / 16;  // 16-row chunks in use
-    int least = 0x7fffffff;    // positions below it are visible to every row
+    constexpr int CH = kN / 32;                          // 16-row chunks of a thread
+    const int r0 = half * 32, nch = max(0, min(CH, n16 / 16 - half * CH));  // (in use)
+    int least = 0x7fffffff;                              // positions below it are visible to every row
     for (int r = 0; r < nrows; ++r) least = min(least, lim[r]);
     const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
     const void* norms = VF == QPS_FMT_TQ3 ? p.v.aux2 : p.v.aux;
-    float l[kN];
-#pragma unroll
-    for (int r = 0; r < kN; ++r) l[r] = 0.f;
-    // the logits (log2 domain) of 16 rows at this thread's position
-    auto logits = [&](uint32_t addr, int c, int at, bool cut, float (&x)[16]) {
-      uint32_t v[16];
-      __syncwarp();
+    auto ld16 = [&](uint32_t (&v)[16], uint32_t addr) {
       asm volatile(
           "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
           "%15}, [%16];"
           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
             "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-          : "r"(addr + 16 * c)
+          : "r"(addr)
           : "memory");
-      tmem_wait_ld();
-      if (cap > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = mma::softcap_tanh(__uint_as_float(v[i]) * p.scale, cap, cap_k) * LOG2E;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]) * qs;
-      }
-      if (cut) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (at >= lim[16 * c + i]) x[i] = -INFINITY;
-      }
     };
+    // Over the 32 lanes, of 16 rows at once by halving exchange: after the steps 16, 8, 4, 2 a
+    // lane holds one row over 16 lanes, the last step joins the pairs; lane 2i ends with row i.
+    auto over_lanes = [&](float (&y)[16], auto join) -> float {
+#pragma unroll
+      for (int h = 8; h >= 1; h /= 2) {
+        const bool up = (lane & (2 * h)) != 0;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+          const float give = up ? y[i] : y[i + h], keep = up ? y[i + h] : y[i];
+          y[i] = join(keep, __shfl_xor_sync(0xffffffffu, give, 2 * h));
+        }
+      }
+      return join(y[0], __shfl_xor_sync(0xffffffffu, y[0], 1));
+    };
+    float* fred = reinterpret_cast<float*>(red);
+    float l[CH][16];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) l[c][i] = 0.f;
     // (After a wait has given up the loop runs on, every further wait returning at once: the
-    // four warps meet at barriers that none of them may stay away from.)
+    // eight warps meet at barriers that none of them may stay away from.)
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
       const int at = t0 + j * kTile + tl;
@@ -527,113 +554,137 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       const float slack = is_tq(VF) && fabsf(norm) > 255.f ? 8.f : 0.f;
       ok &= wait(s_full(j & 1), (j >> 1) & 1);
       fence_after();
-      const uint32_t s_at = tmem + lanes + G::S_COL + (j & 1) * kN;
+      // the logits, in units of log2, of 16 rows at this thread's position (read again for
+      // each use: kept beside the sums they would not fit the registers)
+      const uint32_t s_at = tmem + lanes + (j & 1) * accs * n16 + r0;
+      auto logits = [&](int c, float (&x)[16]) {
+        uint32_t v[16];
+        __syncwarp();
+        ld16(v, s_at + 16 * c);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
+        if (accs == 2) {
+          ld16(v, s_at + n16 + 16 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(v[i]);
+        }
+        if (cap > 0.f) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = mma::softcap_tanh(x[i] * p.scale, cap, cap_k) * LOG2E;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= qs;
+        }
+        if (cut) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (at >= lim[r0 + 16 * c + i]) x[i] = -INFINITY;
+        }
+      };
       bool over = false;
 #pragma unroll 1
       for (int c = 0; c < nch; ++c) {
         float x[16];
-        logits(s_at, c, at, cut, x);
-        float d[2] = {-INFINITY, -INFINITY};
+        logits(c, x);
+        float d[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 th = *reinterpret_cast<const float2*>(thr + 16 * c + i);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 th = *reinterpret_cast<const float4*>(thr + r0 + 16 * c + i);
           d[0] = fmaxf(d[0], x[i] - th.x);  // (+inf without a reference, NaN for -inf - -inf: no maximum)
           d[1] = fmaxf(d[1], x[i + 1] - th.y);
+          d[2] = fmaxf(d[2], x[i + 2] - th.z);
+          d[3] = fmaxf(d[3], x[i + 3] - th.w);
         }
-        over |= fmaxf(d[0], d[1]) + slack > 0.f;
+        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) + slack > 0.f;
       }
       int any;
       asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 256, p;\n selp.s32 %0, 1, 0, q;\n}\n"
           : "=r"(any)
           : "r"((int)over)
           : "memory");
       if (any) {
-        // raise every reference to its row's maximum so far; O and the sums follow
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-          float x[16];
-          logits(s_at, c, at, cut, x);
-          // halving exchange: after the steps 16, 8, 4, 2 a lane holds the maximum of one row
-          // over 16 lanes, the last step joins the pairs (fmaxf drops a NaN)
+        // raise every reference to its row's maximum so far (fmaxf drops a NaN); O and the
+        // sums follow
 #pragma unroll
-          for (int h = 8; h >= 1; h /= 2) {
-            const bool up = (lane & (2 * h)) != 0;
-#pragma unroll
-            for (int i = 0; i < h; ++i) {
-              const float give = up ? x[i] : x[i + h], keep = up ? x[i + h] : x[i];
-              x[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 2 * h));
-            }
-          }
-          x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], 1));
-          if (!(lane & 1)) red[(warp & 3) * kN + 16 * c + (lane >> 1)] = __float_as_int(x[0]);
+        for (int c = 0; c < CH; ++c) {
+          if (c >= nch) break;
+          float y[16];
+          logits(c, y);
+          const float top = over_lanes(y, [](float a, float b) { return fmaxf(a, b); });
+          if (!(lane & 1)) fred[(warp & 3) * kN + r0 + 16 * c + (lane >> 1)] = top;
         }
-        asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+        meet();
         float cr = 1.f;
-        if (tl < 16 * nch) {
-          float top = __int_as_float(red[tl]);
+        if (tid < n16) {
+          float top = fred[tid];
 #pragma unroll
-          for (int w = 1; w < 4; ++w) top = fmaxf(top, __int_as_float(red[w * kN + tl]));
-          const float old = thr[tl] - 8.f;
+          for (int w = 1; w < 4; ++w) top = fmaxf(top, fred[w * kN + tid]);
+          const float old = thr[tid] - 8.f;
           if (top > old) {
             cr = old == -INFINITY ? 0.f : ex2(old - top);
-            thr[tl] = top + 8.f;
-            mneg[tl] = -top;
+            thr[tid] = top + 8.f;
+            mneg[tid] = -top;
           }
         }
-        asm volatile("barrier.cta.sync 2, 128;" ::: "memory");  // (every red has been read)
-        if (tl < 16 * nch) red[tl] = __float_as_int(cr);
-        asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
-        const float* f = reinterpret_cast<const float*>(red);
-#pragma unroll
-        for (int r = 0; r < kN; ++r)
-          if (r < 16 * nch) l[r] *= f[r];
+        meet();  // (every maximum has been read)
+        if (tid < n16) fred[tid] = cr;
+        meet();
         if (j > 0) {
           ok &= wait(p_free((j - 1) & 1), ((j - 1) >> 1) & 1);  // O is at rest
           fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (c >= nch) break;
+          const float* f = fred + r0 + 16 * c;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) l[c][i] *= f[i];
+          if (j > 0) {
 #pragma unroll 1
-          for (int b = 0; b < G::VC; ++b)
-#pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            for (int b = 0; b < G::VC; ++b) {
               uint32_t v[16];
-              const uint32_t o_at = tmem + lanes + G::O_COL + b * kN + 16 * c;
+              const uint32_t o_at = tmem + lanes + o_col + b * n16 + r0 + 16 * c;
               __syncwarp();
-              asm volatile(
-                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                  "%13, %14, %15}, [%16];"
-                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                    "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                  : "r"(o_at)
-                  : "memory");
+              ld16(v, o_at);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f[16 * c + i]);
+              for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f[i]);
               tmem_st16(o_at, v);
             }
+          }
+        }
+        if (j > 0) {
           tmem_wait_st();
           fence_before();
         }
-        asm volatile("barrier.cta.sync 2, 128;" ::: "memory");  // (every red has been read)
+        meet();  // (every factor has been read)
       }
       if (j >= 2) ok &= wait(p_free(j & 1), ((j - 2) >> 1) & 1);  // the buffer's last reader
       uint8_t* pbuf = smem + G::P_OFF + (j & 1) * (kTile * kN * 2) + tl * 128;
 #pragma unroll
-      for (int c = 0; c < kN / 16; ++c) {
+      for (int c = 0; c < CH; ++c) {
         if (c >= nch) break;
         float x[16];
-        logits(s_at, c, at, cut, x);
+        logits(c, x);
         uint32_t pk[8];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float2 mn = *reinterpret_cast<const float2*>(mneg + 16 * c + i);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 mn = *reinterpret_cast<const float4*>(mneg + r0 + 16 * c + i);
           const float a = ex2(x[i] + mn.x), b = ex2(x[i + 1] + mn.y);
-          l[16 * c + i] += a;
-          l[16 * c + i + 1] += b;
+          const float d = ex2(x[i + 2] + mn.z), e = ex2(x[i + 3] + mn.w);
+          l[c][i] += a;
+          l[c][i + 1] += b;
+          l[c][i + 2] += d;
+          l[c][i + 3] += e;
           pk[i / 2] = mma::pack_h2(a * norm, b * norm);
+          pk[i / 2 + 1] = mma::pack_h2(d * norm, e * norm);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint4*>(pbuf + (((2 * c + h) ^ (tl & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(pbuf + (((r0 / 8 + 2 * c + h) ^ (tl & 7)) << 4)) =
               make_uint4(pk[4 * h], pk[4 * h + 1], pk[4 * h + 2], pk[4 * h + 3]);
       }
       mma::fence_proxy_async();
@@ -645,34 +696,21 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     fence_after();
     // ---- sums over the positions, O to shared memory ---------------------------------------------
     if (ok) {
-      float* sums = reinterpret_cast<float*>(red);
-#pragma unroll
-      for (int r = 0; r < kN; ++r) {
-        float v = l[r];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) sums[(warp & 3) * kN + r] = v;
-      }
       float* fin = reinterpret_cast<float*>(smem + G::RING);  // [row][D] over the slots
-      if (ntiles > 0) {
-#pragma unroll 1
-        for (int b = 0; b < G::VC; ++b) {
-          const int dim = b * 128 + (is_tq(VF) ? (tl & ~15) + tq_unswap(tl & 15) : tl);
-#pragma unroll 1
-          for (int c = 0; c < nch; ++c) {
-            uint32_t v[16];
-            __syncwarp();
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                "%14, %15}, [%16];"
-                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                : "r"(tmem + lanes + G::O_COL + b * kN + 16 * c)
-                : "memory");
-            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) fin[(16 * c + i) * D + dim] = __uint_as_float(v[i]);
-          }
+      for (int c = 0; c < CH; ++c) {
+        if (c >= nch) break;
+        const float sum = over_lanes(l[c], [](float a, float b) { return a + b; });
+        if (!(lane & 1)) fred[(warp & 3) * kN + r0 + 16 * c + (lane >> 1)] = sum;
+#pragma unroll 1
+        for (int b = 0; b < G::VC && ntiles > 0; ++b) {
+          const int dim = b * 128 + (is_tq(VF) ? (tl & ~15) + tq_unswap(tl & 15) : tl);
+          uint32_t v[16];
+          __syncwarp();
+          ld16(v, tmem + lanes + o_col + b * n16 + r0 + 16 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) fin[(r0 + 16 * c + i) * D + dim] = __uint_as_float(v[i]);
         }
       }
     }
@@ -759,14 +797,14 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 1) tmem_free(tmem, G::COLS);
+  if (warp == 1) tmem_free(tmem, 512);
 }
 
 template <int D, int KF, int VF>
 qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
   using G = GeoTt<D, KF, VF>;
   static_assert(G::SMEM <= 227 * 1024, "the slots exceed the shared memory of one CTA");
-  static_assert(G::O_COL + G::VC * kN <= G::COLS, "S and O exceed TMEM");
+  static_assert((2 + G::VC) * kN + 128 <= 512, "S, K and O exceed TMEM");
   static_assert(kN * D * 4 <= kSlots * kSlot + 2 * G::RAW_BYTES, "the output rows fit the slots and raw stages");
   TmaSet maps;
   std::memset(&maps, 0, sizeof(maps));
