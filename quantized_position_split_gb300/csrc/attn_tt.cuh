@@ -12,7 +12,7 @@
 // S^T (two buffers), O^T (D / 128 blocks) and two slots of K live in TMEM.  Products that
 // add to one accumulator follow each other at 75 to 100 cycles, whatever N: so S^T has two
 // accumulators a buffer where TMEM has the columns (hi and lo parts, or odd and even steps),
-// and O^T takes two blocks in turn.
+// and S^T's and O^T's products alternate.
 //
 // The stored rows arrive by tensor-map boxes in small raw stages; four warps decode K, one
 // position a thread, from there into TMEM (64 dims a slot), four more V into 32 KB slots of
@@ -165,71 +165,77 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   };
 
   if (warp == 0) {
-    // ---- products: S(0), then S(j + 1) and O(j) for every tile -----------------------------------
+    // ---- products: S(0), S(1), then S(j + 1) beside O(j - 1), while the softmax of tile j runs:
+    // four slots of K, then two of V whose products alternate.  (S(j + 1), then O(j), each
+    // waiting for its decoders in turn, took 11300 cycles a tile at head_dim 512; K's and V's
+    // products alternating, 130 cycles each instead of 75.) ----
     const uint32_t id_s = instr_desc(n16, 0), id_o = instr_desc(n16, 1) | (1u << 15), one = elect_lane();
+    constexpr int PAIR = G::VC > 1 ? 2 : 1;
     int fk = 0, fv = 0;  // slots used
-    auto s_product = [&](int j) -> bool {
+    bool ok = ntiles == 0 || wait(q_full, 0);
+    for (int j = -1; j <= ntiles && ntiles > 0 && ok; ++j) {
+      const bool qk = j + 1 < ntiles, pv = j >= 1;
+      const uint32_t ds = tmem + ((j + 1) & 1) * accs * n16, ds1 = ds + (accs - 1) * n16;
+      const uint64_t bp = smem_desc(sbase + G::P_OFF + ((j - 1) & 1) * (kTile * kN * 2), 16);
 #pragma unroll 1
-      for (int c = 0; c < G::KC; ++c, ++fk) {
-        const int s = fk & 1;
-        if (!wait(k_full(s), (fk >> 1) & 1)) return false;
-        fence_after();
-        const uint32_t d = tmem + (j & 1) * accs * n16, d1 = d + (accs - 1) * n16, a = tmem + k_col + s * 64;
-        const uint64_t b = smem_desc(sbase + c * (kN * 128), 16);
-        const uint32_t fresh = c > 0;  // (0: a tile's first products start their accumulators)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t bk = b + (uint64_t)(kk * 2);
-          if constexpr (KF == QPS_FMT_Q8_0) {
-            mma_ts(d, a + kk * 8, bk, id_s, fresh | (kk > 0), one);
-            mma_ts(d1, a + 32 + kk * 8, bk, id_s, fresh | (kk > 0) | (accs == 1), one);
-          } else {
-            mma_ts(kk & 1 ? d1 : d, a + kk * 8, bk, id_s, fresh | (kk > 1) | (kk == 1 && accs == 1), one);
-          }
-        }
-        commit(k_empty(s), one);
-        if (c == G::KC - 1) commit(s_full(j & 1), one);
-      }
-      return true;
-    };
-    bool ok = ntiles == 0 || (wait(q_full, 0) && s_product(0));
-    for (int j = 0; j < ntiles && ok; ++j) {
-      if (j + 1 < ntiles && !(ok = s_product(j + 1))) break;
-      if (!(ok = wait(p_ready(j & 1), (j >> 1) & 1))) break;
-      constexpr int PAIR = G::VC > 1 ? 2 : 1;  // blocks in turn
+      for (int v0 = 0; v0 < G::VC && ok; v0 += PAIR) {
+        if (qk) {
 #pragma unroll 1
-      for (int c = 0; c < G::VC && ok; c += PAIR, fv += PAIR) {
-        uint64_t a[PAIR];
+          for (int c = 2 * v0; c < 2 * (v0 + PAIR); ++c, ++fk) {
+            const int s = fk & 1;
+            if (!(ok = wait(k_full(s), (fk >> 1) & 1))) break;
+            fence_after();
+            const uint32_t a = tmem + k_col + s * 64;
+            const uint64_t bq = smem_desc(sbase + c * (kN * 128), 16);
+            const uint32_t fresh = c > 0;  // (0: a tile's first products start their accumulators)
 #pragma unroll
-        for (int u = 0; u < PAIR; ++u) {
-          const int s = (fv + u) % kSlots;
-          if (!(ok = wait(v_full(s), ((fv + u) / kSlots) & 1))) break;
-          if constexpr (!VDEC) {
-            // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
-            const int left = t1 - (t0 + j * kTile);
-            if (left < kTile) {
-              for (int i = left * 8 + lane; i < kTile * 8; i += 32)
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                  *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
-              mma::fence_proxy_async();
-              __syncwarp();
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t b = bq + (uint64_t)(kk * 2);
+              if constexpr (KF == QPS_FMT_Q8_0) {
+                mma_ts(ds, a + kk * 8, b, id_s, fresh | (kk > 0), one);
+                mma_ts(ds1, a + 32 + kk * 8, b, id_s, fresh | (kk > 0) | (accs == 1), one);
+              } else {
+                mma_ts(kk & 1 ? ds1 : ds, a + kk * 8, b, id_s, fresh | (kk > 1) | (kk == 1 && accs == 1), one);
+              }
             }
+            commit(k_empty(s), one);
+            if (c == G::KC - 1) commit(s_full((j + 1) & 1), one);
           }
-          a[u] = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
         }
-        if (!ok) break;
-        fence_after();
-        const uint64_t b = smem_desc(sbase + G::P_OFF + (j & 1) * (kTile * kN * 2), 16);
+        if (pv && ok) {
+          if (v0 == 0 && !(ok = wait(p_ready((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
+          uint64_t a[PAIR];
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
+          for (int u = 0; u < PAIR; ++u) {
+            const int s = (fv + u) % kSlots;
+            if (!(ok = wait(v_full(s), ((fv + u) / kSlots) & 1))) break;
+            if constexpr (!VDEC) {
+              // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
+              const int left = t1 - (t0 + (j - 1) * kTile);
+              if (left < kTile) {
+                for (int i = left * 8 + lane; i < kTile * 8; i += 32)
 #pragma unroll
-          for (int u = 0; u < PAIR; ++u)
-            mma_ss(tmem + o_col + (c + u) * n16, a[u] + (uint64_t)((kk * 2048) >> 4), b + (uint64_t)((kk * 2048) >> 4), id_o,
-                   j > 0 || kk > 0, one);
+                  for (int g = 0; g < 2; ++g)
+                    *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+                mma::fence_proxy_async();
+                __syncwarp();
+              }
+            }
+            a[u] = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
+          }
+          if (!ok) break;
+          fence_after();
 #pragma unroll
-        for (int u = 0; u < PAIR; ++u) commit(v_empty((fv + u) % kSlots), one);
-        if (c + PAIR >= G::VC) commit(p_free(j & 1), one);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+#pragma unroll
+            for (int u = 0; u < PAIR; ++u) {
+              const uint64_t o = (uint64_t)((kk * 2048) >> 4);
+              mma_ss(tmem + o_col + (v0 + u) * n16, a[u] + o, bp + o, id_o, j > 1 || kk > 0, one);
+            }
+#pragma unroll
+          for (int u = 0; u < PAIR; ++u, ++fv) commit(v_empty(fv % kSlots), one);
+          if (v0 + PAIR >= G::VC) commit(p_free((j - 1) & 1), one);
+        }
       }
     }
     commit(all_done, one);
