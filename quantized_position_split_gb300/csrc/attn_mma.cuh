@@ -1089,7 +1089,11 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       for (int off = 4; off < 32; off <<= 1) nmx = fmaxf(nmx, __shfl_xor_sync(0xffffffffu, nmx, off));
       lazy = nmx <= 255.f ? 8.f : 0.f;
     }
-    uint32_t pb[SUB][NTW][2];
+    // (paged, q8_0 V) what P's rounding to fp16 leaves, as a second operand: V's own values
+    // are rounded already (code x scale), and a second rounding of the same size would make
+    // the output's error 1.7 times the one its type has
+    constexpr bool PLO = PAGED && VF == QPS_FMT_Q8_0;
+    uint32_t pb[SUB][NTW][2], pl[PLO ? SUB : 1][PLO ? NTW : 1][2];
 #pragma unroll
     for (int nt = 0; nt < NTW; ++nt) {
       float x[SUB][4];
@@ -1149,8 +1153,15 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         const float p2 = exp2f(x[sb][2] - ms0), p3 = exp2f(x[sb][3] - ms1);
         sum0 += p0 + p2;
         sum1 += p1 + p3;
-        pb[sb][nt][0] = movmatrix_t(pack_h2(p0 * n_g[sb], p1 * n_g[sb]));
-        pb[sb][nt][1] = movmatrix_t(pack_h2(p2 * n_g8[sb], p3 * n_g8[sb]));
+        const uint32_t h0 = pack_h2(p0 * n_g[sb], p1 * n_g[sb]), h1 = pack_h2(p2 * n_g8[sb], p3 * n_g8[sb]);
+        pb[sb][nt][0] = movmatrix_t(h0);
+        pb[sb][nt][1] = movmatrix_t(h1);
+        if constexpr (PLO) {
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+          pl[sb][nt][0] = movmatrix_t(pack_h2(p0 - f0.x, p1 - f0.y));
+          pl[sb][nt][1] = movmatrix_t(pack_h2(p2 - f1.x, p3 - f1.y));
+        }
       }
       l[nt][0] = l[nt][0] * cr0 + sum0;
       l[nt][1] = l[nt][1] * cr1 + sum1;
@@ -1227,7 +1238,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
               a[2] = __byte_perm(hv[2][hh], hv[3][hh], 0x5410);
               a[3] = __byte_perm(hv[2][hh], hv[3][hh], 0x7632);
 #pragma unroll
-              for (int nt = 0; nt < NTW; ++nt) mma16816(o[i][nt], a, pb[sb][nt][0], pb[sb][nt][1]);
+              for (int nt = 0; nt < NTW; ++nt) {
+                mma16816(o[i][nt], a, pb[sb][nt][0], pb[sb][nt][1]);
+                if constexpr (PLO) mma16816(o[i][nt], a, pl[sb][nt][0], pl[sb][nt][1]);
+              }
             }
           }
         }

@@ -43,20 +43,26 @@ using namespace tm;
 constexpr int kN = 64;             // query rows per CTA
 constexpr int kTile = 128;         // positions per tile
 constexpr int kThreadsTt = 640;
-constexpr int kSlot = 32 * 1024, kSlots = 3;  // V's fp16 slots
+constexpr int kSlot = 32 * 1024;  // a slot of V's fp16 operands
+constexpr int kPBytes = kTile * kN * 2;  // a buffer of P
 
 template <int D, int KF, int VF>
 struct GeoTt {
   static constexpr int KC = D / 64, VC = D / 128;   // slots of a tile: K's and V's
   static constexpr int Q_BYTES = kN * D * 2;
-  static constexpr int P_OFF = Q_BYTES;             // two buffers [128][64] fp16
-  static constexpr int RING = P_OFF + 2 * kTile * kN * 2;
+  // P: two buffers [128][64] fp16, for a q8_0 V with what the rounding left beside them (V's
+  // values are rounded already, and a second rounding of the same size would make the
+  // output's error 1.7 times the one its type has)
+  static constexpr int PLO = VF == QPS_FMT_Q8_0 ? 1 : 0;
+  static constexpr int P_OFF = Q_BYTES, P_STEP = (1 + PLO) * kPBytes;
+  static constexpr int RING = P_OFF + 2 * P_STEP;
+  static constexpr int SLOTS = PLO ? 2 : 3;         // of V
   // raw stages: [128 positions] of 64 dims of K (codes, or fp16), of 128 of V (codes, or the
   // 2-bit plane and behind it the signs)
   static constexpr int RAW_BYTES = (D == 128 ? 32 : 16) * 1024;  // of each side
   static constexpr int KSTAGE = (KF == QPS_FMT_F16 ? 16 : 8) * 1024, KN = RAW_BYTES / KSTAGE;
   static constexpr int VSTAGE = (VF == QPS_FMT_Q8_0 ? 16 : 8) * 1024, VN = RAW_BYTES / VSTAGE;
-  static constexpr int KRAW = RING + kSlots * kSlot, VRAW = KRAW + RAW_BYTES;
+  static constexpr int KRAW = RING + SLOTS * kSlot, VRAW = KRAW + RAW_BYTES;
   static constexpr int MISC = VRAW + RAW_BYTES;
   static constexpr int MISC_BYTES = D == 128 ? 2304 : 2048;
   static constexpr int SMEM = MISC + MISC_BYTES + 1024;  // + slack for the 1024-byte base alignment
@@ -113,7 +119,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(misc + 1792);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1796);
   const uint32_t bars = sbase + G::MISC + 1800;
-  constexpr int KN = G::KN, VN = G::VN;
+  constexpr int KN = G::KN, VN = G::VN, kSlots = G::SLOTS;
   auto bar_at = [&](int i) { return bars + 8 * i; };
   auto s_full = [&](int w) { return bar_at(w); };
   auto p_free = [&](int w) { return bar_at(2 + w); };
@@ -175,8 +181,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     bool ok = ntiles == 0 || wait(q_full, 0);
     for (int j = -1; j <= ntiles && ntiles > 0 && ok; ++j) {
       const bool qk = j + 1 < ntiles, pv = j >= 1;
+      // (P of tile j - 1 is there: its S, whose buffer S(j + 1) takes, has been read)
+      if (pv && !(ok = wait(p_ready((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
       const uint32_t ds = tmem + ((j + 1) & 1) * accs * n16, ds1 = ds + (accs - 1) * n16;
-      const uint64_t bp = smem_desc(sbase + G::P_OFF + ((j - 1) & 1) * (kTile * kN * 2), 16);
+      const uint64_t bp = smem_desc(sbase + G::P_OFF + ((j - 1) & 1) * G::P_STEP, 16);
 #pragma unroll 1
       for (int v0 = 0; v0 < G::VC && ok; v0 += PAIR) {
         if (qk) {
@@ -203,7 +211,6 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           }
         }
         if (pv && ok) {
-          if (v0 == 0 && !(ok = wait(p_ready((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
           uint64_t a[PAIR];
 #pragma unroll
           for (int u = 0; u < PAIR; ++u) {
@@ -226,12 +233,15 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           if (!ok) break;
           fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
+          for (int part = 0; part <= G::PLO; ++part)
 #pragma unroll
-            for (int u = 0; u < PAIR; ++u) {
-              const uint64_t o = (uint64_t)((kk * 2048) >> 4);
-              mma_ss(tmem + o_col + (v0 + u) * n16, a[u] + o, bp + o, id_o, j > 1 || kk > 0, one);
-            }
+            for (int kk = 0; kk < kTile / 16; ++kk)
+#pragma unroll
+              for (int u = 0; u < PAIR; ++u) {
+                const uint64_t o = (uint64_t)((kk * 2048) >> 4);
+                mma_ss(tmem + o_col + (v0 + u) * n16, a[u] + o, bp + o + (uint64_t)((part * kPBytes) >> 4), id_o,
+                       j > 1 || kk > 0 || part > 0, one);
+              }
 #pragma unroll
           for (int u = 0; u < PAIR; ++u, ++fv) commit(v_empty(fv % kSlots), one);
           if (v0 + PAIR >= G::VC) commit(p_free((j - 1) & 1), one);
@@ -669,13 +679,13 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         meet();  // (every factor has been read)
       }
       if (j >= 2) ok &= wait(p_free(j & 1), ((j - 2) >> 1) & 1);  // the buffer's last reader
-      uint8_t* pbuf = smem + G::P_OFF + (j & 1) * (kTile * kN * 2) + tl * 128;
+      uint8_t* pbuf = smem + G::P_OFF + (j & 1) * G::P_STEP + tl * 128;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (c >= nch) break;
         float x[16];
         logits(c, x);
-        uint32_t pk[8];
+        uint32_t pk[8], pl[G::PLO ? 8 : 1];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 mn = *reinterpret_cast<const float4*>(mneg + r0 + 16 * c + i);
@@ -687,11 +697,23 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           l[c][i + 3] += e;
           pk[i / 2] = mma::pack_h2(a * norm, b * norm);
           pk[i / 2 + 1] = mma::pack_h2(d * norm, e * norm);
+          if constexpr (G::PLO) {
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&pk[i / 2]));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&pk[i / 2 + 1]));
+            pl[i / 2] = mma::pack_h2(a - f0.x, b - f0.y);
+            pl[i / 2 + 1] = mma::pack_h2(d - f1.x, e - f1.y);
+          }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           *reinterpret_cast<uint4*>(pbuf + (((r0 / 8 + 2 * c + h) ^ (tl & 7)) << 4)) =
               make_uint4(pk[4 * h], pk[4 * h + 1], pk[4 * h + 2], pk[4 * h + 3]);
+        if constexpr (G::PLO) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4*>(pbuf + kPBytes + (((r0 / 8 + 2 * c + h) ^ (tl & 7)) << 4)) =
+                make_uint4(pl[4 * h], pl[4 * h + 1], pl[4 * h + 2], pl[4 * h + 3]);
+        }
       }
       mma::fence_proxy_async();
       fence_before();
@@ -702,7 +724,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     fence_after();
     // ---- sums over the positions, O to shared memory ---------------------------------------------
     if (ok) {
-      float* fin = reinterpret_cast<float*>(smem + G::RING);  // [row][D] over the slots
+      float* fin = reinterpret_cast<float*>(smem + G::P_OFF);  // [row][D] over P, the slots and the stages
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (c >= nch) break;
@@ -730,7 +752,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     // in register e (with the row's elements spread over the CTA, the butterflies' addresses
     // and barriers took as many instructions as seven tiles) ----
     constexpr int E = D / 32;
-    const float* fin = reinterpret_cast<const float*>(smem + G::RING);
+    const float* fin = reinterpret_cast<const float*>(smem + G::P_OFF);
     const float* sums = reinterpret_cast<const float*>(red);
     for (int r = warp; r < nrows; r += kThreadsTt / 32) {
       const int rr = row0 + r;
@@ -811,7 +833,7 @@ qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
   using G = GeoTt<D, KF, VF>;
   static_assert(G::SMEM <= 227 * 1024, "the slots exceed the shared memory of one CTA");
   static_assert((2 + G::VC) * kN + 128 <= 512, "S, K and O exceed TMEM");
-  static_assert(kN * D * 4 <= kSlots * kSlot + 2 * G::RAW_BYTES, "the output rows fit the slots and raw stages");
+  static_assert(kN * D * 4 <= G::MISC - G::P_OFF, "the output rows fit P, the slots and the raw stages");
   TmaSet maps;
   std::memset(&maps, 0, sizeof(maps));
   const int page = 1 << p.page_shift, rows = page < kTile ? page : kTile;

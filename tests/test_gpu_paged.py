@@ -350,6 +350,46 @@ def test_attention_shared_prefix(qps, d, kf, vf, page, batch, group, n_q):
         assert_parity(o, lse, ro, rl, (d, kf, vf, batch, group, n_q, shared))
 
 
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(512, "q8_0", "tq3", 5, 8), (512, "q8_0", "tq2", 4, 16), (512, "f16", "f16", 5, 4),
+                                               (256, "q8_0", "q8_0", 5, 3), (256, "f16", "tq3", 2, 8), (128, "q8_0", "tq3", 9, 4),
+                                               (128, "q8_0", "q8_0", 13, 5), (128, "f16", "q8_0", 7, 4), (128, "f16", "f16", 9, 4),
+                                               (64, "f16", "f16", 13, 5)])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_attention_many_rows_many_tiles(qps, d, kf, vf, n_q, group, softcap):
+    """Chunks of a dozen tiles and more for the kernels that take many query rows: every
+    buffer and barrier of their pipelines goes round several times, and maxima that rise
+    late (keys that grow along the sequence) rescale what has been summed."""
+    hkv, page, batch = 8, 64, 3
+    rot, ora = _rotations(d, "whole")
+    lens = [7001, 5990, 6400]
+    cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, d + n_q, rot)
+    if kf == "f16":  # later positions have larger keys
+        for b, n in enumerate(lens):
+            for j in range(-(-n // page)):
+                cache.k_planes[0][int(table[b, j])] *= 0.5 + 1.5 * j * page / n
+    q = torch.randn((batch, n_q, hkv * group, d), generator=torch.Generator().manual_seed(d)).half().cuda()
+    ro, rl = _want(cache, q, table, lens, d ** -0.5, softcap, True, ora)
+    for _ in range(3):  # (a race does not show every time)
+        o, lse = _run(qps, q, cache, table, lens, scale=d ** -0.5, softcap=softcap, causal=True, out_dtype=torch.float32)
+        assert_parity(o, lse, ro, rl, (d, kf, vf, n_q, group))
+
+
+@pytest.mark.parametrize("d,kf,vf", [(128, "f16", "f16"), (64, "f16", "f16"), (128, "q8_0", "tq3"), (512, "q8_0", "tq3")])
+def test_attention_long_prefix(qps, d, kf, vf):
+    """A shared prefix of many tiles per CTA, more rows than one CTA holds."""
+    hkv, page, batch, group, common = 8, 64, 40, 5, 8192
+    rot, ora = _rotations(d, "whole")
+    lens = [common + 1 + 3 * b for b in range(batch)]
+    cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, d, rot, common)
+    q = torch.randn((batch, hkv * group, d), generator=torch.Generator().manual_seed(d)).half().cuda()
+    pick = [0, 1, 17, 39]
+    ro, rl = _want(cache, q[pick], table[pick], [lens[b] for b in pick], d ** -0.5, 0.0, False, ora)
+    for _ in range(3):
+        o, lse = _run(qps, q, cache, table, lens, scale=d ** -0.5, shared_len=common, out_dtype=torch.float32)
+        o, lse = o.reshape(batch, -1, d)[pick].reshape(-1, d), lse.reshape(batch, -1)[pick].reshape(-1)
+        assert_parity(o, lse, ro, rl, (d, kf, vf))
+
+
 def test_attention_long_and_output_types(qps):
     """One long sequence beside short ones; the fp16 and bf16 outputs are the float32 one,
     rounded once; a table with a row stride and query rows with a batch stride."""
