@@ -64,6 +64,8 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, int cols) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// One value for the warp's lanes, which the compiler can keep in a uniform register.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // The products and commits below are issued by one lane, chosen by a predicate on the
 // instruction instead of a branch: the warp stays converged, so descriptors are computed in
 // uniform registers (under a branch each product took 100 cycles to issue, more than it
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this CTA's rows and positions ------------------------------------------------------
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     t1 = ch.t1;
     whole = ch.whole;
   }
-  const int ntiles = t1 > t0 ? (t1 - t0 + kTok - 1) / kTok : 0;  // 0: no own positions
+  const int ntiles = uniform(t1 > t0 ? (t1 - t0 + kTok - 1) / kTok : 0);  // 0: no own positions
 
   // ---- barriers, TMEM, queries ---------------------------------------------------------------
   const uint32_t bars = sbase + G::BAR;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_word;
+  const uint32_t tmem = uniform(*tmem_word);
 
   // Bounded wait of a whole warp, with one answer for all of its lanes; gives up at once
   // when another role has.

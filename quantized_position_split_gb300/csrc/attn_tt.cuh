@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   const uint32_t sbase = smem_addr(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this CTA's rows and positions ------------------------------------------------------
@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     t1 = ch.t1;
     whole = ch.whole;
   }
-  const int ntiles = t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0;  // 0: no own positions
+  const int ntiles = uniform(t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0);  // 0: no own positions
   const int nrows = min(kN, p.rows_per_cta - row0);
-  const int n16 = (nrows + 15) & ~15;  // N of the products
+  const int n16 = uniform((nrows + 15) & ~15);  // N of the products
   // TMEM columns: S (two buffers of one or two accumulators), K (two slots of 32 hi and 32
   // lo), O
   const int accs = (4 + G::VC) * n16 + 128 <= 512 ? 2 : 1;
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *tmem_word;
+  const uint32_t tmem = uniform(*tmem_word);
 
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {  // (as in attn_tm.cuh)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
