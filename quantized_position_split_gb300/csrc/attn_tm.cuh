@@ -251,33 +251,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   int issued_k = 0, issued_v = 0;  // (warp 0) tiles under way or landed
 
   if (warp == 0) {
-    // ---- tiles: each box is min(page, 128) positions of one page and 64 columns ----------------
+    // ---- tiles: each box is min(page, 128) positions of one page and 64 columns, at most 16 of
+    // them a tile, one a lane.  A lane reads its page a tile ahead (read when the box is due, the
+    // table's latency kept the copies 1800 cycles a tile apart, twice the products' time). ------
     const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
     const int32_t* row = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
-    auto load = [&](const TensorMap* map, uint32_t dst, uint32_t bar, int t) {
+    const int cg = lane % G::CG, r = lane / G::CG;
+    auto has = [&](int j) { return r < nb && t0 + j * kTok + r * br < t1; };
+    auto entry = [&](int j) { return has(j) ? row[(t0 + j * kTok + r * br) >> p.page_shift] : 0; };
+    auto load = [&](const TensorMap* map, uint32_t dst, uint32_t bar, int j, int page) {
       if (lane == 0) mbar_expect_tx(bar, G::TILE);
       __syncwarp();
-      for (int i = lane; i < G::CG * nb; i += 32) {
-        const int cg = i % G::CG, r = i / G::CG, at = t + r * br;
-        int page = (int)p.n_pages;  // behind the last position, or out of range: zeros
-        if (at < t1) {
-          const int pg = row[at >> p.page_shift];
-          if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) page = pg;
-          else atomicOr(p.err, kErrIndex);
-        }
-        tma_load_4d(dst + cg * (kTok * 128) + r * br * 128, map, cg * 128, at & ((1 << p.page_shift) - 1), head, page, bar);
-      }
+      if (r < nb)
+        tma_load_4d(dst + cg * (kTok * 128) + r * br * 128, map, cg * 128,
+                    (t0 + j * kTok + r * br) & ((1 << p.page_shift) - 1), head, page, bar);
     };
+    int next = entry(0);
     for (int j = 0; j < ntiles; ++j) {
       const int s = j % ST;
       const uint32_t par = ((j / ST) & 1) ^ 1;
+      int page = (int)p.n_pages;  // behind the last position, or out of range: zeros
+      if (has(j)) {
+        if ((uint64_t)(int64_t)next < (uint64_t)p.n_pages) page = next;
+        else atomicOr(p.err, kErrIndex);
+      }
+      next = entry(j + 1);
       if (j >= ST && !wait(k_empty(s), par)) break;
       __syncwarp();
-      load(&maps.k, sbase + G::K_OFF + s * G::TILE, k_full(s), t0 + j * kTok);
+      load(&maps.k, sbase + G::K_OFF + s * G::TILE, k_full(s), j, page);
       issued_k = j + 1;
       if (j >= ST && !wait(v_empty(s), par)) break;
       __syncwarp();
-      load(&maps.v, sbase + G::V_OFF + s * G::TILE, v_full(s), t0 + j * kTok);
+      load(&maps.v, sbase + G::V_OFF + s * G::TILE, v_full(s), j, page);
       issued_v = j + 1;
     }
   } else if (warp == 1) {

@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     commit(all_done, one);
     wait(all_done, 0);
   } else if (warp == 2 || warp == 3) {
-    // ---- boxes of min(page, 128) positions, K's (warp 2) and V's (warp 3) -------------------------
+    // ---- boxes of min(page, 128) positions, K's (warp 2) and V's (warp 3), each lane's page read
+    // a tile ahead -------------------------------------------------------------------------------
     const bool v = warp == 3;
     const int br = min(1 << p.page_shift, kTile), nb = kTile / br;
     const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
@@ -259,9 +260,21 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     const int rb = v ? (VF == QPS_FMT_F16 || VF == QPS_FMT_Q8_0 ? 128 : 32) : (KF == QPS_FMT_F16 ? 128 : 64);
     const int groups = v && !VDEC ? 2 : 1;
     const bool signs = v && VF == QPS_FMT_TQ3;
-    const int ring = !v ? KN : VDEC ? VN : kSlots, count = ntiles * (v ? G::VC : G::KC);
+    const int ring = !v ? KN : VDEC ? VN : kSlots, nc = v ? G::VC : G::KC, count = ntiles * nc;
+    const int grp = lane / nb, r = lane % nb;  // (16 boxes at most, one a lane)
+    auto has = [&](int j) { return grp < groups && t0 + j * kTile + r * br < t1; };
+    auto entry = [&](int j) { return has(j) ? table[(t0 + j * kTile + r * br) >> p.page_shift] : 0; };
+    int next = entry(0), page = 0;
     for (int f = 0; f < count; ++f) {
-      const int s = f % ring, round = f / ring, j = f / (v ? G::VC : G::KC), c = f % (v ? G::VC : G::KC);
+      const int s = f % ring, round = f / ring, j = f / nc, c = f % nc;
+      if (c == 0) {
+        page = (int)p.n_pages;  // behind the last position, or out of range: zeros
+        if (has(j)) {
+          if ((uint64_t)(int64_t)next < (uint64_t)p.n_pages) page = next;
+          else atomicOr(p.err, kErrIndex);
+        }
+        next = entry(j + 1);
+      }
       if (round > 0 && !wait(!v ? kraw_empty(s) : VDEC ? vraw_empty(s) : v_empty(s), (round & 1) ^ 1)) break;
       const uint32_t bar = !v ? kraw_full(s) : VDEC ? vraw_full(s) : v_full(s);
       const uint32_t dst = sbase + (!v ? G::KRAW + s * G::KSTAGE : VDEC ? G::VRAW + s * G::VSTAGE : G::RING + s * kSlot);
@@ -271,15 +284,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           for (int i = 1; i < 4; ++i) arrive(bar);  // (a slot's barrier counts four)
       }
       __syncwarp();
-      for (int i = lane; i < nb * groups; i += 32) {
-        const int grp = i / nb, r = i % nb, at = t0 + j * kTile + r * br;
-        int page = (int)p.n_pages;  // behind the last position, or out of range: zeros
-        if (at < t1) {
-          const int pg = table[at >> p.page_shift];
-          if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) page = pg;
-          else atomicOr(p.err, kErrIndex);
-        }
-        const int y = at & ((1 << p.page_shift) - 1);
+      if (grp < groups) {
+        const int y = (t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
         tma_load_4d(dst + grp * (kSlot / 2) + r * br * rb, v ? &maps.v : &maps.k, (c * groups + grp) * rb, y, head, page, bar);
         if (signs) tma_load_4d(dst + kTile * 32 + r * br * 16, &maps.va, c * 16, y, head, page, bar);
       }
@@ -332,6 +338,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               q[i] = *reinterpret_cast<const uint4*>(raw + tok * 64 + ((i ^ ((tok >> 1) & 3)) << 4));
+            mma::fence_proxy_async();  // (the reads are done before the next box is written)
             __syncwarp();
             if (lane == 0) arrive(kraw_empty(rs));
             if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
@@ -369,6 +376,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
               x[4 * i + 2] = q.z;
               x[4 * i + 3] = q.w;
             }
+            mma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(kraw_empty(rs));
             if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
@@ -415,6 +423,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
             uint4 q[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) q[i] = *reinterpret_cast<const uint4*>(raw + tok * 128 + ((i ^ (tok & 7)) << 4));
+            mma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(vraw_empty(rs));
             if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1))) break;
@@ -439,6 +448,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) q[i] = *reinterpret_cast<const uint4*>(raw + tok * 32 + ((i ^ ((tok >> 2) & 1)) << 4));
             if constexpr (VF == QPS_FMT_TQ3) sg = *reinterpret_cast<const uint4*>(raw + kTile * 32 + tok * 16);
+            mma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(vraw_empty(rs));
             if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1))) break;
