@@ -1753,6 +1753,14 @@ qps_status launch_mma_t(const P& p, cudaStream_t s) {
   return QPS_OK;
 }
 
+// The most n-tiles an instance is called with (mma_tile_rows; a paged cache in fp16 sends
+// more rows than this to attn_tm.cuh).
+template <int D, int KF, int VF, class P>
+constexpr int most_ntw() {
+  if (std::is_same<P, PagedAttnParams>::value && KF == QPS_FMT_F16 && VF == QPS_FMT_F16 && D <= 128) return D == 64 ? 2 : 1;
+  return D <= 128 ? 3 : 1;
+}
+
 // Every format pairing and n-tile count of one head_dim, with or without the causal
 // limit; SET selects the pairings: 0 K F16 / Q8_0 with V F16 / Q8_0 / TQ3, 1 the same K
 // with V TQ2 / TQ4, 2 a TurboQuant K with V of the same tier.  The sets live in
@@ -1763,8 +1771,9 @@ qps_status launch_mma_d(const P& p, cudaStream_t s) {
   const int ntw = mma_tile_rows(D, p.rows_per_cta, p.shared != 0) / 8;
 #define QPS_MMA_CASE(KF, VF)                                                       \
   if (p.kfmt == KF && p.vfmt == VF) {                                              \
-    if (ntw == 3) return launch_mma_t<D, KF, VF, (D <= 128 ? 3 : 1), CAUSAL>(p, s); \
-    if (ntw == 2) return launch_mma_t<D, KF, VF, (D <= 128 ? 2 : 1), CAUSAL>(p, s); \
+    constexpr int MOST = most_ntw<D, KF, VF, P>();                                 \
+    if (MOST >= 3 && ntw == 3) return launch_mma_t<D, KF, VF, (MOST >= 3 ? 3 : 1), CAUSAL>(p, s); \
+    if (MOST >= 2 && ntw == 2) return launch_mma_t<D, KF, VF, (MOST >= 2 ? 2 : 1), CAUSAL>(p, s); \
     return launch_mma_t<D, KF, VF, 1, CAUSAL>(p, s);                                \
   }
   if constexpr (SET == 2) {

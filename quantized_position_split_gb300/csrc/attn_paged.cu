@@ -157,14 +157,23 @@ constexpr int kWaves = 2;
 constexpr int kMinPositions = 128, kMinMany = 512;
 
 // The kernel for `rows` query rows per KV head, and the rows, positions and CTAs per SM
-// that it works with.
+// that it works with.  The tcgen05 kernels cost the same for few rows as for many; the
+// mma.sync kernel reads a chunk once for each 8, 16 or 24 rows.  16 sequences of 8192
+// positions, us, tcgen05 against mma.sync:
+//   f16 / f16, 8 heads of 128:    12 rows 101 / 114, 24 rows 108 / 131, 40 rows 117 / 200
+//   f16 / f16, 8 heads of 64:     16 rows 69 / 65, 20 rows 71 / 79, 40 rows 76 / 122
+//   q8_0 / tq3, 8 heads of 128:   24 rows 160 / 145, 32 rows 163 / 219
+//   q8_0 / q8_0, 8 heads of 128:  24 rows 149 / 145, 32 rows 153 / 218
+//   q8_0 / tq3, 4 heads of 256:   8 rows 111 / 74, 9 rows 111 / 178
+//   f16 / f16, 4 heads of 256:    8 rows 165 / 93, 9 rows 165 / 170
+//   q8_0 / tq3, 2 heads of 512:   8 rows 87 / 63, 9 rows 87 / 120
 struct Shape {
   PagedKernel kernel;
   int rows, tile, ctas_per_sm;
 };
 Shape shape_for(const PagedKv& kv, int rows, bool shared) {
   if (kv.kfmt == QPS_FMT_F16 && kv.vfmt == QPS_FMT_F16 && kv.d <= 128) {
-    if (rows > 32) return {kTm, 128, 128, 1};
+    if (rows > (kv.d == 64 ? 16 : 8)) return {kTm, 128, 128, 1};
   } else if (kv.d >= 128 && !is_tq(kv.kfmt) && kv.vfmt != QPS_FMT_TQ4) {
     if (rows > (kv.d == 128 ? 24 : 8)) return {kTt, 64, 128, 1};
   }

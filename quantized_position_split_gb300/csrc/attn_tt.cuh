@@ -886,7 +886,9 @@ template <int D>
 qps_status launch_tt_d(const PagedAttnParams& p, cudaStream_t s) {
 #define QPS_TT_CASE(KF, VF) \
   if (p.kfmt == KF && p.vfmt == VF) return launch_tt<D, KF, VF>(p, s);
-  QPS_TT_CASE(QPS_FMT_F16, QPS_FMT_F16)
+  if constexpr (D > 128) {  // (128: attn_tm.cuh)
+    QPS_TT_CASE(QPS_FMT_F16, QPS_FMT_F16)
+  }
   QPS_TT_CASE(QPS_FMT_F16, QPS_FMT_Q8_0)
   QPS_TT_CASE(QPS_FMT_F16, QPS_FMT_TQ3)
   QPS_TT_CASE(QPS_FMT_F16, QPS_FMT_TQ2)
