@@ -415,7 +415,8 @@ typedef struct qps_paged_attn_args {
                                 positions [j*page_size, (j+1)*page_size) of sequence b; entries
                                 behind the last position are not read */
   int64_t table_stride;
-  int32_t table_width;       /* entries per sequence, >= 1; table_width * page_size < 2^31 - 64 */
+  int32_t table_width;       /* entries per sequence, >= 1; table_width * page_size < 2^31 - 1024,
+                                and batch * table_width * page_size < 2^35 (else UNSUPPORTED) */
   int32_t o_dtype;           /* qps_dtype of o */
   const int32_t* kv_lens;    /* device, [batch]: positions of each sequence, the new ones
                                 included; 0 gives O = 0, lse = -inf.  A length outside
@@ -432,8 +433,9 @@ typedef struct qps_paged_attn_args {
 } qps_paged_attn_args;
 
 /* Workspace bytes of qps_attn_decode_paged for these args (host only, no launch; o, lse
- * and workspace are not looked at).  Depends on the batch, the heads and the formats,
- * not on the lengths.  Library utility, no counterpart on the pages.
+ * and workspace are not looked at).  Depends on the batch, n_q, the heads, the formats,
+ * table_width, page_size and shared_len, not on the lengths or the entries.  Library
+ * utility, no counterpart on the pages.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA (the SM count). */
 QPS_API qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* workspace_bytes);
 

@@ -104,7 +104,7 @@ __device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int i
       const int at = index - (before + __shfl_sync(0xffffffffu, sum, src) - n);
       r.b = b0 + src;
       r.t0 = p.prefix_len + at * cu * kPagedUnit;
-      r.t1 = min(__shfl_sync(0xffffffffu, bl, src), r.t0 + cu * kPagedUnit);
+      r.t1 = (int)min((int64_t)__shfl_sync(0xffffffffu, bl, src), r.t0 + (int64_t)cu * kPagedUnit);
       r.count = n;
       r.first = at == 0;
       r.whole = n == 1 && p.prefix_len == 0;

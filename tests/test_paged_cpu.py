@@ -167,6 +167,8 @@ def _attn(kv=None, **kw):
     (dict(hq=4096, q_batch_stride=4096 * 128), UNSUPPORTED), (dict(q_batch_stride=8 * 128 + 4), INVALID),
     (dict(q_batch_stride=128), INVALID), (dict(page_table=None), INVALID), (dict(kv_lens=0x30002), INVALID),
     (dict(table_width=0), INVALID), (dict(table_width=1 << 25, table_stride=1 << 25), INVALID),
+    (dict(table_width=(1 << 25) - 16, table_stride=1 << 25), INVALID),
+    (dict(batch=17, table_width=(1 << 25) - 17, table_stride=1 << 25), UNSUPPORTED),
     (dict(table_stride=15), INVALID), (dict(shared_len=-64), INVALID), (dict(shared_len=32), INVALID),
     (dict(shared_len=17 * 64), INVALID), (dict(o_dtype=3), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(softcap=float("nan")), INVALID),
