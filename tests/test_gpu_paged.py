@@ -70,7 +70,7 @@ def _check_rows(got, x, w, offset, norm, cs, inter, out_dtype):
 
 
 @pytest.mark.parametrize("d", [32, 64, 128, 256, 512])
-@pytest.mark.parametrize("tokens,hq,hkv", [(1, 8, 2), (1, 1, 1), (7, 5, 1), (613, 12, 3)])
+@pytest.mark.parametrize("tokens,hq,hkv", [(1, 8, 2), (1, 1, 1), (7, 5, 1), (613, 10, 3)])
 @pytest.mark.parametrize("inter,part", [(False, 1), (True, 1), (False, 2), (True, 2)])
 def test_norm_rope(qps, d, tokens, hq, hkv, inter, part):
     for i, (dtype, out) in enumerate([(torch.float16, torch.float16), (torch.bfloat16, torch.float16),
@@ -297,7 +297,7 @@ def test_attention_ragged(qps, d, kf, vf):
     """Every format on small and large pages, lengths of zero, one and around page and tile
     borders, garbage behind each sequence's end."""
     hkv = 2
-    for page, group, softcap in ((16, 4, 0.0), (64, 1, 30.0), (256, 3, 0.0)):
+    for page, group, softcap in ((16, 4, 0.0), (64, 1, 30.0), (256, 5, 0.0)):
         rot, ora = _rotations(d, "block" if page == 64 else "whole")
         lens = RAGGED if page < 256 else [257, 0, 300, 2000]
         cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, d + page, rot)
@@ -310,7 +310,7 @@ def test_attention_ragged(qps, d, kf, vf):
 
 @pytest.mark.parametrize("d,kf,vf", [(64, "f16", "f16"), (128, "f16", "f16"), (128, "q8_0", "tq3"), (256, "q8_0", "q8_0"),
                                      (512, "q8_0", "tq3"), (128, "tq4", "tq4")])
-@pytest.mark.parametrize("n_q,group", [(1, 1), (2, 5), (5, 4), (17, 2), (64, 3)])
+@pytest.mark.parametrize("n_q,group", [(1, 1), (2, 5), (5, 4), (17, 2), (64, 5)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_attention_multi_query(qps, d, kf, vf, n_q, group, causal):
     """Verify batches: the causal limit of every query, sequences shorter than the batch of
@@ -411,6 +411,91 @@ def test_attention_long_and_output_types(qps):
     assert_parity(got[torch.float32].cpu().numpy(), lse.cpu().numpy(), ro, rl)
     for dt in (torch.float16, torch.bfloat16):
         assert torch.equal(got[dt], got[torch.float32].to(dt))
+
+
+MANY = [(64, "f16", "f16", 9, 2), (128, "f16", "f16", 3, 4), (128, "q8_0", "tq3", 9, 4), (256, "q8_0", "q8_0", 5, 3),
+        (256, "f16", "f16", 5, 3), (512, "q8_0", "tq2", 3, 8)]
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", MANY)
+def test_attention_many_rows_bad_pages(qps, d, kf, vf, n_q, group):
+    """As test_attention_bad_indexes, for the kernels that take many query rows."""
+    hkv, page = 2, 32
+    lens = [300, 170, 200]
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, 8, rot)
+    q = torch.randn((3, n_q, hkv * group, d), generator=torch.Generator().manual_seed(4)).half().cuda()
+    ro, rl = _want(cache, q, table, lens, d ** -0.5, 0.0, True, ora)
+    rows = n_q * hkv * group
+    keep = np.r_[0:rows, 2 * rows:3 * rows]
+    for bad in (cache.n_pages, 1 << 30, -1):
+        t = table.clone()
+        t[1, 4] = bad
+        o, lse = _run(qps, q, cache, t, lens, scale=d ** -0.5, causal=True, out_dtype=torch.float32)
+        with pytest.raises(qps.QpsError) as e:
+            qps.device_status(reset=True)
+        assert e.value.status == 1
+        assert_parity(o[keep], lse[keep], ro[keep], rl[keep], bad)
+        assert np.isfinite(o).all()
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", MANY)
+def test_attention_many_rows_nan_and_output_types(qps, d, kf, vf, n_q, group):
+    """A NaN value or key reaches its own sequence's rows alone; a NaN or infinity behind a
+    sequence's end reaches none; fp16 and bf16 outputs are the float32 one rounded once."""
+    hkv, page = 2, 64
+    lens = [140, 200, 150, 129]
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, 12, rot)
+    q = torch.randn((4, n_q, hkv * group, d), generator=torch.Generator().manual_seed(5)).half().cuda()
+    ro, rl = _want(cache, q, table, lens, d ** -0.5, 0.0, False, ora)
+    nan = float("nan")
+    v_float = cache.v_planes[-1] if vf != "f16" else cache.v_planes[0]
+    k_float = cache.k_planes[-1] if kf != "f16" else cache.k_planes[0]
+    for t, x in ((v_float, nan), (k_float, float("inf"))):  # behind the ends, in the last pages
+        for b, n in enumerate(lens):
+            t[int(table[b, n // page]), :, n % page:] = x
+    o, lse = _run(qps, q, cache, table, lens, scale=d ** -0.5, out_dtype=torch.float32)
+    assert_parity(o, lse, ro, rl, (d, kf, vf))
+    for dt in (torch.float16, torch.bfloat16):
+        a = qps.paged_attn_args(q, cache, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), scale=d ** -0.5,
+                                out_dtype=dt)
+        assert torch.equal(qps.attn_decode_paged(a)[0].cpu(), torch.from_numpy(o).to(dt))
+    v_float[int(table[0, 1]), :, 7] = nan
+    k_float[int(table[2, 0]), :, 9] = nan
+    o, lse = _run(qps, q, cache, table, lens, scale=d ** -0.5, out_dtype=torch.float32)
+    rows = n_q * hkv * group
+    assert np.isnan(o[:rows]).all() and np.isnan(o[2 * rows:3 * rows]).all()
+    keep = np.r_[rows:2 * rows, 3 * rows:4 * rows]
+    assert_parity(o[keep], lse[keep], ro[keep], rl[keep], (d, kf, vf))
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(128, "f16", "f16", 1, 1), (128, "q8_0", "q8_0", 2, 4), (64, "f16", "f16", 5, 4),
+                                               (128, "q8_0", "tq3", 7, 4)])
+def test_attention_large_batch(qps, d, kf, vf, n_q, group):
+    """More sequences than the lanes' first round of lengths holds, behind a prefix and
+    without, empty and short ones among them, on two streams at once."""
+    hkv, page, batch = 2, 16, 300
+    r = np.random.default_rng(d)
+    common = 2 * page
+    lens = [common + int(n) for n in r.integers(0, 90, batch)]
+    lens[5], lens[140], lens[299] = 0, 3, common
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, 3, rot, common)
+    q = torch.randn((batch, n_q, hkv * group, d), generator=torch.Generator().manual_seed(6)).half().cuda()
+    ro, rl = _want(cache, q, table, lens, d ** -0.5, 0.0, n_q > 1, ora)
+    lt, tt = torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda()
+    blocks = [qps.paged_attn_args(q, cache, tt, lt, scale=d ** -0.5, causal=n_q > 1, shared_len=sh, out_dtype=torch.float32)
+              for sh in (0, common)]
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, a in zip(streams, blocks):
+            qps.attn_decode_paged(a, stream=st)
+    torch.cuda.synchronize()
+    for a in blocks:
+        o, lse = a._out
+        assert_parity(o.cpu().numpy(), lse.cpu().numpy(), ro, rl, (d, kf, vf))
 
 
 def test_attention_bad_indexes(qps):
