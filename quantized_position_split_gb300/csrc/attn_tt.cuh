@@ -9,10 +9,8 @@
 //     S^T [128 positions][N] = K Q^T      A = K (TMEM), B = Q (shared, K-major), per 64 dims
 //     P   = 2^(S' - m)                    one position and 32 rows a thread
 //     O^T [128 dims][N]     += V^T P^T    A = V (shared, MN-major, as stored), B = P (MN-major)
-// S^T (two buffers), O^T (D / 128 blocks) and two slots of K live in TMEM.  Products that
-// add to one accumulator follow each other at 75 to 100 cycles, whatever N: so S^T has two
-// accumulators a buffer where TMEM has the columns (hi and lo parts, or odd and even steps),
-// and S^T's and O^T's products alternate.
+// S^T (two buffers), O^T (D / 128 blocks) and two slots of K live in TMEM; S^T of the next
+// tile and O^T of the last one are issued in turn, as their slots are decoded.
 //
 // The stored rows arrive by tensor-map boxes in small raw stages; four warps decode K, one
 // position a thread, from there into TMEM (64 dims a slot), four more V into 32 KB slots of
@@ -27,6 +25,9 @@
 // A row's maximum over the positions would cross all threads, so the running reference m
 // (in shared memory) is raised only when some position exceeds it by more than 8 (log2):
 // one vote a tile, and on a raise the maxima are taken, O and the sums rescaled.
+//
+// Measured: four sequences of five tokens and 30000 to 32768 positions, two KV heads of 512,
+// q8_0 / tq3 (40 rows): 88 us, 2.1 TB/s; bound by instruction issue, 20 warps of four roles.
 //
 // Roles: warp 0 issues the products, warps 2 and 3 the boxes of K and V, warps 4-11 are the
 // softmax (two groups of rows), 12-15 decode K and 16-19 V.  Waits are bounded as in
@@ -105,10 +106,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   const int ntiles = uniform(t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0);  // 0: no own positions
   const int nrows = min(kN, p.rows_per_cta - row0);
   const int n16 = uniform((nrows + 15) & ~15);  // N of the products
-  // TMEM columns: S (two buffers of one or two accumulators), K (two slots of 32 hi and 32
-  // lo), O
-  const int accs = (4 + G::VC) * n16 + 128 <= 512 ? 2 : 1;
-  const int k_col = 2 * accs * n16, o_col = k_col + 128;
+  // TMEM columns: S (two buffers), K (two slots of 32 hi and 32 lo), O
+  const int k_col = 2 * n16, o_col = k_col + 128;
 
   // ---- barriers, TMEM, queries, row state ----------------------------------------------------
   uint8_t* misc = smem + G::MISC;
@@ -172,38 +171,36 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 
   if (warp == 0) {
     // ---- products: S(0), S(1), then S(j + 1) beside O(j - 1), while the softmax of tile j runs:
-    // four slots of K, then two of V whose products alternate.  (S(j + 1), then O(j), each
-    // waiting for its decoders in turn, took 11300 cycles a tile at head_dim 512; K's and V's
-    // products alternating, 130 cycles each instead of 75.) ----
+    // two slots of K, then one of V.  (S(j + 1), then O(j), each waiting for its decoders in
+    // turn, took 4% longer at head_dim 512; four slots, then two, 2%.) ----
     const uint32_t id_s = instr_desc(n16, 0), id_o = instr_desc(n16, 1) | (1u << 15), one = elect_lane();
-    constexpr int PAIR = G::VC > 1 ? 2 : 1;
     int fk = 0, fv = 0;  // slots used
     bool ok = ntiles == 0 || wait(q_full, 0);
     for (int j = -1; j <= ntiles && ntiles > 0 && ok; ++j) {
       const bool qk = j + 1 < ntiles, pv = j >= 1;
       // (P of tile j - 1 is there: its S, whose buffer S(j + 1) takes, has been read)
       if (pv && !(ok = wait(p_ready((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
-      const uint32_t ds = tmem + ((j + 1) & 1) * accs * n16, ds1 = ds + (accs - 1) * n16;
+      const uint32_t ds = tmem + ((j + 1) & 1) * n16;
       const uint64_t bp = smem_desc(sbase + G::P_OFF + ((j - 1) & 1) * G::P_STEP, 16);
 #pragma unroll 1
-      for (int v0 = 0; v0 < G::VC && ok; v0 += PAIR) {
+      for (int u = 0; u < G::VC && ok; ++u) {
         if (qk) {
 #pragma unroll 1
-          for (int c = 2 * v0; c < 2 * (v0 + PAIR); ++c, ++fk) {
+          for (int c = 2 * u; c < 2 * u + 2; ++c, ++fk) {
             const int s = fk & 1;
             if (!(ok = wait(k_full(s), (fk >> 1) & 1))) break;
             fence_after();
             const uint32_t a = tmem + k_col + s * 64;
             const uint64_t bq = smem_desc(sbase + c * (kN * 128), 16);
-            const uint32_t fresh = c > 0;  // (0: a tile's first products start their accumulators)
+            const uint32_t fresh = c > 0;  // (0: a tile's first product starts its accumulator)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint64_t b = bq + (uint64_t)(kk * 2);
               if constexpr (KF == QPS_FMT_Q8_0) {
                 mma_ts(ds, a + kk * 8, b, id_s, fresh | (kk > 0), one);
-                mma_ts(ds1, a + 32 + kk * 8, b, id_s, fresh | (kk > 0) | (accs == 1), one);
+                mma_ts(ds, a + 32 + kk * 8, b, id_s, 1, one);
               } else {
-                mma_ts(kk & 1 ? ds1 : ds, a + kk * 8, b, id_s, fresh | (kk > 1) | (kk == 1 && accs == 1), one);
+                mma_ts(ds, a + kk * 8, b, id_s, fresh | (kk > 0), one);
               }
             }
             commit(k_empty(s), one);
@@ -211,40 +208,33 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           }
         }
         if (pv && ok) {
-          uint64_t a[PAIR];
+          const int s = fv % kSlots;
+          if (!(ok = wait(v_full(s), (fv / kSlots) & 1))) break;
+          if constexpr (!VDEC) {
+            // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
+            const int left = t1 - (t0 + (j - 1) * kTile);
+            if (left < kTile) {
+              for (int i = left * 8 + lane; i < kTile * 8; i += 32)
 #pragma unroll
-          for (int u = 0; u < PAIR; ++u) {
-            const int s = (fv + u) % kSlots;
-            if (!(ok = wait(v_full(s), ((fv + u) / kSlots) & 1))) break;
-            if constexpr (!VDEC) {
-              // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
-              const int left = t1 - (t0 + (j - 1) * kTile);
-              if (left < kTile) {
-                for (int i = left * 8 + lane; i < kTile * 8; i += 32)
-#pragma unroll
-                  for (int g = 0; g < 2; ++g)
-                    *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
-                mma::fence_proxy_async();
-                __syncwarp();
-              }
+                for (int g = 0; g < 2; ++g)
+                  *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+              mma::fence_proxy_async();
+              __syncwarp();
             }
-            a[u] = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
           }
-          if (!ok) break;
+          const uint64_t a = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
           fence_after();
 #pragma unroll
           for (int part = 0; part <= G::PLO; ++part)
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-#pragma unroll
-              for (int u = 0; u < PAIR; ++u) {
-                const uint64_t o = (uint64_t)((kk * 2048) >> 4);
-                mma_ss(tmem + o_col + (v0 + u) * n16, a[u] + o, bp + o + (uint64_t)((part * kPBytes) >> 4), id_o,
-                       j > 1 || kk > 0 || part > 0, one);
-              }
-#pragma unroll
-          for (int u = 0; u < PAIR; ++u, ++fv) commit(v_empty(fv % kSlots), one);
-          if (v0 + PAIR >= G::VC) commit(p_free((j - 1) & 1), one);
+            for (int kk = 0; kk < kTile / 16; ++kk) {
+              const uint64_t o = (uint64_t)((kk * 2048) >> 4);
+              mma_ss(tmem + o_col + u * n16, a + o, bp + o + (uint64_t)((part * kPBytes) >> 4), id_o, j > 1 || kk > 0 || part > 0,
+                     one);
+            }
+          commit(v_empty(s), one);
+          ++fv;
+          if (u == G::VC - 1) commit(p_free((j - 1) & 1), one);
         }
       }
     }
@@ -582,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       fence_after();
       // the logits, in units of log2, of 16 rows at this thread's position (read again for
       // each use: kept beside the sums they would not fit the registers)
-      const uint32_t s_at = tmem + lanes + (j & 1) * accs * n16 + r0;
+      const uint32_t s_at = tmem + lanes + (j & 1) * n16 + r0;
       auto logits = [&](int c, float (&x)[16]) {
         uint32_t v[16];
         __syncwarp();
@@ -590,12 +580,6 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-        if (accs == 2) {
-          ld16(v, s_at + n16 + 16 * c);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] += __uint_as_float(v[i]);
-        }
         if (cap > 0.f) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[i] = mma::softcap_tanh(x[i] * p.scale, cap, cap_k) * LOG2E;
