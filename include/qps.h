@@ -423,7 +423,11 @@ typedef struct qps_paged_attn_args {
                                 [0, table_width * page_size] is cut to that range */
   int64_t shared_len;        /* the first shared_len positions (a multiple of page_size) lie in
                                 the same pages for every sequence and are read once, through
-                                sequence 0's entries; 0: none */
+                                sequence 0's entries (valid ones, whatever its length); 0: none.
+                                A NaN or infinite value among positions that some rows of the
+                                batch see may reach the others too, and so may one in a
+                                sequence's own positions that causal hides from a query (0 x NaN);
+                                keys, and anything behind the ends, reach no such row */
   float scale, softcap;      /* as in qps_attn_args */
   void* o;                   /* device, [batch*n_q*hq][D] of o_dtype, rows as in qps_attn_args */
   float* lse;                /* device, f32 [batch*n_q*hq] */
