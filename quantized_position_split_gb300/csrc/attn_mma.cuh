@@ -405,6 +405,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       whole = ch.whole;
       t0 = ch.t0;
       t1 = ch.t1;
+    } else {
+      t1 = min(t1, (int64_t)paged_prefix_len(p, lane));
     }
   }
 
@@ -429,12 +431,14 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     for (int idx = threadIdx.x; idx < nrows * D; idx += G::NW * 32) {
       const int r = idx / D, dd = idx % D;
       const int64_t row = out_row(row0 + r);
-      if constexpr (PAGED) {  // (a sequence without own positions: its output, or an empty part)
-        const int64_t at = (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
-        if (!whole) p.own_o[at * D + dd] = 0.f;
+      if constexpr (PAGED) {  // (a sequence without own positions: its output, or an empty part;
+                              // a chunk of the prefix behind every end: an empty part)
+        const int64_t at = p.shared ? (int64_t)part * p.rows_total + row
+                                    : (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
+        if (!whole) (p.shared ? p.pre_o : p.own_o)[at * D + dd] = 0.f;
         else if (p.out_dtype == QPS_DT_F32) reinterpret_cast<float*>(p.out)[row * D + dd] = 0.f;
         else reinterpret_cast<uint16_t*>(p.out)[row * D + dd] = 0;
-        if (dd == 0) (whole ? p.out_lse[row] : p.own_lse[at]) = -INFINITY;
+        if (dd == 0) (whole ? p.out_lse[row] : p.shared ? p.pre_lse[at] : p.own_lse[at]) = -INFINITY;
         continue;
       }
       if (!in_bounds(part < p.parts_cap && row >= 0 && row < p.rows_total, p.err)) continue;

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool whole = false;
   if (p.shared) {
     t0 = split * (int)p.chunk;
-    t1 = min((int)p.end, t0 + (int)p.chunk);
+    t1 = min(paged_prefix_len(p, lane), t0 + (int)p.chunk);  // (at or before t0: an empty part)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)

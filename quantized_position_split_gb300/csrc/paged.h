@@ -64,6 +64,16 @@ __device__ __forceinline__ int paged_chunks(const PagedAttnParams& p, int len, i
   return units <= cu ? 1 : (units + cu - 1) / cu;
 }
 
+// Positions of the prefix that some sequence of the batch has, the same in every lane.  The
+// pages behind the longest sequence's end hold no one's rows, and a NaN there would pass a
+// weight of zero (0 x NaN), so the prefix ends with it.
+__device__ __forceinline__ int paged_prefix_len(const PagedAttnParams& p, int lane) {
+  int n = 0;
+#pragma unroll 4
+  for (int b = lane; b < p.batch; b += 32) n = max(n, paged_len(p, b));
+  return min(__reduce_max_sync(0xffffffffu, n), p.prefix_len);
+}
+
 // Chunk number `index` of the batch: its sequence (-1: there are fewer chunks), positions
 // [t0, t1), whether it is its sequence's first (of `count`) and its only part; the same in
 // every lane.

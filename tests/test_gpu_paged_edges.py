@@ -1,0 +1,57 @@
+"""Calls around a paged cache at the edges of what their documentation allows, on the GPU
+against the float64 oracle: what lies behind every sequence's end, padding rows, the
+extremes of the stored formats, large pages, first calls under capture."""
+
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as op
+from tests.helpers import assert_parity
+from tests.test_gpu_paged import _cache_of, _f, _lib_rot, _rotations, _run, _want, qps  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+# one KV head's rows of a whole batch go to attn_mma.cuh (few rows), attn_tm.cuh (many, fp16
+# pages of head_dim 64 / 128) or attn_tt.cuh (many, other pages)
+PREFIXES = [(128, "f16", "f16", 2, 1), (512, "q8_0", "q8_0", 2, 1), (128, "q8_0", "tq3", 3, 2), (64, "tq2", "tq2", 5, 4),
+            (128, "f16", "f16", 5, 4), (64, "f16", "f16", 7, 5),
+            (128, "q8_0", "tq3", 9, 4), (256, "f16", "f16", 5, 4), (256, "f16", "q8_0", 5, 4), (512, "q8_0", "tq2", 5, 4)]
+
+
+def _value_plane(cache):
+    """The fp16 plane of V (values, scales or norms)."""
+    return cache.v_planes[0] if cache.v_fmt == "f16" else cache.v_planes[-1]
+
+
+def _key_plane(cache):
+    return cache.k_planes[0] if cache.k_fmt == "f16" else cache.k_planes[-1]
+
+
+@pytest.mark.parametrize("d,kf,vf,batch,group", PREFIXES)
+def test_prefix_behind_every_end(qps, d, kf, vf, batch, group):  # noqa: F811
+    """Every sequence ends inside the shared pages: NaN values and infinite keys behind the
+    longest end, in its last page and in whole chunks, reach no row."""
+    hkv, page, common = 2, 64, 64 * 64
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, [common] * batch, page, hkv, d, 3 * d, rot, common)
+    q = torch.randn((batch, hkv * group, d), generator=torch.Generator().manual_seed(d)).half().cuda()
+    for longest in (common - 37, 1203, 37):
+        lens = [longest - 3 * (batch - 1 - b) for b in range(batch)]
+        lens[0] = 0 if batch > 2 else lens[0]
+        ro, rl = _want(cache, q, table, lens, d ** -0.5, 0.0, False, ora)
+        k_was, v_was = _key_plane(cache).clone(), _value_plane(cache).clone()
+        for plane, x in ((_value_plane(cache), float("nan")), (_key_plane(cache), float("inf"))):
+            plane[int(table[0, longest // page]), :, longest % page:] = x
+            for j in range(longest // page + 1, common // page):
+                plane[int(table[0, j])] = x
+        o, lse = _run(qps, q, cache, table, lens, scale=d ** -0.5, shared_len=common, out_dtype=torch.float32)
+        assert_parity(o, lse, ro, rl, (d, kf, vf, batch, group, longest))
+        _key_plane(cache).copy_(k_was)
+        _value_plane(cache).copy_(v_was)
