@@ -422,8 +422,9 @@ typedef struct qps_paged_attn_args {
                                 included; 0 gives O = 0, lse = -inf.  A length outside
                                 [0, table_width * page_size] is cut to that range */
   int64_t shared_len;        /* the first shared_len positions (a multiple of page_size) lie in
-                                the same pages for every sequence and are read once, through
-                                sequence 0's entries (valid ones, whatever its length); 0: none.
+                                the same pages for every sequence that has them and are read
+                                once, through the entries of the first sequence that holds
+                                all of them (or of the longest, where none does); 0: none.
                                 A NaN or infinite value among positions that some rows of the
                                 batch see may reach the others too, and so may one in a
                                 sequence's own positions that causal hides from a query (0 x NaN);

@@ -406,7 +406,9 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       t0 = ch.t0;
       t1 = ch.t1;
     } else {
-      t1 = min(t1, (int64_t)paged_prefix_len(p, lane));
+      const PagedPrefix pre = paged_prefix(p, lane);
+      bz = pre.b;  // (whose page entries the prefix is read through)
+      t1 = min(t1, (int64_t)pre.len);
     }
   }
 
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   auto page_of = [&](int64_t t) -> int {
     if constexpr (PAGED) {
       if (t >= t1) return (int)p.n_pages;
-      const int pg = p.table[(p.shared ? 0 : (int64_t)bz * p.table_stride) + (t >> p.page_shift)];
+      const int pg = p.table[(int64_t)bz * p.table_stride + (t >> p.page_shift)];
       if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
       atomicOr(p.err, kErrIndex);
       return (int)p.n_pages;

@@ -171,11 +171,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rtiles = (p.rows_per_cta + kRows - 1) / kRows;
   const int split = blockIdx.x / rtiles, row0 = (blockIdx.x % rtiles) * kRows;
   const int head = blockIdx.y;
-  int bz = 0, t0, t1;
+  int bz, t0, t1;  // the sequence (of a shared prefix: whose page entries it is read through)
   bool whole = false;
   if (p.shared) {
     t0 = split * (int)p.chunk;
-    t1 = min(paged_prefix_len(p, lane), t0 + (int)p.chunk);  // (at or before t0: an empty part)
+    const PagedPrefix pre = paged_prefix(p, lane);
+    bz = pre.b;
+    t1 = min(pre.len, t0 + (int)p.chunk);  // (at or before t0: an empty part)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // them a tile, one a lane.  A lane reads its page a tile ahead (read when the box is due, the
     // table's latency kept the copies 1800 cycles a tile apart, twice the products' time). ------
     const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
-    const int32_t* row = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
+    const int32_t* row = p.table + (int64_t)bz * p.table_stride;
     const int cg = lane % G::CG, r = lane / G::CG;
     auto has = [&](int j) { return r < nb && t0 + j * kTok + r * br < t1; };
     auto entry = [&](int j) { return has(j) ? row[(t0 + j * kTok + r * br) >> p.page_shift] : 0; };

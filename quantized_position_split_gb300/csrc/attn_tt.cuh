@@ -89,11 +89,13 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   const int rtiles = (p.rows_per_cta + kN - 1) / kN;
   const int split = blockIdx.x / rtiles, row0 = (blockIdx.x % rtiles) * kN;
   const int head = blockIdx.y;
-  int bz = 0, t0, t1;
+  int bz, t0, t1;  // the sequence (of a shared prefix: whose page entries it is read through)
   bool whole = false;
   if (p.shared) {
     t0 = split * (int)p.chunk;
-    t1 = min(paged_prefix_len(p, lane), t0 + (int)p.chunk);  // (at or before t0: an empty part)
+    const PagedPrefix pre = paged_prefix(p, lane);
+    bz = pre.b;
+    t1 = min(pre.len, t0 + (int)p.chunk);  // (at or before t0: an empty part)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     // a tile ahead -------------------------------------------------------------------------------
     const bool v = warp == 3;
     const int br = min(1 << p.page_shift, kTile), nb = kTile / br;
-    const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
+    const int32_t* table = p.table + (int64_t)bz * p.table_stride;
     // bytes of a position's row in a box; V: column groups of a slot, signs behind the codes
     const int rb = v ? (VF == QPS_FMT_F16 || VF == QPS_FMT_Q8_0 ? 128 : 32) : (KF == QPS_FMT_F16 ? 128 : 64);
     const int groups = v && !VDEC ? 2 : 1;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     // ---- decode: one position a thread, K by warps 12-15, V by warps 16-19 ------------------------
     const bool v = warp >= 16;
     const int tok = threadIdx.x & 127;
-    const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
+    const int32_t* table = p.table + (int64_t)bz * p.table_stride;
     // the position's q8_0 scales (0: no position, or no page), loaded a tile ahead
     constexpr int W = D / 64;  // words of two
     auto load_scales = [&](int j, const void* aux, uint32_t (&w)[W]) {
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     const int r0 = half * 32, nch = max(0, min(CH, n16 / 16 - half * CH));  // (in use)
     int least = 0x7fffffff;                              // positions below it are visible to every row
     for (int r = 0; r < nrows; ++r) least = min(least, lim[r]);
-    const int32_t* table = p.table + (p.shared ? 0 : (int64_t)bz * p.table_stride);
+    const int32_t* table = p.table + (int64_t)bz * p.table_stride;
     const void* norms = VF == QPS_FMT_TQ3 ? p.v.aux2 : p.v.aux;
     auto ld16 = [&](uint32_t (&v)[16], uint32_t addr) {
       asm volatile(

@@ -64,14 +64,28 @@ __device__ __forceinline__ int paged_chunks(const PagedAttnParams& p, int len, i
   return units <= cu ? 1 : (units + cu - 1) / cu;
 }
 
-// Positions of the prefix that some sequence of the batch has, the same in every lane.  The
-// pages behind the longest sequence's end hold no one's rows, and a NaN there would pass a
-// weight of zero (0 x NaN), so the prefix ends with it.
-__device__ __forceinline__ int paged_prefix_len(const PagedAttnParams& p, int lane) {
-  int n = 0;
+// The prefix as the batch has it, the same in every lane: its positions, and the sequence
+// through whose entries they are read.  The pages behind the longest sequence's end hold no
+// one's rows, and a NaN there would pass a weight of zero (0 x NaN), so the prefix ends with
+// it; the entries are those of the first sequence that has all of these positions (a padding
+// row's may name any page).
+struct PagedPrefix {
+  int len, b;
+};
+__device__ __forceinline__ PagedPrefix paged_prefix(const PagedAttnParams& p, int lane) {
+  int len = -1, first = 0;
 #pragma unroll 4
-  for (int b = lane; b < p.batch; b += 32) n = max(n, paged_len(p, b));
-  return min(__reduce_max_sync(0xffffffffu, n), p.prefix_len);
+  for (int b = lane; b < p.batch; b += 32) {
+    const int n = min(paged_len(p, b), p.prefix_len);
+    if (n > len) {
+      len = n;
+      first = b;
+    }
+  }
+  PagedPrefix r;
+  r.len = __reduce_max_sync(0xffffffffu, len);
+  r.b = __reduce_min_sync(0xffffffffu, len == r.len ? first : 0x7fffffff);
+  return r;
 }
 
 // Chunk number `index` of the batch: its sequence (-1: there are fewer chunks), positions

@@ -55,3 +55,24 @@ def test_prefix_behind_every_end(qps, d, kf, vf, batch, group):  # noqa: F811
         assert_parity(o, lse, ro, rl, (d, kf, vf, batch, group, longest))
         _key_plane(cache).copy_(k_was)
         _value_plane(cache).copy_(v_was)
+
+
+@pytest.mark.parametrize("d,kf,vf,batch,group", PREFIXES)
+def test_prefix_behind_a_padding_row(qps, d, kf, vf, batch, group):  # noqa: F811
+    """The first row of a padded batch (length zero, or a sequence that ends inside the
+    shared pages) names other pages behind its end: the prefix is the others' all the same."""
+    hkv, page, common = 2, 32, 16 * 32
+    rot, ora = _rotations(d, "whole")
+    for first in (0, 70):
+        lens = [common + 1 + 9 * b for b in range(batch)]
+        cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, 5 * d, rot, common)
+        q = torch.randn((batch, hkv * group, d), generator=torch.Generator().manual_seed(d)).half().cuda()
+        lens[0] = first
+        ro, rl = _want(cache, q, table, lens, d ** -0.5, 0.0, False, ora)
+        own = int(table[1, common // page])  # a page that holds other rows
+        for behind in (own, -7):
+            t = table.clone()
+            t[0, -(-first // page):] = behind
+            o, lse = _run(qps, q, cache, t, lens, scale=d ** -0.5, shared_len=common, out_dtype=torch.float32)
+            assert_parity(o, lse, ro, rl, (d, kf, vf, batch, group, first, behind))
+            qps.device_status(reset=True)
