@@ -17,7 +17,9 @@
 // fp16 operands (128 dims; fp16 values are boxed there as they are).  K by way of shared
 // memory slots too, a tile took 17000 cycles at head_dim 512: 8600 of shared-memory traffic
 // and most of the rest in the decoding warps' waits.  Numerics: a q8_0 key (code x scale)
-// is its hi + lo fp16 parts, two products, so logits keep float32 accuracy; a TurboQuant V
+// is its hi + lo fp16 parts, two products, so logits keep float32 accuracy (where a
+// position's scales reach 2^8 they are halved until its products fit fp16, and its logits
+// doubled back: a key of fp16's largest value is stored as 127 x 516 = 65532); a TurboQuant V
 // is its exact fp16 levels in the rotated domain with the norm folded into P before P's one
 // rounding, the output being rotated back once; a q8_0 V is rounded once to fp16; sums,
 // maxima and O are float32.
@@ -46,6 +48,8 @@ constexpr int kTile = 128;         // positions per tile
 constexpr int kThreadsTt = 640;
 constexpr int kSlot = 32 * 1024;  // a slot of V's fp16 operands
 constexpr int kPBytes = kTile * kN * 2;  // a buffer of P
+// -m of a row without a reference: any finite logit is far above it, and 2^(-inf + it) is 0
+constexpr float kNone = 0x1p126f;
 
 template <int D, int KF, int VF>
 struct GeoTt {
@@ -65,7 +69,8 @@ struct GeoTt {
   static constexpr int VSTAGE = (VF == QPS_FMT_Q8_0 ? 16 : 8) * 1024, VN = RAW_BYTES / VSTAGE;
   static constexpr int KRAW = RING + SLOTS * kSlot, VRAW = KRAW + RAW_BYTES;
   static constexpr int MISC = VRAW + RAW_BYTES;
-  static constexpr int MISC_BYTES = D == 128 ? 2304 : 2048;
+  static constexpr int EXPS = D == 128 ? 4 : 2;     // buffers of the positions' exponents
+  static constexpr int MISC_BYTES = D == 128 ? 2560 : 2048;
   static constexpr int SMEM = MISC + MISC_BYTES + 1024;  // + slack for the 1024-byte base alignment
 };
 
@@ -113,13 +118,18 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 
   // ---- barriers, TMEM, queries, row state ----------------------------------------------------
   uint8_t* misc = smem + G::MISC;
-  float* thr = reinterpret_cast<float*>(misc);            // [64] m + 8 (-inf: no reference yet)
-  float* mneg = reinterpret_cast<float*>(misc + 256);     // [64] -m (0: none)
-  int* lim = reinterpret_cast<int*>(misc + 512);          // [64] positions below it are visible
-  int* red = reinterpret_cast<int*>(misc + 768);          // [4][64] maxima, then sums
-  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(misc + 1792);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1796);
-  const uint32_t bars = sbase + G::MISC + 1800;
+  float* mneg = reinterpret_cast<float*>(misc);           // [64] -m (kNone: no reference yet)
+  int* lim = reinterpret_cast<int*>(misc + 256);          // [64] positions below it are visible
+  int* red = reinterpret_cast<int*>(misc + 512);          // [4][64] maxima, then sums
+  // [EXPS][128] how often a position's q8_0 scales were halved.  A tile's are written when its
+  // buffer's last reader is known to be done: S of two tiles ago (four buffers, the tile's first
+  // slot), or a slot of S of the same tile (two buffers, its third slot) has been issued, and
+  // each S waits for P of two tiles before it.
+  uint8_t* kexp = misc + 1536;
+  constexpr int TAIL = 1536 + G::EXPS * kTile;
+  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(misc + TAIL);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + TAIL + 4);
+  const uint32_t bars = sbase + G::MISC + TAIL + 8;
   constexpr int KN = G::KN, VN = G::VN, kSlots = G::SLOTS;
   auto bar_at = [&](int i) { return bars + 8 * i; };
   auto s_full = [&](int w) { return bar_at(w); };
@@ -137,7 +147,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   auto kraw_empty = [&](int s) { return bar_at(ONES + 5 + kSlots + s); };
   auto vraw_empty = [&](int s) { return bar_at(ONES + 5 + kSlots + KN + s); };
   constexpr int NBARS = ONES + 5 + kSlots + KN + VN;
-  static_assert(1800 + 8 * NBARS <= G::MISC_BYTES, "the row state and barriers fit their region");
+  static_assert(TAIL + 8 + 8 * NBARS <= G::MISC_BYTES, "the row state and barriers fit their region");
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBARS; ++i) mbar_init(bar_at(i), i < ONES ? 1 : i < ONES + 3 ? 8 : 4);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -319,6 +329,19 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           for (int i = 0; i < W; ++i) w[i] = next[i];
           load_scales(j + 1, p.k.aux, next);
         }
+        int halved = 0;
+        if constexpr (KF == QPS_FMT_Q8_0) {
+          uint32_t most = 0u;  // (magnitudes of fp16 compare as integers)
+#pragma unroll
+          for (int i = 0; i < W; ++i) most = __vmaxu2(most, w[i] & 0x7fff7fffu);
+          halved = max(0, (int)(max(most >> 16, most & 0xffffu) >> 10) - 22);  // 2^8: exponent field 23
+          if (halved > 0) {
+            const __half2 f2 = __half2half2(__ushort_as_half((unsigned short)((15 - halved) << 10)));
+#pragma unroll
+            for (int i = 0; i < W; ++i) w[i] = mma::hmul2_u(w[i], f2);
+          }
+          if constexpr (G::EXPS == 4) kexp[(j & 3) * kTile + tok] = (uint8_t)halved;
+        }
 #pragma unroll 1
         for (int c = 0; c < G::KC; ++c, ++f) {
           const int rs = f % KN, s = f & 1;
@@ -335,6 +358,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
             if (lane == 0) arrive(kraw_empty(rs));
             if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
             fence_after();
+            if (G::EXPS == 2 && c == 2) kexp[(j & 1) * kTile + tok] = (uint8_t)halved;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {  // a block of 32
               const __half2 sc = scale_of(w[0], b);
@@ -511,8 +535,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         n = min(n, t1);
       }
       lim[tid] = n;
-      thr[tid] = -INFINITY;
-      mneg[tid] = 0.f;
+      mneg[tid] = kNone;
     }
     auto meet = [&]() { asm volatile("barrier.cta.sync 2, 256;" ::: "memory"); };
     meet();
@@ -572,6 +595,12 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       const float slack = is_tq(VF) && fabsf(norm) > 255.f ? 8.f : 0.f;
       ok &= wait(s_full(j & 1), (j >> 1) & 1);
       fence_after();
+      float qt = qs, st = p.scale;
+      if constexpr (KF == QPS_FMT_Q8_0) {
+        const float twice = __uint_as_float((127u + kexp[(j & (G::EXPS - 1)) * kTile + tl]) << 23);
+        qt *= twice;
+        st *= twice;
+      }
       // the logits, in units of log2, of 16 rows at this thread's position (read again for
       // each use: kept beside the sums they would not fit the registers)
       const uint32_t s_at = tmem + lanes + (j & 1) * n16 + r0;
@@ -584,10 +613,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
         if (cap > 0.f) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = mma::softcap_tanh(x[i] * p.scale, cap, cap_k) * LOG2E;
+          for (int i = 0; i < 16; ++i) x[i] = mma::softcap_tanh(x[i] * st, cap, cap_k) * LOG2E;
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] *= qs;
+          for (int i = 0; i < 16; ++i) x[i] *= qt;
         }
         if (cut) {
 #pragma unroll
@@ -603,13 +632,13 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         float d[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 th = *reinterpret_cast<const float4*>(thr + r0 + 16 * c + i);
-          d[0] = fmaxf(d[0], x[i] - th.x);  // (+inf without a reference, NaN for -inf - -inf: no maximum)
-          d[1] = fmaxf(d[1], x[i + 1] - th.y);
-          d[2] = fmaxf(d[2], x[i + 2] - th.z);
-          d[3] = fmaxf(d[3], x[i + 3] - th.w);
+          const float4 mn = *reinterpret_cast<const float4*>(mneg + r0 + 16 * c + i);
+          d[0] = fmaxf(d[0], x[i] + mn.x);  // (a NaN is no maximum)
+          d[1] = fmaxf(d[1], x[i + 1] + mn.y);
+          d[2] = fmaxf(d[2], x[i + 2] + mn.z);
+          d[3] = fmaxf(d[3], x[i + 3] + mn.w);
         }
-        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) + slack > 0.f;
+        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > 8.f - slack;
       }
       int any;
       asm volatile(
@@ -634,10 +663,9 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           float top = fred[tid];
 #pragma unroll
           for (int w = 1; w < 4; ++w) top = fmaxf(top, fred[w * kN + tid]);
-          const float old = thr[tid] - 8.f;
-          if (top > old) {
-            cr = old == -INFINITY ? 0.f : ex2(old - top);
-            thr[tid] = top + 8.f;
+          const float old = mneg[tid];
+          if (top > -old) {
+            cr = old == kNone ? 0.f : ex2(-old - top);
             mneg[tid] = -top;
           }
         }

@@ -76,3 +76,40 @@ def test_prefix_behind_a_padding_row(qps, d, kf, vf, batch, group):  # noqa: F81
             o, lse = _run(qps, q, cache, t, lens, scale=d ** -0.5, shared_len=common, out_dtype=torch.float32)
             assert_parity(o, lse, ro, rl, (d, kf, vf, batch, group, first, behind))
             qps.device_status(reset=True)
+
+
+# (n_q, group) on both sides of the rows at which the kernel changes
+SIDES = [(128, "q8_0", "f16", 6, 4), (128, "q8_0", "f16", 5, 5), (128, "q8_0", "tq3", 5, 5), (256, "q8_0", "tq3", 2, 4),
+         (256, "q8_0", "f16", 3, 3), (512, "q8_0", "q8_0", 2, 4), (512, "q8_0", "q8_0", 3, 3), (512, "q8_0", "tq2", 13, 4)]
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", SIDES)
+@pytest.mark.parametrize("softcap", [0.0, 25.0])
+def test_q8_keys_at_the_end_of_the_range(qps, d, kf, vf, n_q, group, softcap):  # noqa: F811
+    """q8_0 keys that hold fp16's largest value (the encoder stores scale 516, code 127:
+    65532), scales up to fp16's largest and down to its smallest, in rows beside ordinary
+    ones, against queries small enough for ordinary logits."""
+    hkv, page, n = 2, 64, 700
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, [n], page, hkv, d, 7 * d, rot)
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn((n, hkv, d), generator=g)
+    x[5::9, :, ::37] = 65504.0
+    x[6::9, 0, 3::41] = -65504.0
+    x[7::9] *= 2.0 ** -14
+    slots = torch.tensor([int(table[0, t // page]) * page + t % page for t in range(n)]).cuda()
+    v = torch.randn((n, hkv, d), generator=g).half().cuda()
+    qps.kv_append_paged(qps.paged_append_args(cache, x.half().cuda(), v, slots))
+    at = [(int(table[0, t // page]), t % page) for t in range(n)]
+    assert float(cache.k_planes[1][at[5][0], 0, at[5][1]].max()) == 516
+    for t in range(8, n, 9):  # scales that no encoder of fp16 rows makes, of the largest value's kind
+        cache.k_planes[1][at[t][0], :, at[t][1], ::2] = 65504.0 if t % 2 else 2.0 ** -24
+    q = torch.randn((1, n_q, hkv * group, d), generator=g)
+    q = (q * 2.0 ** -17).half().cuda()  # (subnormal: multiples of 2^-24)
+    scale = 40.0 / d ** 0.5
+    ro, rl = _want(cache, q, table, [n], scale, softcap, True, ora)
+    o, lse = _run(qps, q, cache, table, [n], scale=scale, softcap=softcap, causal=True, out_dtype=torch.float32)
+    # float32 logits of size up to |rl|: 2^-24 a step, D terms of a product
+    size = float(np.abs(rl).max())
+    assert np.isfinite(o).all() and (np.abs(lse - rl) <= d * 2.0 ** -24 * size + 1e-5).all()
+    assert_parity(o, np.zeros(rl.shape), ro, np.zeros(rl.shape), (d, kf, vf, n_q, group))
