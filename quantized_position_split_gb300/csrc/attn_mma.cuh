@@ -114,6 +114,13 @@ __device__ __forceinline__ uint32_t hmul2_u(uint32_t a, __half2 s) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// A q8_0 value is rounded to fp16: its scale is cut to 515.5, so that 127 x scale stays finite
+// there.  Blocks that hold fp16's largest values are stored with scale 516 (127 x 516 = 65532
+// rounds to infinity, and infinity x a weight of 0 is NaN): they come out 2^-10 smaller.
+__device__ __forceinline__ __half2 cut_v_scale(__half2 s) {
+  return __hmin2_nan(s, __half2half2(__ushort_as_half(0x6007)));  // 515.5
+}
+
 // Logit softcap c * tanh(x / c) through tanh(y) = 1 - 2 / (1 + e^(2y)), with the
 // hardware base-2 exponential and reciprocal; k = 2 log2(e) / c.  Its absolute error
 // is a few 1e-7 x c (the 1 - 2r cancellation near 0), and it saturates to +-c.
@@ -1225,7 +1232,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
           }
           __half2 sc[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) sc[u] = __half2half2(vs[tok[u] * (D / 32) + blk]);
+          for (int u = 0; u < 4; ++u) {
+            sc[u] = __half2half2(vs[tok[u] * (D / 32) + blk]);
+            if constexpr (PAGED) sc[u] = cut_v_scale(sc[u]);
+          }
 #pragma unroll
           for (int wi = 0; wi < CH / 4; ++wi) {
             uint32_t hv[4][2];

@@ -426,7 +426,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       for (int j = 0; j < ntiles && ok; ++j) {
         if constexpr (VF == QPS_FMT_Q8_0) {
 #pragma unroll
-          for (int i = 0; i < W; ++i) w[i] = next[i];
+          for (int i = 0; i < W; ++i) {
+            const __half2 x = mma::cut_v_scale(*reinterpret_cast<const __half2*>(&next[i]));
+            w[i] = *reinterpret_cast<const uint32_t*>(&x);
+          }
           load_scales(j + 1, p.v.aux, next);
         }
 #pragma unroll 1

@@ -113,3 +113,28 @@ def test_q8_keys_at_the_end_of_the_range(qps, d, kf, vf, n_q, group, softcap):  
     size = float(np.abs(rl).max())
     assert np.isfinite(o).all() and (np.abs(lse - rl) <= d * 2.0 ** -24 * size + 1e-5).all()
     assert_parity(o, np.zeros(rl.shape), ro, np.zeros(rl.shape), (d, kf, vf, n_q, group))
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(64, "f16", "q8_0", 1, 4), (128, "q8_0", "q8_0", 1, 1), (128, "q8_0", "q8_0", 7, 4),
+                                               (256, "f16", "q8_0", 1, 4), (256, "q8_0", "q8_0", 5, 4), (512, "q8_0", "q8_0", 1, 8),
+                                               (512, "f16", "q8_0", 5, 4)])
+def test_q8_values_at_the_end_of_the_range(qps, d, kf, vf, n_q, group):  # noqa: F811
+    """q8_0 values that hold fp16's largest value (65532 as stored): finite weights of them
+    are finite, and a weight of zero leaves nothing of them."""
+    hkv, page, n = 2, 64, 500
+    cache, table = _cache_of(qps, kf, vf, [n], page, hkv, d, 9 * d)
+    g = torch.Generator().manual_seed(d)
+    k = torch.randn((n, hkv, d), generator=g)
+    x = torch.randn((n, hkv, d), generator=g) * 20000
+    x[3::5, :, ::7] = 65504.0
+    x[4::5, :, 1::9] = -65504.0
+    k[8::10] *= 40  # (a few keys far above and below the others: weights that underflow)
+    slots = torch.tensor([int(table[0, t // page]) * page + t % page for t in range(n)]).cuda()
+    qps.kv_append_paged(qps.paged_append_args(cache, k.half().cuda(), x.clamp(-65504, 65504).half().cuda(), slots))
+    q = torch.randn((1, n_q, hkv * group, d), generator=g).half().cuda()
+    ro, rl = _want(cache, q, table, [n], d ** -0.5, 0.0, False)
+    o, lse = _run(qps, q, cache, table, [n], scale=d ** -0.5, out_dtype=torch.float32)
+    # a value is off by at most 2^-10 (its block's scale cut to 515.5 of 516) + 2^-11 (its
+    # rounding), both relative to the largest value, 65532; P keeps its second part
+    assert (np.abs(o - ro) <= (2.0 ** -10 + 2.0 ** -11 + 2.0 ** -17) * 65532).all()
+    assert (np.abs(lse - rl) <= 1e-4 + 2.0 ** -20 * np.abs(rl)).all()
