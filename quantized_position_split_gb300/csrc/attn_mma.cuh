@@ -121,6 +121,13 @@ __device__ __forceinline__ __half2 cut_v_scale(__half2 s) {
   return __hmin2_nan(s, __half2half2(__ushort_as_half(0x6007)));  // 515.5
 }
 
+// log2 of a stored norm's size, within what fp16 holds (0: -24; a NaN or infinity: a bound).
+__device__ __forceinline__ float norm_log2(float n) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fabsf(n)));
+  return fminf(fmaxf(r, -24.f), 16.f);
+}
+
 // Logit softcap c * tanh(x / c) through tanh(y) = 1 - 2 / (1 + e^(2y)), with the
 // hardware base-2 exponential and reciprocal; k = 2 log2(e) / c.  Its absolute error
 // is a few 1e-7 x c (the 1 - 2r cancellation near 0), and it saturates to +-c.
@@ -1093,8 +1100,22 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     // finite in fp16), else 0 (P <= 1, the exact maximum).  Three n-tiles keep the exact
     // maximum: there the test's registers made the kernel spill (4-token verify batch
     // 64.5 -> 66.8 us).
+    // Paged: what the reference bounds is P x norm, the operand (logit + log2 of the norm in
+    // the place of the logit).  Norms of any size then use fp16's range alike: with P alone
+    // bounded, a long flat softmax over norms of 2^-12 had its operands below 2^-14, where
+    // fp16 loses bits (O off by up to 8e-2).  The sums of P stay float32: a norm is at least
+    // 2^-24, so P <= 2^32.
+    constexpr bool LIFT = PAGED && is_tq(VF);
+    float lift[LIFT ? SUB : 1][2];
+    if constexpr (LIFT) {
+#pragma unroll
+      for (int sb = 0; sb < SUB; ++sb) {
+        lift[sb][0] = norm_log2(n_g[sb]);
+        lift[sb][1] = norm_log2(n_g8[sb]);
+      }
+    }
     float lazy = NTW >= 3 ? 0.f : 8.f;
-    if constexpr (is_tq(VF) && NTW < 3) {
+    if constexpr (is_tq(VF) && NTW < 3 && !PAGED) {
       float nmx = 0.f;
 #pragma unroll
       for (int sb = 0; sb < SUB; ++sb) nmx = fmaxf(nmx, fmaxf(fabsf(n_g[sb]), fabsf(n_g8[sb])));
@@ -1141,8 +1162,13 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
           if (r8 > r0) x[sb][2] = -INFINITY;
           if (r8 > r0 + 1) x[sb][3] = -INFINITY;
         }
-        mx0 = fmaxf(mx0, fmaxf(x[sb][0], x[sb][2]));
-        mx1 = fmaxf(mx1, fmaxf(x[sb][1], x[sb][3]));
+        if constexpr (LIFT) {
+          mx0 = fmaxf(mx0, fmaxf(x[sb][0] + lift[sb][0], x[sb][2] + lift[sb][1]));
+          mx1 = fmaxf(mx1, fmaxf(x[sb][1] + lift[sb][0], x[sb][3] + lift[sb][1]));
+        } else {
+          mx0 = fmaxf(mx0, fmaxf(x[sb][0], x[sb][2]));
+          mx1 = fmaxf(mx1, fmaxf(x[sb][1], x[sb][3]));
+        }
       }
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) {

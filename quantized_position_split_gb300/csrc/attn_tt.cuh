@@ -21,11 +21,12 @@
 // position's scales reach 2^8 they are halved until its products fit fp16, and its logits
 // doubled back: a key of fp16's largest value is stored as 127 x 516 = 65532); a TurboQuant V
 // is its exact fp16 levels in the rotated domain with the norm folded into P before P's one
-// rounding, the output being rotated back once; a q8_0 V is rounded once to fp16; sums,
+// rounding (and into the reference that P x norm is held against), the output being rotated
+// back once; a q8_0 V is rounded once to fp16; sums,
 // maxima and O are float32.
 //
 // A row's maximum over the positions would cross all threads, so the running reference m
-// (in shared memory) is raised only when some position exceeds it by more than 8 (log2):
+// (in shared memory) is raised only when some operand would exceed it by more than 8 (log2):
 // one vote a tile, and on a raise the maxima are taken, O and the sums rescaled.
 //
 // Measured: four sequences of five tokens and 30000 to 32768 positions, two KV heads of 512,
@@ -594,8 +595,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
                                                                       (at & ((1 << p.page_shift) - 1))]);
         }
       }
-      // P x norm stays finite in fp16: the slack above the reference shrinks with a large norm
-      const float slack = is_tq(VF) && fabsf(norm) > 255.f ? 8.f : 0.f;
+      // (a TurboQuant V: the reference bounds P x norm, the operand; see attn_mma.cuh)
+      const float lift = is_tq(VF) ? mma::norm_log2(norm) : 0.f;
       ok &= wait(s_full(j & 1), (j >> 1) & 1);
       fence_after();
       float qt = qs, st = p.scale;
@@ -641,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           d[2] = fmaxf(d[2], x[i + 2] + mn.z);
           d[3] = fmaxf(d[3], x[i + 3] + mn.w);
         }
-        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > 8.f - slack;
+        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) + lift > 8.f;
       }
       int any;
       asm volatile(
@@ -657,6 +658,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           if (c >= nch) break;
           float y[16];
           logits(c, y);
+          if constexpr (is_tq(VF)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] += lift;
+          }
           const float top = over_lanes(y, [](float a, float b) { return fmaxf(a, b); });
           if (!(lane & 1)) fred[(warp & 3) * kN + r0 + 16 * c + (lane >> 1)] = top;
         }

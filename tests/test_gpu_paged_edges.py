@@ -138,3 +138,29 @@ def test_q8_values_at_the_end_of_the_range(qps, d, kf, vf, n_q, group):  # noqa:
     # rounding), both relative to the largest value, 65532; P keeps its second part
     assert (np.abs(o - ro) <= (2.0 ** -10 + 2.0 ** -11 + 2.0 ** -17) * 65532).all()
     assert (np.abs(lse - rl) <= 1e-4 + 2.0 ** -20 * np.abs(rl)).all()
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(64, "tq2", "tq2", 1, 4), (128, "q8_0", "tq3", 1, 4), (128, "f16", "tq4", 3, 4),
+                                               (128, "q8_0", "tq3", 9, 4), (256, "f16", "tq2", 4, 4), (512, "q8_0", "tq3", 1, 8),
+                                               (512, "q8_0", "tq3", 5, 4)])
+@pytest.mark.parametrize("size", [2.0 ** -16, 1.0, 2.0 ** 9])
+def test_turboquant_values_of_any_size(qps, d, kf, vf, n_q, group, size):  # noqa: F811
+    """TurboQuant values far below and far above one, and both in one sequence, keep the
+    accuracy of ordinary ones: P times a small norm does not fall below fp16's normal range."""
+    hkv, page, n = 2, 64, 3001
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, [n, 64], page, hkv, d, 9 * d, rot)
+    g = torch.Generator().manual_seed(d)
+    k, v = (torch.randn((n, hkv, d), generator=g) for _ in range(2))
+    v *= size
+    v[100] = 0  # a zero row, and the largest key with it: the reference is not its alone
+    k[100] *= 3
+    slots = torch.tensor([int(table[0, t // page]) * page + t % page for t in range(n)]).cuda()
+    qps.kv_append_paged(qps.paged_append_args(cache, k.half().cuda(), v.half().cuda(), slots))
+    q = (torch.randn((2, n_q, hkv * group, d), generator=g) * 1.5).half().cuda()
+    if size == 1.0:  # large norms late in the sequence
+        _value_plane(cache)[int(table[0, 40])] = 900.0
+        _value_plane(cache)[int(table[0, 3])] = 2.0 ** -12
+    ro, rl = _want(cache, q, table, [n, 0], d ** -0.5, 0.0, False, ora)
+    o, lse = _run(qps, q, cache, table, [n, 0], scale=d ** -0.5, out_dtype=torch.float32)
+    assert_parity(o / max(size, 1.0), lse, ro / max(size, 1.0), rl, (d, kf, vf, n_q, group, size))
