@@ -1104,7 +1104,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     // the place of the logit).  Norms of any size then use fp16's range alike: with P alone
     // bounded, a long flat softmax over norms of 2^-12 had its operands below 2^-14, where
     // fp16 loses bits (O off by up to 8e-2).  The sums of P stay float32: a norm is at least
-    // 2^-24, so P <= 2^32.
+    // 2^-24, so P <= 2^39.
     constexpr bool LIFT = PAGED && is_tq(VF);
     float lift[LIFT ? SUB : 1][2];
     if constexpr (LIFT) {
@@ -1114,7 +1114,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         lift[sb][1] = norm_log2(n_g8[sb]);
       }
     }
-    float lazy = NTW >= 3 ? 0.f : 8.f;
+    float lazy = NTW >= 3 ? 0.f : PAGED ? kRefLazy : 8.f;
     if constexpr (is_tq(VF) && NTW < 3 && !PAGED) {
       float nmx = 0.f;
 #pragma unroll
@@ -1174,6 +1174,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       for (int off = 4; off < 32; off <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+      }
+      if constexpr (PAGED) {
+        mx0 -= kRefShift;
+        mx1 -= kRefShift;
       }
       float mn0, mn1;
       if constexpr (NTW >= 3) {

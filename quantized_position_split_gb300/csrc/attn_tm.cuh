@@ -11,9 +11,10 @@
 // 128 + 128 + 2 D <= 512 columns), so that one stream's exponentials run beside the other's
 // products; the two states are merged once at the end, as two parts would be.
 //
-// The running reference m of a row is raised only when a tile's maximum exceeds it by more
-// than 8 (log2): P stays <= 2^8 in fp16 and the rescale of O is rare.  P is rounded once to
-// fp16 (the operand type); sums, m and O are float32.
+// The running reference m of a row is set kRefShift (log2) below a tile's maximum, and again
+// only when one exceeds what it was set for by more than kRefLazy: P stays within fp16 and
+// the rescale of O is rare.  P is rounded once to fp16 (the operand type); sums, m and O are
+// float32.
 //
 // Measured: 256 rows per KV head, 8 heads of 128, 32768 shared positions: 40 us, of which
 // the first three tiles take 9 (every CTA's first tiles at once, and the queries behind
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      const bool raise = mx - m > 8.f;  // (false when both are -inf)
+      mx -= kRefShift;
+      const bool raise = mx - m > kRefLazy;  // (false when both are -inf)
       const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
       if (raise) {
         m = mx;

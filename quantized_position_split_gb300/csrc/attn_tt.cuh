@@ -26,7 +26,7 @@
 // maxima and O are float32.
 //
 // A row's maximum over the positions would cross all threads, so the running reference m
-// (in shared memory) is raised only when some operand would exceed it by more than 8 (log2):
+// (in shared memory) is raised only when some operand would leave the room above it (paged.h):
 // one vote a tile, and on a raise the maxima are taken, O and the sums rescaled.
 //
 // Measured: four sequences of five tokens and 30000 to 32768 positions, two KV heads of 512,
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         }
       }
       // (a TurboQuant V: the reference bounds P x norm, the operand; see attn_mma.cuh)
-      const float lift = is_tq(VF) ? mma::norm_log2(norm) : 0.f;
+      const float lift = is_tq(VF) ? mma::norm_log2(norm) : 0.f, room = kRefShift + kRefLazy - lift;
       ok &= wait(s_full(j & 1), (j >> 1) & 1);
       fence_after();
       float qt = qs, st = p.scale;
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           d[2] = fmaxf(d[2], x[i + 2] + mn.z);
           d[3] = fmaxf(d[3], x[i + 3] + mn.w);
         }
-        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) + lift > 8.f;
+        over |= fmaxf(fmaxf(d[0], d[1]), fmaxf(d[2], d[3])) > room;
       }
       int any;
       asm volatile(
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           : "r"((int)over)
           : "memory");
       if (any) {
-        // raise every reference to its row's maximum so far (fmaxf drops a NaN); O and the
+        // raise every reference for its row's maximum so far (fmaxf drops a NaN); O and the
         // sums follow
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -671,6 +671,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           float top = fred[tid];
 #pragma unroll
           for (int w = 1; w < 4; ++w) top = fmaxf(top, fred[w * kN + tid]);
+          top -= kRefShift;
           const float old = mneg[tid];
           if (top > -old) {
             cr = old == kNone ? 0.f : ex2(-old - top);

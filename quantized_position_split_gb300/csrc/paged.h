@@ -157,6 +157,13 @@ qps_status launch_paged_tt_d128(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tt_d256(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tt_d512(const PagedAttnParams& p, cudaStream_t s);
 
+// The softmax's reference is kept below the maximum, so that the largest operand of P V is
+// 2^kRefShift, 2^(kRefShift + kRefLazy) at most before the reference is raised: fp16 holds
+// that, and weights down to 2^-(14 + kRefShift) of the largest keep all their bits.  With the
+// reference at the maximum, a key whose logit is 16 above the others (e^-16 = 2^-23) and whose
+// value is near zero, as a first position's may be, left an output off by 3e-2 of its size.
+constexpr float kRefShift = 11.f, kRefLazy = 4.f;
+
 // The kernels of a paged launch: attn_mma.cuh's, attn_tm.cuh's, attn_tt.cuh's.
 enum PagedKernel { kMma, kTm, kTt };
 

@@ -164,3 +164,27 @@ def test_turboquant_values_of_any_size(qps, d, kf, vf, n_q, group, size):  # noq
     ro, rl = _want(cache, q, table, [n, 0], d ** -0.5, 0.0, False, ora)
     o, lse = _run(qps, q, cache, table, [n, 0], scale=d ** -0.5, out_dtype=torch.float32)
     assert_parity(o / max(size, 1.0), lse, ro / max(size, 1.0), rl, (d, kf, vf, n_q, group, size))
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(128, "f16", "f16", 1, 4), (512, "q8_0", "q8_0", 1, 8), (128, "q8_0", "tq3", 5, 4),
+                                               (64, "f16", "f16", 5, 4), (128, "f16", "f16", 9, 4), (128, "q8_0", "tq3", 9, 4),
+                                               (256, "f16", "f16", 5, 4), (512, "f16", "q8_0", 5, 4)])
+@pytest.mark.parametrize("above", [9.0, 12.0, 16.0])
+def test_one_key_above_all_others(qps, d, kf, vf, n_q, group, above):  # noqa: F811
+    """A first position whose logit is far above all others and whose value is zero: the output
+    is what the others' small weights make of their values."""
+    hkv, page, n = 2, 64, 4001
+    rot, ora = _rotations(d, "whole")
+    cache, table = _cache_of(qps, kf, vf, [n], page, hkv, d, d, rot)
+    g = torch.Generator().manual_seed(d)
+    k, v = torch.randn((n, hkv, d), generator=g) * 0.3, 1 + torch.randn((n, hkv, d), generator=g)
+    q = 1 + 0.1 * torch.randn((1, n_q, hkv * group, d), generator=g)
+    k -= k.mean(-1, keepdim=True)
+    k[0] = (above + 1.0) / d ** 0.5
+    v[0] = 0
+    slots = torch.tensor([int(table[0, t // page]) * page + t % page for t in range(n)]).cuda()
+    qps.kv_append_paged(qps.paged_append_args(cache, k.half().cuda(), v.half().cuda(), slots))
+    q = q.half().cuda()
+    ro, rl = _want(cache, q, table, [n], d ** -0.5, 0.0, False, ora)
+    o, lse = _run(qps, q, cache, table, [n], scale=d ** -0.5, out_dtype=torch.float32)
+    assert_parity(o, lse, ro, rl, (d, kf, vf, n_q, group, above))
