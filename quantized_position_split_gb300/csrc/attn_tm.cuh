@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     t0 = split * (int)p.chunk;
     const PagedPrefix pre = paged_prefix(p, lane);
     bz = pre.b;
-    t1 = min(pre.len, t0 + (int)p.chunk);  // (at or before t0: an empty part)
+    t1 = (int)min((int64_t)pre.len, t0 + p.chunk);  // (at or before t0: an empty part)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)

@@ -188,3 +188,20 @@ def test_one_key_above_all_others(qps, d, kf, vf, n_q, group, above):  # noqa: F
     ro, rl = _want(cache, q, table, [n], d ** -0.5, 0.0, False, ora)
     o, lse = _run(qps, q, cache, table, [n], scale=d ** -0.5, out_dtype=torch.float32)
     assert_parity(o, lse, ro, rl, (d, kf, vf, n_q, group, above))
+
+
+def test_prefix_of_nearly_all_positions(qps):  # noqa: F811
+    """A shared prefix close to 2^31 positions (its table names few pages over and over): the
+    last chunk's end stays in range."""
+    d, hkv, page, batch, group = 64, 1, 1024, 3, 8
+    width = (1 << 21) - 2
+    n = width * page
+    cache = qps.PagedKV.empty("f16", "f16", 2, page, hkv, d)
+    cache.v_planes[0][1] = 1.0
+    table = torch.zeros((1, width), dtype=torch.int32)
+    table[0, -(width // 8):] = 1
+    q = torch.zeros((batch, group, d), dtype=torch.float16).cuda()
+    o, lse = _run(qps, q, cache, table.expand(batch, width).contiguous(), [n] * batch, scale=1.0,
+                  shared_len=(width - 1) * page, out_dtype=torch.float32)
+    assert np.abs(lse - np.log(float(n))).max() <= 1e-4
+    assert np.abs(o - (width // 8) / width).max() <= 1e-4
