@@ -99,12 +99,18 @@ unsigned int* device_error_word() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   std::lock_guard<std::mutex> lk(mu);
   if (!words[dev]) {
-    // (relaxed: the first call on a device may come while a stream is being captured)
+    // (relaxed, and on a stream of its own: the first call on a device may come while a stream
+    // is being captured, and where that one synchronises with the legacy default stream, work
+    // on the latter would end the capture)
     unsigned int* w = nullptr;
+    cudaStream_t own = nullptr;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
-    const bool ok = cudaMalloc(&w, kErrWords * sizeof(unsigned int)) == cudaSuccess &&
-                    cudaMemset(w, 0, kErrWords * sizeof(unsigned int)) == cudaSuccess;
+    const bool ok = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
+                    cudaMalloc(&w, kErrWords * sizeof(unsigned int)) == cudaSuccess &&
+                    cudaMemsetAsync(w, 0, kErrWords * sizeof(unsigned int), own) == cudaSuccess &&
+                    cudaStreamSynchronize(own) == cudaSuccess;
+    if (own) cudaStreamDestroy(own);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (!ok) return nullptr;
     words[dev] = w;

@@ -190,6 +190,37 @@ def test_one_key_above_all_others(qps, d, kf, vf, n_q, group, above):  # noqa: F
     assert_parity(o, lse, ro, rl, (d, kf, vf, n_q, group, above))
 
 
+def _child(code):
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert res.returncode == 0 and "child ok" in res.stdout, (res.stdout + res.stderr)[-3000:]
+
+
+def test_first_call_captured_on_a_blocking_stream(qps):  # noqa: F811
+    """The first call of a process may be captured, also on a stream that synchronises with
+    the legacy default stream."""
+    _child("""
+import ctypes, torch
+import quantized_position_split_gb300 as qps
+rt = ctypes.CDLL("libcudart.so.13")
+x = torch.randn(4, 2, 128, device="cuda").half()
+a = qps.qk_rope_args(x, norm=True)
+torch.cuda.synchronize()
+s = ctypes.c_void_p()
+assert rt.cudaStreamCreate(ctypes.byref(s)) == 0  # (a blocking stream)
+g, e = ctypes.c_void_p(), ctypes.c_void_p()
+assert rt.cudaStreamBeginCapture(s, 0) == 0  # global mode
+qps.qk_norm_rope(a, stream=s.value)
+assert rt.cudaStreamEndCapture(s, ctypes.byref(g)) == 0
+assert rt.cudaGraphInstantiate(ctypes.byref(e), g, ctypes.c_ulonglong(0)) == 0
+assert rt.cudaGraphLaunch(e, s) == 0 and rt.cudaStreamSynchronize(s) == 0
+o = a._out[0].float()
+w = x.float() / (x.float().square().mean(-1, keepdim=True) + 1e-6).sqrt()
+assert (o - w).abs().max() < 4e-3, (o - w).abs().max()
+qps.device_status(reset=True)
+print("child ok")
+""")
+
+
 def test_prefix_of_nearly_all_positions(qps):  # noqa: F811
     """A shared prefix close to 2^31 positions (its table names few pages over and over): the
     last chunk's end stays in range."""
