@@ -92,30 +92,56 @@ bool encode_plane_map(TensorMap* map, const void* base, int row_bytes, int64_t t
   return true;
 }
 
+namespace {
+// A number of the current context, unlike its handle never given twice (0: none).
+unsigned long long context_id() {
+  using GetIdFn = CUresult (*)(CUcontext, unsigned long long*);
+  static GetIdFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<GetIdFn>(p);
+  }();
+  unsigned long long id = 0;
+  if (!fn) return 0;
+  if (fn(nullptr, &id) == CUDA_SUCCESS) return id;
+  // (no context is current before the runtime's first call)
+  return cudaFree(nullptr) == cudaSuccess && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
+}
+}  // namespace
+
+// One word for each context: memory of one is not to be reached from another, and kernels
+// write theirs when an index is out of range.
 unsigned int* device_error_word() {
   static std::mutex mu;
-  static unsigned int* words[64] = {nullptr};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  constexpr int kContexts = 64;  // (more of them: the oldest one's word is forgotten)
+  static struct { unsigned long long id; unsigned int* word; } words[kContexts] = {};
+  static int next = 0;
+  const unsigned long long id = context_id();
+  if (!id) return nullptr;
   std::lock_guard<std::mutex> lk(mu);
-  if (!words[dev]) {
-    // (relaxed, and on a stream of its own: the first call on a device may come while a stream
-    // is being captured, and where that one synchronises with the legacy default stream, work
-    // on the latter would end the capture)
-    unsigned int* w = nullptr;
-    cudaStream_t own = nullptr;
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
-    const bool ok = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
-                    cudaMalloc(&w, kErrWords * sizeof(unsigned int)) == cudaSuccess &&
-                    cudaMemsetAsync(w, 0, kErrWords * sizeof(unsigned int), own) == cudaSuccess &&
-                    cudaStreamSynchronize(own) == cudaSuccess;
-    if (own) cudaStreamDestroy(own);
-    cudaThreadExchangeStreamCaptureMode(&mode);
-    if (!ok) return nullptr;
-    words[dev] = w;
-  }
-  return words[dev];
+  for (const auto& w : words)
+    if (w.id == id) return w.word;
+  // (relaxed, and on a stream of its own: the first call on a device may come while a stream
+  // is being captured, and where that one synchronises with the legacy default stream, work
+  // on the latter would end the capture)
+  unsigned int* w = nullptr;
+  cudaStream_t own = nullptr;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+  const bool ok = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking) == cudaSuccess &&
+                  cudaMalloc(&w, kErrWords * sizeof(unsigned int)) == cudaSuccess &&
+                  cudaMemsetAsync(w, 0, kErrWords * sizeof(unsigned int), own) == cudaSuccess &&
+                  cudaStreamSynchronize(own) == cudaSuccess;
+  if (own) cudaStreamDestroy(own);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (!ok) return nullptr;
+  words[next].id = id;
+  words[next].word = w;
+  next = (next + 1) % kContexts;
+  return w;
 }
 
 // ---- TurboQuant codebooks -----------------------------------------------------------

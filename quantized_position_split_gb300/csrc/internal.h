@@ -35,7 +35,7 @@ bool encode_plane_map(TensorMap* map, const void* base, int row_bytes, int64_t t
 
 // ---- device facts -----------------------------------------------------------------
 int sm_count_current();
-// The current device's error word (library-owned, allocated on first use, zeroed).
+// The current context's error word (library-owned, allocated on first use, zeroed).
 // Bits: kErrTimeout, a bounded in-kernel wait gave up; kErrBounds, a bounds check of the
 // checked build failed and its access was skipped; kErrIndex, a position, slot, page or
 // length that a kernel read was out of range and was not followed.

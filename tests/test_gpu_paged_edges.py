@@ -221,6 +221,63 @@ print("child ok")
 """)
 
 
+def test_attention_in_a_second_context(qps):  # noqa: F811
+    """A second context of a device that has run the same kernels: they are set up there too, and
+    what they report goes to a word of that context."""
+    _child("""
+import ctypes, torch
+import quantized_position_split_gb300 as qps
+from quantized_position_split_gb300 import _native as N
+d, hkv, page = 128, 2, 64
+cache = qps.PagedKV.empty("f16", "f16", 8, page, hkv, d)
+q = torch.ones(2, 8, d, device="cuda").half()
+table = torch.arange(8, device="cuda", dtype=torch.int32).view(2, 4)
+lens = torch.tensor([200, 90], device="cuda", dtype=torch.int32)
+many = torch.ones(2, 9, 8, d, device="cuda").half()
+blocks = [qps.paged_attn_args(q, cache, table, lens, scale=0.1), qps.paged_attn_args(many, cache, table, lens, scale=0.1)]
+for a in blocks:
+    qps.attn_decode_paged(a)
+torch.cuda.synchronize()
+cu = ctypes.CDLL("libcuda.so.1")
+dev, ctx = ctypes.c_int(), ctypes.c_void_p()
+assert cu.cuDeviceGet(ctypes.byref(dev), 0) == 0
+assert cu.cuCtxCreate_v2(ctypes.byref(ctx), 0, dev) == 0  # (current in this thread)
+def put(n, value=None):
+    p = ctypes.c_uint64()
+    assert cu.cuMemAlloc_v2(ctypes.byref(p), ctypes.c_size_t(n)) == 0
+    if value is None:
+        assert cu.cuMemsetD8_v2(p, 0, ctypes.c_size_t(n)) == 0
+    else:
+        assert cu.cuMemcpyHtoD_v2(p, value, ctypes.c_size_t(n)) == 0
+    return p.value
+import numpy as np
+for a in blocks:
+    b = N.PagedAttnArgs()
+    ctypes.memmove(ctypes.byref(b), ctypes.byref(a), ctypes.sizeof(b))
+    rows = b.batch * b.n_q * b.hq
+    b.q = put(rows * d * 2, np.ones(rows * d, np.float16).ctypes.data_as(ctypes.c_void_p))
+    b.kv.k_data = put(8 * hkv * page * d * 2)
+    b.kv.v_data = put(8 * hkv * page * d * 2, np.ones(8 * hkv * page * d, np.float16).ctypes.data_as(ctypes.c_void_p))
+    b.page_table = put(32, np.arange(8, dtype=np.int32).ctypes.data_as(ctypes.c_void_p))
+    b.kv_lens = put(8, np.array([200, 90], np.int32).ctypes.data_as(ctypes.c_void_p))
+    b.o, b.lse, b.workspace = put(rows * d * 2), put(rows * 4), put(b.workspace_bytes)
+    N.check(N.load().qps_attn_decode_paged(ctypes.byref(b), None))
+    assert cu.cuCtxSynchronize() == 0
+    o = np.empty(rows * d, np.float16)
+    assert cu.cuMemcpyDtoH_v2(o.ctypes.data_as(ctypes.c_void_p), ctypes.c_uint64(b.o), ctypes.c_size_t(o.nbytes)) == 0
+    assert (o == 1).all()
+    b.page_table = put(32, np.full(8, 99, np.int32).ctypes.data_as(ctypes.c_void_p))
+    N.check(N.load().qps_attn_decode_paged(ctypes.byref(b), None))  # pages out of range: reported here
+    assert N.load().qps_device_status(1) == N.QPS_ERR_INVALID_ARG
+    assert N.load().qps_device_status(1) == N.QPS_OK
+assert cu.cuCtxPopCurrent_v2(ctypes.byref(ctx)) == 0
+torch.cuda.synchronize()
+qps.device_status()  # the first context's word is its own
+assert float(cache.k_planes[0].abs().max()) == 0
+print("child ok")
+""")
+
+
 def test_prefix_of_nearly_all_positions(qps):  # noqa: F811
     """A shared prefix close to 2^31 positions (its table names few pages over and over): the
     last chunk's end stays in range."""
