@@ -103,7 +103,7 @@ def _call(a, stream):
         stream = _raw_stream(a._index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    st = a._fn(a._ref, stream)
+    st = a._fn(ctypes.byref(a), stream)
     if st:
         N.check(st)
 
@@ -111,7 +111,6 @@ def _call(a, stream):
 def _block(a, fn, device, keep):
     a._fn = getattr(N.load(), fn)
     a._index = device.index
-    a._ref = ctypes.byref(a)
     a._tensors = keep
     return a
 
