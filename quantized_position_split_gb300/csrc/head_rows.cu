@@ -77,6 +77,18 @@ bool apart_in_projection(const qps_rows& a, const qps_rows& b, int d) {
   return off >= wa && off + wb <= t;
 }
 
+// Whether no row of the set touches another of it.
+bool apart_itself(const qps_rows& r, int64_t tokens, int d) {
+  const int64_t t = r.tok_stride, h = r.head_stride;
+  if (tokens < 2 || r.heads < 2 || t >= (r.heads - 1) * h + d || h >= (tokens - 1) * t + d) return true;
+  for (int64_t i = 1; i < r.heads; ++i) {  // rows i heads and n tokens apart
+    const int64_t x = i * h, n = std::min(tokens - 1, x / t);
+    for (int64_t m = n; m <= std::min(n + 1, tokens - 1); ++m)
+      if (x - m * t > -d && x - m * t < d) return false;
+  }
+  return true;
+}
+
 qps_status qk_norm_rope(const qps_qk_rope_args* a, cudaStream_t s) {
   const char* const n = "qk_norm_rope";
   if (!a) return bad(n, "", "args is NULL");
@@ -101,6 +113,7 @@ qps_status qk_norm_rope(const qps_qk_rope_args* a, cudaStream_t s) {
     out_dtype = sd.out->dtype;
     if (a->tokens > 1 && sd.out->tok_stride < a->d)
       return bad(n, sd.out_what, "tok_stride must be >= head_dim");
+    if (!apart_itself(*sd.out, a->tokens, a->d)) return bad(n, sd.out_what, "rows overlap one another");
   }
   qps_status st = check_norm(a->q_norm, n, " q_norm");
   if (st == QPS_OK) st = check_norm(a->k_norm, n, " k_norm");
