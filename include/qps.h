@@ -353,7 +353,8 @@ typedef struct qps_qk_rope_args {
   int32_t reserved0;   /* must be 0 */
   qps_rows q, k;             /* input rows; either may have heads == 0 */
   qps_rows q_out, k_out;     /* F16 or BF16 (heads as the input's); may be the input itself,
-                                element for element and of its type, else must not overlap it */
+                                element for element and of its type, else no row of it may
+                                overlap a row of an input, or another row of the outputs */
   qps_head_norm q_norm, k_norm;
   qps_rotation rot;
   const int64_t* positions;  /* device, [tokens]; unused without a rotation */

@@ -66,17 +66,30 @@ bool same_rows(const qps_rows& a, const qps_rows& b, int64_t tokens) {
   return a.data == b.data && a.dtype == b.dtype && (tokens < 2 || a.tok_stride == b.tok_stride) &&
          (a.heads < 2 || a.head_stride == b.head_stride);
 }
-// Whether two sets of rows interleave without touching (slices of one projection): the
-// same strides, and the offset between them keeps every row apart.
-bool apart_in_projection(const qps_rows& a, const qps_rows& b, int d) {
-  if (dtype_bytes(a.dtype) != dtype_bytes(b.dtype) || a.tok_stride != b.tok_stride || a.tok_stride <= 0) return false;
-  const int64_t sz = dtype_bytes(a.dtype), t = a.tok_stride * sz;
-  const int64_t wa = ((int64_t)(a.heads - 1) * a.head_stride + d) * sz, wb = ((int64_t)(b.heads - 1) * b.head_stride + d) * sz;
-  int64_t off = ((const char*)b.data - (const char*)a.data) % t;
-  if (off < 0) off += t;
-  return off >= wa && off + wb <= t;
+// Whether two sets of rows whose extents meet interleave without touching (slices of one
+// projection, side by side or head by head): the same distance of tokens, and no row of one
+// within a row's width of a row of the other.  More heads than this looks through count as
+// touching.
+bool apart(const qps_rows& a, const qps_rows& b, int64_t tokens, int d) {
+  const int64_t sa = dtype_bytes(a.dtype), sb = dtype_bytes(b.dtype), t = a.tok_stride * sa;
+  if (tokens > 1 && (t != b.tok_stride * sb || t <= 0)) return false;
+  const int64_t ha = a.head_stride * sa, hb = b.head_stride * sb, wa = d * sa, wb = d * sb;
+  const int64_t base = (const char*)b.data - (const char*)a.data;
+  if (tokens > 1) {  // whole tokens side by side
+    const int64_t off = (base % t + t) % t;
+    if (off >= (a.heads - 1) * ha + wa && off + (b.heads - 1) * hb + wb <= t) return true;
+  }
+  if ((int64_t)a.heads * b.heads > 1 << 16) return false;
+  for (int64_t i = 0; i < a.heads; ++i)
+    for (int64_t j = 0; j < b.heads; ++j) {
+      const int64_t x = base + j * hb - i * ha;  // of b's row (0, j) from a's (0, i)
+      // some token distance n, |n| < tokens, with -wb < x + n t < wa?
+      const int64_t n = tokens > 1 ? std::max(-(tokens - 1), std::min(tokens - 1, -(x / t))) : 0;
+      for (int64_t m = std::max(n - 1, -(tokens - 1)); m <= std::min(n + 1, tokens - 1); ++m)
+        if (x + m * t > -wb && x + m * t < wa) return false;
+    }
+  return true;
 }
-
 // Whether no row of the set touches another of it.
 bool apart_itself(const qps_rows& r, int64_t tokens, int d) {
   const int64_t t = r.tok_stride, h = r.head_stride;
@@ -128,12 +141,12 @@ qps_status qk_norm_rope(const qps_qk_rope_args* a, cudaStream_t s) {
     for (int i = 0; i < 2; ++i) {
       if (sides[i].in->heads == 0 || !overlap(*sides[o].out, *sides[i].in, a->tokens, a->d)) continue;
       if (i == o && same_rows(*sides[o].out, *sides[i].in, a->tokens)) continue;
-      if (!apart_in_projection(*sides[o].out, *sides[i].in, a->d))
+      if (!apart(*sides[o].out, *sides[i].in, a->tokens, a->d))
         return bad(n, sides[o].out_what, "overlaps an input without being it");
     }
   }
   if (a->q.heads && a->k.heads && overlap(a->q_out, a->k_out, a->tokens, a->d) &&
-      !apart_in_projection(a->q_out, a->k_out, a->d))
+      !apart(a->q_out, a->k_out, a->tokens, a->d))
     return bad(n, "", "q_out and k_out overlap");
   RopeP p{};
   p.tokens = a->tokens;

@@ -278,6 +278,20 @@ print("child ok")
 """)
 
 
+def test_in_place_over_interleaved_heads(qps):  # noqa: F811
+    """Query and key rows that alternate in one projection, normed in place: no row of one
+    is a row of the other."""
+    d, tokens, heads = 64, 11, 6
+    x = torch.randn((tokens, heads, 3, d), generator=torch.Generator().manual_seed(3)).half().cuda()
+    was = x.clone()
+    q, k = x[:, :, 0], x[:, :, 1]
+    qps.qk_norm_rope(qps.qk_rope_args(q, k, norm=True, q_out=q, k_out=k))
+    for i in (0, 1):
+        want = torch.from_numpy(op.norm_rope_f32(_f(was[:, :, i]), norm=True)).half()
+        assert torch.equal(x[:, :, i].cpu(), want)
+    assert torch.equal(x[:, :, 2], was[:, :, 2])
+
+
 def test_prefix_of_nearly_all_positions(qps):  # noqa: F811
     """A shared prefix close to 2^31 positions (its table names few pages over and over): the
     last chunk's end stays in range."""

@@ -58,3 +58,21 @@ def test_rope_output_rows_overlap_one_another(lib, layout, tokens):  # noqa: F81
     a = _rope(tokens=tokens, q__heads=n, q__tok_stride=n * 128, q_out=N.Rows(0x300000, 0, n, t, h), k__heads=0, k_out__heads=0)
     refused = lib.qps_qk_norm_rope(ctypes.byref(a), None) == INVALID
     assert refused == _touch(layout, layout, tokens, 128)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up: an accepted call must not run")
+@pytest.mark.parametrize("off", [0, 8, 64, 120, 128, 136, 192, 256, 384, 512, 640, 1024, 1280, 4096])
+@pytest.mark.parametrize("q", LAYOUTS[::2] + [(0, 768, 384, 2)])
+@pytest.mark.parametrize("k", [(0, 384, 128, 1), (0, 768, 384, 2), (0, 256, 128, 1), (0, 640, 256, 2)])
+def test_rope_outputs_overlap(lib, off, q, k):  # noqa: F811
+    """Outputs of both sides in one buffer: side by side, head by head, or over one another
+    (tokens the same distance apart, else any meeting of their extents is refused)."""
+    tokens, base = 4, 0x800000
+    if _touch(q, q, tokens, 128) or _touch(k, k, tokens, 128):
+        return
+    k = (off,) + k[1:]
+    a = _rope(tokens=tokens, q__heads=q[3], q__tok_stride=q[3] * 128, k__heads=k[3], k__tok_stride=k[3] * 128,
+              q_out=N.Rows(base, 0, q[3], q[1], q[2]), k_out=N.Rows(base + 2 * off, 0, k[3], k[1], k[2]))
+    refused = lib.qps_qk_norm_rope(ctypes.byref(a), None) == INVALID
+    meet = off < (tokens - 1) * q[1] + (q[3] - 1) * q[2] + 128
+    assert refused == (_touch(q, k, tokens, 128) if q[1] == k[1] else meet)
