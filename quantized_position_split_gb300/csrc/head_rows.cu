@@ -30,6 +30,14 @@ qps_status check_rows(const qps_rows& r, int d, const char* call, const char* wh
   return QPS_OK;
 }
 
+// Sizes whose products stay in 64 bits: what the checks and the kernels compute with them.
+// (kMaxTokens: each token takes a warp at least, and launch_rows holds the warps to this.)
+constexpr int64_t kMaxTokens = (int64_t)1 << 27;
+bool reachable(const qps_rows& r, int64_t tokens, int d) {
+  const __int128 last = (__int128)(tokens - 1) * r.tok_stride + (__int128)(r.heads - 1) * r.head_stride + d;
+  return r.heads == 0 || last < (__int128)1 << 56;
+}
+
 qps_status check_norm(const qps_head_norm& n, const char* call, const char* what) {
   if (!n.on) return QPS_OK;
   if (!std::isfinite(n.eps) || n.eps < 0.f || !std::isfinite(n.offset))
@@ -110,6 +118,7 @@ qps_status qk_norm_rope(const qps_qk_rope_args* a, cudaStream_t s) {
   if (a->d != 32 && a->d != 64 && a->d != 128 && a->d != 256 && a->d != 512)
     return bad(n, "", "head_dim must be 32, 64, 128, 256 or 512", QPS_ERR_UNSUPPORTED);
   if (a->tokens == 0) return QPS_OK;
+  if (a->tokens >= kMaxTokens) return bad(n, "", "too many tokens in one call", QPS_ERR_UNSUPPORTED);
   const struct { const qps_rows *in, *out; const char *what, *out_what; } sides[2] = {
       {&a->q, &a->q_out, " q", " q_out"}, {&a->k, &a->k_out, " k", " k_out"}};
   int in_dtype = -1, out_dtype = -1;
@@ -117,6 +126,8 @@ qps_status qk_norm_rope(const qps_qk_rope_args* a, cudaStream_t s) {
     qps_status st = check_rows(*sd.in, a->d, n, sd.what);
     if (st == QPS_OK) st = check_rows(*sd.out, a->d, n, sd.out_what);
     if (st != QPS_OK) return st;
+    if (!reachable(*sd.in, a->tokens, a->d) || !reachable(*sd.out, a->tokens, a->d))
+      return bad(n, sd.what, "strides reach behind any memory");
     if (sd.in->heads != sd.out->heads) return bad(n, sd.what, "input and output heads differ");
     if (sd.in->heads == 0) continue;
     if (sd.out->dtype == QPS_DT_F32) return bad(n, sd.out_what, "the output type is F16 or BF16", QPS_ERR_UNSUPPORTED);
@@ -175,6 +186,7 @@ qps_status kv_append(const qps_paged_append_args* a, cudaStream_t s) {
   qps_status st = check_paged_kv(a->kv, "kv_append_paged", &kv);
   if (st == QPS_OK) st = check_norm(a->k_norm, n, " k_norm");
   if (st != QPS_OK || a->tokens == 0) return st;
+  if (a->tokens >= kMaxTokens) return bad(n, "", "too many tokens in one call", QPS_ERR_UNSUPPORTED);
   st = check_rotation(a->rot, a->positions, kv.d, n);
   if (st != QPS_OK) return st;
   if (a->k.heads != kv.hkv || a->v.heads != kv.hkv)
@@ -182,6 +194,8 @@ qps_status kv_append(const qps_paged_append_args* a, cudaStream_t s) {
   st = check_rows(a->k, kv.d, n, " k");
   if (st == QPS_OK) st = check_rows(a->v, kv.d, n, " v");
   if (st != QPS_OK) return st;
+  if (!reachable(a->k, a->tokens, kv.d) || !reachable(a->v, a->tokens, kv.d))
+    return bad(n, "", "strides reach behind any memory");
   if (a->k.dtype != a->v.dtype) return bad(n, "", "k and v must have the same type");
   if (!a->slots || !aligned_to(a->slots, 8)) return bad(n, "", "slots is NULL or misaligned");
   AppendP p{};

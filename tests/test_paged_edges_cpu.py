@@ -10,7 +10,7 @@ import torch
 
 from quantized_position_split_gb300 import _native as N
 from quantized_position_split_gb300 import paged
-from tests.test_paged_cpu import INVALID, _rope, lib  # noqa: F401
+from tests.test_paged_cpu import INVALID, UNSUPPORTED, _append, _rope, _rows, lib  # noqa: F401
 
 
 def test_a_dropped_block_frees_its_tensors(lib):  # noqa: F811
@@ -76,3 +76,20 @@ def test_rope_outputs_overlap(lib, off, q, k):  # noqa: F811
     refused = lib.qps_qk_norm_rope(ctypes.byref(a), None) == INVALID
     meet = off < (tokens - 1) * q[1] + (q[3] - 1) * q[2] + 128
     assert refused == (_touch(q, k, tokens, 128) if q[1] == k[1] else meet)
+
+
+# ---- sizes ------------------------------------------------------------------------------
+@pytest.mark.parametrize("tokens", [1 << 27, 1 << 40, 1 << 62, (1 << 63) - 1])
+def test_more_tokens_than_a_launch_holds(lib, tokens):  # noqa: F811
+    """Refused before anything is computed from them."""
+    assert lib.qps_qk_norm_rope(ctypes.byref(_rope(tokens=tokens)), None) == UNSUPPORTED
+    assert lib.qps_kv_append_paged(ctypes.byref(_append(tokens=tokens)), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("stride", [1 << 58, (1 << 62) + 8, (1 << 63) - 8])
+def test_strides_behind_any_memory(lib, stride):  # noqa: F811
+    for kw in (dict(q__tok_stride=stride), dict(q_out__tok_stride=stride), dict(k__head_stride=stride, k__tok_stride=stride),
+               dict(k_out__head_stride=stride)):
+        assert lib.qps_qk_norm_rope(ctypes.byref(_rope(tokens=9, **kw)), None) == INVALID, kw
+    a = _append(tokens=9, v=_rows(0x20000, tok=stride))
+    assert lib.qps_kv_append_paged(ctypes.byref(a), None) == INVALID
