@@ -79,7 +79,7 @@
 extern "C" {
 #endif
 
-#define QPS_ABI_VERSION 8
+#define QPS_ABI_VERSION 9
 
 #if defined(__GNUC__)
 #define QPS_API __attribute__((visibility("default")))
@@ -453,6 +453,16 @@ QPS_API qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* wor
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 QPS_API qps_status qps_attn_decode_paged(const qps_paged_attn_args* a, void* stream);
 
+/* One-shot fault for tests of the attention's bounded waits (no counterpart on the pages;
+ * like qps_ring_inject_fault it needs no GPU fault): in the next qps_attn_decode_paged call
+ * of the process, the keys of tile `tile` of each chunk (128 positions) never arrive in the
+ * tcgen05 kernels (many query rows; the others run as always), and their waits give up after
+ * wait_ms (1..1000) instead of a second.  That call's outputs are then invalid,
+ * qps_device_status reports TIMEOUT and qps_device_wait_record where; later calls are not
+ * affected.  tile == -1 disarms.
+ * Errors: INVALID_ARG. */
+QPS_API qps_status qps_paged_inject_fault(int32_t tile, int32_t wait_ms);
+
 /* ---- Pinned host storage of the tail ------------------------------------------- */
 
 /* Page-locked host memory for the tail ("F5 M7 — Rolling KV: position-windowed KV
@@ -681,8 +691,9 @@ QPS_API qps_status qps_device_status(int32_t reset);
  *   [0] status bits (1: a wait gave up, 2: a bounds check failed, 4: an index out of range), [1] number of waits
  *   that gave up, [2..4] that CTA's block index x / y / z, [5] its warp, [6] the warp's
  *   tile whose wait ran out, [7] tiles the warp had issued, [8] tiles the warp owns,
- *   [9] positions in the CTA's chunk, [10] ns the drain wait of that tile took,
- *   [11] 1 if the tile's copy completed during it, [12] ns of the last
+ *   [9] positions in the CTA's chunk, [10] ns the drain wait of that tile took (the
+ *   tcgen05 kernels: of every copy under way, [7] counting the copies that the warp itself
+ *   issued), [11] 1 if the copy completed during it, [12] ns of the last
  *   qps_selftest_bounded_wait's full bounded wait.
  * qps_device_status with reset clears all of it.  Errors: INVALID_ARG, CUDA. */
 QPS_API qps_status qps_device_wait_record(uint32_t* words, int32_t n);

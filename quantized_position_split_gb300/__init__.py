@@ -56,6 +56,7 @@ __all__ = [
     "kv_append_paged",
     "paged_attn_args",
     "attn_decode_paged",
+    "paged_inject_fault",
 ]
 
 
@@ -675,4 +676,4 @@ def choose_tier(kv_bytes_per_tier, budget_bytes: float, t_star_bytes: float) -> 
 
 
 from .paged import (PagedKV, Rope, attn_decode_paged, kv_append_paged, paged_append_args,  # noqa: E402
-                    paged_attn_args, qk_norm_rope, qk_rope_args, rope_table)
+                    paged_attn_args, paged_inject_fault, qk_norm_rope, qk_rope_args, rope_table)

@@ -252,6 +252,7 @@ SIGNATURES = [
     ("qps_kv_append_paged", c_int32, [POINTER(PagedAppendArgs), c_void_p]),
     ("qps_attn_paged_plan", c_int32, [POINTER(PagedAttnArgs), POINTER(c_size_t)]),
     ("qps_attn_decode_paged", c_int32, [POINTER(PagedAttnArgs), c_void_p]),
+    ("qps_paged_inject_fault", c_int32, [c_int32, c_int32]),
     ("qps_host_alloc", c_int32, [c_size_t, c_int32, POINTER(c_void_p)]),
     ("qps_host_free", c_int32, [c_void_p]),
     ("qps_copy_host", c_int32, [c_void_p, c_void_p, c_size_t, c_void_p]),

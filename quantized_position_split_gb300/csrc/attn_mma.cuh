@@ -300,9 +300,8 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 // Bounded wait for the phase with the given parity: false once `limit_ns` of the GPU's
 // global timer have passed without it (the clock is read only after a first poll
-// fails).  A tile copy lands in microseconds; the bound, one second, only has to end a
-// wait that would otherwise never end.
-constexpr uint64_t kWaitLimitNs = 1000000000ull;
+// fails).  A tile copy lands in microseconds; the bound only has to end a wait that would
+// otherwise never end.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();

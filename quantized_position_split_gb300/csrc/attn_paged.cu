@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <exception>
 #include <string>
@@ -17,6 +18,11 @@
 
 namespace qps {
 namespace {
+
+// qps_paged_inject_fault: the tile withheld from the next call (+ 1; 0: none) and the limit of
+// its waits in milliseconds.
+std::atomic<uint64_t> g_fault{0};
+
 
 // ---- merge --------------------------------------------------------------------------------
 // M = max lse, w = exp(lse - M), o = sum w o / sum w over the prefix's parts and the row's
@@ -336,6 +342,9 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   p.chunks = reinterpret_cast<int2*>(ws + pl.off_chunks);
   p.out = a->o;
   p.out_lse = a->lse;
+  const uint64_t fault = g_fault.load(std::memory_order_relaxed) ? g_fault.exchange(0) : 0;
+  p.drop_tile = (int)(fault & 0xffffffffu) - 1;
+  p.wait_ns = fault ? (uint32_t)(fault >> 32) * 1000000u : (uint32_t)kWaitLimitNs;
   const int rows = p.n_q * p.group;
   if (p.n_prefix > 0) {
     PagedAttnParams f = p;
@@ -378,6 +387,13 @@ qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* workspace_b
   } catch (const std::exception&) {
     return QPS_ERR_INTERNAL;
   }
+}
+
+qps_status qps_paged_inject_fault(int32_t tile, int32_t wait_ms) {
+  if (tile < -1 || tile >= 1 << 30 || (tile >= 0 && (wait_ms < 1 || wait_ms > 1000)))
+    return fail(QPS_ERR_INVALID_ARG, "paged_inject_fault: need tile >= -1 and wait_ms in [1, 1000]");
+  g_fault.store(tile < 0 ? 0 : (uint64_t)(uint32_t)wait_ms << 32 | (uint32_t)(tile + 1));
+  return QPS_OK;
 }
 
 qps_status qps_attn_decode_paged(const qps_paged_attn_args* a, void* stream) {

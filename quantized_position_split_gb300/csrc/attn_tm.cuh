@@ -156,6 +156,26 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// The CTA's word for a wait that has run out: its tile and warp; not 0, which lets the others go on.
+__device__ __forceinline__ int gave_up(int tile, int warp) { return (tile << 5 | warp) + 1; }
+// At the end of a CTA in which one has (the waits themselves stay short: this in each of them
+// cost 2 us of 24 in instruction fetches), one lane: the report, and the record if it is the
+// launch's first (internal.h), which is then finished by the drain.
+static __device__ __noinline__ bool report_give_up(unsigned int* err, int word, int issued, int tiles, int positions) {
+  atomicOr(err, kErrTimeout);
+  if (atomicAdd(err + 1, 1u) != 0) return false;
+  unsigned int* r = err + 2;
+  r[0] = blockIdx.x;
+  r[1] = blockIdx.y;
+  r[2] = blockIdx.z;
+  r[3] = (word - 1) & 31;
+  r[4] = (word - 1) >> 5;
+  r[5] = issued;
+  r[6] = tiles;
+  r[7] = positions;
+  return true;
+}
+
 // ---- the kernel ------------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -214,9 +234,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = uniform(*tmem_word);
 
-  // Bounded wait of a whole warp, with one answer for all of its lanes; gives up at once
-  // when another role has.
-  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+  int issued = 0;  // (warp 0) copies of K and V under way or landed, two a tile
+  // Bounded wait of a whole warp (at `tile`), with one answer for all of its lanes; gives up at
+  // once when another role has.
+  auto wait = [&](uint32_t bar, uint32_t parity, int tile) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t since = global_ns();
     for (;;) {
@@ -224,11 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int over = 0;
       if (lane == 0) {
         over = *abort_flag;
-        if (!over && global_ns() - since >= mma::kWaitLimitNs) {
-          atomicOr(p.err, kErrTimeout);
-          atomicAdd(p.err + 1, 1u);
-          *abort_flag = over = 1;
-        }
+        if (!over && global_ns() - since >= p.wait_ns) *abort_flag = over = gave_up(tile, warp);
       }
       if (__shfl_sync(0xffffffffu, over, 0)) return false;
     }
@@ -257,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(q_full) : "memory");
   };
-  int issued_k = 0, issued_v = 0;  // (warp 0) tiles under way or landed
 
   if (warp == 0) {
     // ---- tiles: each box is min(page, 128) positions of one page and 64 columns, at most 16 of
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto load = [&](const TensorMap* map, uint32_t dst, uint32_t bar, int j, int page) {
       if (lane == 0) mbar_expect_tx(bar, G::TILE);
       __syncwarp();
-      if (r < nb)
+      if (r < nb && (map != &maps.k || j != p.drop_tile))
         tma_load_4d(dst + cg * (kTok * 128) + r * br * 128, map, cg * 128,
                     (t0 + j * kTok + r * br) & ((1 << p.page_shift) - 1), head, page, bar);
     };
@@ -285,14 +301,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         else atomicOr(p.err, kErrIndex);
       }
       next = entry(j + 1);
-      if (j >= ST && !wait(k_empty(s), par)) break;
+      if (j >= ST && !wait(k_empty(s), par, j)) break;
       __syncwarp();
       load(&maps.k, sbase + G::K_OFF + s * G::TILE, k_full(s), j, page);
-      issued_k = j + 1;
-      if (j >= ST && !wait(v_empty(s), par)) break;
+      issued = 2 * j + 1;
+      if (j >= ST && !wait(v_empty(s), par, j)) break;
       __syncwarp();
       load(&maps.v, sbase + G::V_OFF + s * G::TILE, v_full(s), j, page);
-      issued_v = j + 1;
+      issued = 2 * j + 2;
     }
   } else if (warp == 1) {
     // ---- products --------------------------------------------------------------------------------
@@ -300,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t one = elect_lane();
     auto s_product = [&](int j) -> bool {  // S of tile j
       const int s = j % ST;
-      if (!wait(k_full(s), (j / ST) & 1)) return false;
+      if (!wait(k_full(s), (j / ST) & 1, j)) return false;
       fence_after();
       const uint32_t d = tmem + G::S_COL + (j & 1) * kTok;
       const uint64_t a = smem_desc(sbase, 16), b = smem_desc(sbase + G::K_OFF + s * G::TILE, 16);
@@ -313,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(s_full(j & 1), one);
       return true;
     };
-    bool ok = ntiles == 0 || wait(q_full, 0);
+    bool ok = ntiles == 0 || wait(q_full, 0, 0);
     for (int j = 0; j < min(2, ntiles) && ok; ++j) ok = s_product(j);
     for (int j = 0; j < ntiles && ok; ++j) {
       const int s = j % ST, w = j & 1;
-      if (!(ok = wait(v_full(s), (j / ST) & 1))) break;
+      if (!(ok = wait(v_full(s), (j / ST) & 1, j))) break;
       const int left = t1 - (t0 + j * kTok);
       const uint32_t vb = G::V_OFF + s * G::TILE;
       if (left < kTok) {
@@ -329,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma::fence_proxy_async();
         __syncwarp();
       }
-      if (!(ok = wait(p_ready(w), (j >> 1) & 1))) break;
+      if (!(ok = wait(p_ready(w), (j >> 1) & 1, j))) break;
       fence_after();
       const uint32_t d = tmem + G::O_COL + w * D, a = tmem + G::S_COL + w * kTok;
       const uint64_t b = smem_desc(sbase + vb, kTok * 128);
@@ -362,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = w; j < ntiles; j += 2) {
-      if (!(ok = wait(s_full(w), (j >> 1) & 1))) break;
+      if (!(ok = wait(s_full(w), (j >> 1) & 1, j))) break;
       fence_after();
       const int first = t0 + j * kTok;
       // Whole tiles of plain logits, the common case, have a body of their own: maxima and
@@ -478,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(w)) : "memory");
     }
     // ---- merge the streams, write the chunk's part --------------------------------------------
-    if (ok) ok = wait(all_done, 0);
+    if (ok) ok = wait(all_done, 0, ntiles);
     fence_after();
     // The streams exchange halves of O through the stages (every tile has been consumed), and
     // their states: stream w finishes the columns [w D/2, (w + 1) D/2).  Column-major, so that
@@ -574,17 +590,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" :::);
   if (*abort_flag) {  // (uniform: the flag is only set before the barrier above)
-    auto drain = [&](uint32_t bar, uint32_t parity) {
-      const uint64_t since = global_ns();
-      while (!mbar_try_wait(bar, parity) && global_ns() - since < mma::kWaitLimitNs) {
-      }
-    };
+    // (one more bounded wait for each copy still under way: none may land after the CTA has gone)
     if (warp == 0) {
-      for (int j = max(0, issued_k - ST); j < issued_k; ++j) drain(k_full(j % ST), (j / ST) & 1);
-      for (int j = max(0, issued_v - ST); j < issued_v; ++j) drain(v_full(j % ST), (j / ST) & 1);
-    } else if (warp == 1) {
-      drain(all_done, 0);
+      const bool first = lane == 0 && report_give_up(p.err, *abort_flag, issued, ntiles, t1 - t0);
+      const uint64_t since = global_ns();
+      bool done = true;
+#pragma unroll 1
+      for (int i = max(0, issued - 2 * ST); i < issued; ++i) {  // K and V of a tile in turn
+        const int j = i >> 1;
+        done &= mma::mbar_wait(i & 1 ? v_full(j % ST) : k_full(j % ST), (j / ST) & 1, p.wait_ns);
+      }
+      if (first) {
+        p.err[10] = (unsigned)min((uint64_t)0xffffffffu, global_ns() - since);
+        p.err[11] = done ? 1u : 0u;
+      }
     }
+    if (warp == 1) mma::mbar_wait(all_done, 0, p.wait_ns);
     __syncthreads();
   }
   fence_after();

@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   fence_after();
   const uint32_t tmem = uniform(*tmem_word);
 
-  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {  // (as in attn_tm.cuh)
+  int issued = 0;  // (warps 2, 3) stages or slots boxed
+  auto wait = [&](uint32_t bar, uint32_t parity, int tile) -> bool {  // (as in attn_tm.cuh)
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const uint64_t since = global_ns();
     for (;;) {
@@ -168,16 +169,11 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       int over = 0;
       if (lane == 0) {
         over = *abort_flag;
-        if (!over && global_ns() - since >= mma::kWaitLimitNs) {
-          atomicOr(p.err, kErrTimeout);
-          atomicAdd(p.err + 1, 1u);
-          *abort_flag = over = 1;
-        }
+        if (!over && global_ns() - since >= p.wait_ns) *abort_flag = over = gave_up(tile, warp);
       }
       if (__shfl_sync(0xffffffffu, over, 0)) return false;
     }
   };
-  int issued = 0;  // (warps 2, 3) stages or slots boxed
   auto arrive = [&](uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
   };
@@ -188,11 +184,11 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     // turn, took 4% longer at head_dim 512; four slots, then two, 2%.) ----
     const uint32_t id_s = instr_desc(n16, 0), id_o = instr_desc(n16, 1) | (1u << 15), one = elect_lane();
     int fk = 0, fv = 0;  // slots used
-    bool ok = ntiles == 0 || wait(q_full, 0);
+    bool ok = ntiles == 0 || wait(q_full, 0, 0);
     for (int j = -1; j <= ntiles && ntiles > 0 && ok; ++j) {
       const bool qk = j + 1 < ntiles, pv = j >= 1;
       // (P of tile j - 1 is there: its S, whose buffer S(j + 1) takes, has been read)
-      if (pv && !(ok = wait(p_ready((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
+      if (pv && !(ok = wait(p_ready((j - 1) & 1), ((j - 1) >> 1) & 1, j))) break;
       const uint32_t ds = tmem + ((j + 1) & 1) * n16;
       const uint64_t bp = smem_desc(sbase + G::P_OFF + ((j - 1) & 1) * G::P_STEP, 16);
 #pragma unroll 1
@@ -201,7 +197,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll 1
           for (int c = 2 * u; c < 2 * u + 2; ++c, ++fk) {
             const int s = fk & 1;
-            if (!(ok = wait(k_full(s), (fk >> 1) & 1))) break;
+            if (!(ok = wait(k_full(s), (fk >> 1) & 1, j))) break;
             fence_after();
             const uint32_t a = tmem + k_col + s * 64;
             const uint64_t bq = smem_desc(sbase + c * (kN * 128), 16);
@@ -222,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         }
         if (pv && ok) {
           const int s = fv % kSlots;
-          if (!(ok = wait(v_full(s), (fv / kSlots) & 1))) break;
+          if (!(ok = wait(v_full(s), (fv / kSlots) & 1, j))) break;
           if constexpr (!VDEC) {
             // fp16 rows behind the end hold whatever was there, and 0 x NaN is NaN
             const int left = t1 - (t0 + (j - 1) * kTile);
@@ -252,7 +248,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       }
     }
     commit(all_done, one);
-    wait(all_done, 0);
+    wait(all_done, 0, ntiles);
   } else if (warp == 2 || warp == 3) {
     // ---- boxes of min(page, 128) positions, K's (warp 2) and V's (warp 3), each lane's page read
     // a tile ahead -------------------------------------------------------------------------------
@@ -278,7 +274,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         }
         next = entry(j + 1);
       }
-      if (round > 0 && !wait(!v ? kraw_empty(s) : VDEC ? vraw_empty(s) : v_empty(s), (round & 1) ^ 1)) break;
+      if (round > 0 && !wait(!v ? kraw_empty(s) : VDEC ? vraw_empty(s) : v_empty(s), (round & 1) ^ 1, j)) break;
       const uint32_t bar = !v ? kraw_full(s) : VDEC ? vraw_full(s) : v_full(s);
       const uint32_t dst = sbase + (!v ? G::KRAW + s * G::KSTAGE : VDEC ? G::VRAW + s * G::VSTAGE : G::RING + s * kSlot);
       if (lane == 0) {
@@ -287,7 +283,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           for (int i = 1; i < 4; ++i) arrive(bar);  // (a slot's barrier counts four)
       }
       __syncwarp();
-      if (grp < groups) {
+      if (grp < groups && (v || j != p.drop_tile)) {
         const int y = (t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
         tma_load_4d(dst + grp * (kSlot / 2) + r * br * rb, v ? &maps.v : &maps.k, (c * groups + grp) * rb, y, head, page, bar);
         if (signs) tma_load_4d(dst + kTile * 32 + r * br * 16, &maps.va, c * 16, y, head, page, bar);
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll 1
         for (int c = 0; c < G::KC; ++c, ++f) {
           const int rs = f % KN, s = f & 1;
-          if (!(ok = wait(kraw_full(rs), (f / KN) & 1))) break;
+          if (!(ok = wait(kraw_full(rs), (f / KN) & 1, j))) break;
           const uint8_t* raw = smem + G::KRAW + rs * G::KSTAGE;
           const uint32_t dst = tmem + lanes + k_col + s * 64;
           if constexpr (KF == QPS_FMT_Q8_0) {
@@ -357,7 +353,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
             mma::fence_proxy_async();  // (the reads are done before the next box is written)
             __syncwarp();
             if (lane == 0) arrive(kraw_empty(rs));
-            if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
+            if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1, j))) break;
             fence_after();
             if (G::EXPS == 2 && c == 2) kexp[(j & 1) * kTile + tok] = (uint8_t)halved;
 #pragma unroll
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
             mma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(kraw_empty(rs));
-            if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1))) break;
+            if (f >= 2 && !(ok = wait(k_empty(s), ((f >> 1) & 1) ^ 1, j))) break;
             fence_after();
             tmem_st32(dst, x);
           }
@@ -436,7 +432,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll 1
         for (int c = 0; c < G::VC; ++c, ++f) {
           const int rs = f % VN, s = f % kSlots;
-          if (!(ok = wait(vraw_full(rs), (f / VN) & 1))) break;
+          if (!(ok = wait(vraw_full(rs), (f / VN) & 1, j))) break;
           const uint8_t* raw = smem + G::VRAW + rs * G::VSTAGE;
           uint8_t* slot = smem + G::RING + s * kSlot;
           if constexpr (VF == QPS_FMT_Q8_0) {
@@ -446,7 +442,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
             mma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(vraw_empty(rs));
-            if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1))) break;
+            if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1, j))) break;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {  // 16 dims
               const __half2 sc = scale_of(w[i >> 2], (i >> 1) & 1);
@@ -471,7 +467,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
             mma::fence_proxy_async();
             __syncwarp();
             if (lane == 0) arrive(vraw_empty(rs));
-            if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1))) break;
+            if (f >= kSlots && !(ok = wait(v_empty(s), ((f / kSlots) & 1) ^ 1, j))) break;
             const uint32_t words[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
             const uint32_t sgw[4] = {sg.x, sg.y, sg.z, sg.w};
 #pragma unroll
@@ -597,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       }
       // (a TurboQuant V: the reference bounds P x norm, the operand; see attn_mma.cuh)
       const float lift = is_tq(VF) ? mma::norm_log2(norm) : 0.f, room = kRefShift + kRefLazy - lift;
-      ok &= wait(s_full(j & 1), (j >> 1) & 1);
+      ok &= wait(s_full(j & 1), (j >> 1) & 1, j);
       fence_after();
       float qt = qs, st = p.scale;
       if constexpr (KF == QPS_FMT_Q8_0) {
@@ -682,7 +678,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         if (tid < n16) fred[tid] = cr;
         meet();
         if (j > 0) {
-          ok &= wait(p_free((j - 1) & 1), ((j - 1) >> 1) & 1);  // O is at rest
+          ok &= wait(p_free((j - 1) & 1), ((j - 1) >> 1) & 1, j);  // O is at rest
           fence_after();
         }
 #pragma unroll
@@ -711,7 +707,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         }
         meet();  // (every factor has been read)
       }
-      if (j >= 2) ok &= wait(p_free(j & 1), ((j - 2) >> 1) & 1);  // the buffer's last reader
+      if (j >= 2) ok &= wait(p_free(j & 1), ((j - 2) >> 1) & 1, j);  // the buffer's last reader
       uint8_t* pbuf = smem + G::P_OFF + (j & 1) * G::P_STEP + tl * 128;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -753,7 +749,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       __syncwarp();
       if (lane == 0) arrive(p_ready(j & 1));
     }
-    if (ok) ok = wait(all_done, 0);
+    if (ok) ok = wait(all_done, 0, ntiles);
     fence_after();
     // ---- sums over the positions, O to shared memory ---------------------------------------------
     if (ok) {
@@ -841,18 +837,21 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       }
     }
   } else {  // the products and boxes under way, before their operands and TMEM go
-    auto drain = [&](uint32_t bar, uint32_t parity) {
+    if (warp == 0) mma::mbar_wait(all_done, 0, p.wait_ns);
+    if (warp == 2 || warp == 3) {
+      const bool v = warp == 3, first = !v && lane == 0 && report_give_up(p.err, *abort_flag, issued, ntiles, t1 - t0);
+      const int ring = !v ? KN : VDEC ? VN : kSlots;
       const uint64_t since = global_ns();
-      while (!mbar_try_wait(bar, parity) && global_ns() - since < mma::kWaitLimitNs) {
+      bool done = true;
+#pragma unroll 1
+      for (int i = max(0, issued - ring); i < issued; ++i) {
+        const int s = i % ring;
+        done &= mma::mbar_wait(!v ? kraw_full(s) : VDEC ? vraw_full(s) : v_full(s), (i / ring) & 1, p.wait_ns);
       }
-    };
-    if (warp == 0) drain(all_done, 0);
-    if (warp == 2)
-      for (int i = max(0, issued - KN); i < issued; ++i) drain(kraw_full(i % KN), (i / KN) & 1);
-    if (warp == 3) {
-      const int ring = VDEC ? VN : kSlots;
-      for (int i = max(0, issued - ring); i < issued; ++i)
-        drain(VDEC ? vraw_full(i % ring) : v_full(i % ring), (i / ring) & 1);
+      if (first) {
+        p.err[10] = (unsigned)min((uint64_t)0xffffffffu, global_ns() - since);
+        p.err[11] = done ? 1u : 0u;
+      }
     }
   }
   fence_before();

@@ -46,6 +46,7 @@ int sm_count_current();
 unsigned int* device_error_word();
 constexpr unsigned int kErrTimeout = 1u, kErrBounds = 2u, kErrIndex = 4u;
 constexpr int kErrWords = 16;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // the kernels' waits: one second
 
 // ---- the checked build ----------------------------------------------------------------
 // Compiled with -DQPS_CHECK_BOUNDS=1 (the library variant libqps_checked.so), the kernels

@@ -38,6 +38,9 @@ struct PagedAttnParams : AttnParams {
   float* own_o;       // f32 [chunk][n_q*hq][D], [chunk][n_q*hq]
   float* own_lse;
   int2* chunks;       // [batch] first chunk and count, for the merge; written by first chunks
+  int drop_tile;      // (tcgen05 kernels) the tile of each chunk whose keys are not brought (-1:
+                      // none; see qps_paged_inject_fault), and the limit of the waits
+  uint32_t wait_ns;
   void* out;          // the call's o (out_dtype) and lse
   float* out_lse;
   int out_dtype;

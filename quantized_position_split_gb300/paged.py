@@ -314,3 +314,10 @@ def attn_decode_paged(a: N.PagedAttnArgs, stream=None):
     """Decode attention of ``paged_attn_args``; returns (o, lse)."""
     _call(a, stream)
     return a._out
+
+
+def paged_inject_fault(tile: int, wait_ms: int = 20) -> None:
+    """Withhold the keys of tile ``tile`` of each chunk from the next ``attn_decode_paged`` call
+    of many query rows, whose waits then give up after ``wait_ms`` (``qps_paged_inject_fault``;
+    -1 disarms)."""
+    N.check(N.load().qps_paged_inject_fault(tile, wait_ms))

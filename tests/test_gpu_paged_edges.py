@@ -307,3 +307,45 @@ def test_prefix_of_nearly_all_positions(qps):  # noqa: F811
                   shared_len=(width - 1) * page, out_dtype=torch.float32)
     assert np.abs(lse - np.log(float(n))).max() <= 1e-4
     assert np.abs(o - (width // 8) / width).max() <= 1e-4
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(128, "f16", "f16", 9, 4), (64, "f16", "f16", 9, 4), (128, "q8_0", "tq3", 9, 4),
+                                               (256, "f16", "f16", 5, 4), (512, "q8_0", "q8_0", 5, 4)])
+@pytest.mark.parametrize("tile", [0, 1, 7])
+def test_a_tile_that_never_comes(qps, d, kf, vf, n_q, group, tile):  # noqa: F811
+    """A tile withheld on the host: the kernel's waits give up after their limit, its roles
+    stop, the call ends, the error word and the record say where, and the next call is right."""
+    from quantized_position_split_gb300 import _native as N
+    hkv, page, n = 1, 64, 150000
+    rot, ora = _rotations(d, "whole")
+    cache = qps.PagedKV.empty(kf, vf, -(-n // page), page, hkv, d, signs=_lib_rot(qps, rot))
+    table = torch.arange(-(-n // page), dtype=torch.int32)[None]
+    q = torch.randn((1, n_q, hkv * group, d), generator=torch.Generator().manual_seed(1)).half().cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    a = qps.paged_attn_args(q, cache, table.cuda(), lens, scale=d ** -0.5, out_dtype=torch.float32)
+    qps.attn_decode_paged(a)
+    torch.cuda.synchronize()
+    qps.device_status(reset=True)
+    qps.paged_inject_fault(tile, 20)
+    qps.attn_decode_paged(a)
+    torch.cuda.synchronize()
+    rec = qps.device_wait_record()
+    with pytest.raises(N.QpsError) as e:
+        qps.device_status(reset=True)
+    assert e.value.status == N.QPS_ERR_TIMEOUT
+    assert rec[0] == 1 and rec[1] >= 1 and rec[8] > 0 and rec[9] > 0, rec
+    assert 15e6 < rec[10] < 200e6 and rec[11] == 0, rec  # the tile's own drain ran its limit too
+    lens.fill_(300)
+    o, lse = qps.attn_decode_paged(a)
+    torch.cuda.synchronize()
+    qps.device_status(reset=True)
+    ro, rl = _want(cache, q, table, [300], d ** -0.5, 0.0, False, ora)
+    assert_parity(o.cpu().numpy(), lse.cpu().numpy(), ro, rl)
+
+
+def test_fault_arguments(qps):  # noqa: F811
+    for tile, ms in ((-2, 20), (0, 0), (0, 1001), (1 << 30, 5)):
+        with pytest.raises(qps.QpsError):
+            qps.paged_inject_fault(tile, ms)
+    qps.paged_inject_fault(3, 5)
+    qps.paged_inject_fault(-1)  # disarmed
