@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     if (!p.shared) {  // chunk number `split` of the batch: find its sequence and positions
       const PagedChunk ch = paged_find(p, split, lane);
       if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
-      if (ch.first && head == 0 && rg == 0 && threadIdx.x == 0) p.chunks[ch.b] = make_int2(split, ch.count);
+      if (ch.first && head == 0 && rg == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err)) p.chunks[ch.b] = make_int2(split, ch.count);
       bz = ch.b;
       whole = ch.whole;
       t0 = ch.t0;
@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
                               // a chunk of the prefix behind every end: an empty part)
         const int64_t at = p.shared ? (int64_t)part * p.rows_total + row
                                     : (int64_t)part * (p.n_q * p.hq) + (row - (int64_t)bz * (p.n_q * p.hq));
+        if (!out_in_bounds(p, whole, part, whole || p.shared ? row : row - (int64_t)bz * (p.n_q * p.hq))) continue;
         if (!whole) (p.shared ? p.pre_o : p.own_o)[at * D + dd] = 0.f;
         else if (p.out_dtype == QPS_DT_F32) reinterpret_cast<float*>(p.out)[row * D + dd] = 0.f;
         else reinterpret_cast<uint16_t*>(p.out)[row * D + dd] = 0;
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   };
   auto page_of = [&](int64_t t) -> int {
     if constexpr (PAGED) {
-      if (t >= t1) return (int)p.n_pages;
+      if (t >= t1 || !entry_in_bounds(p, bz * p.table_stride + (t >> p.page_shift))) return (int)p.n_pages;
       const int pg = p.table[(int64_t)bz * p.table_stride + (t >> p.page_shift)];
       if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
       atomicOr(p.err, kErrIndex);
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         };
         const int64_t ra = row_of(pg.a), rb2 = row_of(pg.b);
         const bool ina = (int64_t)pg.a < p.n_pages, inb = (int64_t)pg.b < p.n_pages;
-        auto stage_small = [&](int off, int bytes, const void* plane, int rb) {
+        auto stage_small = [&](int off, int bytes, const void* plane, int rb, int64_t rows) {
           for (int ch = lane; ch < bytes / 16; ch += 32) {
             const int row = ch * 16 / rb;  // (16 divides 16 rows: a chunk is of one half)
             const bool second = row >= split_at;
@@ -708,13 +709,15 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
             nb = nb < 0 || !(second ? inb : ina) ? 0 : (nb > 16 ? 16 : nb);
             const uint8_t* src = reinterpret_cast<const uint8_t*>(plane) + (second ? rb2 : ra) * rb + ch * 16 -
                                  (second ? split_at * rb : 0);
+            const int64_t from = src - reinterpret_cast<const uint8_t*>(plane);
+            if (nb > 0 && !in_bounds(from >= 0 && from + nb <= rows * rb && off + ch * 16 + 16 <= G::STAGE, p.err)) nb = 0;
             cp_async16(smem_addr(st + off) + ch * 16, nb > 0 ? src : safe, nb);
           }
         };
-        if constexpr (G::K_ARB > 0 && !G::PKA::TMA) stage_small(G::KA_OFF, G::PKA::BYTES, p.k.aux, G::K_ARB);
-        if constexpr (G::V_ARB > 0 && !G::PVA::TMA) stage_small(G::VA_OFF, G::PVA::BYTES, p.v.aux, G::V_ARB);
-        if constexpr (G::K_A2RB > 0) stage_small(G::KA2_OFF, G::PKA2::BYTES, p.k.aux2, G::K_A2RB);
-        if constexpr (G::V_A2RB > 0) stage_small(G::VA2_OFF, G::PVA2::BYTES, p.v.aux2, G::V_A2RB);
+        if constexpr (G::K_ARB > 0 && !G::PKA::TMA) stage_small(G::KA_OFF, G::PKA::BYTES, p.k.aux, G::K_ARB, p.k_rows);
+        if constexpr (G::V_ARB > 0 && !G::PVA::TMA) stage_small(G::VA_OFF, G::PVA::BYTES, p.v.aux, G::V_ARB, p.v_rows);
+        if constexpr (G::K_A2RB > 0) stage_small(G::KA2_OFF, G::PKA2::BYTES, p.k.aux2, G::K_A2RB, p.k_rows);
+        if constexpr (G::V_A2RB > 0) stage_small(G::VA2_OFF, G::PVA2::BYTES, p.v.aux2, G::V_A2RB, p.v_rows);
         cp_async_arrive_noinc(bar);
       }
       return;
@@ -1469,7 +1472,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         for (int idx = first + lane; NB > 0 && idx < last; idx += 32)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
-            *reinterpret_cast<uint4*>(wpipe + (k % G::STAGES) * G::STAGE + OFF + b * (TT * IB) + idx * 16) =
+            if (in_bounds(left >= 0 && OFF + b * (TT * IB) + idx * 16 + 16 <= G::STAGE, p.err))
+              *reinterpret_cast<uint4*>(wpipe + (k % G::STAGES) * G::STAGE + OFF + b * (TT * IB) + idx * 16) =
                 make_uint4(0, 0, 0, 0);
         __syncwarp();
       }

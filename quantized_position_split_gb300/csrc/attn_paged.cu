@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 own = p.chunks[b];
   const int first = own.x, count = own.y;
-  const bool mine = real && !(count == 1 && p.n_prefix == 0);  // (else written by the attention)
+  const bool mine = real && !(count == 1 && p.n_prefix == 0) &&  // (else written by the attention)
+                    in_bounds(first >= 0 && count > 0 && first + count <= p.max_chunks, p.err);
   const int total = mine ? p.n_prefix + count : 0;
   float m = -INFINITY, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

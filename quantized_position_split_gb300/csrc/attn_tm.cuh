@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
-    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0) p.chunks[ch.b] = make_int2(split, ch.count);
+    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err)) p.chunks[ch.b] = make_int2(split, ch.count);
     bz = ch.b;
     t0 = ch.t0;
     t1 = ch.t1;
@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rr < p.rows_per_cta) {
         const int e = rr / p.group, h = head * p.group + rr % p.group;
         const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
-        v[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+        const int64_t at = (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8;
+        if (q_in_bounds(p, at)) v[k] = *reinterpret_cast<const uint4*>(p.q + at);
       }
     }
 #pragma unroll
@@ -283,11 +284,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t* row = p.table + (int64_t)bz * p.table_stride;
     const int cg = lane % G::CG, r = lane / G::CG;
     auto has = [&](int j) { return r < nb && t0 + j * kTok + r * br < t1; };
-    auto entry = [&](int j) { return has(j) ? row[(t0 + j * kTok + r * br) >> p.page_shift] : 0; };
+    auto entry = [&](int j) {
+      const int i = (t0 + j * kTok + r * br) >> p.page_shift;
+      return has(j) && entry_in_bounds(p, bz * p.table_stride + i) ? row[i] : 0;
+    };
     auto load = [&](const TensorMap* map, uint32_t dst, uint32_t bar, int j, int page) {
       if (lane == 0) mbar_expect_tx(bar, G::TILE);
       __syncwarp();
-      if (r < nb && (map != &maps.k || j != p.drop_tile))
+      if (r < nb && (map != &maps.k || j != p.drop_tile) &&
+          in_bounds(cg * (kTok * 128) + (r + 1) * br * 128 <= G::TILE && dst - sbase + G::TILE <= G::BAR && page <= p.n_pages &&
+                        head < p.hkv && ((t0 + j * kTok + r * br) & ((1 << p.page_shift) - 1)) + br <= 1 << p.page_shift,
+                    p.err))
         tma_load_4d(dst + cg * (kTok * 128) + r * br * 128, map, cg * 128,
                     (t0 + j * kTok + r * br) & ((1 << p.page_shift) - 1), head, page, bar);
     };
@@ -341,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = left * 8 + lane; i < kTok * 8; i += 32)
 #pragma unroll
           for (int cg = 0; cg < G::CG; ++cg)
-            *reinterpret_cast<uint4*>(smem + vb + cg * (kTok * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+            if (in_bounds(left >= 0 && cg * (kTok * 128) + i * 16 + 16 <= G::TILE, p.err))
+              *reinterpret_cast<uint4*>(smem + vb + cg * (kTok * 128) + i * 16) = make_uint4(0, 0, 0, 0);
         mma::fence_proxy_async();
         __syncwarp();
       }
@@ -529,13 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float w0 = f0 * inv, w1 = f1 * inv;  // of this stream's columns, and of the other's
       const bool has0 = ntiles > w, has1 = ntiles > 1 - w;
       int64_t at = 0;
-      if (rr < p.rows_per_cta) {
+      bool mine = rr < p.rows_per_cta;
+      if (mine) {
         const int h = head * p.group + rr % p.group;
         const int64_t local = (int64_t)(rr / p.group) * p.hq + h;  // of the batch, or of the sequence
         at = p.shared ? (int64_t)split * p.rows_total + local
              : whole  ? (int64_t)bz * (p.n_q * p.hq) + local
                       : (int64_t)split * (p.n_q * p.hq) + local;
-        if (w == 0)
+        mine = out_in_bounds(p, whole, split, whole ? at : local);
+        if (mine && w == 0)
           (whole ? p.out_lse : p.shared ? p.pre_lse : p.own_lse)[at] =
               empty ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
       }
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (two && w1 != 0.f) o[i] = fmaf(hand[(1 - w) * H * kRows + (32 * c + i) * kRows + r], w1, o[i]);
         }
         const int64_t to = at * D + w * H + 32 * c;
-        if (rr >= p.rows_per_cta) {
+        if (!mine) {
           // (no row: nothing to store)
         } else if (!whole || p.out_dtype == QPS_DT_F32) {
           float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : parts) + to);

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
-    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0) p.chunks[ch.b] = make_int2(split, ch.count);
+    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err)) p.chunks[ch.b] = make_int2(split, ch.count);
     bz = ch.b;
     t0 = ch.t0;
     t1 = ch.t1;
@@ -262,7 +262,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     const int ring = !v ? KN : VDEC ? VN : kSlots, nc = v ? G::VC : G::KC, count = ntiles * nc;
     const int grp = lane / nb, r = lane % nb;  // (16 boxes at most, one a lane)
     auto has = [&](int j) { return grp < groups && t0 + j * kTile + r * br < t1; };
-    auto entry = [&](int j) { return has(j) ? table[(t0 + j * kTile + r * br) >> p.page_shift] : 0; };
+    auto entry = [&](int j) {
+      const int i = (t0 + j * kTile + r * br) >> p.page_shift;
+      return has(j) && entry_in_bounds(p, bz * p.table_stride + i) ? table[i] : 0;
+    };
     int next = entry(0), page = 0;
     for (int f = 0; f < count; ++f) {
       const int s = f % ring, round = f / ring, j = f / nc, c = f % nc;
@@ -283,8 +286,16 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           for (int i = 1; i < 4; ++i) arrive(bar);  // (a slot's barrier counts four)
       }
       __syncwarp();
-      if (grp < groups && (v || j != p.drop_tile)) {
-        const int y = (t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
+      const int y = (t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
+      // the box stays in its page and its stage (or slot), the stage in its ring
+      const bool fits = in_bounds(
+          grp >= groups || (y + br <= 1 << p.page_shift && page <= p.n_pages && head < p.hkv &&
+                            grp * (kSlot / 2) + (r + 1) * br * rb <= (!v ? G::KSTAGE : VDEC ? G::VSTAGE : kSlot) &&
+                            dst - sbase + (!v ? G::KSTAGE : VDEC ? G::VSTAGE : kSlot) <=
+                                (!v ? G::VRAW : VDEC ? G::MISC : G::KRAW) &&
+                            (!signs || kTile * 32 + (r + 1) * br * 16 <= G::VSTAGE)),
+          p.err);
+      if (grp < groups && (v || j != p.drop_tile) && fits) {
         tma_load_4d(dst + grp * (kSlot / 2) + r * br * rb, v ? &maps.v : &maps.k, (c * groups + grp) * rb, y, head, page, bar);
         if (signs) tma_load_4d(dst + kTile * 32 + r * br * 16, &maps.va, c * 16, y, head, page, bar);
       }
@@ -302,9 +313,11 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       for (int i = 0; i < W; ++i) w[i] = 0u;
       const int at = t0 + j * kTile + tok;
       if (j >= ntiles || at >= t1) return;
+      if (!entry_in_bounds(p, bz * p.table_stride + (at >> p.page_shift))) return;
       const int pg = table[at >> p.page_shift];
       if ((uint64_t)(int64_t)pg >= (uint64_t)p.n_pages) return;  // (reported by the boxes' warps)
       const int64_t row = (((int64_t)pg * p.hkv + head) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+      if (!in_bounds(row < (v ? p.v_rows : p.k_rows), p.err)) return;
       const uint2* src = reinterpret_cast<const uint2*>(reinterpret_cast<const __half*>(aux) + row * (D / 32));
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) {
@@ -415,7 +428,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       if constexpr (VF == QPS_FMT_Q8_0) load_scales(0, p.v.aux, next);
       // 16-byte chunk c of the position's row in a slot's column group g
       auto put = [&](uint8_t* slot, int g, int c, const uint32_t* o) {
-        *reinterpret_cast<uint4*>(slot + g * (kSlot / 2) + tok * 128 + ((c ^ (tok & 7)) << 4)) =
+        if (in_bounds(g < 2 && c < 8 && slot - smem + kSlot <= G::KRAW, p.err))
+          *reinterpret_cast<uint4*>(slot + g * (kSlot / 2) + tok * 128 + ((c ^ (tok & 7)) << 4)) =
             make_uint4(o[0], o[1], o[2], o[3]);
       };
       int f = 0;
@@ -513,7 +527,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         if (rr < p.rows_per_cta) {
           const int e = rr / p.group, h = head * p.group + rr % p.group;
           const int b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
-          v[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8);
+          const int64_t at = (int64_t)b * p.q_bstride + ((int64_t)qi * p.hq + h) * D + c * 8;
+          if (q_in_bounds(p, at)) v[k] = *reinterpret_cast<const uint4*>(p.q + at);
         }
       }
 #pragma unroll
@@ -584,9 +599,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       float norm = 1.f;
       if constexpr (is_tq(VF)) {  // (0 behind the end and for a bad page: nothing there is read)
         norm = 0.f;
-        if (at < t1) {
+        if (at < t1 && entry_in_bounds(p, bz * p.table_stride + (at >> p.page_shift))) {
           const int pg = table[at >> p.page_shift];
-          if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages)
+          if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages &&
+              in_bounds((((int64_t)pg * p.hkv + head) << p.page_shift) + (at & ((1 << p.page_shift) - 1)) < p.v_rows, p.err))
             norm = __half2float(reinterpret_cast<const __half*>(norms)[(((int64_t)pg * p.hkv + head) << p.page_shift) +
                                                                       (at & ((1 << p.page_shift) - 1))]);
         }
@@ -767,7 +783,9 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           ld16(v, tmem + lanes + o_col + b * n16 + r0 + 16 * c);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fin[(r0 + 16 * c + i) * D + dim] = __uint_as_float(v[i]);
+          for (int i = 0; i < 16; ++i)
+            if (in_bounds(dim < D && ((r0 + 16 * c + i) * D + dim + 1) * 4 <= G::MISC - G::P_OFF, p.err))
+              fin[(r0 + 16 * c + i) * D + dim] = __uint_as_float(v[i]);
         }
       }
     }
@@ -823,6 +841,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       const int64_t at = p.shared ? (int64_t)split * p.rows_total + local
                          : whole  ? (int64_t)bz * (p.n_q * p.hq) + local
                                   : (int64_t)split * (p.n_q * p.hq) + local;
+      if (!out_in_bounds(p, whole, split, whole ? at : local)) continue;
       if (lane == 0)
         (whole ? p.out_lse : p.shared ? p.pre_lse : p.own_lse)[at] =
             none ? -INFINITY : (log2f(den) - mneg[r]) * 0.6931471805599453f;

@@ -162,8 +162,9 @@ qps_status qk_norm_rope(const qps_qk_rope_args* a, cudaStream_t s) {
   RopeP p{};
   p.tokens = a->tokens;
   p.one = 1.0f;
-  auto rows = [](const qps_rows& in, const qps_rows& out) {
-    return RowsP{in.data, out.data, in.tok_stride, in.head_stride, out.tok_stride, out.head_stride, in.heads};
+  auto elems = [a](const qps_rows& r) { return r.heads ? extent(r, a->tokens, a->d) / dtype_bytes(r.dtype) : 0; };
+  auto rows = [&](const qps_rows& in, const qps_rows& out) {
+    return RowsP{in.data, out.data, in.tok_stride, in.head_stride, out.tok_stride, out.head_stride, in.heads, elems(in), elems(out)};
   };
   p.q = rows(a->q, a->q_out);
   p.k = rows(a->k, a->k_out);
@@ -201,8 +202,9 @@ qps_status kv_append(const qps_paged_append_args* a, cudaStream_t s) {
   AppendP p{};
   p.tokens = a->tokens;
   p.one = 1.0f;
-  p.k = SideP{a->k.data, a->k.tok_stride, a->k.head_stride, kv.kfmt, kv.k[0], kv.k[1], kv.k[2]};
-  p.v = SideP{a->v.data, a->v.tok_stride, a->v.head_stride, kv.vfmt, kv.v[0], kv.v[1], kv.v[2]};
+  auto elems = [&](const qps_rows& r) { return extent(r, a->tokens, kv.d) / dtype_bytes(r.dtype); };
+  p.k = SideP{a->k.data, a->k.tok_stride, a->k.head_stride, elems(a->k), kv.kfmt, kv.k[0], kv.k[1], kv.k[2]};
+  p.v = SideP{a->v.data, a->v.tok_stride, a->v.head_stride, elems(a->v), kv.vfmt, kv.v[0], kv.v[1], kv.v[2]};
   p.kn = norm_of(a->k_norm);
   p.rot = RotP{a->rot.table, a->positions, a->rot.len, a->rot.dim, a->rot.pairs};
   p.slots = a->slots;

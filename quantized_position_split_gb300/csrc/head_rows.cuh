@@ -53,6 +53,7 @@ struct RowsP {
   void* out;
   int64_t in_tok, in_head, out_tok, out_head;
   int heads;
+  int64_t in_elems, out_elems;  // extents that the checked build holds accesses against
 };
 
 struct RopeP {
@@ -77,6 +78,7 @@ struct TqP {
 struct SideP {
   const void* in;
   int64_t tok, head;
+  int64_t elems;  // (as above)
   int fmt;
   uint8_t *data, *aux, *aux2;
 };
@@ -225,6 +227,11 @@ struct Part {
 template <int D>
 __device__ __forceinline__ int elem0(int sub, int c) {
   return c * (D / 2) + 8 * sub;
+}
+
+// (checked build) `n` elements or rows from `at` on lie within `extent`.
+__device__ __forceinline__ bool row_in_bounds(int64_t at, int n, int64_t extent, unsigned int* err) {
+  return in_bounds(at >= 0 && at + n <= extent, err);
 }
 
 template <typename T>
@@ -442,12 +449,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, T, MODE>)
   const int heads = r.heads;
   const int64_t in_step = R::PER_WARP * r.in_head, out_step = R::PER_WARP * r.out_head;
   const T* src = reinterpret_cast<const T*>(r.in) + tok * r.in_tok + h * r.in_head;
+  auto row_in = [&](const T* at) { return row_in_bounds(at - reinterpret_cast<const T*>(r.in), D, r.in_elems, p.err); };
   uint16_t* dst = reinterpret_cast<uint16_t*>(r.out) + tok * r.out_tok + h * r.out_head;
   Raw<T> ring[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
     ring[u].zero();
-    if (u < iters && h + u * R::PER_WARP < heads) ring[u].template load<D>(src, sub);
+    if (u < iters && h + u * R::PER_WARP < heads && row_in(src)) ring[u].template load<D>(src, sub);
     src += in_step;
   }
   Angles ang;
@@ -468,10 +476,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, T, MODE>)
       if (it + u >= iters) break;
       Part x;
       ring[u].get(x);
-      if (it + u + kAhead < iters && h + kAhead * R::PER_WARP < heads) ring[u].template load<D>(src, sub);
+      if (it + u + kAhead < iters && h + kAhead * R::PER_WARP < heads && row_in(src)) ring[u].template load<D>(src, sub);
       if (n.on) norm_row<D>(x, n, w, one);
       if constexpr (MODE != kNone) rotate_row<D, MODE>(x, ang, p.rot, sub, lane, one);
-      if (h >= heads) continue;
+      if (h >= heads || !row_in_bounds(dst - reinterpret_cast<uint16_t*>(r.out), D, r.out_elems, p.err)) continue;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         *reinterpret_cast<uint4*>(dst + elem0<D>(sub, c)) =
@@ -654,11 +662,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, T, MODE>)
   if constexpr (MODE != kNone) pos = p.rot.pos[tok];
   const int64_t in_step = R::PER_WARP * s.head;
   const T* src = reinterpret_cast<const T*>(s.in) + tok * s.tok + h * s.head;
+  auto row_in = [&](const T* at) { return row_in_bounds(at - reinterpret_cast<const T*>(s.in), D, s.elems, p.err); };
   Raw<T> ring[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
     ring[u].zero();
-    if (u < p.iters && h + u * R::PER_WARP < p.hkv) ring[u].template load<D>(src, sub);
+    if (u < p.iters && h + u * R::PER_WARP < p.hkv && row_in(src)) ring[u].template load<D>(src, sub);
     src += in_step;
   }
   if (slot < 0) return;  // padding
@@ -678,10 +687,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm<D, T, MODE>)
 #pragma unroll
     for (int u = 0; u < kAhead; ++u, h += R::PER_WARP, row += (int64_t)R::PER_WARP << p.page_shift, src += in_step) {
       if (it + u >= p.iters) break;
-      const bool on = h < p.hkv;
+      const bool on = h < p.hkv && row_in_bounds(row, 1, p.n_slots * p.hkv, p.err);
       Part y;
       ring[u].get(y);
-      if (it + u + kAhead < p.iters && h + kAhead * R::PER_WARP < p.hkv) ring[u].template load<D>(src, sub);
+      if (it + u + kAhead < p.iters && h + kAhead * R::PER_WARP < p.hkv && row_in(src)) ring[u].template load<D>(src, sub);
       if (key) {
         if (p.kn.on) norm_row<D>(y, p.kn, w, one);
         if constexpr (MODE != kNone) rotate_row<D, MODE>(y, ang, p.rot, sub, lane, one);

@@ -58,6 +58,21 @@ __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
   if (cut != n) atomicOr(p.err, kErrIndex);
   return cut;
 }
+// What the checked build holds the paged kernels' accesses against: entry `at` of the page
+// tables, 16 bytes of the queries from element `at`, row `at` of the outputs or of a part
+// (its number and its row).
+__device__ __forceinline__ bool entry_in_bounds(const PagedAttnParams& p, int64_t at) {
+  return in_bounds(at >= 0 && at < (p.batch - 1) * p.table_stride + p.table_width, p.err);
+}
+__device__ __forceinline__ bool q_in_bounds(const PagedAttnParams& p, int64_t at) {
+  return in_bounds(at >= 0 && at + 8 <= p.q_elems, p.err);
+}
+__device__ __forceinline__ bool out_in_bounds(const PagedAttnParams& p, bool whole, int part, int64_t row) {
+  return in_bounds(whole      ? row >= 0 && row < p.rows_total
+                   : p.shared ? part >= 0 && part < p.n_prefix && row >= 0 && row < p.rows_total
+                              : part >= 0 && part < p.max_chunks && row >= 0 && row < (int64_t)p.n_q * p.hq,
+                   p.err);
+}
 constexpr int kPagedUnit = 32;  // a whole number of any instance's tiles
 __device__ __forceinline__ int paged_units(int len, int prefix) {
   return len > prefix ? (len - prefix + kPagedUnit - 1) / kPagedUnit : 0;

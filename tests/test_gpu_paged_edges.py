@@ -190,6 +190,22 @@ def test_one_key_above_all_others(qps, d, kf, vf, n_q, group, above):  # noqa: F
     assert_parity(o, lse, ro, rl, (d, kf, vf, n_q, group, above))
 
 
+@pytest.mark.parametrize("page", [128, 256, 512, 1024])
+@pytest.mark.parametrize("d,kf,vf,n_q,group", [(64, "f16", "f16", 5, 4), (128, "f16", "f16", 9, 4), (128, "q8_0", "tq3", 9, 4),
+                                               (256, "f16", "q8_0", 3, 4), (512, "q8_0", "tq2", 5, 4), (128, "q8_0", "q8_0", 1, 4)])
+def test_large_pages(qps, page, d, kf, vf, n_q, group):  # noqa: F811
+    """Pages as large as a tile and larger: every offset in a page, prefix and own positions."""
+    hkv, common = 2, 2 * page
+    rot, ora = _rotations(d, "whole")
+    lens = [common + 5 * page // 2 + 3, common + page, common + page + 1, common - 30]
+    cache, table = _cache_of(qps, kf, vf, lens, page, hkv, d, page + d, rot, common)
+    q = torch.randn((len(lens), n_q, hkv * group, d), generator=torch.Generator().manual_seed(d)).half().cuda()
+    ro, rl = _want(cache, q, table, lens, d ** -0.5, 0.0, True, ora)
+    for shared in (0, common):
+        o, lse = _run(qps, q, cache, table, lens, scale=d ** -0.5, causal=True, shared_len=shared, out_dtype=torch.float32)
+        assert_parity(o, lse, ro, rl, (d, kf, vf, n_q, group, page, shared))
+
+
 def _child(code):
     res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert res.returncode == 0 and "child ok" in res.stdout, (res.stdout + res.stderr)[-3000:]
