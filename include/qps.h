@@ -434,7 +434,8 @@ typedef struct qps_paged_attn_args {
   void* o;                   /* device, [batch*n_q*hq][D] of o_dtype, rows as in qps_attn_args */
   float* lse;                /* device, f32 [batch*n_q*hq] */
   void* workspace;           /* device, 256-byte aligned, as large as qps_attn_paged_plan says;
-                                calls that overlap on the GPU need one each */
+                                calls that overlap on the GPU need one each.  o, lse and the
+                                workspace lie apart from one another and from q */
   size_t workspace_bytes;
 } qps_paged_attn_args;
 

@@ -323,6 +323,11 @@ qps_status launch_paged(const PagedAttnParams& p, cudaStream_t s) {
   }
 }
 
+bool meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char *pa = (const char*)a, *pb = (const char*)b;
+  return pa < pb + nb && pb < pa + na;
+}
+
 qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   Plan pl;
   qps_status st = plan_paged(a, &pl);
@@ -333,6 +338,15 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
     return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: workspace missing or smaller than qps_attn_paged_plan reports");
   if (!aligned_to(a->workspace, 256)) return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: workspace must be 256-byte aligned");
   PagedAttnParams& p = pl.p;
+  // what is written lies apart from the queries (read until the last CTA) and from the rest
+  const int64_t o_bytes = p.rows_total * p.d * dtype_bytes(a->o_dtype);
+  const struct { const void* at; int64_t bytes; } out[3] = {
+      {a->o, o_bytes}, {a->lse, p.rows_total * (int64_t)sizeof(float)}, {a->workspace, (int64_t)pl.bytes}};
+  for (int i = 0; i < 3; ++i) {
+    if (meet(out[i].at, out[i].bytes, a->q, p.q_elems * (int64_t)sizeof(__half)) ||
+        meet(out[i].at, out[i].bytes, out[(i + 1) % 3].at, out[(i + 1) % 3].bytes))
+      return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: o, lse and workspace overlap one another or q");
+  }
   p.err = device_error_word();
   if (!p.err) return fail(QPS_ERR_CUDA, "attn_decode_paged: cannot allocate the device error word");
   char* ws = reinterpret_cast<char*>(a->workspace);

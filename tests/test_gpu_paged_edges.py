@@ -365,3 +365,29 @@ def test_fault_arguments(qps):  # noqa: F811
             qps.paged_inject_fault(tile, ms)
     qps.paged_inject_fault(3, 5)
     qps.paged_inject_fault(-1)  # disarmed
+
+
+def test_outputs_lie_apart(qps):  # noqa: F811
+    """Outputs over the queries, or over one another, are refused."""
+    d, hkv, page, batch, hq = 128, 2, 64, 2, 4
+    cache, table = _cache_of(qps, "f16", "f16", [70, 90], page, hkv, d, 3)
+    raw = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    q = raw[4096:4096 + batch * hq * d * 2].view(torch.float16).view(batch, hq, d)
+    lens, rows = torch.tensor([70, 90], dtype=torch.int32).cuda(), batch * hq
+    o = lambda at: raw[at:at + rows * d * 2].view(torch.float16).view(rows, d)  # noqa: E731
+    lse = lambda at: raw[at:at + rows * 4].view(torch.float32)  # noqa: E731
+    ws = raw[1 << 16:]
+    for kw, ok in ((dict(o=o(4096)), False), (dict(o=o(4096 + 16)), False), (dict(o=o(4096 + rows * d * 2), lse=lse(0)), True),
+                   (dict(o=o(8192), lse=lse(8192 + rows * d * 2 - 4)), False), (dict(lse=lse(4096)), False),
+                   (dict(workspace=ws, o=o(1 << 16)), False), (dict(workspace=ws, lse=lse((1 << 16) + 256)), False),
+                   (dict(workspace=ws, o=o(8192), lse=lse(0)), True), (dict(workspace=raw[4096:]), False)):
+        a = qps.paged_attn_args(q, cache, table.cuda(), lens, scale=0.1, **kw)
+        if "workspace" in kw:
+            a.workspace_bytes = min(a.workspace_bytes, 1 << 19)
+        if ok:
+            qps.attn_decode_paged(a)
+            continue
+        with pytest.raises(qps.QpsError) as e:
+            qps.attn_decode_paged(a)
+        assert e.value.status == 1, kw
+    torch.cuda.synchronize()
