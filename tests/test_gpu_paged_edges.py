@@ -391,3 +391,31 @@ def test_outputs_lie_apart(qps):  # noqa: F811
             qps.attn_decode_paged(a)
         assert e.value.status == 1, kw
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d,kf,vf,n_q,group,pages", [(512, "f16", "f16", 1, 4, 700), (512, "f16", "q8_0", 5, 4, 700),
+                                                     (512, "q8_0", "tq3", 5, 4, 1400), (128, "f16", "f16", 9, 4, 2500),
+                                                     (128, "q8_0", "q8_0", 1, 4, 5000), (64, "f16", "f16", 5, 4, 5000)])
+def test_cache_past_32_bits(qps, d, kf, vf, n_q, group, pages):  # noqa: F811
+    """Pages whose first byte, and for the largest planes first element, is past 2^32: appended
+    to and attended at both ends of the cache."""
+    hkv, page, n = 8, 1024, 1500
+    rot, ora = _rotations(d, "whole")
+    cache = qps.PagedKV.empty(kf, vf, pages, page, hkv, d, signs=_lib_rot(qps, rot))
+    assert cache.k_planes[0].numel() * cache.k_planes[0].element_size() > 1 << 32
+    table = torch.tensor([[pages - 1, 0], [1, pages - 2]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(d)
+    x = torch.randn((2, n, 2 * hkv, d), generator=g).half().cuda()
+    for b in range(2):
+        at = torch.arange(n)
+        slots = table[b].long()[at // page] * page + at % page
+        qps.kv_append_paged(qps.paged_append_args(cache, x[b, :, :hkv], x[b, :, hkv:], slots.cuda()))
+    q = torch.randn((2, n_q, hkv * group, d), generator=g).half().cuda()
+    o, lse = _run(qps, q, cache, table, [n, n], scale=d ** -0.5, causal=True, out_dtype=torch.float32)
+    used = [pages - 1, 0, 1, pages - 2]  # (the oracle reads these four alone)
+    small = qps.PagedKV(kf, vf, [p[used].contiguous() for p in cache.k_planes], [p[used].contiguous() for p in cache.v_planes],
+                        signs=_lib_rot(qps, rot))
+    del cache
+    ro, rl = _want(small, q, torch.tensor([[0, 1], [2, 3]], dtype=torch.int32), [n, n], d ** -0.5, 0.0, True, ora)
+    assert_parity(o, lse, ro, rl, (d, kf, vf))
+
