@@ -1802,11 +1802,14 @@ qps_status launch_mma_t(const P& p, cudaStream_t s) {
   return QPS_OK;
 }
 
-// The most n-tiles an instance is called with (mma_tile_rows; a paged cache in fp16 sends
-// more rows than this to attn_tm.cuh).
+// The most n-tiles an instance is called with (mma_tile_rows; a paged cache sends more rows
+// than this to attn_tm.cuh or attn_tt.cuh, see attn_paged.cu).
 template <int D, int KF, int VF, class P>
 constexpr int most_ntw() {
-  if (std::is_same<P, PagedAttnParams>::value && KF == QPS_FMT_F16 && VF == QPS_FMT_F16 && D <= 128) return D == 64 ? 2 : 1;
+  if (std::is_same<P, PagedAttnParams>::value) {
+    if (KF == QPS_FMT_F16 && VF == QPS_FMT_F16 && D <= 128) return D == 64 ? 2 : 1;
+    if (D == 128 && !is_tq(VF)) return 2;
+  }
   return D <= 128 ? 3 : 1;
 }
 

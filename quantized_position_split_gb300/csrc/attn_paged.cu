@@ -172,13 +172,18 @@ constexpr int kMinPositions = 128, kMinMany = 512;
 // that it works with.  The tcgen05 kernels cost the same for few rows as for many; the
 // mma.sync kernel reads a chunk once for each 8, 16 or 24 rows.  16 sequences of 8192
 // positions, us, tcgen05 against mma.sync:
-//   f16 / f16, 8 heads of 128:    12 rows 101 / 114, 24 rows 108 / 131, 40 rows 117 / 200
-//   f16 / f16, 8 heads of 64:     16 rows 69 / 65, 20 rows 71 / 79, 40 rows 76 / 122
-//   q8_0 / tq3, 8 heads of 128:   24 rows 160 / 145, 32 rows 163 / 219
-//   q8_0 / q8_0, 8 heads of 128:  24 rows 149 / 145, 32 rows 153 / 218
-//   q8_0 / tq3, 4 heads of 256:   8 rows 111 / 74, 9 rows 111 / 178
+//   f16 / f16, 8 heads of 128:    8 rows 99 / 96, 12 rows 101 / 113, 24 rows 107 / 131, 40 rows 116 / 202
+//   f16 / f16, 8 heads of 64:     16 rows 68 / 65, 20 rows 70 / 79, 40 rows 76 / 123
+//   q8_0 / q8_0, 8 heads of 128:  16 rows 109 / 114, 17 rows 137 / 148, 24 rows 143 / 151, 32 rows 147 / 225
+//   f16 / q8_0, 8 heads of 128:   16 rows 108 / 103, 17 rows 116 / 132
+//   q8_0 / f16, 8 heads of 128:   16 rows 100 / 94, 17 rows 111 / 115
+//   q8_0 / tq3, 8 heads of 128:   24 rows 156 / 149, 32 rows 163 / 224
+//   f16 / tq3, 8 heads of 128:    24 rows 135 / 136
+//   q8_0 / tq3, 4 heads of 256:   8 rows 110 / 75, 9 rows 110 / 179
 //   f16 / f16, 4 heads of 256:    8 rows 165 / 93, 9 rows 165 / 170
-//   q8_0 / tq3, 2 heads of 512:   8 rows 87 / 63, 9 rows 87 / 120
+//   q8_0 / tq3, 2 heads of 512:   8 rows 85 / 63, 9 rows 86 / 120
+// (A TurboQuant K, a TQ4 V and compressed rows at head_dim 64 have no tcgen05 instance, which
+// is not a measured choice: any number of rows goes to the mma.sync kernel.)
 struct Shape {
   PagedKernel kernel;
   int rows, tile, ctas_per_sm;
@@ -187,7 +192,7 @@ Shape shape_for(const PagedKv& kv, int rows, bool shared) {
   if (kv.kfmt == QPS_FMT_F16 && kv.vfmt == QPS_FMT_F16 && kv.d <= 128) {
     if (rows > (kv.d == 64 ? 16 : 8)) return {kTm, 128, 128, 1};
   } else if (kv.d >= 128 && !is_tq(kv.kfmt) && kv.vfmt != QPS_FMT_TQ4) {
-    if (rows > (kv.d == 128 ? 24 : 8)) return {kTt, 64, 128, 1};
+    if (rows > (kv.d > 128 ? 8 : is_tq(kv.vfmt) ? 24 : 16)) return {kTt, 64, 128, 1};
   }
   const int n = mma_tile_rows(kv.d, rows, shared);
   return {kMma, n, 32, mma_ctas_per_sm(kv.d, n / 8, kv.vfmt)};

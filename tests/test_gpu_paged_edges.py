@@ -79,8 +79,9 @@ def test_prefix_behind_a_padding_row(qps, d, kf, vf, batch, group):  # noqa: F81
 
 
 # (n_q, group) on both sides of the rows at which the kernel changes
-SIDES = [(128, "q8_0", "f16", 6, 4), (128, "q8_0", "f16", 5, 5), (128, "q8_0", "tq3", 5, 5), (256, "q8_0", "tq3", 2, 4),
-         (256, "q8_0", "f16", 3, 3), (512, "q8_0", "q8_0", 2, 4), (512, "q8_0", "q8_0", 3, 3), (512, "q8_0", "tq2", 13, 4)]
+SIDES = [(128, "q8_0", "f16", 4, 4), (128, "q8_0", "f16", 6, 4), (128, "q8_0", "f16", 5, 5), (128, "q8_0", "tq3", 5, 5),
+         (256, "q8_0", "tq3", 2, 4), (256, "q8_0", "f16", 3, 3), (512, "q8_0", "q8_0", 2, 4), (512, "q8_0", "q8_0", 3, 3),
+         (512, "q8_0", "tq2", 13, 4)]
 
 
 @pytest.mark.parametrize("d,kf,vf,n_q,group", SIDES)
