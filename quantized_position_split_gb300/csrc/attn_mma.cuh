@@ -1149,8 +1149,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
           if (t + 8 >= lim[nt][0]) x[sb][2] = -INFINITY;
           if (t + 8 >= lim[nt][1]) x[sb][3] = -INFINITY;
         } else {
-        if (!in_g[sb]) x[sb][0] = x[sb][1] = -INFINITY;
-        if (!in_g8[sb]) x[sb][2] = x[sb][3] = -INFINITY;
+          if (!in_g[sb]) x[sb][0] = x[sb][1] = -INFINITY;
+          if (!in_g8[sb]) x[sb][2] = x[sb][3] = -INFINITY;
         }
         if constexpr (CAUSAL) {
           // position t is visible to CTA row r (query token r / group) iff
@@ -1751,15 +1751,16 @@ qps_status launch_mma_t(const P& p, cudaStream_t s) {
     if constexpr (G::PVA::TMA)
       if (!map(&maps.va, p.v.aux, G::V_ARB, G::PVA::IB, G::PVA::SW)) return QPS_ERR_CUDA;
   } else {
-  if (!encode_plane_map(&maps.k, p.k.data, G::K_RB, p.end, p.hkv, p.k.head, nb, p.k.batch, G::PK::IB, G::PK::SW, G::TT) ||
-      !encode_plane_map(&maps.v, p.v.data, G::V_RB, p.end, p.hkv, p.v.head, nb, p.v.batch, G::PV::IB, G::PV::SW, G::TT))
-    return QPS_ERR_CUDA;
-  if constexpr (G::PKA::TMA)
-    if (!encode_plane_map(&maps.ka, p.k.aux, G::K_ARB, p.end, p.hkv, p.k.head, nb, p.k.batch, G::PKA::IB, G::PKA::SW, G::TT))
+    auto map = [&](TensorMap* m, const KvSide& side, const void* base, int rb, int ib, int sw) {
+      return encode_plane_map(m, base, rb, p.end, p.hkv, side.head, nb, side.batch, ib, sw, G::TT);
+    };
+    if (!map(&maps.k, p.k, p.k.data, G::K_RB, G::PK::IB, G::PK::SW) ||
+        !map(&maps.v, p.v, p.v.data, G::V_RB, G::PV::IB, G::PV::SW))
       return QPS_ERR_CUDA;
-  if constexpr (G::PVA::TMA)
-    if (!encode_plane_map(&maps.va, p.v.aux, G::V_ARB, p.end, p.hkv, p.v.head, nb, p.v.batch, G::PVA::IB, G::PVA::SW, G::TT))
-      return QPS_ERR_CUDA;
+    if constexpr (G::PKA::TMA)
+      if (!map(&maps.ka, p.k, p.k.aux, G::K_ARB, G::PKA::IB, G::PKA::SW)) return QPS_ERR_CUDA;
+    if constexpr (G::PVA::TMA)
+      if (!map(&maps.va, p.v, p.v.aux, G::V_ARB, G::PVA::IB, G::PVA::SW)) return QPS_ERR_CUDA;
   }
   auto kern = attn_mma_kernel<D, KF, VF, NTW, CAUSAL, P>;
   // Ask for enough shared memory that no more than G::CTAS CTAs fit on an SM: under

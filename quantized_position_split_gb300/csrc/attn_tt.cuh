@@ -1,7 +1,9 @@
-// Decode attention of up to 64 query rows per KV head on the fifth-generation tensor cores,
-// over pages of any width and format: verify batches and shared prefixes of compressed
+// Decode attention of many query rows, up to 64 a CTA, on the fifth-generation tensor cores,
+// over pages of head_dim 128, 256 and 512 with K F16 / Q8_0 and V F16 / Q8_0 / TQ3 / TQ2 (but
+// F16 / F16 at 128, which is attn_tm.cuh's): verify batches and shared prefixes of compressed
 // caches, where the products on the older path (mma.sync, 8 rows a warp) decode the same
-// positions again for every 8 to 24 rows.
+// positions again for every 8 to 24 rows, as they still do for a TurboQuant K, a TQ4 V and
+// compressed rows of head_dim 64.
 //
 // The products run with the positions and the head dimension on the wide side (M = 128)
 // and the query rows on the narrow one (N = 16 .. 64), so their time follows the number of
@@ -30,7 +32,9 @@
 // one vote a tile, and on a raise the maxima are taken, O and the sums rescaled.
 //
 // Measured: four sequences of five tokens and 30000 to 32768 positions, two KV heads of 512,
-// q8_0 / tq3 (40 rows): 88 us, 2.1 TB/s; bound by instruction issue, 20 warps of four roles.
+// q8_0 / tq3 (40 rows): 87 us, 2.1 TB/s.  57% of the issue slots are used and the tensor pipe
+// runs 20% of the time: no unit is at its limit, the roles wait for one another (each tile's
+// softmax behind its page and norm loads and two readings of S).
 //
 // Roles: warp 0 issues the products, warps 2 and 3 the boxes of K and V, warps 4-11 are the
 // softmax (two groups of rows), 12-15 decode K and 16-19 V.  Waits are bounded as in
@@ -922,7 +926,7 @@ qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
   return QPS_OK;
 }
 
-// Every format pairing of one head_dim.
+// The format pairings of one head_dim.
 template <int D>
 qps_status launch_tt_d(const PagedAttnParams& p, cudaStream_t s) {
 #define QPS_TT_CASE(KF, VF) \

@@ -1,5 +1,4 @@
-// The paged attention kernel for up to 64 rows per CTA of any format, head_dim 512 (see
-// attn_tt.cuh).
+// The many-row paged attention kernel over compressed and fp16 pages, head_dim 512 (see attn_tt.cuh).
 #include "attn_tt.cuh"
 
 namespace qps {
