@@ -451,6 +451,9 @@ QPS_API qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* wor
  * device from kv_lens, so a captured graph replays with new lengths, tables and rows.
  * With shared_len the prefix's chunks are attended once for the rows of the whole batch
  * ([POLY, "S1 — SharedKVPool"]).  A table entry outside [0, n_pages) reads as zero rows.
+ * Logits, softmax sums and O are float32; the operands of the product with V are fp16, each
+ * rounded once: the weights (times the norm of a TurboQuant value; in two parts for a q8_0
+ * V), and q8_0 values (code x scale, scales above 515.5 taken as that).
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 QPS_API qps_status qps_attn_decode_paged(const qps_paged_attn_args* a, void* stream);
 

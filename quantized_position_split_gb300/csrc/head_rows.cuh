@@ -19,11 +19,11 @@
 //   * the token's cosines and sines, and the weights, are loaded once per warp and stay in
 //     registers for all of its heads;
 //   * products and sums run two to an instruction (f32x2, each half rounded to nearest).
-// Measured: 8192 tokens x 48 heads of 128, fp16, normed and rotated: 40.4 us, 5.1 TB/s (HBM
-// and instruction issue together; steps of a warp over several tokens were no faster, nor
-// were other counts of rounds under way and blocks per SM).  8191 tokens x 8 heads of 128,
-// K and V, bf16 into q8_0: 24.0 us, 2.3 TB/s, bound by instruction issue (norm, rotation and
-// the encoder, each in its fixed order of operations).
+// Measured: 8192 tokens x 48 heads of 128, fp16, normed and rotated: 40.7 us, 5.1 TB/s (55% of
+// the issue slots; steps of a warp over several tokens were no faster, nor were other counts of
+// rounds under way and blocks per SM; the instance spills 28 bytes of stores, 48 of loads).
+// 8191 tokens x 8 heads of 128, K and V, bf16 into q8_0: 24.2 us, 2.3 TB/s, 50% of the issue
+// slots: held to 80 registers, the instance spills 152 bytes of stores and 104 of loads.
 // One token: 2.0 us on the GPU, launch and load latency.
 #pragma once
 
