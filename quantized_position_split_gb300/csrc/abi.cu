@@ -107,8 +107,13 @@ unsigned long long context_id() {
   unsigned long long id = 0;
   if (!fn) return 0;
   if (fn(nullptr, &id) == CUDA_SUCCESS) return id;
-  // (no context is current before the runtime's first call)
-  return cudaFree(nullptr) == cudaSuccess && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
+  // (no context is current before the thread's first call of the runtime; relaxed, as another
+  // thread may be capturing, whose capture this would end otherwise)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return 0;
+  const bool ok = cudaFree(nullptr) == cudaSuccess;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return ok && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
 }
 }  // namespace
 

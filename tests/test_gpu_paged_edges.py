@@ -238,6 +238,41 @@ print("child ok")
 """)
 
 
+def test_a_thread_first_call_beside_a_capture(qps):  # noqa: F811
+    """A thread whose first CUDA call is the library's, on a stream of its own, while another
+    thread captures in the global mode: neither disturbs the other."""
+    _child("""
+import threading, torch
+import quantized_position_split_gb300 as qps
+x = torch.randn(4, 2, 128, device="cuda").half()
+w = (x.float() / (x.float().square().mean(-1, keepdim=True) + 1e-6).sqrt()).cpu()
+a, b = (qps.qk_rope_args(x, norm=True) for _ in range(2))
+side, other = torch.cuda.Stream(), torch.cuda.Stream()
+qps.qk_norm_rope(a)
+torch.cuda.synchronize()
+a._out[0].zero_()
+torch.cuda.synchronize()
+raw, errors = other.cuda_stream, []
+def call():
+    try:
+        qps.qk_norm_rope(b, stream=raw)
+    except Exception as e:
+        errors.append(e)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=side, capture_error_mode="global"):
+    qps.qk_norm_rope(a)
+    t = threading.Thread(target=call)
+    t.start()
+    t.join()
+assert not errors, errors
+g.replay()
+torch.cuda.synchronize()
+for blk in (a, b):
+    assert (blk._out[0].float().cpu() - w).abs().max() < 4e-3
+print("child ok")
+""")
+
+
 def test_attention_in_a_second_context(qps):  # noqa: F811
     """A second context of a device that has run the same kernels: they are set up there too, and
     what they report goes to a word of that context."""
