@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     if (!p.shared) {  // chunk number `split` of the batch: find its sequence and positions
       const PagedChunk ch = paged_find(p, split, lane);
       if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
-      if (ch.first && head == 0 && rg == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err)) p.chunks[ch.b] = make_int2(split, ch.count);
+      if (ch.first && head == 0 && rg == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err))
+        p.chunks[ch.b] = make_int2(split, ch.count);
       bz = ch.b;
       whole = ch.whole;
       t0 = ch.t0;

@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
-    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err)) p.chunks[ch.b] = make_int2(split, ch.count);
+    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err))
+      p.chunks[ch.b] = make_int2(split, ch.count);
     bz = ch.b;
     t0 = ch.t0;
     t1 = ch.t1;

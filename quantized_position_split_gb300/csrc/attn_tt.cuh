@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   } else {
     const PagedChunk ch = paged_find(p, split, lane);
     if (ch.b < 0) return;  // more CTAs than chunks (every warp finds the same)
-    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err)) p.chunks[ch.b] = make_int2(split, ch.count);
+    if (ch.first && head == 0 && row0 == 0 && threadIdx.x == 0 && in_bounds(ch.b < p.batch, p.err))
+      p.chunks[ch.b] = make_int2(split, ch.count);
     bz = ch.b;
     t0 = ch.t0;
     t1 = ch.t1;
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       auto put = [&](uint8_t* slot, int g, int c, const uint32_t* o) {
         if (in_bounds(g < 2 && c < 8 && slot - smem + kSlot <= G::KRAW, p.err))
           *reinterpret_cast<uint4*>(slot + g * (kSlot / 2) + tok * 128 + ((c ^ (tok & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
+              make_uint4(o[0], o[1], o[2], o[3]);
       };
       int f = 0;
       bool ok = true;

@@ -76,8 +76,8 @@ bool same_rows(const qps_rows& a, const qps_rows& b, int64_t tokens) {
 }
 // Whether two sets of rows whose extents meet interleave without touching (slices of one
 // projection, side by side or head by head): the same distance of tokens, and no row of one
-// within a row's width of a row of the other.  More heads than this looks through count as
-// touching.
+// within a row's width of a row of the other.  More pairs of heads than this looks through
+// count as touching.
 bool apart(const qps_rows& a, const qps_rows& b, int64_t tokens, int d) {
   const int64_t sa = dtype_bytes(a.dtype), sb = dtype_bytes(b.dtype), t = a.tok_stride * sa;
   if (tokens > 1 && (t != b.tok_stride * sb || t <= 0)) return false;
@@ -87,15 +87,21 @@ bool apart(const qps_rows& a, const qps_rows& b, int64_t tokens, int d) {
     const int64_t off = (base % t + t) % t;
     if (off >= (a.heads - 1) * ha + wa && off + (b.heads - 1) * hb + wb <= t) return true;
   }
+  auto touch = [&](int64_t x) {  // rows x bytes apart, or any token distance n, |n| < tokens, more?
+    const int64_t n = tokens > 1 ? std::max(-(tokens - 1), std::min(tokens - 1, -(x / t))) : 0;
+    for (int64_t m = std::max(n - 1, -(tokens - 1)); m <= std::min(n + 1, tokens - 1); ++m)
+      if (x + m * t > -wb && x + m * t < wa) return true;
+    return false;
+  };
+  if (ha == hb) {  // only the distance of the heads counts
+    for (int64_t i = -(int64_t)(a.heads - 1); i < b.heads; ++i)
+      if (touch(base + i * hb)) return false;
+    return true;
+  }
   if ((int64_t)a.heads * b.heads > 1 << 16) return false;
   for (int64_t i = 0; i < a.heads; ++i)
-    for (int64_t j = 0; j < b.heads; ++j) {
-      const int64_t x = base + j * hb - i * ha;  // of b's row (0, j) from a's (0, i)
-      // some token distance n, |n| < tokens, with -wb < x + n t < wa?
-      const int64_t n = tokens > 1 ? std::max(-(tokens - 1), std::min(tokens - 1, -(x / t))) : 0;
-      for (int64_t m = std::max(n - 1, -(tokens - 1)); m <= std::min(n + 1, tokens - 1); ++m)
-        if (x + m * t > -wb && x + m * t < wa) return false;
-    }
+    for (int64_t j = 0; j < b.heads; ++j)
+      if (touch(base + j * hb - i * ha)) return false;
   return true;
 }
 // Whether no row of the set touches another of it.
