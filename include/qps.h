@@ -79,7 +79,7 @@
 extern "C" {
 #endif
 
-#define QPS_ABI_VERSION 9
+#define QPS_ABI_VERSION 10
 
 #if defined(__GNUC__)
 #define QPS_API __attribute__((visibility("default")))
@@ -437,6 +437,14 @@ typedef struct qps_paged_attn_args {
                                 calls that overlap on the GPU need one each.  o, lse and the
                                 workspace lie apart from one another and from q */
   size_t workspace_bytes;
+  /* Sliding window (0: none).  Query token i of sequence b, its position
+   * q = kv_lens[b] - n_q + i, sees the positions of (q - window, q] and those of
+   * [0, sinks) up to q; `causal` is needed where n_q > 1.  Table entries of pages that no
+   * query token sees are not read (their pages may have been given back, see
+   * qps_kv_extend_paged).  A call with a window reads every sequence through its own entries:
+   * shared_len then saves nothing.  Zero-initialised fields keep the plain attention. */
+  int32_t window;
+  int32_t sinks;             /* unused without a window */
 } qps_paged_attn_args;
 
 /* Workspace bytes of qps_attn_decode_paged for these args (host only, no launch; o, lse

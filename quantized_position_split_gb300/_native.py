@@ -224,6 +224,8 @@ class PagedAttnArgs(ctypes.Structure):
         ("lse", c_void_p),
         ("workspace", c_void_p),
         ("workspace_bytes", c_size_t),
+        ("window", c_int32),
+        ("sinks", c_int32),
     ]
 
 

@@ -425,6 +425,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
       t1 = min(t1, (int64_t)pre.len);
     }
   }
+  PagedWindow win = {0, 0, 0, 0};
+  if constexpr (PAGED) win = paged_window(p, bz);
 
   // CTA row rr: (batch entry, head) in a shared tile; (query token rr / group, head)
   // of batch entry bz otherwise
@@ -614,8 +616,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   };
   auto page_of = [&](int64_t t) -> int {
     if constexpr (PAGED) {
-      if (t >= t1 || !entry_in_bounds(p, bz * p.table_stride + (t >> p.page_shift))) return (int)p.n_pages;
-      const int pg = p.table[(int64_t)bz * p.table_stride + (t >> p.page_shift)];
+      const int at = t < t1 ? paged_true(win, (int)t) >> p.page_shift : 0;
+      if (t >= t1 || paged_unseen(p, win, (int)t, min(1 << p.page_shift, TT)) || !entry_in_bounds(p, bz * p.table_stride + at))
+        return (int)p.n_pages;
+      const int pg = p.table[(int64_t)bz * p.table_stride + at];
       if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
       atomicOr(p.err, kErrIndex);
       return (int)p.n_pages;
@@ -656,7 +660,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     }
     uint8_t* st = wpipe + (k % G::STAGES) * G::STAGE;
     const int64_t tb = tile0 + (int64_t)tile * TT;
-    const int tok = (int)tb;
+    int tok = (int)tb;
+    if constexpr (PAGED) tok = paged_true(win, tok);
     const uint32_t bar = bars + (k % G::STAGES) * 8;
     if (lane == 0) mbar_expect_tx(bar, G::TX);
     __syncwarp();
@@ -813,10 +818,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         const int e = (row0 + nt * 8 + 2 * c + u) / p.group;
         const int i = p.shared ? e % p.n_q : e, b = p.shared ? e / p.n_q : bz;
         int n = (int)t1;
-        if (p.shared || p.causal) {
+        if (p.shared || p.causal || p.window) {
           n = b < p.batch ? paged_len(p, b) : 0;
           if (p.causal) n += i + 1 - p.n_q;
-          n = min(n, (int)t1);
+          if (p.window == 0) n = min(n, (int)t1);  // (a window's start is counted from it; chunks end with tiles)
         }
         lim[nt][u] = n;
       }
@@ -1093,6 +1098,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         const __half* nrm = reinterpret_cast<const __half*>(st + G::NORM_OFF);
         n_g[sb] = __half2float(nrm[16 * sb + g]);
         n_g8[sb] = __half2float(nrm[16 * sb + g + 8]);
+        if constexpr (PAGED) {  // (a norm behind the window may be anything: 0 x NaN)
+          if (t_g >= p.sinks && t_g < win.none_lo) n_g[sb] = 0.f;
+          if (t_g + 8 >= p.sinks && t_g + 8 < win.none_lo) n_g8[sb] = 0.f;
+        }
       }
     }
     // The reference maximum of the online softmax is raised only when a tile's maximum
@@ -1149,6 +1158,13 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
           if (t >= lim[nt][1]) x[sb][1] = -INFINITY;
           if (t + 8 >= lim[nt][0]) x[sb][2] = -INFINITY;
           if (t + 8 >= lim[nt][1]) x[sb][3] = -INFINITY;
+          if ((int)tb < win.all_lo) {  // (uniform) the start of the window lies in the tile for some row
+            const int w0 = lim[nt][0] - p.window, w1 = lim[nt][1] - p.window;
+            if (t >= p.sinks && t < w0) x[sb][0] = -INFINITY;
+            if (t >= p.sinks && t < w1) x[sb][1] = -INFINITY;
+            if (t + 8 >= p.sinks && t + 8 < w0) x[sb][2] = -INFINITY;
+            if (t + 8 >= p.sinks && t + 8 < w1) x[sb][3] = -INFINITY;
+          }
         } else {
           if (!in_g[sb]) x[sb][0] = x[sb][1] = -INFINITY;
           if (!in_g8[sb]) x[sb][2] = x[sb][3] = -INFINITY;
@@ -1476,6 +1492,21 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
             if (in_bounds(left >= 0 && OFF + b * (TT * IB) + idx * 16 + 16 <= G::STAGE, p.err))
               *reinterpret_cast<uint4*>(wpipe + (k % G::STAGES) * G::STAGE + OFF + b * (TT * IB) + idx * 16) =
                 make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
+      // The same for positions that no row's window reaches (TurboQuant norms: attend_tile).
+      const int tb = (int)(tile0 + (int64_t)(warp + k * kWarps) * TT);
+      if (tb < win.none_lo && tb + TT > p.sinks && !is_tq(VF)) {
+        constexpr int OFF = VF == QPS_FMT_F16 ? G::V_OFF : G::VA_OFF;
+        constexpr bool BOX = VF == QPS_FMT_F16 || G::PVA::TMA;
+        constexpr int IB = VF == QPS_FMT_F16 ? G::PV::IB : BOX ? G::PVA::IB : G::V_ARB;  // bytes of a row
+        constexpr int NB = VF == QPS_FMT_F16 ? G::PV::NB : 1;
+        const int first = max(0, p.sinks - tb) * (IB / 4), last = min(TT, win.none_lo - tb) * (IB / 4);
+        for (int idx = first + lane; idx < last; idx += 32)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            if (in_bounds(OFF + b * (TT * IB) + idx * 4 + 4 <= G::STAGE, p.err))
+              *reinterpret_cast<uint32_t*>(wpipe + (k % G::STAGES) * G::STAGE + OFF + b * (TT * IB) + idx * 4) = 0u;
         __syncwarp();
       }
     }

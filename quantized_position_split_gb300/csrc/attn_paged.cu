@@ -228,6 +228,8 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
     return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: unknown o_dtype");
   if (!std::isfinite(a->scale) || !std::isfinite(a->softcap))
     return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: scale and softcap must be finite");
+  if (a->window < 0 || a->sinks < 0 || (a->window > 0 && a->n_q > 1 && !a->causal))
+    return fail(QPS_ERR_INVALID_ARG, "attn_decode_paged: window and sinks must be >= 0, and a window of several query tokens causal");
   const int64_t rows_total = (int64_t)a->batch * a->n_q * a->hq;
   if (rows_total > 0x7fffffffLL) return fail(QPS_ERR_UNSUPPORTED, "attn_decode_paged: too many rows");
   const int sms = sm_count_current();
@@ -274,10 +276,15 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
   p.page_shift = kv.page_shift;
   p.table_width = a->table_width;
   p.out_dtype = a->o_dtype;
+  // (a window that no sequence outgrows is none; one that they do leaves no common prefix)
+  const int held = a->table_width << kv.page_shift;
+  p.window = a->window > 0 && a->window < held && a->sinks < held ? a->window : 0;
+  p.sinks = p.window ? a->sinks : 0;
+  p.win_round = 1;
 
   // the prefix: whole tiles of the shared positions (what is left of them is read through
   // each sequence's own entries, which name the same pages)
-  p.prefix_len = a->batch > 1 ? (int)(a->shared_len & ~(int64_t)31) : 0;
+  p.prefix_len = a->batch > 1 && p.window == 0 ? (int)(a->shared_len & ~(int64_t)31) : 0;
   if (p.prefix_len > 0) {
     const int all = a->batch * rows;
     const Shape sh = shape_for(kv, all, true);
@@ -300,8 +307,10 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
     const int least = a->batch >= round ? kMinMany : kMinPositions;
     p.min_units = least / kPagedUnit;
     p.unit_round = sh.tile / kPagedUnit;
-    // chunks of a sequence that fills its table, and of all of them
-    const int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
+    p.win_round = sh.tile;
+    // chunks of a sequence that fills its table (of what its window leaves), and of all of them
+    int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
+    if (p.window) most = std::min<int64_t>(most, (int64_t)p.window + a->n_q + p.sinks + 2 * sh.tile);
     const int64_t each = std::max<int64_t>(1, (most + least - 1) / least);
     p.max_chunks = (int)std::min<int64_t>((int64_t)p.target + a->batch, each * a->batch);
     out->parts = p.n_prefix + (int)std::min<int64_t>(each, p.target + 1);

@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     whole = ch.whole;
   }
   const int ntiles = uniform(t1 > t0 ? (t1 - t0 + kTok - 1) / kTok : 0);  // 0: no own positions
+  const PagedWindow win = paged_window(p, bz);
 
   // ---- barriers, TMEM, queries ---------------------------------------------------------------
   const uint32_t bars = sbase + G::BAR;
@@ -284,9 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
     const int32_t* row = p.table + (int64_t)bz * p.table_stride;
     const int cg = lane % G::CG, r = lane / G::CG;
-    auto has = [&](int j) { return r < nb && t0 + j * kTok + r * br < t1; };
+    auto has = [&](int j) {
+      const int t = t0 + j * kTok + r * br;
+      return r < nb && t < t1 && !paged_unseen(p, win, t, br);
+    };
+    auto at = [&](int j) { return paged_true(win, t0 + j * kTok + r * br); };
     auto entry = [&](int j) {
-      const int i = (t0 + j * kTok + r * br) >> p.page_shift;
+      const int i = at(j) >> p.page_shift;
       return has(j) && entry_in_bounds(p, bz * p.table_stride + i) ? row[i] : 0;
     };
     auto load = [&](const TensorMap* map, uint32_t dst, uint32_t bar, int j, int page) {
@@ -294,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (r < nb && (map != &maps.k || j != p.drop_tile) &&
           in_bounds(cg * (kTok * 128) + (r + 1) * br * 128 <= G::TILE && dst - sbase + G::TILE <= G::BAR && page <= p.n_pages &&
-                        head < p.hkv && ((t0 + j * kTok + r * br) & ((1 << p.page_shift) - 1)) + br <= 1 << p.page_shift,
+                        head < p.hkv && (at(j) & ((1 << p.page_shift) - 1)) + br <= 1 << p.page_shift,
                     p.err))
         tma_load_4d(dst + cg * (kTok * 128) + r * br * 128, map, cg * 128,
-                    (t0 + j * kTok + r * br) & ((1 << p.page_shift) - 1), head, page, bar);
+                    at(j) & ((1 << p.page_shift) - 1), head, page, bar);
     };
     int next = entry(0);
     for (int j = 0; j < ntiles; ++j) {
@@ -354,6 +359,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma::fence_proxy_async();
         __syncwarp();
       }
+      if (t0 + j * kTok < win.none_lo && t0 + (j + 1) * kTok > p.sinks) {  // nor do rows that no window reaches
+        const int tb = t0 + j * kTok;
+        for (int i = max(0, p.sinks - tb) * 8 + lane; i < min(kTok, win.none_lo - tb) * 8; i += 32)
+#pragma unroll
+          for (int cg = 0; cg < G::CG; ++cg)
+            if (in_bounds(cg * (kTok * 128) + i * 16 + 16 <= G::TILE, p.err))
+              *reinterpret_cast<uint4*>(smem + vb + cg * (kTok * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        mma::fence_proxy_async();
+        __syncwarp();
+      }
       if (!(ok = wait(p_ready(w), (j >> 1) & 1, j))) break;
       fence_after();
       const uint32_t d = tmem + G::O_COL + w * D, a = tmem + G::S_COL + w * kTok;
@@ -371,11 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t s_at = tmem + lanes + G::S_COL + w * kTok, o_at = tmem + lanes + G::O_COL + w * D;
     load_q();
-    int lim = 0;  // positions below it are visible to the row
+    int lim = 0, low = 0;  // positions below lim are visible to the row, but for [sinks, low)
     if (rr < p.rows_per_cta) {
       const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
       lim = paged_len(p, b);
       if (p.causal) lim += qi + 1 - p.n_q;
+      if (p.window) low = lim - p.window;
       lim = min(lim, t1);
     }
     constexpr float LOG2E = 1.4426950408889634f;
@@ -393,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Whole tiles of plain logits, the common case, have a body of their own: maxima and
       // exponentials straight from S (a positive scale keeps the order), four chains each,
       // the next 32 columns read beside the present ones' arithmetic.
-      const bool fast = __all_sync(0xffffffffu, first + kTok <= lim || rr >= p.rows_per_cta) && cap <= 0.f && qs >= 0.f;
+      const bool fast = __all_sync(0xffffffffu, (first + kTok <= lim && first >= low) || rr >= p.rows_per_cta) &&
+                        cap <= 0.f && qs >= 0.f;
+      auto hidden = [&](int t) { return t >= lim || (t < low && t >= p.sinks); };
       uint32_t va[32], vb[32];
       float mx = -INFINITY;
       if (fast) {
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (first + 32 * c + i < lim) mx = fmaxf(mx, logit(va[i]));
+            if (!hidden(first + 32 * c + i)) mx = fmaxf(mx, logit(va[i]));
         }
         __syncwarp();
       }
@@ -486,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a = ex2(logit(va[2 * i]) - ms), b = ex2(logit(va[2 * i + 1]) - ms);
-            if (first + 32 * c + 2 * i >= lim) a = 0.f;
-            if (first + 32 * c + 2 * i + 1 >= lim) b = 0.f;
+            if (hidden(first + 32 * c + 2 * i)) a = 0.f;
+            if (hidden(first + 32 * c + 2 * i + 1)) b = 0.f;
             sum += a + b;
             pk[i] = mma::pack_h2(a, b);
           }

@@ -117,6 +117,9 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     whole = ch.whole;
   }
   const int ntiles = uniform(t1 > t0 ? (t1 - t0 + kTile - 1) / kTile : 0);  // 0: no own positions
+  const PagedWindow win = paged_window(p, bz);
+  // (no row sees the position: behind the end, or behind every row's window)
+  auto unseen = [&](int t) { return t >= t1 || paged_unseen(p, win, t, 1); };
   const int nrows = min(kN, p.rows_per_cta - row0);
   const int n16 = uniform((nrows + 15) & ~15);  // N of the products
   // TMEM columns: S (two buffers), K (two slots of 32 hi and 32 lo), O
@@ -235,6 +238,15 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
               mma::fence_proxy_async();
               __syncwarp();
             }
+            const int tb = t0 + (j - 1) * kTile;
+            if (tb < win.none_lo && tb + kTile > p.sinks) {  // nor do rows that no window reaches
+              for (int i = max(0, p.sinks - tb) * 8 + lane; i < min(kTile, win.none_lo - tb) * 8; i += 32)
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                  *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+              mma::fence_proxy_async();
+              __syncwarp();
+            }
           }
           const uint64_t a = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
           fence_after();
@@ -266,9 +278,12 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     const bool signs = v && VF == QPS_FMT_TQ3;
     const int ring = !v ? KN : VDEC ? VN : kSlots, nc = v ? G::VC : G::KC, count = ntiles * nc;
     const int grp = lane / nb, r = lane % nb;  // (16 boxes at most, one a lane)
-    auto has = [&](int j) { return grp < groups && t0 + j * kTile + r * br < t1; };
+    auto has = [&](int j) {
+      const int t = t0 + j * kTile + r * br;
+      return grp < groups && t < t1 && !paged_unseen(p, win, t, br);
+    };
     auto entry = [&](int j) {
-      const int i = (t0 + j * kTile + r * br) >> p.page_shift;
+      const int i = paged_true(win, t0 + j * kTile + r * br) >> p.page_shift;
       return has(j) && entry_in_bounds(p, bz * p.table_stride + i) ? table[i] : 0;
     };
     int next = entry(0), page = 0;
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           for (int i = 1; i < 4; ++i) arrive(bar);  // (a slot's barrier counts four)
       }
       __syncwarp();
-      const int y = (t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
+      const int y = paged_true(win, t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
       // the box stays in its page and its stage (or slot), the stage in its ring
       const bool fits = in_bounds(
           grp >= groups || (y + br <= 1 << p.page_shift && page <= p.n_pages && head < p.hkv &&
@@ -316,8 +331,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     auto load_scales = [&](int j, const void* aux, uint32_t (&w)[W]) {
 #pragma unroll
       for (int i = 0; i < W; ++i) w[i] = 0u;
-      const int at = t0 + j * kTile + tok;
-      if (j >= ntiles || at >= t1) return;
+      if (j >= ntiles || unseen(t0 + j * kTile + tok)) return;
+      const int at = paged_true(win, t0 + j * kTile + tok);
       if (!entry_in_bounds(p, bz * p.table_stride + (at >> p.page_shift))) return;
       const int pg = table[at >> p.page_shift];
       if ((uint64_t)(int64_t)pg >= (uint64_t)p.n_pages) return;  // (reported by the boxes' warps)
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
         n = paged_len(p, b);
         if (p.causal) n += qi + 1 - p.n_q;
-        n = min(n, t1);
+        if (p.window == 0) n = min(n, t1);  // (a window's start is counted from it; chunks end with tiles)
       }
       lim[tid] = n;
       mneg[tid] = kNone;
@@ -600,16 +615,18 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
       const int at = t0 + j * kTile + tl;
-      const bool cut = t0 + (j + 1) * kTile > least;  // (uniform) some row does not see the whole tile
+      // (uniform) some row does not see the whole tile
+      const bool cut = t0 + (j + 1) * kTile > least || t0 + j * kTile < win.all_lo;
       float norm = 1.f;
       if constexpr (is_tq(VF)) {  // (0 behind the end and for a bad page: nothing there is read)
         norm = 0.f;
-        if (at < t1 && entry_in_bounds(p, bz * p.table_stride + (at >> p.page_shift))) {
-          const int pg = table[at >> p.page_shift];
+        const int to = paged_true(win, at);
+        if (!unseen(at) && entry_in_bounds(p, bz * p.table_stride + (to >> p.page_shift))) {
+          const int pg = table[to >> p.page_shift];
           if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages &&
-              in_bounds((((int64_t)pg * p.hkv + head) << p.page_shift) + (at & ((1 << p.page_shift) - 1)) < p.v_rows, p.err))
+              in_bounds((((int64_t)pg * p.hkv + head) << p.page_shift) + (to & ((1 << p.page_shift) - 1)) < p.v_rows, p.err))
             norm = __half2float(reinterpret_cast<const __half*>(norms)[(((int64_t)pg * p.hkv + head) << p.page_shift) +
-                                                                      (at & ((1 << p.page_shift) - 1))]);
+                                                                      (to & ((1 << p.page_shift) - 1))]);
         }
       }
       // (a TurboQuant V: the reference bounds P x norm, the operand; see attn_mma.cuh)
@@ -641,8 +658,10 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         }
         if (cut) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (at >= lim[r0 + 16 * c + i]) x[i] = -INFINITY;
+          for (int i = 0; i < 16; ++i) {
+            const int n = lim[r0 + 16 * c + i];
+            if (at >= n || (p.window && at >= p.sinks && at < n - p.window)) x[i] = -INFINITY;
+          }
         }
       };
       bool over = false;

@@ -27,6 +27,8 @@ struct PagedAttnParams : AttnParams {
   int64_t n_pages;
   int page_shift, table_width;
   int prefix_len;     // positions attended by the prefix launch (a multiple of 32)
+  int window, sinks;  // sliding window (0: none; then prefix_len is 0) and first positions that stay visible
+  int win_round;      // what the window leaves out is a multiple of this many positions (a power of two)
   int target;         // chunks per (KV head, row group) the sequences are cut into, about
   int min_units;      // smallest chunk, in units
   int unit_round;     // chunks are multiples of this many units (a power of two)
@@ -51,12 +53,51 @@ struct PagedAttnParams : AttnParams {
 // unit_round), sequence b's chunks numbered behind those of the sequences before it.  C is
 // such that all chunks together number at most `target` + batch.  A sequence without own
 // positions has one chunk, which writes an empty part.
-__device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
+__device__ __forceinline__ int paged_true_len(const PagedAttnParams& p, int b) {
   const int n = p.lens[b];
   const int most = p.table_width << p.page_shift;
   const int cut = min(max(n, 0), most);
   if (cut != n) atomicOr(p.err, kErrIndex);
   return cut;
+}
+// A sliding window.  Query token i of a sequence of n positions is its position n - n_q + i and
+// sees the `window` positions that end with it, and the first `sinks`.  What lies between the
+// sinks and the first token's window is left out of the sequence: the kernels count positions
+// without that gap, as if the sequence were shorter, and add it where they look a page up.  The
+// gap starts and ends at multiples of win_round, so that no box or tile crosses it.
+__device__ __forceinline__ int paged_gap_from(const PagedAttnParams& p) {
+  return (p.sinks + p.win_round - 1) & ~(p.win_round - 1);
+}
+__device__ __forceinline__ int paged_gap(const PagedAttnParams& p, int n) {
+  if (p.window == 0) return 0;
+  const int low = max(0, n - p.n_q + 1 - p.window);
+  return max(0, (low & ~(p.win_round - 1)) - paged_gap_from(p));
+}
+// Positions of sequence b, without its gap.
+__device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
+  const int n = paged_true_len(p, b);
+  return n - paged_gap(p, n);
+}
+// The window as a CTA of sequence b needs it (all in positions without the gap): row e of the
+// sequence does not see [sinks, lim(e) - window), lim(e) being the end of what it sees.
+struct PagedWindow {
+  int gap, from;        // position t is position t + gap of the sequence where t >= from
+  int none_lo, all_lo;  // no row sees [sinks, none_lo); every row sees its window's part behind all_lo
+};
+__device__ __forceinline__ PagedWindow paged_window(const PagedAttnParams& p, int b) {
+  PagedWindow w = {0, 0, 0, 0};
+  if (p.window == 0) return w;
+  const int n = paged_true_len(p, b);
+  w.gap = paged_gap(p, n);
+  w.from = paged_gap_from(p);
+  w.none_lo = max(0, n - p.n_q + 1 - p.window - w.gap);
+  w.all_lo = max(0, n - p.window - w.gap);
+  return w;
+}
+__device__ __forceinline__ int paged_true(const PagedWindow& w, int t) { return t >= w.from ? t + w.gap : t; }
+// Whether no row sees any of the positions [t, t + n): their page may have been given back.
+__device__ __forceinline__ bool paged_unseen(const PagedAttnParams& p, const PagedWindow& w, int t, int n) {
+  return t + n <= w.none_lo && t >= p.sinks;
 }
 // What the checked build holds the paged kernels' accesses against: entry `at` of the page
 // tables, 16 bytes of the queries from element `at`, row `at` of the outputs or of a part

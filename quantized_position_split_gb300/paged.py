@@ -259,13 +259,14 @@ def kv_append_paged(a: N.PagedAppendArgs, stream=None) -> None:
 
 def paged_attn_args(q: torch.Tensor, cache: PagedKV, page_table: torch.Tensor, kv_lens: torch.Tensor, *, scale: float,
                     softcap: float = 0.0, causal: bool = False, shared_len: int = 0, out_dtype=torch.float16, o=None,
-                    lse=None, workspace=None) -> N.PagedAttnArgs:
+                    lse=None, workspace=None, window: int = 0, sinks: int = 0) -> N.PagedAttnArgs:
     """Argument block of ``attn_decode_paged`` for float16 ``q[batch, hq, D]`` or
     ``q[batch, n_q, hq, D]``, ``page_table[batch, width]`` and ``kv_lens[batch]`` (int32).
 
     ``causal``: query token i of a sequence sees its positions < len - n_q + i + 1.
     ``shared_len``: positions whose pages are the same in every sequence's table (a
-    shared prefix, a multiple of the page size), read once for the batch.  ``o``
+    shared prefix, a multiple of the page size), read once for the batch.  ``window`` > 0: a
+    query token sees the ``window`` positions that end with its own, and the first ``sinks``.  ``o``
     [batch*n_q*hq, D] of ``out_dtype``, ``lse`` [batch*n_q*hq] f32 and ``workspace``
     (uint8) are allocated if None.
     """
@@ -293,6 +294,7 @@ def paged_attn_args(q: torch.Tensor, cache: PagedKV, page_table: torch.Tensor, k
     a.table_stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
     a.kv_lens = kv_lens.data_ptr()
     a.shared_len, a.scale, a.softcap, a.o_dtype = int(shared_len), scale, softcap, _DTYPES[out_dtype]
+    a.window, a.sinks = int(window), int(sinks)
     need = ctypes.c_size_t()
     with torch.cuda.device(dev):
         N.check(N.load().qps_attn_paged_plan(ctypes.byref(a), ctypes.byref(need)))
