@@ -465,9 +465,62 @@ QPS_API qps_status qps_attn_paged_plan(const qps_paged_attn_args* a, size_t* wor
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 QPS_API qps_status qps_attn_decode_paged(const qps_paged_attn_args* a, void* stream);
 
+typedef struct qps_paged_prompt_args {
+  const void* q;             /* device, fp16: token t, head h at t*q_tok_stride + h*D; 16-byte aligned */
+  int64_t q_tok_stride;      /* elements, >= hq*D, a multiple of 8 */
+  int64_t tokens;            /* query tokens of the whole batch */
+  int32_t batch, hq;
+  const int32_t* q_starts;   /* device, [batch + 1]: the query tokens of sequence b are
+                                [q_starts[b], q_starts[b + 1]), none of them allowed, and its
+                                newest positions; ascending, within [0, tokens] (where they are
+                                not, that sequence has none, and a row that two others then name
+                                holds either one's).  Rows of o and lse before the first and
+                                behind the last stay as they were */
+  qps_paged_kv kv;
+  const int32_t* page_table; /* as in qps_paged_attn_args, the lengths too */
+  int64_t table_stride;
+  int32_t table_width;       /* table_width * page_size < 2^31 - 1024 */
+  int32_t o_dtype;           /* qps_dtype of o */
+  const int32_t* kv_lens;    /* device, [batch]: positions of each sequence, those of its query
+                                tokens included (a token before the first position, where there
+                                are fewer, gets O = 0, lse = -inf) */
+  float scale, softcap;      /* as in qps_attn_args */
+  int32_t window, sinks;     /* as in qps_paged_attn_args */
+  void* o;                   /* device, [tokens*hq][D] of o_dtype, row t*hq + h; 16-byte aligned */
+  float* lse;                /* device, f32 [tokens*hq] */
+  void* workspace;           /* device, 256-byte aligned, as large as qps_attn_prompt_plan says (it may
+                                be 0); calls that overlap on the GPU need one each.  o, lse and the
+                                workspace lie apart from one another and from q */
+  size_t workspace_bytes;
+  int64_t reserved0;         /* must be 0 */
+} qps_paged_prompt_args;
+
+/* Workspace bytes of qps_attn_prompt_paged for these args (host only, no launch; o, lse and
+ * workspace are not looked at).  Depends on tokens, the batch, the heads, the formats,
+ * table_width, page_size, window and sinks, not on the lengths, starts or entries.  Over
+ * compressed pages it holds the positions that the window leaves of every sequence (of a full
+ * table, without one) as fp16 rows: a narrow table saves memory.  Library utility, no
+ * counterpart on the pages.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA (the SM count). */
+QPS_API qps_status qps_attn_prompt_plan(const qps_paged_prompt_args* a, size_t* workspace_bytes);
+
+/* Causal attention of prompt chunks, any number of query tokens a sequence (one and none too),
+ * over a paged cache that holds their keys and values already (qps_kv_append_paged): the
+ * attention of [RKV] for whole prompts, of which the pages use their engine's.  Query token i
+ * of sequence b is its position q = kv_lens[b] - (its tokens) + i and sees the positions <= q,
+ * with a window those of (q - window, q] and of [0, sinks).  A table entry outside [0, n_pages)
+ * reads as zero rows; entries of pages that no query token sees are not read.  Logits, softmax
+ * sums and O are float32; the weights are rounded once to fp16, the operand type.  Compressed
+ * rows are decoded once a call: keys to two fp16 parts (logits as accurate as the decode
+ * call's), values rounded once to fp16, beyond its largest value taken as that.  A NaN or
+ * infinite value among positions that some tokens see may reach tokens before it (0 x NaN);
+ * keys, and anything that no token of the sequence sees, reach no row.
+ * tokens == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+QPS_API qps_status qps_attn_prompt_paged(const qps_paged_prompt_args* a, void* stream);
+
 /* One-shot fault for tests of the attention's bounded waits (no counterpart on the pages;
- * like qps_ring_inject_fault it needs no GPU fault): in the next qps_attn_decode_paged call
- * of the process, the keys of tile `tile` of each chunk (128 positions) never arrive in the
+ * like qps_ring_inject_fault it needs no GPU fault): in the next qps_attn_decode_paged or
+ * qps_attn_prompt_paged call of the process, the keys of tile `tile` of each chunk (128 positions) never arrive in the
  * tcgen05 kernels (many query rows; the others run as always), and their waits give up after
  * wait_ms (1..1000) instead of a second.  That call's outputs are then invalid,
  * qps_device_status reports TIMEOUT and qps_device_wait_record where; later calls are not

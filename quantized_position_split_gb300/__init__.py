@@ -8,7 +8,8 @@ is no CPU or eager-PyTorch fallback, and a missing library raises at first use.
 Names follow the ABI without its ``qps_`` prefix (``kv_quant_q8_0``,
 ``kv_quant_tq3``, ``attn_decode_window``, ``attn_decode_tail``, ``lse_combine``,
 ``Ring`` for ``qps_ring_*``, ``StepPlan`` for ``qps_decode_step``).  The calls around a
-paged cache (``qk_norm_rope``, ``kv_append_paged``, ``attn_decode_paged``) are in
+paged cache (``qk_norm_rope``, ``kv_append_paged``, ``attn_decode_paged``,
+``attn_prompt_paged``) are in
 ``paged.py``.
 """
 
@@ -56,6 +57,8 @@ __all__ = [
     "kv_append_paged",
     "paged_attn_args",
     "attn_decode_paged",
+    "paged_prompt_args",
+    "attn_prompt_paged",
     "paged_inject_fault",
 ]
 
@@ -675,5 +678,6 @@ def choose_tier(kv_bytes_per_tier, budget_bytes: float, t_star_bytes: float) -> 
     return out.value
 
 
-from .paged import (PagedKV, Rope, attn_decode_paged, kv_append_paged, paged_append_args,  # noqa: E402
-                    paged_attn_args, paged_inject_fault, qk_norm_rope, qk_rope_args, rope_table)
+from .paged import (PagedKV, Rope, attn_decode_paged, attn_prompt_paged, kv_append_paged,  # noqa: E402
+                    paged_append_args, paged_attn_args, paged_inject_fault, paged_prompt_args, qk_norm_rope,
+                    qk_rope_args, rope_table)

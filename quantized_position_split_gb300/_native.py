@@ -229,6 +229,32 @@ class PagedAttnArgs(ctypes.Structure):
     ]
 
 
+class PagedPromptArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", c_void_p),
+        ("q_tok_stride", c_int64),
+        ("tokens", c_int64),
+        ("batch", c_int32),
+        ("hq", c_int32),
+        ("q_starts", c_void_p),
+        ("kv", PagedKvStruct),
+        ("page_table", c_void_p),
+        ("table_stride", c_int64),
+        ("table_width", c_int32),
+        ("o_dtype", c_int32),
+        ("kv_lens", c_void_p),
+        ("scale", c_float),
+        ("softcap", c_float),
+        ("window", c_int32),
+        ("sinks", c_int32),
+        ("o", c_void_p),
+        ("lse", c_void_p),
+        ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t),
+        ("reserved0", c_int64),
+    ]
+
+
 # (name, restype, argtypes) of every exported function, in header order.
 SIGNATURES = [
     ("qps_abi_version", c_int32, []),
@@ -254,6 +280,8 @@ SIGNATURES = [
     ("qps_kv_append_paged", c_int32, [POINTER(PagedAppendArgs), c_void_p]),
     ("qps_attn_paged_plan", c_int32, [POINTER(PagedAttnArgs), POINTER(c_size_t)]),
     ("qps_attn_decode_paged", c_int32, [POINTER(PagedAttnArgs), c_void_p]),
+    ("qps_attn_prompt_plan", c_int32, [POINTER(PagedPromptArgs), POINTER(c_size_t)]),
+    ("qps_attn_prompt_paged", c_int32, [POINTER(PagedPromptArgs), c_void_p]),
     ("qps_paged_inject_fault", c_int32, [c_int32, c_int32]),
     ("qps_host_alloc", c_int32, [c_size_t, c_int32, POINTER(c_void_p)]),
     ("qps_host_free", c_int32, [c_void_p]),

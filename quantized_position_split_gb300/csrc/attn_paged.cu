@@ -19,10 +19,7 @@
 namespace qps {
 namespace {
 
-// qps_paged_inject_fault: the tile withheld from the next call (+ 1; 0: none) and the limit of
-// its waits in milliseconds.
 std::atomic<uint64_t> g_fault{0};
-
 
 // ---- merge --------------------------------------------------------------------------------
 // M = max lse, w = exp(lse - M), o = sum w o / sum w over the prefix's parts and the row's
@@ -371,7 +368,7 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   p.chunks = reinterpret_cast<int2*>(ws + pl.off_chunks);
   p.out = a->o;
   p.out_lse = a->lse;
-  const uint64_t fault = g_fault.load(std::memory_order_relaxed) ? g_fault.exchange(0) : 0;
+  const uint64_t fault = take_paged_fault();
   p.drop_tile = (int)(fault & 0xffffffffu) - 1;
   p.wait_ns = fault ? (uint32_t)(fault >> 32) * 1000000u : (uint32_t)kWaitLimitNs;
   const int rows = p.n_q * p.group;
@@ -401,6 +398,9 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
 }
 
 }  // namespace
+
+uint64_t take_paged_fault() { return g_fault.load(std::memory_order_relaxed) ? g_fault.exchange(0) : 0; }
+
 }  // namespace qps
 
 using namespace qps;

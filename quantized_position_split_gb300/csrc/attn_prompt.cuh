@@ -1,0 +1,581 @@
+// Attention of prompt chunks over fp16 pages (or compressed rows decoded to fp16) on the
+// fifth-generation tensor cores, causal, with or without a sliding window:
+//     S = Q K^T          tcgen05.mma, Q and K in shared memory (K-major), S in TMEM (f32)
+//     P = 2^(S' - m)     4 warps, one query row a thread: no reduction crosses lanes
+//     O += P V           tcgen05.mma, P (fp16) in TMEM over the S it came from, V in shared
+//                        memory as it lies in the page (MN-major), O in TMEM (f32)
+// The rows of a CTA are the query tokens of one sequence times the heads of one KV head's group.
+// At head_dim 64 and 128 there are two tiles of 128 rows (streams), each with an S, an O and
+// softmax state of its own, so that one's exponentials run beside the other's products and every
+// tile of K and V that is brought serves both.  At 256 and 512 O takes half of TMEM: one tile of
+// rows, two buffers of S, so that S of the next tile is ready when P of this one is; at 512 two
+// CTAs share a row, each computing all of S and half of O's columns.
+//
+// K and V pass through one ring of slots, [128 positions][SD columns] each, in the order of their
+// first use.  A K that was compressed comes in two parts, the fp16 value and what its rounding
+// left, whose products are summed: logits keep float32 accuracy.
+//
+// The running reference m of a row is set kRefShift (log2) below a tile's maximum, and again only
+// when one exceeds what it was set for by more than kRefLazy (paged.h): P stays within fp16, and
+// the rescale of O is rare.  P is rounded once to fp16 (the operand type); sums, m and O are
+// float32.
+//
+// Roles: warp 0 brings the slots, warp 1 issues the products, warps 4.. are the streams' softmax.
+// Waits are bounded as in attn_tm.cuh.
+#pragma once
+
+#include <atomic>
+#include <cstring>
+
+#include "attn_prompt.h"
+#include "attn_tm.cuh"
+
+namespace qps {
+namespace prompt {
+
+using namespace tm;
+
+template <int D, int KP>
+struct GeoP {
+  static constexpr int NQ = D <= 128 ? 2 : 1;      // tiles of rows
+  static constexpr int SD = D < 128 ? D : 128;     // columns of a slot
+  static constexpr int VD = D <= 256 ? D : 256;    // columns of O
+  static constexpr int CG = SD / 64;               // 128-byte column groups of a slot
+  static constexpr int SLOT = kTok * SD * 2;
+  static constexpr int KS = KP * D / SD, VS = VD / SD;  // slots of a tile
+  static constexpr int Q_TILE = kRows * D * 2;
+  static constexpr int STAGES = D == 64 ? 10 : D == 512 ? 3 : 5;
+  static constexpr int RING = NQ * Q_TILE;
+  static constexpr int BAR = RING + STAGES * SLOT;
+  static constexpr int SMEM = BAR + 256 + 1024;    // + slack for the 1024-byte base alignment
+  static constexpr int THREADS = 128 + 128 * NQ;
+  static constexpr int S_COL = 0, O_COL = 256;     // TMEM columns
+};
+
+template <int D, int KP>
+__global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
+    attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ TmaSet maps) {
+  using G = GeoP<D, KP>;
+  constexpr int ST = G::STAGES, NQ = G::NQ;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint32_t sbase = smem_addr(smem);
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // ---- this CTA's rows and tiles -------------------------------------------------------------
+  int idx = blockIdx.x;
+  const int head = idx % p.hkv;
+  idx /= p.hkv;
+  const int half = idx % (D / G::VD);
+  idx /= D / G::VD;
+  const int split = idx % p.n_split;
+  idx /= p.n_split;
+  // row tile `idx`: sequences in order, the last rows of each first (they see the most)
+  PromptSeq sq = {0, 0, 0};
+  int bz = -1, row0 = 0;
+  {
+    int before = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      PromptSeq mine = {0, 0, 0};
+      if (b0 + lane < p.batch) mine = prompt_seq(p, b0 + lane);
+      const int cnt = (int)(((int64_t)mine.n * p.group + NQ * kRows - 1) / (NQ * kRows));
+      int sum = cnt;  // inclusive scan over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > idx);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        bz = b0 + src;
+        sq.first = __shfl_sync(0xffffffffu, mine.first, src);
+        sq.n = __shfl_sync(0xffffffffu, mine.n, src);
+        sq.len = __shfl_sync(0xffffffffu, mine.len, src);
+        row0 = (before + __shfl_sync(0xffffffffu, sum, src) - 1 - idx) * NQ * kRows;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  if (bz < 0) return;  // more CTAs than row tiles (every warp finds the same)
+  const int rows = min(NQ * kRows, (int)min((int64_t)sq.n * p.group - row0, (int64_t)NQ * kRows));
+  const int pos0 = sq.len - sq.n;  // position of the sequence's first query token
+  const int q_lo = pos0 + row0 / p.group, q_hi = pos0 + (row0 + rows - 1) / p.group;
+  const PromptTiles all = prompt_tiles(p, q_lo, q_hi);
+  const PromptTiles dense = prompt_tiles(p, pos0, sq.len - 1);
+  const int i0 = (int)((int64_t)all.count * split / p.n_split), i1 = (int)((int64_t)all.count * (split + 1) / p.n_split);
+  const int ntiles = uniform(i1 - i0);
+  const int end = q_hi + 1;                                       // no row sees a position from here on
+  const int none_lo = p.window ? max(0, q_lo - p.window + 1) : 0; // nor any of [sinks, none_lo)
+  const int live = uniform(NQ == 1 || rows > kRows ? NQ : 1);     // streams that have rows
+  auto first_of = [&](int j) { return prompt_tile(all, i0 + j) * kPromptTile; };
+
+  // ---- barriers, TMEM --------------------------------------------------------------------------
+  const uint32_t bars = sbase + G::BAR;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (ST + s); };
+  auto s_full = [&](int w) { return bars + 8 * (2 * ST + w); };
+  auto p_ready = [&](int w) { return bars + 8 * (2 * ST + 2 + w); };
+  const uint32_t all_done = bars + 8 * (2 * ST + 4), q_full = bars + 8 * (2 * ST + 5), pv_done = bars + 8 * (2 * ST + 6);
+  static_assert(8 * (2 * ST + 7) <= 240, "barriers fit their region");
+  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + G::BAR + 240);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::BAR + 244);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * ST + 7; ++i)
+      mbar_init(bars + 8 * i, i == 2 * ST + 5 ? 4 * NQ : i >= 2 * ST + 2 && i < 2 * ST + 4 ? 4 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    *abort_flag = 0;
+  }
+  if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = uniform(*tmem_word);
+
+  int issued = 0;  // (warp 0) slots under way or landed
+  auto wait = [&](uint32_t bar, uint32_t parity, int tile) -> bool {  // (as in attn_tm.cuh)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t since = global_ns();
+    for (;;) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+      int over = 0;
+      if (lane == 0) {
+        over = *abort_flag;
+        if (!over && global_ns() - since >= p.wait_ns) *abort_flag = over = gave_up(tile, warp);
+      }
+      if (__shfl_sync(0xffffffffu, over, 0)) return false;
+    }
+  };
+  // Places of the tiles' slots in the ring's order: K(0), V(0), K(1), V(1), .. where a tile of K
+  // serves two streams before V(j) does, else K(0), K(1), V(0), K(2), V(1), .. (S of the next
+  // tile is issued before O of this one).
+  constexpr int KV = G::KS + G::VS;
+  auto k_at = [&](int j) { return NQ == 2 || j == 0 ? j * KV : G::KS + (j - 1) * KV; };
+  auto v_at = [&](int j) { return NQ == 2 ? j * KV + G::KS : G::KS + j * KV + (j + 1 < ntiles ? G::KS : 0); };
+
+  if (warp == 0) {
+    // ---- slots: boxes of min(page, 128) positions of one page and 64 columns, one a lane; a
+    // lane's page of the next tile is read a tile ahead.  Decoded rows: boxes of 128 positions. ----
+    const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
+    const int cg = lane % G::CG, r = lane / G::CG;
+    const int32_t* row = p.table + (int64_t)bz * p.table_stride;
+    const bool paged = !p.dense_k || !p.dense_v;
+    auto entry = [&](int j) -> int {  // the lane's page of tile j (n_pages: none, zeros)
+      if (!paged || j >= ntiles || r >= nb) return (int)p.n_pages;
+      const int t = first_of(j) + r * br;
+      if (t >= end || (t >= p.sinks && t + br <= none_lo)) return (int)p.n_pages;
+      const int at = t >> p.page_shift;
+      if (!in_bounds(at < p.table_width, p.err)) return (int)p.n_pages;
+      const int pg = row[at];
+      if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
+      atomicOr(p.err, kErrIndex);
+      return (int)p.n_pages;
+    };
+    int f = 0;
+    auto put = [&](const TensorMap* map, bool decoded, int col, int j, int page) -> bool {
+      const int s = f % ST;
+      if (f >= ST && !wait(empty(s), ((f / ST) & 1) ^ 1, j)) return false;
+      __syncwarp();
+      if (lane == 0) mbar_expect_tx(full(s), G::SLOT);
+      __syncwarp();
+      const uint32_t dst = sbase + G::RING + s * G::SLOT + cg * (kTok * 128);
+      const int x = (col + cg * 64) * 2, t = first_of(j);
+      const bool drop = map == &maps.k && j == p.drop_tile;
+      if (decoded) {
+        const int at = prompt_dense(dense, t / kPromptTile);
+        if (r == 0 && !drop && in_bounds(at >= 0 && at < p.dense_tiles && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
+          tma_load_4d(dst, map, x, 0, head, bz * p.dense_tiles + at, full(s));
+      } else if (r < nb && !drop) {
+        const int y = (t + r * br) & ((1 << p.page_shift) - 1);
+        if (in_bounds(page <= p.n_pages && y + br <= 1 << p.page_shift && head < p.hkv && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
+          tma_load_4d(dst + r * br * 128, map, x, y, head, page, full(s));
+      }
+      issued = ++f;
+      return true;
+    };
+    auto put_k = [&](int j, int page) -> bool {
+      for (int s = 0; s < G::KS; ++s)
+        if (!put(&maps.k, p.dense_k != nullptr, s * G::SD, j, page)) return false;
+      return true;
+    };
+    auto put_v = [&](int j, int page) -> bool {
+      for (int s = 0; s < G::VS; ++s)
+        if (!put(&maps.v, p.dense_v != nullptr, half * G::VD + s * G::SD, j, page)) return false;
+      return true;
+    };
+    int page = entry(0), next = entry(1);
+    bool ok = true;
+    if constexpr (NQ == 1) ok = ntiles == 0 || put_k(0, page);
+    for (int j = 0; j < ntiles && ok; ++j) {
+      const int after = entry(j + 2);
+      if constexpr (NQ == 2) ok = put_k(j, page);
+      else ok = j + 1 >= ntiles || put_k(j + 1, next);
+      ok = ok && put_v(j, page);
+      page = next;
+      next = after;
+    }
+  } else if (warp == 1) {
+    // ---- products: step i is tile i / NQ of stream i % NQ, S(i) in buffer i % 2.  S(0), S(1),
+    // then O(i) and S(i + 2) in turn. ------------------------------------------------------------
+    constexpr uint32_t ID_S = instr_desc(kTok, 0), ID_O = instr_desc(G::SD, 1);
+    const uint32_t one = elect_lane();
+    const int steps = ntiles * NQ;
+    auto qk = [&](int i) -> bool {
+      const int j = i / NQ, w = i % NQ, at = k_at(j);
+      const uint32_t d = tmem + G::S_COL + (i & 1) * kTok;
+#pragma unroll 1
+      for (int s = 0; s < G::KS; ++s) {
+        const int st = (at + s) % ST;
+        if (w == 0 && !wait(full(st), ((at + s) / ST) & 1, j)) return false;
+        fence_after();
+        if (w < live) {
+          const uint64_t a = smem_desc(sbase + w * G::Q_TILE + (s * G::CG % (D / 64)) * (kRows * 128), 16);
+          const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, 16);
+#pragma unroll
+          for (int kk = 0; kk < G::SD / 16; ++kk) {
+            const uint64_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+            mma_ss(d, a + off, b + off, ID_S, s > 0 || kk > 0, one);
+          }
+        }
+        if (w == NQ - 1) commit(empty(st), one);
+      }
+      commit(s_full(i & 1), one);
+      return true;
+    };
+    bool ok = steps == 0 || wait(q_full, 0, 0);
+    for (int i = 0; i < min(2, steps) && ok; ++i) ok = qk(i);
+    for (int i = 0; i < steps && ok; ++i) {
+      const int j = i / NQ, w = i % NQ, at = v_at(j);
+      if (w == 0) {
+        // rows that no query sees hold whatever was there, and 0 x NaN is NaN
+        const int t = first_of(j), a0 = max(0, p.sinks - t), a1 = min(kTok, none_lo - t), b0 = end - t;
+        for (int s = 0; s < G::VS && ok; ++s) {
+          const int st = (at + s) % ST;
+          if (!(ok = wait(full(st), ((at + s) / ST) & 1, j))) break;
+          if (b0 < kTok || a0 < a1) {
+            for (int r = lane >> 3; r < kTok; r += 4)
+              if (r >= b0 || (r >= a0 && r < a1))
+#pragma unroll
+                for (int g = 0; g < G::CG; ++g)
+                  *reinterpret_cast<uint4*>(smem + G::RING + st * G::SLOT + g * (kTok * 128) + r * 128 + (lane & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+            mma::fence_proxy_async();
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+      }
+      if (w < live) {
+        if (!(ok = wait(p_ready(i & 1), NQ == 2 ? j & 1 : (j >> 1) & 1, j))) break;
+        fence_after();
+      }
+#pragma unroll 1
+      for (int s = 0; s < G::VS; ++s) {
+        const int st = (at + s) % ST;
+        if (w < live) {
+          const uint32_t d = tmem + G::O_COL + w * D + s * G::SD, a = tmem + G::S_COL + (i & 1) * kTok;
+          const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, kTok * 128);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            mma_ts(d, a + kk * 8, b + (uint64_t)((kk * 2048) >> 4), ID_O, j > 0 || kk > 0, one);
+        }
+        if (w == NQ - 1) commit(empty(st), one);
+      }
+      if constexpr (NQ == 1) commit(pv_done, one);
+      if (i + 2 < steps) ok = qk(i + 2);
+    }
+    commit(all_done, one);  // completes when everything issued above has
+  } else if (warp >= 4) {
+    // ---- softmax: stream w, one row a thread --------------------------------------------------
+    const int w = (warp - 4) >> 2, r = (warp & 3) * 32 + lane, rr = w * kRows + r;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
+    const uint32_t o_at = tmem + lanes + G::O_COL + w * D;
+    {
+      // Q [128][D] of the stream, K-major: row r's 16-byte chunk c of a column group at r * 128 +
+      // (c ^ r % 8) * 16; loads of one round together
+      constexpr int N = kRows * D / 8 / 128, U = N < 16 ? N : 16;
+      const int tid = threadIdx.x & 127;
+#pragma unroll 1
+      for (int k0 = 0; k0 < N; k0 += U) {
+        uint4 v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int i = tid + (k0 + k) * 128, qr = w * kRows + i / (D / 8), c = i % (D / 8);
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (qr < rows) {
+            const int e = (row0 + qr) / p.group, h = head * p.group + (row0 + qr) % p.group;
+            const int64_t at = (int64_t)(sq.first + e) * p.q_tok + (int64_t)h * D + c * 8;
+            if (in_bounds(sq.first + e < p.tokens, p.err)) v[k] = *reinterpret_cast<const uint4*>(p.q + at);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int i = tid + (k0 + k) * 128, qr = i / (D / 8), c = i % (D / 8);
+          *reinterpret_cast<uint4*>(smem + w * G::Q_TILE + (c >> 3) * (kRows * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = v[k];
+        }
+      }
+      mma::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(q_full) : "memory");
+    }
+    const bool mine = rr < rows;
+    // positions below lim are visible to the row, but for [sinks, low)
+    const int lim = mine ? pos0 + (row0 + rr) / p.group + 1 : 0, low = p.window ? lim - p.window : 0;
+    constexpr float LOG2E = 1.4426950408889634f;
+    const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap : 0.f;
+    auto logit = [&](uint32_t v) -> float {
+      const float s = __uint_as_float(v);
+      return cap > 0.f ? mma::softcap_tanh(s * p.scale, cap, cap_k) * LOG2E : s * qs;
+    };
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < ntiles && w < live; ++j) {
+      const int buf = NQ == 2 ? w : j & 1, par = NQ == 2 ? j & 1 : (j >> 1) & 1;
+      const uint32_t s_at = tmem + lanes + G::S_COL + buf * kTok;
+      if (!(ok = wait(s_full(buf), par, j))) break;
+      fence_after();
+      const int first = first_of(j);
+      // Whole tiles of plain logits, the common case, have a body of their own: maxima and
+      // exponentials straight from S (a positive scale keeps the order), four chains each,
+      // the next 32 columns read beside the present ones' arithmetic.
+      const bool fast = __all_sync(0xffffffffu, (first + kTok <= lim && (first >= low || first + kTok <= p.sinks)) || !mine) &&
+                        cap <= 0.f && qs >= 0.f;
+      auto hidden = [&](int t) { return t >= lim || (t < low && t >= p.sinks); };
+      uint32_t va[32], vb[32];
+      float mx = -INFINITY;
+      if (fast) {
+        float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto most = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mm[k] = fmaxf(fmaxf(mm[k], __uint_as_float(v[i + k])), __uint_as_float(v[i + 4 + k]));
+        };
+        tmem_ld32(va, s_at);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kTok / 32; c += 2) {
+          tmem_ld32(vb, s_at + 32 * (c + 1));
+          most(va);
+          tmem_wait_ld();
+          if (c + 2 < kTok / 32) tmem_ld32(va, s_at + 32 * (c + 2));
+          most(vb);
+          if (c + 2 < kTok / 32) tmem_wait_ld();
+        }
+        mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * qs;
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+          __syncwarp();
+          tmem_ld32(va, s_at + 32 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!hidden(first + 32 * c + i)) mx = fmaxf(mx, logit(va[i]));
+        }
+        __syncwarp();
+      }
+      mx -= kRefShift;
+      const bool raise = mx - m > kRefLazy;  // (false when both are -inf)
+      const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
+      if (raise) {
+        m = mx;
+        l *= cr;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, raise)) {
+        // two streams: S of this tile was issued behind this stream's last product, so O is at
+        // rest; one: the last product may still run
+        if constexpr (NQ == 1) {
+          if (!(ok = wait(pv_done, (j - 1) & 1, j))) break;
+          fence_after();
+        }
+#pragma unroll 1
+        for (int c = 0; c < G::VD / 32; ++c) {
+          __syncwarp();
+          tmem_ld32(va, o_at + 32 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * cr);
+          tmem_st32(o_at + 32 * c, va);
+        }
+      }
+      const float ms = m == -INFINITY ? 0.f : m;
+      float sum = 0.f;
+      if (fast) {
+        float ss[4] = {0.f, 0.f, 0.f, 0.f};
+        auto weigh = [&](const uint32_t (&v)[32], int c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = ex2(fmaf(__uint_as_float(v[2 * i]), qs, -ms));
+            const float b = ex2(fmaf(__uint_as_float(v[2 * i + 1]), qs, -ms));
+            ss[(2 * i) & 3] += a;
+            ss[(2 * i + 1) & 3] += b;
+            pk[i] = mma::pack_h2(a, b);
+          }
+          tmem_st16(s_at + 16 * c, pk);  // (over columns of S that are already read, none under way)
+        };
+        tmem_ld32(va, s_at);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kTok / 32; c += 2) {
+          tmem_ld32(vb, s_at + 32 * (c + 1));
+          weigh(va, c);
+          tmem_wait_ld();
+          if (c + 2 < kTok / 32) tmem_ld32(va, s_at + 32 * (c + 2));
+          weigh(vb, c + 1);
+          if (c + 2 < kTok / 32) tmem_wait_ld();
+        }
+        sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kTok / 32; ++c) {
+          __syncwarp();
+          tmem_ld32(va, s_at + 32 * c);
+          tmem_wait_ld();
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a = ex2(logit(va[2 * i]) - ms), b = ex2(logit(va[2 * i + 1]) - ms);
+            if (hidden(first + 32 * c + 2 * i)) a = 0.f;
+            if (hidden(first + 32 * c + 2 * i + 1)) b = 0.f;
+            sum += a + b;
+            pk[i] = mma::pack_h2(a, b);
+          }
+          __syncwarp();
+          tmem_st16(s_at + 16 * c, pk);
+        }
+        __syncwarp();
+      }
+      l += sum;
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(buf)) : "memory");
+    }
+    // ---- the rows' output, or their part of it ---------------------------------------------------
+    if (ok) ok = wait(all_done, 0, ntiles);
+    fence_after();
+    if (ok && !__any_sync(0xffffffffu, *abort_flag)) {
+      const bool none = l == 0.f;  // (a NaN stays one)
+      const float inv = none ? 0.f : 1.f / l;
+      const bool whole = p.n_split == 1;
+      const int h = head * p.group + (row0 + rr) % p.group;
+      const int64_t at = (int64_t)(sq.first + (row0 + rr) / p.group) * p.hq + h;
+      const bool store = mine && in_bounds(at < p.tokens * p.hq, p.err);
+      const int64_t to = whole ? at : (int64_t)split * p.tokens * p.hq + at;
+      if (store && half == 0) (whole ? p.out_lse : p.part_lse)[to] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+#pragma unroll 1
+      for (int c = 0; c < G::VD / 32; ++c) {
+        uint32_t v[32];
+        __syncwarp();
+        if (ntiles > 0 && w < live) {
+          tmem_ld32(v, o_at + 32 * c);
+          tmem_wait_ld();
+        }
+        if (!store) continue;
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(v[i]) * inv;
+        const int64_t x = to * D + half * G::VD + 32 * c;
+        if (!whole || p.out_dtype == QPS_DT_F32) {
+          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float a = o[8 * i + 2 * q], b = o[8 * i + 2 * q + 1];
+              if (p.out_dtype == QPS_DT_F16) {
+                y[q] = mma::pack_h2(a, b);
+              } else {
+                const __nv_bfloat162 hb = __floats2bfloat162_rn(a, b);
+                y[q] = *reinterpret_cast<const uint32_t*>(&hb);
+              }
+            }
+            dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+    }
+    fence_before();
+  }
+
+  // ---- end: nothing may be in flight when the CTA leaves -----------------------------------------
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" :::);
+  if (*abort_flag) {  // (uniform: the flag is only set before the barrier above)
+    if (warp == 0) {
+      const bool first = lane == 0 && report_give_up(p.err, *abort_flag, issued, ntiles, ntiles * kTok);
+      const uint64_t since = global_ns();
+      bool done = true;
+#pragma unroll 1
+      for (int f = max(0, issued - ST); f < issued; ++f) done &= mma::mbar_wait(full(f % ST), (f / ST) & 1, p.wait_ns);
+      if (first) {
+        p.err[10] = (unsigned)min((uint64_t)0xffffffffu, global_ns() - since);
+        p.err[11] = done ? 1u : 0u;
+      }
+    }
+    if (warp == 1) mma::mbar_wait(all_done, 0, p.wait_ns);
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 2) tmem_free(tmem, 512);
+}
+
+template <int D, int KP>
+qps_status launch_prompt(const PromptParams& p, cudaStream_t s) {
+  using G = GeoP<D, KP>;
+  static_assert(G::SMEM <= 227 * 1024, "the slots exceed the shared memory of one CTA");
+  static_assert(G::O_COL + G::NQ * G::VD <= 512, "S and O exceed TMEM");
+  TmaSet maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int page = 1 << p.page_shift, rows = page < kTok ? page : kTok;
+  for (int i = 0; i < 2; ++i) {
+    const __half* dense = i ? p.dense_v : p.dense_k;
+    const int cols = i ? D : KP * D;
+    const bool ok = dense ? encode_plane_map(i ? &maps.v : &maps.k, dense, 2 * cols, kTok, p.hkv, kTok, p.batch * p.dense_tiles,
+                                             (int64_t)p.hkv * kTok, 128, 128, kTok)
+                          : encode_plane_map(i ? &maps.v : &maps.k, i ? p.v[0] : p.k[0], 2 * D, page, p.hkv, page, (int)p.n_pages,
+                                             (int64_t)p.hkv * page, 128, 128, rows);
+    if (!ok) return QPS_ERR_CUDA;
+  }
+  auto kern = attn_prompt_kernel<D, KP>;
+  static std::atomic<uint64_t> sized{0};
+  int dev = 0;
+  QPS_CUDA_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!(sized.load(std::memory_order_relaxed) & bit) || !bit) {
+    QPS_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
+    sized.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.tiles * p.n_split * (D / G::VD) * p.hkv));
+  cfg.blockDim = dim3(G::THREADS);
+  cfg.dynamicSmemBytes = G::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  QPS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, maps));
+  count_launch();
+  QPS_CUDA_TRY(cudaGetLastError());
+  return QPS_OK;
+}
+
+template <int D>
+qps_status launch_prompt_d(const PromptParams& p, cudaStream_t s) {
+  return p.dense_k ? launch_prompt<D, 2>(p, s) : launch_prompt<D, 1>(p, s);
+}
+
+}  // namespace prompt
+}  // namespace qps

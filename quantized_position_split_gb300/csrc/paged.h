@@ -223,6 +223,10 @@ qps_status launch_paged_tt_d512(const PagedAttnParams& p, cudaStream_t s);
 // value is near zero, as a first position's may be, left an output off by 3e-2 of its size.
 constexpr float kRefShift = 11.f, kRefLazy = 4.f;
 
+// The fault armed by qps_paged_inject_fault for the next call (0: none): the tile + 1, and in the
+// upper half the limit of the waits in milliseconds.
+uint64_t take_paged_fault();
+
 // The kernels of a paged launch: attn_mma.cuh's, attn_tm.cuh's, attn_tt.cuh's.
 enum PagedKernel { kMma, kTm, kTt };
 

@@ -318,6 +318,65 @@ def attn_decode_paged(a: N.PagedAttnArgs, stream=None):
     return a._out
 
 
+def paged_prompt_args(q: torch.Tensor, cache: PagedKV, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                      q_starts: torch.Tensor, *, scale: float, softcap: float = 0.0, window: int = 0, sinks: int = 0,
+                      out_dtype=torch.float16, o=None, lse=None, workspace=None) -> N.PagedPromptArgs:
+    """Argument block of ``attn_prompt_paged`` for the query tokens float16 ``q[tokens, hq, D]``
+    of a ragged batch (a slice of a fused projection is taken as it lies): those of sequence b
+    are ``[q_starts[b], q_starts[b + 1])`` (int32 ``q_starts[batch + 1]``) and its newest
+    positions, whose rows the cache holds already.  ``page_table`` and ``kv_lens`` as in
+    ``paged_attn_args``.
+
+    ``window`` > 0: a token sees the ``window`` positions that end with its own, and the first
+    ``sinks``.  ``o`` [tokens*hq, D] of ``out_dtype``, ``lse`` [tokens*hq] f32 and ``workspace``
+    (uint8) are allocated if None; rows of no sequence stay as they were.
+    """
+    dev = cache.device
+    _tensor(q, "q", dev, torch.float16, contiguous=False)
+    if q.dim() != 3 or q.shape[2] != cache.d:
+        raise _bad(f"q must be [tokens, hq, {cache.d}]")
+    tokens, hq, d = q.shape
+    if tokens and not q[0].is_contiguous():
+        raise _bad("q must be contiguous per token")
+    _tensor(page_table, "page_table", dev, torch.int32, contiguous=False)
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise _bad("page_table must be [batch, width] with contiguous rows")
+    batch = page_table.shape[0]
+    _tensor(kv_lens, "kv_lens", dev, torch.int32, (batch,))
+    _tensor(q_starts, "q_starts", dev, torch.int32, (batch + 1,))
+    if out_dtype not in _DTYPES:
+        raise _bad("out_dtype is float16, bfloat16 or float32")
+    a = N.PagedPromptArgs()
+    a.q, a.q_tok_stride, a.tokens = q.data_ptr(), q.stride(0) if tokens > 1 else hq * d, tokens
+    a.batch, a.hq = batch, hq
+    a.q_starts, a.kv = q_starts.data_ptr(), cache.struct
+    a.page_table, a.table_width = page_table.data_ptr(), page_table.shape[1]
+    a.table_stride = page_table.stride(0) if batch > 1 else page_table.shape[1]
+    a.kv_lens = kv_lens.data_ptr()
+    a.scale, a.softcap, a.window, a.sinks, a.o_dtype = scale, softcap, int(window), int(sinks), _DTYPES[out_dtype]
+    need = ctypes.c_size_t()
+    with torch.cuda.device(dev):
+        N.check(N.load().qps_attn_prompt_plan(ctypes.byref(a), ctypes.byref(need)))
+    if o is None:
+        o = torch.empty((tokens * hq, d), dtype=out_dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((tokens * hq,), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty((need.value,), dtype=torch.uint8, device=dev)
+    _tensor(o, "o", dev, out_dtype, (tokens * hq, d))
+    _tensor(lse, "lse", dev, torch.float32, (tokens * hq,))
+    _tensor(workspace, "workspace", dev, torch.uint8)
+    a.o, a.lse, a.workspace, a.workspace_bytes = o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel()
+    a._out = (o, lse)
+    return _block(a, "qps_attn_prompt_paged", dev, (q, cache, page_table, kv_lens, q_starts, o, lse, workspace))
+
+
+def attn_prompt_paged(a: N.PagedPromptArgs, stream=None):
+    """Attention of ``paged_prompt_args``; returns (o, lse)."""
+    _call(a, stream)
+    return a._out
+
+
 def paged_inject_fault(tile: int, wait_ms: int = 20) -> None:
     """Withhold the keys of tile ``tile`` of each chunk from the next ``attn_decode_paged`` call
     of many query rows, whose waits then give up after ``wait_ms`` (``qps_paged_inject_fault``;
