@@ -518,6 +518,107 @@ QPS_API qps_status qps_attn_prompt_plan(const qps_paged_prompt_args* a, size_t* 
  * tokens == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 QPS_API qps_status qps_attn_prompt_paged(const qps_paged_prompt_args* a, void* stream);
 
+/* ---- Pages of a paged cache: given out, shared, given back, moved ---------------------- */
+
+/* The sequences of a paged cache, all of whose state lies on the device: a row of page_table and
+ * a length each, and for every page the number of entries that name it.  A page whose count is 0
+ * is free.  The caller may hold a page too (one that a prefix index names, say) by counting it.
+ * Entry j of a sequence matters while j * page_size < its length; -1 (any value outside
+ * [0, n_pages)) is no page.  The caches are those of the layers: one page size, one number of
+ * pages, any formats and heads; page p is page p of each.
+ * The calls below change this state on their stream.  Two of them on the same sequences, or one
+ * beside a call that reads them, must not overlap on the GPU.  No call reads anything back: a
+ * captured graph of them replays. */
+typedef struct qps_paged_seqs {
+  const qps_paged_kv* caches; /* host, [n_caches] */
+  int32_t n_caches;
+  int32_t batch;
+  int32_t* page_table;        /* device, [batch][table_stride] */
+  int64_t table_stride;       /* >= table_width */
+  int32_t table_width;        /* table_width * page_size < 2^31 - 1024 */
+  int32_t reserved0;          /* must be 0 */
+  int32_t* kv_lens;           /* device, [batch] */
+  int32_t* refs;              /* device, [n_pages] */
+} qps_paged_seqs;
+
+typedef struct qps_paged_extend_args {
+  qps_paged_seqs seqs;
+  const int32_t* n_new;      /* device, [batch]: positions that each sequence grows by; negative: it
+                                is cut back by so many (to none at least) */
+  int32_t window, sinks;     /* of the attention that reads the cache (0: none) */
+  int64_t max_tokens;        /* rows of slots and positions, < 2^31 */
+  int32_t* q_starts;         /* device, out, [batch + 1]: the new positions' rows of sequence b are
+                                [q_starts[b], q_starts[b + 1]), as qps_attn_prompt_paged takes them */
+  int64_t* slots;            /* device, out, [max_tokens]: as qps_kv_append_paged takes them; rows
+                                behind the last are padding (slot -1, position 0) */
+  int64_t* positions;        /* device, out, [max_tokens] */
+  void* workspace;           /* device, 256-byte aligned, as large as the plan says */
+  size_t workspace_bytes;
+} qps_paged_extend_args;
+
+/* Workspace bytes of qps_kv_extend_paged for these args (host only, no launch; outputs and
+ * workspace are not looked at).  Library utility, no counterpart on the pages.
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+QPS_API qps_status qps_kv_extend_plan(const qps_paged_extend_args* a, size_t* workspace_bytes);
+
+/* Make room for the next positions of every sequence (what a serving loop does before a step's
+ * append and attention; no counterpart on the pages, whose caches are one block).  In this order:
+ *   - entries behind a cut sequence's end are given back;
+ *   - with a window, entries whose positions the next query token (position kv_lens[b], or the
+ *     new end where the sequence does not grow) and those after it do not see: whole pages of
+ *     [sinks, that position - window + 1);
+ *   - sequences in order, the lowest free pages first: a growing sequence whose last page is not
+ *     full and has other uses gets a copy of it (its rows, in every cache), then pages for its
+ *     new positions;
+ *   - kv_lens, q_starts, slots and positions are written.
+ * A sequence that no longer fits its table row, the rows of slots, or the free pages keeps its
+ * length and gets slots of -1; qps_device_status then returns INVALID_ARG, as it does where a
+ * count would fall below 0.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+QPS_API qps_status qps_kv_extend_paged(const qps_paged_extend_args* a, void* stream);
+
+typedef struct qps_paged_fork_args {
+  qps_paged_seqs seqs;
+  const int32_t* src;        /* device, [n]: the sequence that dst[i] becomes a copy of; negative:
+                                none, dst[i] is given back and has no positions */
+  const int32_t* dst;        /* device, [n], each sequence once (a second time is left out, and
+                                qps_device_status says so; so is an index out of range) */
+  int32_t n;
+  int32_t reserved0;         /* must be 0 */
+  void* workspace;           /* device, 256-byte aligned, as large as the plan says */
+  size_t workspace_bytes;
+} qps_paged_fork_args;
+
+/* Workspace bytes of qps_kv_fork_paged for these args, as qps_kv_extend_plan.  Library utility,
+ * no counterpart on the pages.  Errors: INVALID_ARG, UNSUPPORTED. */
+QPS_API qps_status qps_kv_fork_plan(const qps_paged_fork_args* a, size_t* workspace_bytes);
+
+/* Sequences that continue others (beams, agents behind one conversation) or end ([POLY, "S1 —
+ * SharedKVPool"]: many readers of one prefix; its pool has no pages).  All at once: the sources
+ * are read as they were, so rows may trade places; what a destination held is given back.  Full
+ * pages are shared; the rows of a last page that is not full are copied, in every cache, to the
+ * lowest pages that are free then, in the order of i.  Where there is none left, the destination
+ * ends with its full pages and qps_device_status returns INVALID_ARG.  src[i] == dst[i] changes
+ * nothing.  n == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+QPS_API qps_status qps_kv_fork_paged(const qps_paged_fork_args* a, void* stream);
+
+typedef struct qps_paged_compact_args {
+  qps_paged_seqs seqs;
+  int32_t* new_ids;          /* device, out, [n_pages]: what each page has become (-1: it was free) */
+  int32_t* live;             /* device, out, [1]: pages in use */
+  void* workspace;           /* device, 256-byte aligned, as large as the plan says */
+  size_t workspace_bytes;
+} qps_paged_compact_args;
+
+/* Workspace bytes of qps_kv_compact_paged for these args, as qps_kv_extend_plan.  Library
+ * utility, no counterpart on the pages.  Errors: INVALID_ARG, UNSUPPORTED. */
+QPS_API qps_status qps_kv_compact_plan(const qps_paged_compact_args* a, size_t* workspace_bytes);
+
+/* Move the pages in use to [0, live), so that the pool behind may shrink: the i-th page in use
+ * at or behind `live` goes, in every cache, to the i-th free page before it; its count and the
+ * entries that name it follow (no counterpart on the pages).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+QPS_API qps_status qps_kv_compact_paged(const qps_paged_compact_args* a, void* stream);
+
 /* One-shot fault for tests of the attention's bounded waits (no counterpart on the pages;
  * like qps_ring_inject_fault it needs no GPU fault): in the next qps_attn_decode_paged or
  * qps_attn_prompt_paged call of the process, the keys of tile `tile` of each chunk (128 positions) never arrive in the

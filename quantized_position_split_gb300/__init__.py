@@ -9,8 +9,8 @@ Names follow the ABI without its ``qps_`` prefix (``kv_quant_q8_0``,
 ``kv_quant_tq3``, ``attn_decode_window``, ``attn_decode_tail``, ``lse_combine``,
 ``Ring`` for ``qps_ring_*``, ``StepPlan`` for ``qps_decode_step``).  The calls around a
 paged cache (``qk_norm_rope``, ``kv_append_paged``, ``attn_decode_paged``,
-``attn_prompt_paged``) are in
-``paged.py``.
+``attn_prompt_paged``) and on its pages (``kv_extend_paged``, ``kv_fork_paged``,
+``kv_compact_paged``) are in ``paged.py``.
 """
 
 from __future__ import annotations
@@ -59,6 +59,13 @@ __all__ = [
     "attn_decode_paged",
     "paged_prompt_args",
     "attn_prompt_paged",
+    "PagedSeqs",
+    "paged_extend_args",
+    "kv_extend_paged",
+    "paged_fork_args",
+    "kv_fork_paged",
+    "paged_compact_args",
+    "kv_compact_paged",
     "paged_inject_fault",
 ]
 
@@ -678,6 +685,7 @@ def choose_tier(kv_bytes_per_tier, budget_bytes: float, t_star_bytes: float) -> 
     return out.value
 
 
-from .paged import (PagedKV, Rope, attn_decode_paged, attn_prompt_paged, kv_append_paged,  # noqa: E402
-                    paged_append_args, paged_attn_args, paged_inject_fault, paged_prompt_args, qk_norm_rope,
-                    qk_rope_args, rope_table)
+from .paged import (PagedKV, PagedSeqs, Rope, attn_decode_paged, attn_prompt_paged, kv_append_paged,  # noqa: E402
+                    kv_compact_paged, kv_extend_paged, kv_fork_paged, paged_append_args, paged_attn_args,
+                    paged_compact_args, paged_extend_args, paged_fork_args, paged_inject_fault, paged_prompt_args,
+                    qk_norm_rope, qk_rope_args, rope_table)

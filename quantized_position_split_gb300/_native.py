@@ -255,6 +255,57 @@ class PagedPromptArgs(ctypes.Structure):
     ]
 
 
+class PagedSeqsStruct(ctypes.Structure):
+    _fields_ = [
+        ("caches", POINTER(PagedKvStruct)),
+        ("n_caches", c_int32),
+        ("batch", c_int32),
+        ("page_table", c_void_p),
+        ("table_stride", c_int64),
+        ("table_width", c_int32),
+        ("reserved0", c_int32),
+        ("kv_lens", c_void_p),
+        ("refs", c_void_p),
+    ]
+
+
+class PagedExtendArgs(ctypes.Structure):
+    _fields_ = [
+        ("seqs", PagedSeqsStruct),
+        ("n_new", c_void_p),
+        ("window", c_int32),
+        ("sinks", c_int32),
+        ("max_tokens", c_int64),
+        ("q_starts", c_void_p),
+        ("slots", c_void_p),
+        ("positions", c_void_p),
+        ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t),
+    ]
+
+
+class PagedForkArgs(ctypes.Structure):
+    _fields_ = [
+        ("seqs", PagedSeqsStruct),
+        ("src", c_void_p),
+        ("dst", c_void_p),
+        ("n", c_int32),
+        ("reserved0", c_int32),
+        ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t),
+    ]
+
+
+class PagedCompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("seqs", PagedSeqsStruct),
+        ("new_ids", c_void_p),
+        ("live", c_void_p),
+        ("workspace", c_void_p),
+        ("workspace_bytes", c_size_t),
+    ]
+
+
 # (name, restype, argtypes) of every exported function, in header order.
 SIGNATURES = [
     ("qps_abi_version", c_int32, []),
@@ -282,6 +333,12 @@ SIGNATURES = [
     ("qps_attn_decode_paged", c_int32, [POINTER(PagedAttnArgs), c_void_p]),
     ("qps_attn_prompt_plan", c_int32, [POINTER(PagedPromptArgs), POINTER(c_size_t)]),
     ("qps_attn_prompt_paged", c_int32, [POINTER(PagedPromptArgs), c_void_p]),
+    ("qps_kv_extend_plan", c_int32, [POINTER(PagedExtendArgs), POINTER(c_size_t)]),
+    ("qps_kv_extend_paged", c_int32, [POINTER(PagedExtendArgs), c_void_p]),
+    ("qps_kv_fork_plan", c_int32, [POINTER(PagedForkArgs), POINTER(c_size_t)]),
+    ("qps_kv_fork_paged", c_int32, [POINTER(PagedForkArgs), c_void_p]),
+    ("qps_kv_compact_plan", c_int32, [POINTER(PagedCompactArgs), POINTER(c_size_t)]),
+    ("qps_kv_compact_paged", c_int32, [POINTER(PagedCompactArgs), c_void_p]),
     ("qps_paged_inject_fault", c_int32, [c_int32, c_int32]),
     ("qps_host_alloc", c_int32, [c_size_t, c_int32, POINTER(c_void_p)]),
     ("qps_host_free", c_int32, [c_void_p]),

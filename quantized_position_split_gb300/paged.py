@@ -1,5 +1,6 @@
-"""Serving calls around a paged KV cache: ``qk_norm_rope``, ``kv_append_paged`` and
-``attn_decode_paged`` of ``include/qps.h``, as argument blocks and calls.
+"""Serving calls around a paged KV cache: ``qk_norm_rope``, ``kv_append_paged``,
+``attn_decode_paged`` and ``attn_prompt_paged`` of ``include/qps.h``, and those on its pages,
+``kv_extend_paged``, ``kv_fork_paged`` and ``kv_compact_paged``, as argument blocks and calls.
 
 Like ``attn_args`` / ``attn_decode_window``, each call takes an argument block that a
 decode loop builds once for a layer and keeps: the block holds the addresses of its
@@ -373,6 +374,132 @@ def paged_prompt_args(q: torch.Tensor, cache: PagedKV, page_table: torch.Tensor,
 
 def attn_prompt_paged(a: N.PagedPromptArgs, stream=None):
     """Attention of ``paged_prompt_args``; returns (o, lse)."""
+    _call(a, stream)
+    return a._out
+
+
+class PagedSeqs:
+    """The sequences of one or more paged caches (the layers', of one page size and number of
+    pages): ``page_table`` [batch, width], ``kv_lens`` [batch] and ``refs`` [n_pages], int32, all
+    on the device.  ``refs`` counts the entries that name a page; 0: the page is free."""
+
+    def __init__(self, caches, page_table: torch.Tensor, kv_lens: torch.Tensor, refs: torch.Tensor):
+        self.caches = (caches,) if isinstance(caches, PagedKV) else tuple(caches)
+        if not self.caches or not all(isinstance(c, PagedKV) for c in self.caches):
+            raise _bad("caches must be a PagedKV or a list of them")
+        first = self.caches[0]
+        self.device, self.n_pages, self.page_size = first.device, first.n_pages, first.page_size
+        for c in self.caches:
+            if c.device != self.device or c.n_pages != self.n_pages or c.page_size != self.page_size:
+                raise _bad("the caches must share a device, a page size and a number of pages")
+        _tensor(page_table, "page_table", self.device, torch.int32, contiguous=False)
+        if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise _bad("page_table must be [batch, width] with contiguous rows")
+        self.batch = page_table.shape[0]
+        _tensor(kv_lens, "kv_lens", self.device, torch.int32, (self.batch,))
+        _tensor(refs, "refs", self.device, torch.int32, (self.n_pages,))
+        self.page_table, self.kv_lens, self.refs = page_table, kv_lens, refs
+        self._array = (N.PagedKvStruct * len(self.caches))(*[c.struct for c in self.caches])
+        s = N.PagedSeqsStruct()
+        s.caches = ctypes.cast(self._array, ctypes.POINTER(N.PagedKvStruct))
+        s.n_caches, s.batch = len(self.caches), self.batch
+        s.page_table, s.table_width = page_table.data_ptr(), page_table.shape[1]
+        s.table_stride = page_table.stride(0) if self.batch > 1 else page_table.shape[1]
+        s.kv_lens, s.refs = kv_lens.data_ptr(), refs.data_ptr()
+        self.struct = s
+
+    @classmethod
+    def empty(cls, caches, batch: int, width: int):
+        """Sequences without positions, over pages that are all free."""
+        first = caches if isinstance(caches, PagedKV) else caches[0]
+        make = lambda shape, x: torch.full(shape, x, dtype=torch.int32, device=first.device)  # noqa: E731
+        return cls(caches, make((batch, width), -1), make((batch,), 0), make((first.n_pages,), 0))
+
+
+def _workspace(a, plan: str, workspace, dev) -> torch.Tensor:
+    need = ctypes.c_size_t()
+    N.check(getattr(N.load(), plan)(ctypes.byref(a), ctypes.byref(need)))
+    if workspace is None:
+        workspace = torch.empty((need.value,), dtype=torch.uint8, device=dev)
+    _tensor(workspace, "workspace", dev, torch.uint8)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return workspace
+
+
+def _out(t, what: str, shape: tuple, dtype, dev) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _tensor(t, what, dev, dtype, shape)
+
+
+def paged_extend_args(seqs: PagedSeqs, n_new: torch.Tensor, *, max_tokens: int, window: int = 0, sinks: int = 0, q_starts=None,
+                      slots=None, positions=None, workspace=None) -> N.PagedExtendArgs:
+    """Argument block of ``kv_extend_paged``: sequence b grows by ``n_new[b]`` (int32) positions,
+    or is cut back by so many where that is negative.  ``max_tokens``: rows of ``slots`` and
+    ``positions``, at least the new positions of any call.  ``window`` and ``sinks``: those of the
+    attention, so that pages that it no longer reads are given back.  ``q_starts`` [batch + 1]
+    int32, ``slots`` and ``positions`` [max_tokens] int64 are allocated if None.
+    """
+    dev = seqs.device
+    if max_tokens < 0:
+        raise _bad("max_tokens must be >= 0")
+    a = N.PagedExtendArgs()
+    a.seqs = seqs.struct
+    a.n_new = _tensor(n_new, "n_new", dev, torch.int32, (seqs.batch,)).data_ptr()
+    a.window, a.sinks, a.max_tokens = int(window), int(sinks), int(max_tokens)
+    q_starts = _out(q_starts, "q_starts", (seqs.batch + 1,), torch.int32, dev)
+    slots = _out(slots, "slots", (max_tokens,), torch.int64, dev)
+    positions = _out(positions, "positions", (max_tokens,), torch.int64, dev)
+    a.q_starts, a.slots, a.positions = q_starts.data_ptr(), slots.data_ptr(), positions.data_ptr()
+    workspace = _workspace(a, "qps_kv_extend_plan", workspace, dev)
+    a._out = (q_starts, slots, positions)
+    return _block(a, "qps_kv_extend_paged", dev, (seqs, n_new, q_starts, slots, positions, workspace))
+
+
+def kv_extend_paged(a: N.PagedExtendArgs, stream=None):
+    """Room for the next positions of ``paged_extend_args``; returns (q_starts, slots,
+    positions), as ``attn_prompt_paged`` and ``kv_append_paged`` take them."""
+    _call(a, stream)
+    return a._out
+
+
+def paged_fork_args(seqs: PagedSeqs, src: torch.Tensor, dst: torch.Tensor, *, workspace=None) -> N.PagedForkArgs:
+    """Argument block of ``kv_fork_paged``: sequence ``dst[i]`` becomes a copy of ``src[i]``
+    (int32 [n]), or is given back where that is negative."""
+    dev = seqs.device
+    _tensor(src, "src", dev, torch.int32)
+    if src.dim() != 1:
+        raise _bad("src must be [n]")
+    _tensor(dst, "dst", dev, torch.int32, tuple(src.shape))
+    a = N.PagedForkArgs()
+    a.seqs, a.n = seqs.struct, src.shape[0]
+    a.src, a.dst = src.data_ptr(), dst.data_ptr()
+    workspace = _workspace(a, "qps_kv_fork_plan", workspace, dev)
+    return _block(a, "qps_kv_fork_paged", dev, (seqs, src, dst, workspace))
+
+
+def kv_fork_paged(a: N.PagedForkArgs, stream=None) -> None:
+    """Fork and give back the sequences of ``paged_fork_args``."""
+    _call(a, stream)
+
+
+def paged_compact_args(seqs: PagedSeqs, *, new_ids=None, live=None, workspace=None) -> N.PagedCompactArgs:
+    """Argument block of ``kv_compact_paged``.  ``new_ids`` [n_pages] and ``live`` [1], int32,
+    are allocated if None."""
+    dev = seqs.device
+    a = N.PagedCompactArgs()
+    a.seqs = seqs.struct
+    new_ids = _out(new_ids, "new_ids", (seqs.n_pages,), torch.int32, dev)
+    live = _out(live, "live", (1,), torch.int32, dev)
+    a.new_ids, a.live = new_ids.data_ptr(), live.data_ptr()
+    workspace = _workspace(a, "qps_kv_compact_plan", workspace, dev)
+    a._out = (new_ids, live)
+    return _block(a, "qps_kv_compact_paged", dev, (seqs, new_ids, live, workspace))
+
+
+def kv_compact_paged(a: N.PagedCompactArgs, stream=None):
+    """Move the pages in use of ``paged_compact_args`` to the front; returns (new_ids, live):
+    what each page has become (-1: it was free), and how many there are."""
     _call(a, stream)
     return a._out
 
