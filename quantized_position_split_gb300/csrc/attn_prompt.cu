@@ -13,8 +13,8 @@ namespace qps {
 namespace {
 
 // ---- decoding -------------------------------------------------------------------------------
-// The tiles that any query token of a sequence sees, once, to fp16 rows: V rounded, K as the fp16
-// value and what its rounding left.  A value beyond fp16's largest is taken as that (a q8_0 code
+// The tiles that any query token of a sequence sees, once, to fp16 rows: the value, and behind it
+// what its rounding left (V: where v_parts is 2).  The value is cut to fp16's range (a q8_0 code
 // times its scale may pass it by a rounding: 127 x 516).  A warp takes a row: lane L holds the
 // elements E L .. E L + E - 1 (E = D / 32).  A tile decoded here is read by many row tiles; over
 // the row tiles themselves the decoding would be repeated for each.
@@ -130,11 +130,12 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) prompt_decode_kernel(const 
         const float left = x[i] - __half2float(hi[i]);
         lo[i] = __float2half_rn(fabsf(left) <= 65504.f ? left : 0.f);
       }
-      __half* out = dst + to * (side ? D : 2 * D) + lane * E;
+      const bool two = !side || p.v_parts == 2;
+      __half* out = dst + to * (two ? 2 * D : D) + lane * E;
 #pragma unroll
       for (int i = 0; i < E; i += 2) {
         *reinterpret_cast<__half2*>(out + i) = __halves2half2(hi[i], hi[i + 1]);
-        if (!side) *reinterpret_cast<__half2*>(out + D + i) = __halves2half2(lo[i], lo[i + 1]);
+        if (two) *reinterpret_cast<__half2*>(out + D + i) = __halves2half2(lo[i], lo[i + 1]);
       }
     }
   }
@@ -293,6 +294,7 @@ qps_status plan_prompt(const qps_paged_prompt_args* a, Plan* out) {
   p.out_dtype = a->o_dtype;
   p.kfmt = kv.kfmt;
   p.vfmt = kv.vfmt;
+  p.v_parts = kv.vfmt != QPS_FMT_F16 && a->o_dtype != QPS_DT_BF16 ? 2 : 1;
   for (int i = 0; i < 3; ++i) {
     p.k[i] = kv.k[i];
     p.v[i] = kv.v[i];
@@ -329,7 +331,7 @@ qps_status plan_prompt(const qps_paged_prompt_args* a, Plan* out) {
       return bad("batch * table_width * page_size is too large for compressed rows", QPS_ERR_UNSUPPORTED);
     const size_t side = (size_t)a->batch * most * kv.hkv * kPromptTile * kv.d * sizeof(__half);
     out->off_v = out->off_k + (kv.kfmt != QPS_FMT_F16 ? up(2 * side) : 0);
-    out->bytes = out->off_v + (kv.vfmt != QPS_FMT_F16 ? up(side) : 0);
+    out->bytes = out->off_v + (kv.vfmt != QPS_FMT_F16 ? up(p.v_parts * side) : 0);
   }
   return QPS_OK;
 }
@@ -373,12 +375,12 @@ qps_status attn_prompt_paged(const qps_paged_prompt_args* a, cudaStream_t s) {
     st = p.d == 64 ? launch_decode<64>(p, s) : p.d == 128 ? launch_decode<128>(p, s) : p.d == 256 ? launch_decode<256>(p, s) : launch_decode<512>(p, s);
     if (st != QPS_OK) return st;
   }
-  switch (p.d) {
-    case 64: st = launch_prompt_d64(p, s); break;
-    case 128: st = launch_prompt_d128(p, s); break;
-    case 256: st = launch_prompt_d256(p, s); break;
-    default: st = launch_prompt_d512(p, s);
-  }
+  using Launch = qps_status (*)(const PromptParams&, cudaStream_t);
+  static const Launch launches[4][2] = {{launch_prompt_d64, launch_prompt_d64_q},
+                                        {launch_prompt_d128, launch_prompt_d128_q},
+                                        {launch_prompt_d256, launch_prompt_d256_q},
+                                        {launch_prompt_d512, launch_prompt_d512_q}};
+  st = launches[p.d == 64 ? 0 : p.d == 128 ? 1 : p.d == 256 ? 2 : 3][p.dense_k ? 1 : 0](p, s);
   if (st != QPS_OK || p.n_split == 1) return st;
   switch (p.d) {
     case 64: return launch_merge<64>(p, s);

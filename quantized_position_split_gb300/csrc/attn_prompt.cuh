@@ -12,8 +12,11 @@
 // CTAs share a row, each computing all of S and half of O's columns.
 //
 // K and V pass through one ring of slots, [128 positions][SD columns] each, in the order of their
-// first use.  A K that was compressed comes in two parts, the fp16 value and what its rounding
-// left, whose products are summed: logits keep float32 accuracy.
+// first use; one stream gives a slot back when its products have run, two when the second's have
+// (K and V of a tile are then held together: at most 4 of 5 slots).  A K that was compressed comes in two parts, the fp16 value and what its rounding
+// left, whose products are summed: logits keep float32 accuracy.  So does a compressed V, but for
+// a bf16 output: one part's rounding beside that of P made an fp16 output's error 1.7 times the
+// one its type has (3.6e-4 against 2.1e-4), and is lost in bf16's.
 //
 // The running reference m of a row is set kRefShift (log2) below a tile's maximum, and again only
 // when one exceeds what it was set for by more than kRefLazy (paged.h): P stays within fp16, and
@@ -35,27 +38,59 @@ namespace prompt {
 
 using namespace tm;
 
-template <int D, int KP>
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 16 columns of the warp's 32 lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+
+template <int D, int KP, int VP>
 struct GeoP {
   static constexpr int NQ = D <= 128 ? 2 : 1;      // tiles of rows
   static constexpr int SD = D < 128 ? D : 128;     // columns of a slot
   static constexpr int VD = D <= 256 ? D : 256;    // columns of O
   static constexpr int CG = SD / 64;               // 128-byte column groups of a slot
   static constexpr int SLOT = kTok * SD * 2;
-  static constexpr int KS = KP * D / SD, VS = VD / SD;  // slots of a tile
+  static constexpr int KS = KP * D / SD, VC = VD / SD, VS = VP * VC;  // slots of a tile
   static constexpr int Q_TILE = kRows * D * 2;
   static constexpr int STAGES = D == 64 ? 10 : D == 512 ? 3 : 5;
   static constexpr int RING = NQ * Q_TILE;
   static constexpr int BAR = RING + STAGES * SLOT;
   static constexpr int SMEM = BAR + 256 + 1024;    // + slack for the 1024-byte base alignment
   static constexpr int THREADS = 128 + 128 * NQ;
+  // two streams: registers a thread of the first warps and of the softmax (3 x 168 at launch)
+  static constexpr int FEW = 72, MANY = 216;
   static constexpr int S_COL = 0, O_COL = 256;     // TMEM columns
 };
 
-template <int D, int KP>
-__global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
+template <int D, int KP, int VP>
+__global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
     attn_prompt_kernel(const __grid_constant__ PromptParams p, const __grid_constant__ TmaSet maps) {
-  using G = GeoP<D, KP>;
+  using G = GeoP<D, KP, VP>;
   constexpr int ST = G::STAGES, NQ = G::NQ;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -117,14 +152,14 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (ST + s); };
   auto s_full = [&](int w) { return bars + 8 * (2 * ST + w); };
-  auto p_ready = [&](int w) { return bars + 8 * (2 * ST + 2 + w); };
-  const uint32_t all_done = bars + 8 * (2 * ST + 4), q_full = bars + 8 * (2 * ST + 5), pv_done = bars + 8 * (2 * ST + 6);
-  static_assert(8 * (2 * ST + 7) <= 240, "barriers fit their region");
+  auto p_ready = [&](int w, int h) { return bars + 8 * (2 * ST + 2 + 2 * w + h); };  // (half a tile's positions)
+  const uint32_t q_full = bars + 8 * (2 * ST + 6), all_done = bars + 8 * (2 * ST + 7), pv_done = bars + 8 * (2 * ST + 8);
+  static_assert(8 * (2 * ST + 9) <= 240, "barriers fit their region");
   uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + G::BAR + 240);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::BAR + 244);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * ST + 7; ++i)
-      mbar_init(bars + 8 * i, i == 2 * ST + 5 ? 4 * NQ : i >= 2 * ST + 2 && i < 2 * ST + 4 ? 4 : 1);
+    for (int i = 0; i < 2 * ST + 9; ++i)
+      mbar_init(bars + 8 * i, i == 2 * ST + 6 ? 4 * NQ : i >= 2 * ST + 2 && i < 2 * ST + 6 ? 4 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     *abort_flag = 0;
   }
@@ -155,6 +190,8 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
   auto k_at = [&](int j) { return NQ == 2 || j == 0 ? j * KV : G::KS + (j - 1) * KV; };
   auto v_at = [&](int j) { return NQ == 2 ? j * KV + G::KS : G::KS + j * KV + (j + 1 < ntiles ? G::KS : 0); };
 
+  if (warp < 4) {
+  if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::FEW));
   if (warp == 0) {
     // ---- slots: boxes of min(page, 128) positions of one page and 64 columns, one a lane; a
     // lane's page of the next tile is read a tile ahead.  Decoded rows: boxes of 128 positions. ----
@@ -202,7 +239,7 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
     };
     auto put_v = [&](int j, int page) -> bool {
       for (int s = 0; s < G::VS; ++s)
-        if (!put(&maps.v, p.dense_v != nullptr, half * G::VD + s * G::SD, j, page)) return false;
+        if (!put(&maps.v, p.dense_v != nullptr, s / G::VC * D + half * G::VD + s % G::VC * G::SD, j, page)) return false;
       return true;
     };
     int page = entry(0), next = entry(1);
@@ -248,11 +285,12 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
     for (int i = 0; i < min(2, steps) && ok; ++i) ok = qk(i);
     for (int i = 0; i < steps && ok; ++i) {
       const int j = i / NQ, w = i % NQ, at = v_at(j);
-      if (w == 0) {
-        // rows that no query sees hold whatever was there, and 0 x NaN is NaN
-        const int t = first_of(j), a0 = max(0, p.sinks - t), a1 = min(kTok, none_lo - t), b0 = end - t;
-        for (int s = 0; s < G::VS && ok; ++s) {
-          const int st = (at + s) % ST;
+      // (rows that no query sees hold whatever was there, and 0 x NaN is NaN)
+      const int t = first_of(j), a0 = max(0, p.sinks - t), a1 = min(kTok, none_lo - t), b0 = end - t;
+#pragma unroll 1
+      for (int s = 0; s < G::VS && ok; ++s) {
+        const int st = (at + s) % ST;
+        if (w == 0) {
           if (!(ok = wait(full(st), ((at + s) / ST) & 1, j))) break;
           if (b0 < kTok || a0 < a1) {
             for (int r = lane >> 3; r < kTok; r += 4)
@@ -265,29 +303,28 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
             __syncwarp();
           }
         }
-        if (!ok) break;
-      }
-      if (w < live) {
-        if (!(ok = wait(p_ready(i & 1), NQ == 2 ? j & 1 : (j >> 1) & 1, j))) break;
-        fence_after();
-      }
-#pragma unroll 1
-      for (int s = 0; s < G::VS; ++s) {
-        const int st = (at + s) % ST;
-        if (w < live) {
-          const uint32_t d = tmem + G::O_COL + w * D + s * G::SD, a = tmem + G::S_COL + (i & 1) * kTok;
-          const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, kTok * 128);
+        const uint32_t d = tmem + G::O_COL + w * D + s % G::VC * G::SD, a = tmem + G::S_COL + (i & 1) * kTok;
+        const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, kTok * 128);
+        const uint32_t more = j > 0 || s >= G::VC;  // (0: a stream's first product starts its O)
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk)
-            mma_ts(d, a + kk * 8, b + (uint64_t)((kk * 2048) >> 4), ID_O, j > 0 || kk > 0, one);
+        for (int h = 0; h < 2; ++h) {
+          if (w >= live) continue;
+          if (s == 0 && !(ok = wait(p_ready(i & 1, h), NQ == 2 ? j & 1 : (j >> 1) & 1, j))) break;
+          fence_after();
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_ts(d, a + kk * 8, b + (uint64_t)((kk * 2048) >> 4), ID_O, more | (kk > 0), one);
         }
-        if (w == NQ - 1) commit(empty(st), one);
+        if (ok && w == NQ - 1) commit(empty(st), one);
       }
+      if (!ok) break;
       if constexpr (NQ == 1) commit(pv_done, one);
       if (i + 2 < steps) ok = qk(i + 2);
     }
     commit(all_done, one);  // completes when everything issued above has
-  } else if (warp >= 4) {
+  }
+  } else {
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::MANY));
     // ---- softmax: stream w, one row a thread --------------------------------------------------
     const int w = (warp - 4) >> 2, r = (warp & 3) * 32 + lane, rr = w * kRows + r;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
@@ -324,11 +361,7 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
     // positions below lim are visible to the row, but for [sinks, low)
     const int lim = mine ? pos0 + (row0 + rr) / p.group + 1 : 0, low = p.window ? lim - p.window : 0;
     constexpr float LOG2E = 1.4426950408889634f;
-    const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap : 0.f;
-    auto logit = [&](uint32_t v) -> float {
-      const float s = __uint_as_float(v);
-      return cap > 0.f ? mma::softcap_tanh(s * p.scale, cap, cap_k) * LOG2E : s * qs;
-    };
+    const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap * p.scale : 0.f;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < ntiles && w < live; ++j) {
@@ -336,49 +369,46 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
       const uint32_t s_at = tmem + lanes + G::S_COL + buf * kTok;
       if (!(ok = wait(s_full(buf), par, j))) break;
       fence_after();
+      // the row's 128 logits, in registers
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(v[c], s_at + 32 * c);
+      tmem_wait_ld();
+      float f = qs;  // from here on logits, in units of log2, are f v
+      if (cap > 0.f) {  // c tanh(x / c) = c - 2 c / (1 + e^(2 x / c))
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float r;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(__uint_as_float(v[c][i]) * cap_k)));
+            v[c][i] = __float_as_uint(fmaf(-2.f * LOG2E * cap, r, LOG2E * cap));
+          }
+        f = 1.f;
+      } else if (!(qs > 0.f)) {  // (the maximum below is of v)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * qs);
+        f = 1.f;
+      }
       const int first = first_of(j);
-      // Whole tiles of plain logits, the common case, have a body of their own: maxima and
-      // exponentials straight from S (a positive scale keeps the order), four chains each,
-      // the next 32 columns read beside the present ones' arithmetic.
-      const bool fast = __all_sync(0xffffffffu, (first + kTok <= lim && (first >= low || first + kTok <= p.sinks)) || !mine) &&
-                        cap <= 0.f && qs >= 0.f;
-      auto hidden = [&](int t) { return t >= lim || (t < low && t >= p.sinks); };
-      uint32_t va[32], vb[32];
-      float mx = -INFINITY;
-      if (fast) {
-        float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto most = [&](const uint32_t (&v)[32]) {
+      if (__any_sync(0xffffffffu, first + kTok > lim || (first < low && first + kTok > p.sinks))) {
+        const int b0 = lim - first, b1 = low - first, b2 = p.sinks - first;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mm[k] = fmaxf(fmaxf(mm[k], __uint_as_float(v[i + k])), __uint_as_float(v[i + 4 + k]));
-        };
-        tmem_ld32(va, s_at);
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < kTok / 32; c += 2) {
-          tmem_ld32(vb, s_at + 32 * (c + 1));
-          most(va);
-          tmem_wait_ld();
-          if (c + 2 < kTok / 32) tmem_ld32(va, s_at + 32 * (c + 2));
-          most(vb);
-          if (c + 2 < kTok / 32) tmem_wait_ld();
-        }
-        mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * qs;
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
-          __syncwarp();
-          tmem_ld32(va, s_at + 32 * c);
-          tmem_wait_ld();
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (!hidden(first + 32 * c + i)) mx = fmaxf(mx, logit(va[i]));
-        }
-        __syncwarp();
+            if (32 * c + i >= b0 || (32 * c + i < b1 && 32 * c + i >= b2)) v[c][i] = 0xff800000u;
       }
-      mx -= kRefShift;
+      float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is no maximum)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mm[k] = fmaxf(fmaxf(mm[k], __uint_as_float(v[c][i + k])), __uint_as_float(v[c][i + 4 + k]));
+      const float mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * f - kRefShift;
       const bool raise = mx - m > kRefLazy;  // (false when both are -inf)
       const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
       if (raise) {
@@ -393,68 +423,39 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
           fence_after();
         }
 #pragma unroll 1
-        for (int c = 0; c < G::VD / 32; ++c) {
+        for (int c = 0; c < G::VD / 16; ++c) {
+          uint32_t o[16];
           __syncwarp();
-          tmem_ld32(va, o_at + 32 * c);
+          tmem_ld16(o, o_at + 16 * c);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * cr);
-          tmem_st32(o_at + 32 * c, va);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * cr);
+          tmem_st16(o_at + 16 * c, o);
         }
       }
       const float ms = m == -INFINITY ? 0.f : m;
-      float sum = 0.f;
-      if (fast) {
-        float ss[4] = {0.f, 0.f, 0.f, 0.f};
-        auto weigh = [&](const uint32_t (&v)[32], int c) {
-          uint32_t pk[16];
+      const uint64_t f2 = pack2(f, f), m2 = pack2(-ms, -ms);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float a = ex2(fmaf(__uint_as_float(v[2 * i]), qs, -ms));
-            const float b = ex2(fmaf(__uint_as_float(v[2 * i + 1]), qs, -ms));
-            ss[(2 * i) & 3] += a;
-            ss[(2 * i + 1) & 3] += b;
-            pk[i] = mma::pack_h2(a, b);
-          }
-          tmem_st16(s_at + 16 * c, pk);  // (over columns of S that are already read, none under way)
-        };
-        tmem_ld32(va, s_at);
-        tmem_wait_ld();
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < kTok / 32; c += 2) {
-          tmem_ld32(vb, s_at + 32 * (c + 1));
-          weigh(va, c);
-          tmem_wait_ld();
-          if (c + 2 < kTok / 32) tmem_ld32(va, s_at + 32 * (c + 2));
-          weigh(vb, c + 1);
-          if (c + 2 < kTok / 32) tmem_wait_ld();
+        for (int i = 0; i < 16; ++i) {
+          const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), f2, m2));
+          const float a = ex2(x.x), b = ex2(x.y);
+          sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+          pk[i] = mma::pack_h2(a, b);
         }
-        sum = (ss[0] + ss[1]) + (ss[2] + ss[3]);
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < kTok / 32; ++c) {
+        tmem_st16(s_at + 16 * c, pk);
+        if (c & 1) {  // half of the positions: the product with their values may start
+          tmem_wait_st();
+          fence_before();
           __syncwarp();
-          tmem_ld32(va, s_at + 32 * c);
-          tmem_wait_ld();
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float a = ex2(logit(va[2 * i]) - ms), b = ex2(logit(va[2 * i + 1]) - ms);
-            if (hidden(first + 32 * c + 2 * i)) a = 0.f;
-            if (hidden(first + 32 * c + 2 * i + 1)) b = 0.f;
-            sum += a + b;
-            pk[i] = mma::pack_h2(a, b);
-          }
-          __syncwarp();
-          tmem_st16(s_at + 16 * c, pk);
+          if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(buf, c >> 1)) : "memory");
         }
-        __syncwarp();
       }
-      l += sum;
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(buf)) : "memory");
+      const float2 s2 = unpack2(add2(sum[0], sum[1]));
+      l += s2.x + s2.y;
     }
     // ---- the rows' output, or their part of it ---------------------------------------------------
     if (ok) ok = wait(all_done, 0, ntiles);
@@ -530,9 +531,10 @@ __global__ void __launch_bounds__(GeoP<D, KP>::THREADS, 1)
   if (warp == 2) tmem_free(tmem, 512);
 }
 
-template <int D, int KP>
+template <int D, int KP, int VP>
 qps_status launch_prompt(const PromptParams& p, cudaStream_t s) {
-  using G = GeoP<D, KP>;
+  using G = GeoP<D, KP, VP>;
+  static_assert(G::NQ == 1 || G::FEW + 2 * G::MANY <= 3 * 168, "the registers of three warpgroups at launch");
   static_assert(G::SMEM <= 227 * 1024, "the slots exceed the shared memory of one CTA");
   static_assert(G::O_COL + G::NQ * G::VD <= 512, "S and O exceed TMEM");
   TmaSet maps;
@@ -540,14 +542,14 @@ qps_status launch_prompt(const PromptParams& p, cudaStream_t s) {
   const int page = 1 << p.page_shift, rows = page < kTok ? page : kTok;
   for (int i = 0; i < 2; ++i) {
     const __half* dense = i ? p.dense_v : p.dense_k;
-    const int cols = i ? D : KP * D;
+    const int cols = (i ? VP : KP) * D;
     const bool ok = dense ? encode_plane_map(i ? &maps.v : &maps.k, dense, 2 * cols, kTok, p.hkv, kTok, p.batch * p.dense_tiles,
                                              (int64_t)p.hkv * kTok, 128, 128, kTok)
                           : encode_plane_map(i ? &maps.v : &maps.k, i ? p.v[0] : p.k[0], 2 * D, page, p.hkv, page, (int)p.n_pages,
                                              (int64_t)p.hkv * page, 128, 128, rows);
     if (!ok) return QPS_ERR_CUDA;
   }
-  auto kern = attn_prompt_kernel<D, KP>;
+  auto kern = attn_prompt_kernel<D, KP, VP>;
   static std::atomic<uint64_t> sized{0};
   int dev = 0;
   QPS_CUDA_TRY(cudaGetDevice(&dev));
@@ -570,11 +572,6 @@ qps_status launch_prompt(const PromptParams& p, cudaStream_t s) {
   count_launch();
   QPS_CUDA_TRY(cudaGetLastError());
   return QPS_OK;
-}
-
-template <int D>
-qps_status launch_prompt_d(const PromptParams& p, cudaStream_t s) {
-  return p.dense_k ? launch_prompt<D, 2>(p, s) : launch_prompt<D, 1>(p, s);
 }
 
 }  // namespace prompt

@@ -32,8 +32,10 @@ struct PromptParams {
   int drop_tile;          // (see qps_paged_inject_fault)
   uint32_t wait_ns;
   // Compressed rows decoded to fp16: [sequence][dense_tiles][KV head][128 positions][columns],
-  // columns = 2 D for keys (value, what its rounding left) and D for values; NULL: fp16 pages
+  // columns = 2 D (value, what its rounding left), or D for values where v_parts is 1; NULL: fp16
+  // pages
   __half *dense_k, *dense_v;
+  int v_parts;
   int dense_tiles;        // tiles of a sequence there
   // the cache's planes, for the decoding
   int kfmt, vfmt;
@@ -82,10 +84,15 @@ __device__ __forceinline__ int prompt_dense(const PromptTiles& seq, int tile) {
   return tile < seq.few ? tile : tile >= seq.low && tile < seq.end ? tile - seq.low + seq.few : -1;
 }
 
+// The kernel for fp16 keys, and for keys in two parts.
 qps_status launch_prompt_d64(const PromptParams& p, cudaStream_t s);
+qps_status launch_prompt_d64_q(const PromptParams& p, cudaStream_t s);
 qps_status launch_prompt_d128(const PromptParams& p, cudaStream_t s);
+qps_status launch_prompt_d128_q(const PromptParams& p, cudaStream_t s);
 qps_status launch_prompt_d256(const PromptParams& p, cudaStream_t s);
+qps_status launch_prompt_d256_q(const PromptParams& p, cudaStream_t s);
 qps_status launch_prompt_d512(const PromptParams& p, cudaStream_t s);
+qps_status launch_prompt_d512_q(const PromptParams& p, cudaStream_t s);
 
 // Query rows (tokens x heads of a group) per CTA, and CTAs that share a row's columns.
 __host__ __device__ constexpr int prompt_rows(int d) { return d <= 128 ? 256 : 128; }

@@ -1,6 +1,8 @@
-// The prompt attention kernel for head_dim 128 (see attn_prompt.cuh).
+// The prompt attention kernel for head_dim 128, fp16 keys (see attn_prompt.cuh).
 #include "attn_prompt.cuh"
 
 namespace qps {
-qps_status launch_prompt_d128(const PromptParams& p, cudaStream_t s) { return prompt::launch_prompt_d<128>(p, s); }
+qps_status launch_prompt_d128(const PromptParams& p, cudaStream_t s) {
+  return p.v_parts == 2 ? prompt::launch_prompt<128, 1, 2>(p, s) : prompt::launch_prompt<128, 1, 1>(p, s);
+}
 }  // namespace qps

@@ -1,6 +1,8 @@
-// The prompt attention kernel for head_dim 256 (see attn_prompt.cuh).
+// The prompt attention kernel for head_dim 256, fp16 keys (see attn_prompt.cuh).
 #include "attn_prompt.cuh"
 
 namespace qps {
-qps_status launch_prompt_d256(const PromptParams& p, cudaStream_t s) { return prompt::launch_prompt_d<256>(p, s); }
+qps_status launch_prompt_d256(const PromptParams& p, cudaStream_t s) {
+  return p.v_parts == 2 ? prompt::launch_prompt<256, 1, 2>(p, s) : prompt::launch_prompt<256, 1, 1>(p, s);
+}
 }  // namespace qps

@@ -1,6 +1,8 @@
-// The prompt attention kernel for head_dim 512 (see attn_prompt.cuh).
+// The prompt attention kernel for head_dim 512, fp16 keys (see attn_prompt.cuh).
 #include "attn_prompt.cuh"
 
 namespace qps {
-qps_status launch_prompt_d512(const PromptParams& p, cudaStream_t s) { return prompt::launch_prompt_d<512>(p, s); }
+qps_status launch_prompt_d512(const PromptParams& p, cudaStream_t s) {
+  return p.v_parts == 2 ? prompt::launch_prompt<512, 1, 2>(p, s) : prompt::launch_prompt<512, 1, 1>(p, s);
+}
 }  // namespace qps
