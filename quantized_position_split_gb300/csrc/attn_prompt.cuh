@@ -58,6 +58,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // 16 columns of the warp's 32 lanes
 __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
@@ -97,6 +102,23 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   const uint32_t sbase = smem_addr(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
+  // ---- barriers, TMEM --------------------------------------------------------------------------
+  const uint32_t bars = sbase + G::BAR;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (ST + s); };
+  auto s_full = [&](int w) { return bars + 8 * (2 * ST + w); };
+  auto p_ready = [&](int w, int h) { return bars + 8 * (2 * ST + 2 + 2 * w + h); };  // (half a tile's positions)
+  const uint32_t q_full = bars + 8 * (2 * ST + 6), all_done = bars + 8 * (2 * ST + 7), pv_done = bars + 8 * (2 * ST + 8);
+  static_assert(8 * (2 * ST + 9) <= 240, "barriers fit their region");
+  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + G::BAR + 240);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::BAR + 244);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2 * ST + 9; ++i)
+      mbar_init(bars + 8 * i, i == 2 * ST + 6 ? 4 * NQ : i >= 2 * ST + 2 && i < 2 * ST + 6 ? 4 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    *abort_flag = 0;
+  }
+  if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this CTA's rows and tiles -------------------------------------------------------------
   int idx = blockIdx.x;
@@ -134,7 +156,14 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
-  if (bz < 0) return;  // more CTAs than row tiles (every warp finds the same)
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = uniform(*tmem_word);
+  if (bz < 0) {  // more CTAs than row tiles (every warp finds the same)
+    if (warp == 2) tmem_free(tmem, 512);
+    return;
+  }
   const int rows = min(NQ * kRows, (int)min((int64_t)sq.n * p.group - row0, (int64_t)NQ * kRows));
   const int pos0 = sq.len - sq.n;  // position of the sequence's first query token
   const int q_lo = pos0 + row0 / p.group, q_hi = pos0 + (row0 + rows - 1) / p.group;
@@ -146,28 +175,6 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   const int none_lo = p.window ? max(0, q_lo - p.window + 1) : 0; // nor any of [sinks, none_lo)
   const int live = uniform(NQ == 1 || rows > kRows ? NQ : 1);     // streams that have rows
   auto first_of = [&](int j) { return prompt_tile(all, i0 + j) * kPromptTile; };
-
-  // ---- barriers, TMEM --------------------------------------------------------------------------
-  const uint32_t bars = sbase + G::BAR;
-  auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (ST + s); };
-  auto s_full = [&](int w) { return bars + 8 * (2 * ST + w); };
-  auto p_ready = [&](int w, int h) { return bars + 8 * (2 * ST + 2 + 2 * w + h); };  // (half a tile's positions)
-  const uint32_t q_full = bars + 8 * (2 * ST + 6), all_done = bars + 8 * (2 * ST + 7), pv_done = bars + 8 * (2 * ST + 8);
-  static_assert(8 * (2 * ST + 9) <= 240, "barriers fit their region");
-  uint32_t* tmem_word = reinterpret_cast<uint32_t*>(smem + G::BAR + 240);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + G::BAR + 244);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * ST + 9; ++i)
-      mbar_init(bars + 8 * i, i == 2 * ST + 6 ? 4 * NQ : i >= 2 * ST + 2 && i < 2 * ST + 6 ? 4 : 1);
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    *abort_flag = 0;
-  }
-  if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = uniform(*tmem_word);
 
   int issued = 0;  // (warp 0) slots under way or landed
   auto wait = [&](uint32_t bar, uint32_t parity, int tile) -> bool {  // (as in attn_tm.cuh)
@@ -329,27 +336,29 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
     const int w = (warp - 4) >> 2, r = (warp & 3) * 32 + lane, rr = w * kRows + r;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t o_at = tmem + lanes + G::O_COL + w * D;
+    const bool mine = rr < rows;
+    // the row's query token, counted from the CTA's first, and head
+    const int t_first = row0 / p.group, tok = (row0 + rr) / p.group - t_first, h = head * p.group + (row0 + rr) % p.group;
     {
       // Q [128][D] of the stream, K-major: row r's 16-byte chunk c of a column group at r * 128 +
-      // (c ^ r % 8) * 16; loads of one round together
-      constexpr int N = kRows * D / 8 / 128, U = N < 16 ? N : 16;
-      const int tid = threadIdx.x & 127;
+      // (c ^ r % 8) * 16; each warp its own 32 rows, the loads of one round together
+      constexpr int N = D / 8, U = N < 16 ? N : 16;
 #pragma unroll 1
       for (int k0 = 0; k0 < N; k0 += U) {
         uint4 v[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const int i = tid + (k0 + k) * 128, qr = w * kRows + i / (D / 8), c = i % (D / 8);
+          const int i = (k0 + k) * 32 + lane, qr = i / (D / 8), c = i % (D / 8);
+          const int qt = __shfl_sync(0xffffffffu, tok, qr), qh = __shfl_sync(0xffffffffu, h, qr);
           v[k] = make_uint4(0, 0, 0, 0);
-          if (qr < rows) {
-            const int e = (row0 + qr) / p.group, h = head * p.group + (row0 + qr) % p.group;
-            const int64_t at = (int64_t)(sq.first + e) * p.q_tok + (int64_t)h * D + c * 8;
-            if (in_bounds(sq.first + e < p.tokens, p.err)) v[k] = *reinterpret_cast<const uint4*>(p.q + at);
+          if (w * kRows + (warp & 3) * 32 + qr < rows) {
+            const int64_t t = (int64_t)sq.first + t_first + qt;
+            if (in_bounds(t < p.tokens && qh < p.hq, p.err)) v[k] = *reinterpret_cast<const uint4*>(p.q + t * p.q_tok + qh * D + c * 8);
           }
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const int i = tid + (k0 + k) * 128, qr = i / (D / 8), c = i % (D / 8);
+          const int i = (k0 + k) * 32 + lane, qr = (warp & 3) * 32 + i / (D / 8), c = i % (D / 8);
           *reinterpret_cast<uint4*>(smem + w * G::Q_TILE + (c >> 3) * (kRows * 128) + qr * 128 + (((c & 7) ^ (qr & 7)) << 4)) = v[k];
         }
       }
@@ -357,9 +366,8 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       __syncwarp();
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(q_full) : "memory");
     }
-    const bool mine = rr < rows;
     // positions below lim are visible to the row, but for [sinks, low)
-    const int lim = mine ? pos0 + (row0 + rr) / p.group + 1 : 0, low = p.window ? lim - p.window : 0;
+    const int lim = mine ? pos0 + t_first + tok + 1 : 0, low = p.window ? lim - p.window : 0;
     constexpr float LOG2E = 1.4426950408889634f;
     const float qs = p.scale * LOG2E, cap = p.softcap, cap_k = cap > 0.f ? 2.f * LOG2E / cap * p.scale : 0.f;
     float m = -INFINITY, l = 0.f;
@@ -393,118 +401,157 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
         f = 1.f;
       }
       const int first = first_of(j);
-      if (__any_sync(0xffffffffu, first + kTok > lim || (first < low && first + kTok > p.sinks))) {
-        const int b0 = lim - first, b1 = low - first, b2 = p.sinks - first;
+      if (__any_sync(0xffffffffu, first + kTok > lim)) {
+        const int b0 = lim - first;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (32 * c + i >= b0 || (32 * c + i < b1 && 32 * c + i >= b2)) v[c][i] = 0xff800000u;
+            if (32 * c + i >= b0) v[c][i] = 0xff800000u;
       }
+      if (__any_sync(0xffffffffu, first < low && first + kTok > p.sinks)) {
+        const int b1 = low - first, b2 = p.sinks - first;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i < b1 && 32 * c + i >= b2) v[c][i] = 0xff800000u;
+      }
+      // Exponentials of the first half against the present reference, before the maximum is known:
+      // it is rarely raised, and the two then run beside each other (in turn, the products waited
+      // 360 cycles a tile for them).
+      float ms = m == -INFINITY ? 0.f : m;
+      uint64_t sum[2];
+      uint32_t pk[2][16];
+      auto weigh = [&](const uint32_t (&x)[32], uint32_t (&o)[16]) {
+        const uint64_t f2 = pack2(f, f), m2 = pack2(-ms, -ms);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2, m2));
+          const float a = ex2(y.x), b = ex2(y.y);
+          sum[i & 1] = add2(sum[i & 1], pack2(a, b));
+          o[i] = mma::pack_h2(a, b);
+        }
+      };
+      sum[0] = sum[1] = 0;
+      weigh(v[0], pk[0]);
+      weigh(v[1], pk[1]);
       float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is no maximum)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int i = 0; i < 32; i += 8)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mm[k] = fmaxf(fmaxf(mm[k], __uint_as_float(v[c][i + k])), __uint_as_float(v[c][i + 4 + k]));
+          for (int k = 0; k < 4; ++k) mm[k] = max3(mm[k], __uint_as_float(v[c][i + k]), __uint_as_float(v[c][i + 4 + k]));
       const float mx = fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])) * f - kRefShift;
       const bool raise = mx - m > kRefLazy;  // (false when both are -inf)
-      const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
-      if (raise) {
-        m = mx;
-        l *= cr;
-      }
-      if (j > 0 && __any_sync(0xffffffffu, raise)) {
-        // two streams: S of this tile was issued behind this stream's last product, so O is at
-        // rest; one: the last product may still run
-        if constexpr (NQ == 1) {
-          if (!(ok = wait(pv_done, (j - 1) & 1, j))) break;
-          fence_after();
+      if (__any_sync(0xffffffffu, raise)) {
+        const float cr = raise ? ex2(m - mx) : 1.f;  // (0 from -inf)
+        if (raise) {
+          m = mx;
+          l *= cr;
         }
+        if (j > 0) {
+          // two streams: S of this tile was issued behind this stream's last product, so O is at
+          // rest; one: the last product may still run
+          if constexpr (NQ == 1) {
+            if (!(ok = wait(pv_done, (j - 1) & 1, j))) break;
+            fence_after();
+          }
 #pragma unroll 1
-        for (int c = 0; c < G::VD / 16; ++c) {
-          uint32_t o[16];
-          __syncwarp();
-          tmem_ld16(o, o_at + 16 * c);
-          tmem_wait_ld();
+          for (int c = 0; c < G::VD / 16; ++c) {
+            uint32_t o[16];
+            __syncwarp();
+            tmem_ld16(o, o_at + 16 * c);
+            tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * cr);
-          tmem_st16(o_at + 16 * c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * cr);
+            tmem_st16(o_at + 16 * c, o);
+          }
         }
+        ms = m == -INFINITY ? 0.f : m;
+        sum[0] = sum[1] = 0;
+        weigh(v[0], pk[0]);
+        weigh(v[1], pk[1]);
       }
-      const float ms = m == -INFINITY ? 0.f : m;
-      const uint64_t f2 = pack2(f, f), m2 = pack2(-ms, -ms);
-      uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = unpack2(fma2(pack2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), f2, m2));
-          const float a = ex2(x.x), b = ex2(x.y);
-          sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-          pk[i] = mma::pack_h2(a, b);
+      for (int hf = 0; hf < 2; ++hf) {
+        if (hf) {
+          weigh(v[2], pk[0]);
+          weigh(v[3], pk[1]);
         }
-        tmem_st16(s_at + 16 * c, pk);
-        if (c & 1) {  // half of the positions: the product with their values may start
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(buf, c >> 1)) : "memory");
-        }
+        tmem_st16(s_at + 32 * hf, pk[0]);
+        tmem_st16(s_at + 32 * hf + 16, pk[1]);
+        tmem_wait_st();  // half of the positions: the product with their values may start
+        fence_before();
+        __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(p_ready(buf, hf)) : "memory");
       }
       const float2 s2 = unpack2(add2(sum[0], sum[1]));
       l += s2.x + s2.y;
     }
-    // ---- the rows' output, or their part of it ---------------------------------------------------
+    // ---- the rows' output, or their part of it: a thread's row through shared memory (the ring, all
+    // of whose slots have been used) and out as one bulk copy (stores from the registers, 32 rows an
+    // instruction, took 7200 cycles) ----------------------------------------------------------------
     if (ok) ok = wait(all_done, 0, ntiles);
     fence_after();
     if (ok && !__any_sync(0xffffffffu, *abort_flag)) {
+      constexpr int PC = G::VD < 128 ? G::VD : 128;  // columns at a time
       const bool none = l == 0.f;  // (a NaN stays one)
       const float inv = none ? 0.f : 1.f / l;
-      const bool whole = p.n_split == 1;
-      const int h = head * p.group + (row0 + rr) % p.group;
-      const int64_t at = (int64_t)(sq.first + (row0 + rr) / p.group) * p.hq + h;
+      const bool whole = p.n_split == 1, wide = !whole || p.out_dtype == QPS_DT_F32;
+      const int64_t at = ((int64_t)sq.first + t_first + tok) * p.hq + h;
       const bool store = mine && in_bounds(at < p.tokens * p.hq, p.err);
       const int64_t to = whole ? at : (int64_t)split * p.tokens * p.hq + at;
       if (store && half == 0) (whole ? p.out_lse : p.part_lse)[to] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      // (16 bytes between rows: the 32 rows' chunks fall on all banks)
+      const uint32_t bytes = PC * (wide ? 4 : 2);
+      uint8_t* row = smem + G::RING + (uint32_t)(w * kRows + r) * (bytes + 16);
+      static_assert(NQ * kRows * (PC * 4 + 16) <= ST * G::SLOT, "the rows fit the ring");
 #pragma unroll 1
-      for (int c = 0; c < G::VD / 32; ++c) {
-        uint32_t v[32];
-        __syncwarp();
-        if (ntiles > 0 && w < live) {
-          tmem_ld32(v, o_at + 32 * c);
-          tmem_wait_ld();
-        }
-        if (!store) continue;
-        float o[32];
+      for (int x = 0; x < G::VD; x += PC) {
+        if (x > 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(v[i]) * inv;
-        const int64_t x = to * D + half * G::VD + 32 * c;
-        if (!whole || p.out_dtype == QPS_DT_F32) {
-          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + x);
+        for (int c = 0; c < PC / 32; ++c) {
+          uint32_t v[32];
+          __syncwarp();
+          if (ntiles > 0 && w < live) {
+            tmem_ld32(v, o_at + x + 32 * c);
+            tmem_wait_ld();
+          }
+          float o[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + x);
+          for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : __uint_as_float(v[i]) * inv;
+          if (wide) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t y[4];
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(row + 128 * c + 16 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float a = o[8 * i + 2 * q], b = o[8 * i + 2 * q + 1];
-              if (p.out_dtype == QPS_DT_F16) {
-                y[q] = mma::pack_h2(a, b);
-              } else {
-                const __nv_bfloat162 hb = __floats2bfloat162_rn(a, b);
-                y[q] = *reinterpret_cast<const uint32_t*>(&hb);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float a = o[8 * i + 2 * q], b = o[8 * i + 2 * q + 1];
+                if (p.out_dtype == QPS_DT_F16) {
+                  y[q] = mma::pack_h2(a, b);
+                } else {
+                  const __nv_bfloat162 hb = __floats2bfloat162_rn(a, b);
+                  y[q] = *reinterpret_cast<const uint32_t*>(&hb);
+                }
               }
+              *reinterpret_cast<uint4*>(row + 64 * c + 16 * i) = make_uint4(y[0], y[1], y[2], y[3]);
             }
-            dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         }
+        mma::fence_proxy_async();
+        if (store) {
+          uint8_t* dst = reinterpret_cast<uint8_t*>(whole ? p.out : p.part_o) + (to * D + half * G::VD + x) * (wide ? 4 : 2);
+          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(row)), "r"(bytes) : "memory");
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     fence_before();
   }
