@@ -15,127 +15,219 @@ namespace {
 // ---- decoding -------------------------------------------------------------------------------
 // The tiles that any query token of a sequence sees, once, to fp16 rows: the value, and behind it
 // what its rounding left (V: where v_parts is 2).  The value is cut to fp16's range (a q8_0 code
-// times its scale may pass it by a rounding: 127 x 516).  A warp takes a row: lane L holds the
-// elements E L .. E L + E - 1 (E = D / 32).  A tile decoded here is read by many row tiles; over
-// the row tiles themselves the decoding would be repeated for each.
-constexpr int kDecodeWarps = 8, kDecodeRows = 32;  // rows per CTA
+// times its scale may pass it by a rounding: 127 x 516).  A tile decoded here is read by many row
+// tiles; over the row tiles themselves the decoding would be repeated for each.
+//
+// A lane holds 16 elements of a row, a warp 512 / D rows at a time and kAhead such groups under way:
+// compressed rows are small, and what bounds this is how many bytes are (13
+// sequences of 1040 to 3500 positions, 8 heads of 128, q8_0 to 182 MB of bytes read and written:
+// 32 us; a warp with one row, four under way, took 52).  A grid of a few CTAs an SM goes over all tiles: the lengths are on the device, and a CTA
+// for each tile that there may be spent most of its time on those that are not.
+constexpr int kDecodeWarps = 8, kAhead = 4;
+
+// 16 elements as they are stored, and their scale or norm.
+struct Raw {
+  uint4 a, b;
+  __half s;
+};
+// What a lane keeps from row to row: the rotation's signs of its elements.
+struct LaneSigns {
+  uint32_t s1, s2;
+};
 
 template <int D>
-__device__ __forceinline__ void decode_row(const PromptParams& p, int fmt, const uint8_t* const (&plane)[3], int64_t row,
-                                           int lane, float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  const int e0 = lane * E;
+__device__ __forceinline__ Raw load_raw(int fmt, const uint8_t* const (&plane)[3], int64_t row, int c) {
+  Raw r;
+  r.a = r.b = make_uint4(0, 0, 0, 0);
+  r.s = __float2half_rn(0.f);
+  if (row < 0) return r;
   if (fmt == QPS_FMT_F16) {
-    const __half* src = reinterpret_cast<const __half*>(plane[0]) + row * D + e0;
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(src + i));
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    }
+    const uint4* src = reinterpret_cast<const uint4*>(plane[0] + row * (2 * D)) + 2 * c;
+    r.a = src[0];
+    r.b = src[1];
   } else if (fmt == QPS_FMT_Q8_0) {
-    const int8_t* src = reinterpret_cast<const int8_t*>(plane[0]) + row * D + e0;
-    const float sc = __half2float(reinterpret_cast<const __half*>(plane[1])[row * (D / 32) + e0 / 32]);
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const char2 c = *reinterpret_cast<const char2*>(src + i);
-      x[i] = (float)c.x * sc;
-      x[i + 1] = (float)c.y * sc;
-    }
+    r.a = reinterpret_cast<const uint4*>(plane[0] + row * D)[c];
+    r.s = reinterpret_cast<const __half*>(plane[1])[row * (D / 32) + c / 2];
+  } else if (fmt == QPS_FMT_TQ4) {
+    const uint2 x = reinterpret_cast<const uint2*>(plane[0] + row * (D / 2))[c];
+    r.a.x = x.x;
+    r.a.y = x.y;
+    r.s = reinterpret_cast<const __half*>(plane[1])[row];
   } else {
-    const int bits = tq_bits(fmt);
-    const float norm = __half2float(reinterpret_cast<const __half*>(fmt == QPS_FMT_TQ3 ? plane[2] : plane[1])[row]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int e = e0 + i;
-      int k;
-      if (bits == 4) {
-        const int f = plane[0][row * (D / 2) + e / 2] >> (4 * (e & 1)) & 15;
-        k = f & 8 ? 8 + (f & 7) : 7 - (f & 7);
-      } else {
-        const int f = plane[0][row * (D / 4) + e / 4] >> (2 * (e & 3)) & 3;
-        if (bits == 3) k = plane[1][row * (D / 8) + e / 8] >> (e & 7) & 1 ? 4 + f : 3 - f;
-        else k = f & 2 ? 2 + (f & 1) : 1 - (f & 1);
-      }
-      const float c = p.tq_levels[k];
-      x[i] = (p.signs2[e >> 5] >> (e & 31)) & 1u ? -c : c;
-    }
-    // (a + b, a - b) over spans 1 .. G / 2: in the lane below E, between lanes from there
-#pragma unroll
-    for (int h = 1; h < E; h *= 2)
-      if (h < p.tq_block)
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (!(i & h)) {
-            const float a = x[i], b = x[i + h];
-            x[i] = a + b;
-            x[i + h] = a - b;
-          }
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2)
-      if (o * E < p.tq_block)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const float other = __shfl_xor_sync(0xffffffffu, x[i], o);
-          x[i] = lane & o ? other - x[i] : x[i] + other;
-        }
-    const float f = norm * p.tq_scale;
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = (p.signs1[(e0 + i) >> 5] >> ((e0 + i) & 31)) & 1u ? -(x[i] * f) : x[i] * f;
+    r.a.x = reinterpret_cast<const uint32_t*>(plane[0] + row * (D / 4))[c];
+    if (fmt == QPS_FMT_TQ3) r.a.z = reinterpret_cast<const uint16_t*>(plane[1] + row * (D / 8))[c];
+    r.s = reinterpret_cast<const __half*>(fmt == QPS_FMT_TQ3 ? plane[2] : plane[1])[row];
   }
+  return r;
 }
 
 __device__ __forceinline__ float in_range(float x) { return fabsf(x) < INFINITY ? fminf(fmaxf(x, -65504.f), 65504.f) : x; }
+// Two values as fp16, and what that left.
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  const __half2 h = __floats2half2_rn(in_range(a), in_range(b));
+  const float2 f = __half22float2(h);
+  const float c = a - f.x, d = b - f.y;
+  const __half2 l = __floats2half2_rn(fabsf(c) <= 65504.f ? c : 0.f, fabsf(d) <= 65504.f ? d : 0.f);
+  *hi = *reinterpret_cast<const uint32_t*>(&h);
+  *lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// levels: the codebook, in shared memory (the parameters' constant bank serves one address at a time).
+template <int D>
+__device__ __forceinline__ void decode_raw(const PromptParams& p, int fmt, const Raw& r, int lane, const LaneSigns& sg,
+                                           const float* levels, uint32_t (&hi)[8], uint32_t (&lo)[8]) {
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  const float f = __half2float(r.s);
+  if (fmt == QPS_FMT_F16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi[i] = w[i];
+      lo[i] = 0u;
+    }
+  } else if (fmt == QPS_FMT_Q8_0) {
+    if (fabsf(f) <= 512.f) {  // the product fits fp16, and what its rounding leaves is exact
+      const __half2 s2 = __half2half2(r.s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // code + 128 in the low bits of 1024 is exact
+        const uint32_t c = __byte_perm(w[i / 2] ^ 0x80808080u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1152.f));
+        const __half2 h = __hmul2(x, s2), l = __hfma2(x, s2, __hneg2(h));
+        hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+        lo[i] = *reinterpret_cast<const uint32_t*>(&l);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t c = w[i / 2] >> (16 * (i & 1));
+        split2((float)(int8_t)c * f, (float)(int8_t)(c >> 8) * f, &hi[i], &lo[i]);
+      }
+    }
+  } else {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      int k;
+      if (fmt == QPS_FMT_TQ4) {
+        const int c = (int)(w[i / 8] >> (4 * (i % 8))) & 15;
+        k = c & 8 ? c : 7 - c;
+      } else {
+        const int c = (int)(w[0] >> (2 * i)) & 3;
+        if (fmt == QPS_FMT_TQ3) k = w[2] >> i & 1 ? 4 + c : 3 - c;
+        else k = c & 2 ? c : 1 - c;
+      }
+      x[i] = __uint_as_float(__float_as_uint(levels[k]) ^ (sg.s2 >> i << 31));
+    }
+    // (a + b, a - b) over spans 1 .. G / 2: in the lane below 16, between lanes from there
+#pragma unroll
+    for (int h = 1; h < 16; h *= 2)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!(i & h)) {
+          const float a = x[i], b = x[i + h];
+          x[i] = a + b;
+          x[i + h] = a - b;
+        }
+#pragma unroll
+    for (int o = 1; o < D / 16; o *= 2)
+      if (16 * o < p.tq_block)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float other = __shfl_xor_sync(0xffffffffu, x[i], o);
+          x[i] = lane & o ? other - x[i] : x[i] + other;
+        }
+    const float g = f * p.tq_scale;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(__float_as_uint(x[i] * g) ^ (sg.s1 >> i << 31));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split2(x[2 * i], x[2 * i + 1], &hi[i], &lo[i]);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(32 * kDecodeWarps) prompt_decode_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int E = D / 32, PARTS = kPromptTile / kDecodeRows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.y;
+  constexpr int LANES = D / 16, ROWS = 32 / LANES;      // lanes of a row, rows at a time
+  constexpr int R = kPromptTile / kDecodeWarps, N = R / ROWS, A = N < kAhead ? N : kAhead;  // rows of a warp, its groups
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LANES;
+  __shared__ float levels[16];
+  if (threadIdx.x < 16) levels[threadIdx.x] = p.tq_levels[threadIdx.x];
+  __syncthreads();
+  const LaneSigns sg = {p.signs1[c / 2] >> (16 * (c & 1)), p.signs2[c / 2] >> (16 * (c & 1))};
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" :::);
-  const int b = blockIdx.x / PARTS / p.dense_tiles, at = blockIdx.x / PARTS % p.dense_tiles;
-  const PromptSeq sq = prompt_seq(p, b);
-  if (sq.n == 0) return;
-  const PromptTiles t = prompt_tiles(p, sq.len - sq.n, sq.len - 1);
-  if (at >= t.count) return;
-  const int first = prompt_tile(t, at) * kPromptTile;
-  const int low = p.window ? max(0, sq.len - sq.n - p.window + 1) : 0;
-  for (int r = blockIdx.x % PARTS * kDecodeRows + warp; r < (blockIdx.x % PARTS + 1) * kDecodeRows; r += kDecodeWarps) {
-    const int pos = first + r;
-    // (what no query token sees is zeros, and its page is not looked up)
-    int64_t row = -1;
-    if (pos < sq.len && (pos >= low || pos < p.sinks) && in_bounds(pos >> p.page_shift < p.table_width, p.err)) {
-      const int pg = p.table[b * p.table_stride + (pos >> p.page_shift)];
-      if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages)
-        row = (((int64_t)pg * p.hkv + head) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-      else
-        atomicOr(p.err, kErrIndex);
+  // the sequences from b0 on, one a lane; the tiles before them, and up to each
+  int b0 = 0, before = 0, upto = 0, cnt = 0;
+  PromptSeq mine = {0, 0, 0};
+  auto load = [&]() {
+    mine = {0, 0, 0};
+    if (b0 + lane < p.batch) mine = prompt_seq(p, b0 + lane);
+    cnt = upto = mine.n > 0 ? prompt_tiles(p, mine.len - mine.n, mine.len - 1).count : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    const int64_t to = (((int64_t)b * p.dense_tiles + at) * p.hkv + head) * kPromptTile + r;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      __half* dst = side ? p.dense_v : p.dense_k;
-      if (!dst) continue;
-      float x[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = 0.f;
-      if (row >= 0) {
-        if (side) decode_row<D>(p, p.vfmt, p.v, row, lane, x);
-        else decode_row<D>(p, p.kfmt, p.k, row, lane, x);
+  };
+  load();
+  const int head = blockIdx.y;
+  for (int tile = blockIdx.x;; tile += gridDim.x) {
+    unsigned hit;
+    while (!(hit = __ballot_sync(0xffffffffu, before + upto > tile))) {
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      b0 += 32;
+      if (b0 >= p.batch) return;
+      load();
+    }
+    if (tile >= p.dense_tiles) {  // (starts out of order can name more tokens than there are)
+      if (lane == 0) atomicOr(p.err, kErrIndex);
+      return;
+    }
+    const int src = __ffs(hit) - 1, b = b0 + src;
+    const int n = __shfl_sync(0xffffffffu, mine.n, src), len = __shfl_sync(0xffffffffu, mine.len, src);
+    const int at = tile - before - (__shfl_sync(0xffffffffu, upto, src) - __shfl_sync(0xffffffffu, cnt, src));
+    const int first = prompt_tile(prompt_tiles(p, len - n, len - 1), at) * kPromptTile;
+    const int low = p.window ? max(0, len - n - p.window + 1) : 0;
+    // the page of position lane of the warp's rows (what no query token sees is zeros, and its page is
+    // not looked up)
+    int page = -1;
+    const int pos = first + warp * R + lane % R;
+    if (pos < len && (pos >= low || pos < p.sinks) && in_bounds(pos >> p.page_shift < p.table_width, p.err)) {
+      page = p.table[b * p.table_stride + (pos >> p.page_shift)];
+      if ((uint64_t)(int64_t)page >= (uint64_t)p.n_pages) {
+        atomicOr(p.err, kErrIndex);
+        page = -1;
       }
-      __half hi[E], lo[E];
+    }
+    const int64_t to = ((int64_t)tile * p.hkv + head) * kPromptTile + warp * R;
+#pragma unroll 1
+    for (int g0 = blockIdx.z * A; g0 < N; g0 += gridDim.z * A) {
+      int64_t row[A];
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        hi[i] = __float2half_rn(in_range(x[i]));
-        const float left = x[i] - __half2float(hi[i]);
-        lo[i] = __float2half_rn(fabsf(left) <= 65504.f ? left : 0.f);
+      for (int g = 0; g < A; ++g) {
+        const int r = (g0 + g) * ROWS + lane / LANES, pg = __shfl_sync(0xffffffffu, page, r);
+        row[g] = pg < 0 ? -1 : (((int64_t)pg * p.hkv + head) << p.page_shift) + ((first + warp * R + r) & ((1 << p.page_shift) - 1));
       }
-      const bool two = !side || p.v_parts == 2;
-      __half* out = dst + to * (two ? 2 * D : D) + lane * E;
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        *reinterpret_cast<__half2*>(out + i) = __halves2half2(hi[i], hi[i + 1]);
-        if (two) *reinterpret_cast<__half2*>(out + D + i) = __halves2half2(lo[i], lo[i + 1]);
+      for (int side = 0; side < 2; ++side) {
+        __half* dst = side ? p.dense_v : p.dense_k;
+        if (!dst) continue;
+        const int fmt = side ? p.vfmt : p.kfmt;
+        const bool two = !side || p.v_parts == 2;
+        Raw raw[A];
+#pragma unroll
+        for (int g = 0; g < A; ++g) raw[g] = load_raw<D>(fmt, side ? p.v : p.k, row[g], c);
+#pragma unroll
+        for (int g = 0; g < A; ++g) {
+          uint32_t hi[8], lo[8];
+          decode_raw<D>(p, fmt, raw[g], lane, sg, levels, hi, lo);
+          const int r = (g0 + g) * ROWS + lane / LANES;
+          uint4* out = reinterpret_cast<uint4*>(dst + (to + r) * (two ? 2 * D : D) + 16 * c);
+          out[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          out[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          if (two) {
+            out[D / 8] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            out[D / 8 + 1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          }
+        }
       }
     }
   }
@@ -144,7 +236,10 @@ __global__ void __launch_bounds__(32 * kDecodeWarps) prompt_decode_kernel(const 
 template <int D>
 qps_status launch_decode(const PromptParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.batch * p.dense_tiles * (kPromptTile / kDecodeRows)), p.hkv);
+  // (few tiles of wide rows: the rows of a warp are shared out)
+  const int sms = sm_count_current(), most = std::max(1, kPromptTile / kDecodeWarps / (512 / D) / kAhead);
+  const int parts = std::min<int64_t>(most, std::max<int64_t>(1, sms * 4 / ((int64_t)p.dense_tiles * p.hkv)));
+  cfg.gridDim = dim3((unsigned)std::min(p.dense_tiles, (sms * 4 + p.hkv - 1) / p.hkv), p.hkv, parts);
   cfg.blockDim = dim3(32 * kDecodeWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -326,10 +421,15 @@ qps_status plan_prompt(const qps_paged_prompt_args* a, Plan* out) {
   out->off_k = out->off_lse + up(parts * sizeof(float));
   out->off_v = out->bytes = out->off_k;
   if (kv.kfmt != QPS_FMT_F16 || kv.vfmt != QPS_FMT_F16) {
-    p.dense_tiles = (int)most;
-    if (a->batch * most * (kPromptTile / kDecodeRows) >= (int64_t)1 << 31)
-      return bad("batch * table_width * page_size is too large for compressed rows", QPS_ERR_UNSUPPORTED);
-    const size_t side = (size_t)a->batch * most * kv.hkv * kPromptTile * kv.d * sizeof(__half);
+    // tiles of all sequences that have tokens; a window leaves each its own length, its sinks and
+    // what its tokens add
+    const int64_t some = std::min<int64_t>(a->batch, a->tokens);
+    int64_t dense = some * ((held + kPromptTile - 1) / kPromptTile);
+    if (p.window)
+      dense = std::min(dense, some * ((p.sinks + kPromptTile - 1) / kPromptTile + p.window / kPromptTile + 3) + a->tokens / kPromptTile);
+    if (dense >= (int64_t)1 << 30) return bad("batch * table_width * page_size is too large for compressed rows", QPS_ERR_UNSUPPORTED);
+    p.dense_tiles = (int)std::max<int64_t>(1, dense);
+    const size_t side = (size_t)p.dense_tiles * kv.hkv * kPromptTile * kv.d * sizeof(__half);
     out->off_v = out->off_k + (kv.kfmt != QPS_FMT_F16 ? up(2 * side) : 0);
     out->bytes = out->off_v + (kv.vfmt != QPS_FMT_F16 ? up(p.v_parts * side) : 0);
   }

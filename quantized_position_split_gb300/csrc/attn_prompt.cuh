@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   idx /= p.n_split;
   // row tile `idx`: sequences in order, the last rows of each first (they see the most)
   PromptSeq sq = {0, 0, 0};
-  int bz = -1, row0 = 0;
+  int bz = -1, row0 = 0, dense0 = 0;  // dense0: the sequence's first decoded tile
+  const bool decoded = p.dense_k || p.dense_v;
   {
     int before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
@@ -144,8 +145,12 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
         if (lane >= o) sum += v;
       }
       const unsigned hit = __ballot_sync(0xffffffffu, before + sum > idx);
+      const int src = hit ? __ffs(hit) - 1 : 32;
+      if (decoded) {
+        const int tiles = lane < src && mine.n > 0 ? prompt_tiles(p, mine.len - mine.n, mine.len - 1).count : 0;
+        dense0 += __reduce_add_sync(0xffffffffu, tiles);
+      }
       if (hit) {
-        const int src = __ffs(hit) - 1;
         bz = b0 + src;
         sq.first = __shfl_sync(0xffffffffu, mine.first, src);
         sq.n = __shfl_sync(0xffffffffu, mine.n, src);
@@ -218,7 +223,7 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       return (int)p.n_pages;
     };
     int f = 0;
-    auto put = [&](const TensorMap* map, bool decoded, int col, int j, int page) -> bool {
+    auto put = [&](const TensorMap* map, bool dec, int col, int j, int page) -> bool {
       const int s = f % ST;
       if (f >= ST && !wait(empty(s), ((f / ST) & 1) ^ 1, j)) return false;
       __syncwarp();
@@ -227,10 +232,10 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       const uint32_t dst = sbase + G::RING + s * G::SLOT + cg * (kTok * 128);
       const int x = (col + cg * 64) * 2, t = first_of(j);
       const bool drop = map == &maps.k && j == p.drop_tile;
-      if (decoded) {
+      if (dec) {  // (behind the room: zeros)
         const int at = prompt_dense(dense, t / kPromptTile);
-        if (r == 0 && !drop && in_bounds(at >= 0 && at < p.dense_tiles && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
-          tma_load_4d(dst, map, x, 0, head, bz * p.dense_tiles + at, full(s));
+        if (r == 0 && !drop && in_bounds(at >= 0 && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
+          tma_load_4d(dst, map, x, 0, head, min(dense0 + at, p.dense_tiles), full(s));
       } else if (r < nb && !drop) {
         const int y = (t + r * br) & ((1 << p.page_shift) - 1);
         if (in_bounds(page <= p.n_pages && y + br <= 1 << p.page_shift && head < p.hkv && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
@@ -590,7 +595,7 @@ qps_status launch_prompt(const PromptParams& p, cudaStream_t s) {
   for (int i = 0; i < 2; ++i) {
     const __half* dense = i ? p.dense_v : p.dense_k;
     const int cols = (i ? VP : KP) * D;
-    const bool ok = dense ? encode_plane_map(i ? &maps.v : &maps.k, dense, 2 * cols, kTok, p.hkv, kTok, p.batch * p.dense_tiles,
+    const bool ok = dense ? encode_plane_map(i ? &maps.v : &maps.k, dense, 2 * cols, kTok, p.hkv, kTok, p.dense_tiles,
                                              (int64_t)p.hkv * kTok, 128, 128, kTok)
                           : encode_plane_map(i ? &maps.v : &maps.k, i ? p.v[0] : p.k[0], 2 * D, page, p.hkv, page, (int)p.n_pages,
                                              (int64_t)p.hkv * page, 128, 128, rows);

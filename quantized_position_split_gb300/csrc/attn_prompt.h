@@ -31,12 +31,12 @@ struct PromptParams {
   unsigned int* err;
   int drop_tile;          // (see qps_paged_inject_fault)
   uint32_t wait_ns;
-  // Compressed rows decoded to fp16: [sequence][dense_tiles][KV head][128 positions][columns],
-  // columns = 2 D (value, what its rounding left), or D for values where v_parts is 1; NULL: fp16
-  // pages
+  // Compressed rows decoded to fp16: [dense_tiles][KV head][128 positions][columns], columns = 2 D
+  // (value, what its rounding left), or D for values where v_parts is 1; NULL: fp16 pages.  The
+  // tiles of the sequences follow one another.
   __half *dense_k, *dense_v;
   int v_parts;
-  int dense_tiles;        // tiles of a sequence there
+  int dense_tiles;        // tiles there is room for
   // the cache's planes, for the decoding
   int kfmt, vfmt;
   const uint8_t *k[3], *v[3];
