@@ -532,7 +532,7 @@ QPS_API qps_status qps_attn_prompt_paged(const qps_paged_prompt_args* a, void* s
 typedef struct qps_paged_seqs {
   const qps_paged_kv* caches; /* host, [n_caches] */
   int32_t n_caches;
-  int32_t batch;
+  int32_t batch;              /* in [1, 4096] */
   int32_t* page_table;        /* device, [batch][table_stride] */
   int64_t table_stride;       /* >= table_width */
   int32_t table_width;        /* table_width * page_size < 2^31 - 1024 */
@@ -582,7 +582,7 @@ typedef struct qps_paged_fork_args {
                                 none, dst[i] is given back and has no positions */
   const int32_t* dst;        /* device, [n], each sequence once (a second time is left out, and
                                 qps_device_status says so; so is an index out of range) */
-  int32_t n;
+  int32_t n;                 /* in [0, 4096] */
   int32_t reserved0;         /* must be 0 */
   void* workspace;           /* device, 256-byte aligned, as large as the plan says */
   size_t workspace_bytes;

@@ -3,11 +3,14 @@
 // live pages of a pool moved to its front; pages copied where that needs it.
 //
 // All three are integer work on a few hundred KB, in steps of which each needs all of the one
-// before: reference counts changed, free pages counted, the lowest ones listed, entries written.
-// One cluster of CTAs takes them with a cluster barrier between (a grid per step would cost a
-// launch each): its size is chosen by how much there is to scan (pages_ctas).  Free pages are
-// ranked by a scan in order, so results do not depend on the order of threads.  What the steps
-// share lies in global memory and is read past L1 (__ldcg).
+// before: reference counts changed, free pages counted, the lowest ones given out.  One cluster of
+// CTAs takes them with a cluster barrier between (a grid per step would cost a launch each); its
+// size is chosen by how much there is to scan (pages_ctas).  Every CTA keeps the sequences' state
+// in shared memory and scans it for itself, so that a step waits for what it needs of the others
+// alone: with state in global memory, scanned by one CTA, five to seven barriers with loads behind
+// each took 23 us for a decode step of 64 sequences over 65536 pages.  A free page's rank is found
+// by a scan in order and leads the CTA that finds it to the entry that it is for, so results do not
+// depend on the order of threads.  What a step reads of another CTA's is read past L1 (__ldcg).
 //
 // The copies that follow are a second launch, over a list of (from, to, rows) in the workspace:
 // every plane of every cache in chunks of kChunk bytes, one a CTA at a time.  They are bound by
@@ -24,6 +27,7 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kClusterMost = 8;
+constexpr int kMostSeqs = 4096;  // their state lies in shared memory
 
 struct SeqsP {
   int32_t* table;
@@ -35,19 +39,14 @@ struct SeqsP {
   unsigned int* err;
 };
 
-// Workspace of a call: counts of each CTA, totals, lists.
+// Workspace of a call.
 struct PagesWs {
-  int* counts;     // [2][kClusterMost]
-  int* totals;     // [2 + kClusterMost]: pages needed, copies; (compact) far pages of each CTA
-  int* list;       // free pages, in order (compact: holes)
-  int* list2;      // (compact) pages behind the live count, in order
-  int* base;       // [items] rank of the item's first page
-  int* need;       // [items] pages it needs; -1: it cannot be served
-  int* copy_rank;  // [items] place of its copy, -1: none
-  int* rows;       // (fork) [items][width] source rows as they were
-  int* len;        // (fork) [items] source lengths
-  int* owner;      // (fork) [batch]
-  int4* jobs;      // (from, to, rows, 0)
+  int* counts;   // [kClusterMost] pages found by each CTA
+  int* copies;   // [1] jobs
+  int* list;     // (compact) free pages before the live count, in order
+  int* list2;    // (compact) pages in use from it on, in order
+  int* rows;     // (fork) [items][width] source rows as they were
+  int4* jobs;    // (from, to, rows, 0)
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -117,23 +116,23 @@ __device__ __forceinline__ int count_pages(const SeqsP& s, int p0, int p1, int* 
   block_scan(n, tmp, &all);
   return all;
 }
-// The same pages in order, to list[rank ..), as far as `most` of them.
-template <class F>
-__device__ __forceinline__ void list_pages(const SeqsP& s, int p0, int p1, int rank, int most, int* list, int* tmp, F f) {
+// The same pages in order as take(rank, page), rank from `rank` on and below `most`, by whole warps:
+// take is called by all lanes, with page -1 where a lane has none.
+template <class F, class T>
+__device__ __forceinline__ void take_pages(const SeqsP& s, int p0, int p1, int rank, int most, int* tmp, F f, T take) {
   for (int at = p0; at < p1 && rank < most; at += 4 * kThreads) {
     const int p = at + 4 * (int)threadIdx.x;
     const int4 r = refs4(s, p, p1);
-    const bool a = p < p1 && f(p, r.x), b = p + 1 < p1 && f(p + 1, r.y), c = p + 2 < p1 && f(p + 2, r.z), d = p + 3 < p1 && f(p + 3, r.w);
-    const int n = a + b + c + d;
+    const bool is[4] = {p < p1 && f(p, r.x), p + 1 < p1 && f(p + 1, r.y), p + 2 < p1 && f(p + 2, r.z), p + 3 < p1 && f(p + 3, r.w)};
+    const int n = is[0] + is[1] + is[2] + is[3];
     int all;
     int to = rank + block_scan(n, tmp, &all) - n;
-    if (a && to < most) list[to] = p;
-    to += a;
-    if (b && to < most) list[to] = p + 1;
-    to += b;
-    if (c && to < most) list[to] = p + 2;
-    to += c;
-    if (d && to < most) list[to] = p + 3;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool mine = is[k] && to < most;
+      if (__any_sync(0xffffffffu, mine)) take(to, mine ? p + k : -1);
+      to += is[k];
+    }
     rank += all;
   }
 }
@@ -155,23 +154,61 @@ __device__ __forceinline__ void drop_ref(const SeqsP& s, int pg) {
 }
 __device__ __forceinline__ bool is_free(int, int refs) { return refs == 0; }
 
-// The free pages' numbers: counted by every CTA (each its share), then listed, the lowest `need`
-// of them; `need` is known to all after the barrier between.
+// Free pages: counted by every CTA (each its share) before a barrier; behind it, the first of them
+// given to take(rank, page), `most` in all.  Returns how many there are.
 __device__ __forceinline__ void count_free(const SeqsP& s, const PagesWs& w, int* tmp) {
   const int2 sh = page_share(s.n_pages);
   const int n = count_pages(s, sh.x, sh.y, tmp, is_free);
   if (threadIdx.x == 0) w.counts[blockIdx.x] = n;
 }
-__device__ __forceinline__ int list_free(const SeqsP& s, const PagesWs& w, int need, int* tmp) {
-  int before = 0, all = 0;
-  for (int c = 0; c < (int)gridDim.x; ++c) {
-    const int n = __ldcg(w.counts + c);
-    if (c < (int)blockIdx.x) before += n;
-    all += n;
-  }
+struct Found {
+  int before, all;  // by the CTAs before this one, by all
+};
+__device__ __forceinline__ Found found(const int* counts) {
+  int n = 0;
+  const int lane = threadIdx.x & 31;
+  if (lane < (int)gridDim.x) n = __ldcg(counts + lane);
+  return {__reduce_add_sync(0xffffffffu, lane < (int)blockIdx.x ? n : 0), __reduce_add_sync(0xffffffffu, n)};
+}
+template <class T>
+__device__ __forceinline__ void give_free(const SeqsP& s, Found n, int most, int* tmp, T take) {
   const int2 sh = page_share(s.n_pages);
-  list_pages(s, sh.x, sh.y, before, min(need, all), w.list, tmp, is_free);
-  return all;
+  take_pages(s, sh.x, sh.y, n.before, min(most, n.all), tmp, is_free, take);
+}
+
+// f(j, entry) for the entries [j0, j1) of a row, by the warps part, part + parts, ..: four neighbours
+// a lane (16 bytes, where they lie so), kGroups such under way.
+template <class F>
+__device__ __forceinline__ void for_entries(const SeqsP& s, const int32_t* row, int j0, int j1, int part, int parts, F f) {
+  constexpr int kGroups = 4;
+  if (j0 >= j1) return;
+  const int lane = threadIdx.x & 31, off = (int)(reinterpret_cast<uintptr_t>(row) >> 2 & 3);
+  // group g: entries 4 g - off .. 4 g - off + 3
+  const int g0 = (j0 + off) >> 2, g1 = (j1 + off + 3) >> 2;
+  for (int g = g0 + part * 32 + lane; __any_sync(0xffffffffu, g < g1); g += parts * 32 * kGroups) {
+    int4 v[kGroups];
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+      const int j = 4 * (g + u * parts * 32) - off;
+      v[u] = make_int4(-1, -1, -1, -1);
+      if (j >= j0 && j + 3 < j1) {
+        v[u] = __ldcg(reinterpret_cast<const int4*>(row + j));
+      } else if (j + 3 >= j0 && j < j1) {
+        if (j >= j0) v[u].x = __ldcg(row + j);
+        if (j + 1 >= j0 && j + 1 < j1) v[u].y = __ldcg(row + j + 1);
+        if (j + 2 >= j0 && j + 2 < j1) v[u].z = __ldcg(row + j + 2);
+        if (j + 3 >= j0 && j + 3 < j1) v[u].w = __ldcg(row + j + 3);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+      const int j = 4 * (g + u * parts * 32) - off;
+      if (page_ok(s, v[u].x)) f(j, v[u].x);
+      if (page_ok(s, v[u].y)) f(j + 1, v[u].y);
+      if (page_ok(s, v[u].z)) f(j + 2, v[u].z);
+      if (page_ok(s, v[u].w)) f(j + 3, v[u].w);
+    }
+  }
 }
 
 // ---- extend -----------------------------------------------------------------------------------
@@ -186,144 +223,162 @@ struct ExtendP {
   int64_t* positions;
 };
 
-struct Growth {
-  int len;        // before
-  int64_t more;   // new positions asked for
-  int64_t end;    // after, if it can be served
+// A sequence's state in shared memory.
+struct ExtendSeq {
+  int len;     // before the call
+  int grow;    // n_new
+  int start;   // first row of its new tokens
+  int base;    // rank of its first page
+  int part;    // the page that its first new position lies in, if the sequence holds one; else -1
+  int rank;    // place of its copy, -1: none; -2: it does not fit its row or the rows of slots
 };
-__device__ __forceinline__ Growth growth(const ExtendP& p, int b) {
-  Growth g;
-  g.len = seq_len(p.s, b);
-  const int n = p.n_new[b];
-  g.more = n > 0 ? n : 0;
-  g.end = max((int64_t)0, (int64_t)g.len + n);
-  return g;
-}
 
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_constant__ ExtendP p) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int tmp[kWarps];
   __shared__ int64_t tmp64[kWarps];
+  ExtendSeq* const seq = reinterpret_cast<ExtendSeq*>(smem);
   const SeqsP& s = p.s;
   const int lane = threadIdx.x & 31, page = 1 << s.page_shift;
+  const int64_t held = (int64_t)s.width << s.page_shift;
+  asm volatile("griddepcontrol.launch_dependents;" :::);  // (the copies: they wait for this grid's end)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // ---- pages behind a trimmed end, and those that no later token's window reaches -----------
-  for_items(s.batch, [&](int b, int part, int parts) {
-    const Growth g = growth(p, b);
-    int32_t* row = s.table + b * s.stride;
-    const int had = pages_of(s, g.len);
-    auto give = [&](int j0, int j1) {
-#pragma unroll 4
-      for (int j = j0 + part * 32 + lane; j < j1; j += parts * 32) {
-        const int pg = row[j];
-        if (page_ok(s, pg)) {
-          drop_ref(s, pg);
-          row[j] = -1;
-        }
-      }
-    };
-    const int keep = min(had, pages_of(s, min((int64_t)g.len, g.end)));
-    give(keep, had);
-    if (p.window) {
-      const int64_t low = (g.more ? (int64_t)g.len : g.end) - p.window + 1;
-      if (low > 0) give(pages_of(s, p.sinks), min(keep, (int)(low >> s.page_shift)));
+  // ---- every sequence, and where its tokens' rows start ----------------------------------------
+  int64_t tokens = 0;
+  for (int b0 = 0; b0 < s.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    ExtendSeq q = {0, 0, 0, 0, -1, -1};
+    if (b < s.batch) {
+      q.grow = p.n_new[b];
+      q.len = seq_len(s, b);
     }
-  });
-  cluster_sync();
-  // ---- free pages; what each sequence needs, in order ------------------------------------------
-  count_free(s, p.w, tmp);
-  if (blockIdx.x == 0) {
-    int64_t tokens = 0, pages = 0;
-    int copies = 0;
-    for (int b0 = 0; b0 < s.batch; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      Growth g = {0, 0, 0};
-      if (b < s.batch) g = growth(p, b);
-      int64_t all;
-      const int64_t upto = tokens + block_scan(g.more, tmp64, &all);
-      if (b < s.batch) p.starts[b] = (int32_t)min(upto - g.more, p.max_tokens);
-      tokens += all;
-      const bool grows = g.more > 0, fits = g.end <= (int64_t)s.width << s.page_shift && upto <= p.max_tokens;
-      bool copy = false;
-      int need = 0;
-      if (grows && fits) {
-        if (g.len & (page - 1)) {  // (a last page that others name too is copied before it is written)
-          const int pg = __ldcg(s.table + b * s.stride + (g.len >> s.page_shift));
-          copy = page_ok(s, pg) && __ldcg(s.refs + pg) > 1;
-        }
-        need = pages_of(s, g.end) - pages_of(s, g.len) + copy;
-      }
-      const int64_t upto_pages = pages + block_scan((int64_t)need, tmp64, &all);
-      pages += all;
-      int all_copies;
-      const int upto_copies = copies + block_scan((int)copy, tmp, &all_copies);
-      copies += all_copies;
-      if (b < s.batch) {
-        p.w.base[b] = (int)min(upto_pages - need, (int64_t)0x7fffffff);
-        p.w.need[b] = grows && !fits ? -1 : need;
-        p.w.copy_rank[b] = copy ? upto_copies - 1 : -1;
-      }
-    }
-    if (threadIdx.x == 0) {
-      p.starts[s.batch] = (int32_t)min(tokens, p.max_tokens);
-      p.w.totals[0] = (int)min(pages, (int64_t)s.n_pages);
-      p.w.totals[1] = copies;
+    const int64_t more = max(0, q.grow);
+    int64_t all;
+    const int64_t upto = tokens + block_scan(more, tmp64, &all);
+    tokens += all;
+    q.start = (int)min(upto - more, p.max_tokens);
+    if (more > 0 && (q.len + more > held || upto > p.max_tokens)) q.rank = -2;
+    if (b < s.batch) {
+      seq[b] = q;
+      if (blockIdx.x == 0) p.starts[b] = q.start;
     }
   }
-  cluster_sync();
-  const int free = list_free(s, p.w, __ldcg(p.w.totals), tmp);
-  cluster_sync();
-  // ---- the new tokens' rows and the new entries ---------------------------------------------------
+  const int total = (int)min(tokens, p.max_tokens);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.starts[s.batch] = total;
+  __syncthreads();
+  auto end_of = [&](const ExtendSeq& q) { return max((int64_t)0, (int64_t)q.len + q.grow); };
+  // ---- pages behind a trimmed end, and those that no later token's window reaches; the tokens'
+  // positions -----------------------------------------------------------------------------------
   for_items(s.batch, [&](int b, int part, int parts) {
-    const Growth g = growth(p, b);  // (lengths, and the entries of pages that are copied, change behind the next barrier)
-    const int need = __ldcg(p.w.need + b), base = __ldcg(p.w.base + b), rank = __ldcg(p.w.copy_rank + b);
-    const bool served = need == 0 || (need > 0 && base <= free - need);
-    const int copy = rank >= 0, had = pages_of(s, g.len);
+    const ExtendSeq q = seq[b];
     int32_t* row = s.table + b * s.stride;
-    int32_t old = -1;  // the page of the rows behind the last position
-    if (g.more && (g.len & (page - 1))) old = copy ? -1 : __ldcg(row + (g.len >> s.page_shift));
-    if (!served) atomicOr(s.err, kErrIndex);
-    const int64_t s0 = __ldcg(p.starts + b), s1 = __ldcg(p.starts + b + 1);
-    for (int64_t i = s0 + part * 32 + lane; i < s1; i += parts * 32) {
-      const int64_t at = g.len + (i - s0);
-      const int j = (int)(at >> s.page_shift);
-      int pg = -1;
-      if (served) pg = j >= had ? __ldcg(p.w.list + base + copy + (j - had)) : copy ? __ldcg(p.w.list + base) : old;
-      p.slots[i] = page_ok(s, pg) ? (int64_t)pg * page + (at & (page - 1)) : -1;
-      p.positions[i] = at;
+    auto give = [&](int j, int pg) {
+      drop_ref(s, pg);
+      row[j] = -1;
+    };
+    const int had = pages_of(s, q.len), keep = min(had, pages_of(s, min((int64_t)q.len, end_of(q))));
+    for_entries(s, row, keep, had, part, parts, give);
+    if (p.window) {
+      const int64_t low = (q.grow > 0 ? (int64_t)q.len : end_of(q)) - p.window + 1;
+      if (low > 0) for_entries(s, row, pages_of(s, p.sinks), min(keep, (int)(low >> s.page_shift)), part, parts, give);
     }
-    if (served && need > 0) {
-      for (int k = part * 32 + lane; k < need - copy; k += parts * 32) {
-        const int pg = __ldcg(p.w.list + base + copy + k);
-        row[had + k] = pg;
-        s.refs[pg] = 1;
-      }
-    }
+    const int n = (b + 1 < s.batch ? seq[b + 1].start : total) - q.start;
+    for (int i = part * 32 + lane; i < n; i += parts * 32) p.positions[q.start + i] = (int64_t)q.len + i;
   });
-  const int64_t total = __ldcg(p.starts + s.batch);
   for (int64_t i = total + blockIdx.x * kThreads + threadIdx.x; i < p.max_tokens; i += (int64_t)gridDim.x * kThreads) {
     p.slots[i] = -1;
     p.positions[i] = 0;
   }
   cluster_sync();
-  // ---- copies and lengths -------------------------------------------------------------------------
-  for (int b = blockIdx.x * kThreads + threadIdx.x; b < s.batch; b += gridDim.x * kThreads) {
-    const Growth g = growth(p, b);
-    const int need = __ldcg(p.w.need + b), base = __ldcg(p.w.base + b), rank = __ldcg(p.w.copy_rank + b);
-    const bool served = need == 0 || (need > 0 && base <= free - need);
-    if (rank >= 0) {
-      int4 job = make_int4(0, 0, 0, 0);
-      if (served) {
-        int32_t* at = s.table + b * s.stride + (g.len >> s.page_shift);
-        const int from = __ldcg(at), to = __ldcg(p.w.list + base);
-        job = make_int4(from, to, g.len & (page - 1), 0);
-        *at = to;
-        s.refs[to] = 1;
-        drop_ref(s, from);
+  // ---- free pages; what each sequence needs, in order ------------------------------------------
+  count_free(s, p.w, tmp);
+  int need = 0, copies = 0;
+  for (int b0 = 0; b0 < s.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int n = 0, copy = 0;
+    if (b < s.batch && seq[b].grow > 0 && seq[b].rank != -2) {
+      const int len = seq[b].len;
+      if (len & (page - 1)) {  // (a last page that others name too is copied before it is written)
+        const int pg = __ldcg(s.table + b * s.stride + (len >> s.page_shift));
+        if (page_ok(s, pg)) {
+          seq[b].part = pg;
+          copy = __ldcg(s.refs + pg) > 1;
+        }
       }
-      p.w.jobs[rank] = job;
+      n = pages_of(s, end_of(seq[b])) - pages_of(s, len) + copy;
     }
-    if (served) s.lens[b] = (int32_t)g.end;
+    int all, all_copies;
+    const int upto = need + block_scan(n, tmp, &all), upto_copies = copies + block_scan(copy, tmp, &all_copies);
+    need += all;
+    copies += all_copies;
+    if (b < s.batch) {
+      seq[b].base = upto - n;
+      if (copy) seq[b].rank = upto_copies - 1;
+    }
   }
+  cluster_sync();
+  // ---- a free page finds its entry by its rank ---------------------------------------------------
+  const Found free = found(p.w.counts);
+  // of a sequence that grows: whether it gets its pages
+  auto served = [&](int b) {
+    return seq[b].rank != -2 && (b + 1 < s.batch ? seq[b + 1].base : need) <= free.all;
+  };
+  // rows of the new positions [t0, t1) of sequence b, on page pg: by a warp
+  auto put_slots = [&](int b, int64_t t0, int64_t t1, int pg) {
+    const ExtendSeq& q = seq[b];
+    t0 = max(t0, (int64_t)q.len);
+    t1 = min(t1, end_of(q));
+    for (int64_t t = t0 + lane; t < t1; t += 32) p.slots[q.start + (t - q.len)] = pg < 0 ? -1 : (int64_t)pg * page + (t & (page - 1));
+  };
+  give_free(s, free, need, tmp, [&](int rank, int pg) {
+    int b = 0, j = 0;
+    if (pg >= 0) {
+      int lo = 0, hi = s.batch;  // the last sequence with base <= rank
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (seq[mid].base <= rank) lo = mid;
+        else hi = mid;
+      }
+      b = lo;
+      if (served(b)) {
+        const ExtendSeq& q = seq[b];
+        j = pages_of(s, q.len) + rank - q.base - (q.rank >= 0);  // (the copy first, in the place before)
+        if (q.rank >= 0 && rank == q.base) p.w.jobs[q.rank] = make_int4(q.part, pg, q.len & (page - 1), 0);
+        s.table[b * s.stride + j] = pg;
+        s.refs[pg] = 1;
+      } else {
+        pg = -1;
+      }
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, pg >= 0); left; left &= left - 1) {
+      const int src = __ffs(left) - 1, bb = __shfl_sync(0xffffffffu, b, src);
+      const int64_t t = (int64_t)__shfl_sync(0xffffffffu, j, src) << s.page_shift;
+      put_slots(bb, t, t + page, __shfl_sync(0xffffffffu, pg, src));
+    }
+  });
+  for_items(s.batch, [&](int b, int part, int) {
+    const ExtendSeq& q = seq[b];
+    if (part != 0) return;
+    const bool ok = q.grow <= 0 || served(b) || (q.rank != -2 && (b + 1 < s.batch ? seq[b + 1].base : need) == q.base);
+    if (lane == 0) {
+      if (!ok) atomicOr(s.err, kErrIndex);
+      else s.lens[b] = (int32_t)end_of(q);
+      if (q.rank >= 0 && !ok) p.w.jobs[q.rank] = make_int4(0, 0, 0, 0);
+    }
+    if (q.grow <= 0) return;
+    if (!ok) {  // (its rows as far as there are any)
+      const int n = (b + 1 < s.batch ? seq[b + 1].start : total) - q.start;
+      for (int i = lane; i < n; i += 32) p.slots[q.start + i] = -1;
+    } else if ((q.len & (page - 1)) && q.rank < 0) {
+      put_slots(b, q.len, (int64_t)pages_of(s, q.len) << s.page_shift, q.part);
+    }
+  });
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.w.copies = copies;
+  if (copies == 0) return;
+  // ---- what is copied has a use less (it was none of the free ones) ------------------------------
+  cluster_sync();
+  for (int b = blockIdx.x * kThreads + threadIdx.x; b < s.batch; b += gridDim.x * kThreads)
+    if (seq[b].rank >= 0 && served(b)) drop_ref(s, seq[b].part);
 }
 
 // ---- fork -------------------------------------------------------------------------------------
@@ -335,93 +390,119 @@ struct ForkP {
   int n;
 };
 
+// One of the n in shared memory.
+struct ForkItem {
+  int src, dst;  // dst -1: nothing to do
+  int len;       // of the source
+  int part;      // its last page, if that is not full; else -1
+  int rank;      // place of its copy, -1: none
+};
+
 __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant__ ForkP p) {
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int tmp[kWarps];
+  ForkItem* const item = reinterpret_cast<ForkItem*>(smem);
+  int* const of_rank = reinterpret_cast<int*>(item + p.n);  // [n] the item of a copy
+  int* const owner = of_rank + p.n;                          // [batch]
   const SeqsP& s = p.s;
   const int lane = threadIdx.x & 31, page = 1 << s.page_shift;
+  asm volatile("griddepcontrol.launch_dependents;" :::);  // (the copies: they wait for this grid's end)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  auto each = [&](int n, auto f) {
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) f(i);
-  };
-  // ---- a row that is named twice goes to the first ----------------------------------------------
-  each(s.batch, [&](int b) { p.w.owner[b] = 0x7fffffff; });
-  cluster_sync();
-  auto valid = [&](int i) { return p.src[i] < s.batch && (uint32_t)p.dst[i] < (uint32_t)s.batch; };
-  each(p.n, [&](int i) {
-    if (valid(i)) atomicMin(p.w.owner + p.dst[i], i);
+  // ---- the items; a row that is named twice goes to the first ------------------------------------
+  for (int b = threadIdx.x; b < s.batch; b += kThreads) owner[b] = 0x7fffffff;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.n; i += kThreads) {
+    const int a = p.src[i], b = p.dst[i];
+    const bool valid = a < s.batch && (uint32_t)b < (uint32_t)s.batch;
+    item[i] = ForkItem{a, valid ? b : -1, 0, -1, -1};
+    if (valid) atomicMin(owner + b, i);
     else atomicOr(s.err, kErrIndex);
+  }
+  __syncthreads();
+  int copies = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    ForkItem q = {-1, -1, 0, -1, -1};
+    if (i < p.n) {
+      q = item[i];
+      if (q.dst >= 0 && owner[q.dst] != i) {
+        atomicOr(s.err, kErrIndex);
+        q.dst = -1;
+      }
+      if (q.src == q.dst) q.dst = -1;
+      if (q.dst >= 0 && q.src >= 0) {
+        q.len = seq_len(s, q.src);
+        if (q.len & (page - 1)) {
+          const int pg = __ldcg(s.table + q.src * s.stride + (q.len >> s.page_shift));
+          if (page_ok(s, pg)) q.part = pg;
+        }
+      }
+    }
+    int all;
+    const int upto = copies + block_scan(q.part >= 0 ? 1 : 0, tmp, &all);
+    copies += all;
+    if (q.part >= 0) {
+      q.rank = upto - 1;
+      of_rank[q.rank] = i;
+    }
+    if (i < p.n) item[i] = q;
+  }
+  __syncthreads();
+  // ---- the sources' rows as they are, each of their pages held once more; what the destinations
+  // held is given back (no count falls to zero that is used again) ---------------------------------
+  for_items(p.n, [&](int i, int part, int parts) {
+    const ForkItem q = item[i];
+    if (q.dst < 0) return;
+    int* to = p.w.rows + (int64_t)i * s.width;
+    const int n = pages_of(s, q.len);
+    const int32_t* row = s.table + max(q.src, 0) * s.stride;
+#pragma unroll 4
+    for (int j = part * 32 + lane; j < n; j += parts * 32) {
+      const int pg = __ldcg(row + j);
+      const bool ok = page_ok(s, pg);
+      to[j] = ok ? pg : -1;
+      if (ok) atomicAdd(s.refs + pg, 1);
+    }
+    for_entries(s, s.table + q.dst * s.stride, 0, pages_of(s, seq_len(s, q.dst)), part, parts, [&](int, int pg) { drop_ref(s, pg); });
   });
   cluster_sync();
-  auto active = [&](int i) { return valid(i) && __ldcg(p.w.owner + p.dst[i]) == i && p.src[i] != p.dst[i]; };
-  // ---- the sources as they are, each of their pages held once more ------------------------------
+  // ---- free pages; the rows, but for the pages that are copied -----------------------------------
+  count_free(s, p.w, tmp);
   for_items(p.n, [&](int i, int part, int parts) {
-    if (!active(i)) {
-      if (valid(i) && __ldcg(p.w.owner + p.dst[i]) != i) atomicOr(s.err, kErrIndex);
-      return;
-    }
-    const int b = p.src[i], n = b < 0 ? 0 : seq_len(s, b);
-    if (part == 0 && lane == 0) p.w.len[i] = n;
-    int* row = p.w.rows + (int64_t)i * s.width;
+    const ForkItem q = item[i];
+    if (q.dst < 0) return;
+    const int n = pages_of(s, q.len), last = q.part >= 0 ? n - 1 : -1;
+    const int* from = p.w.rows + (int64_t)i * s.width;
+    int32_t* row = s.table + q.dst * s.stride;
 #pragma unroll 4
-    for (int j = part * 32 + lane; j < s.width; j += parts * 32) {
-      int pg = j < pages_of(s, n) ? __ldcg(s.table + b * s.stride + j) : -1;
-      if (!page_ok(s, pg)) pg = -1;
-      row[j] = pg;
-      if (pg >= 0) atomicAdd(s.refs + pg, 1);
-    }
-  });
-  cluster_sync();
-  for_items(p.n, [&](int i, int part, int parts) {
-    if (!active(i)) return;
-    const int b = p.dst[i], n = pages_of(s, seq_len(s, b));
-#pragma unroll 4
-    for (int j = part * 32 + lane; j < n; j += parts * 32) drop_ref(s, __ldcg(s.table + b * s.stride + j));
+    for (int j = part * 32 + lane; j < s.width; j += parts * 32)
+      if (j != last) row[j] = j < n ? __ldcg(from + j) : -1;
   });
   cluster_sync();
   // ---- a page for each last one that is not full -------------------------------------------------
-  auto part_of = [&](int i) -> int {  // the page that is copied, or -1
-    const int n = __ldcg(p.w.len + i);
-    return n & (page - 1) ? __ldcg(p.w.rows + (int64_t)i * s.width + (n >> s.page_shift)) : -1;
-  };
-  count_free(s, p.w, tmp);
-  if (blockIdx.x == 0) {
-    int copies = 0;
-    for (int i0 = 0; i0 < p.n; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      const int copy = i < p.n && active(i) && part_of(i) >= 0;
-      int all;
-      const int upto = copies + block_scan(copy, tmp, &all);
-      copies += all;
-      if (i < p.n) p.w.copy_rank[i] = copy ? upto - 1 : -1;
-    }
-    if (threadIdx.x == 0) p.w.totals[0] = p.w.totals[1] = copies;
-  }
-  cluster_sync();
-  const int free = list_free(s, p.w, __ldcg(p.w.totals), tmp);
-  cluster_sync();
-  // ---- the new rows ------------------------------------------------------------------------------
-  for_items(p.n, [&](int i, int part, int parts) {
-    if (!active(i)) return;
-    const int b = p.dst[i], n = __ldcg(p.w.len + i), rank = __ldcg(p.w.copy_rank + i);
-    const int last = rank >= 0 ? n >> s.page_shift : -1;
-    const bool served = rank < free;
-    int32_t* row = s.table + b * s.stride;
-    for (int j = part * 32 + lane; j < s.width; j += parts * 32) {
-      int pg = __ldcg(p.w.rows + (int64_t)i * s.width + j);
-      if (j == last) {
-        const int from = pg;
-        pg = served ? __ldcg(p.w.list + rank) : -1;
-        p.w.jobs[rank] = served ? make_int4(from, pg, n & (page - 1), 0) : make_int4(0, 0, 0, 0);
-        if (served) s.refs[pg] = 1;
-        drop_ref(s, from);
-      }
-      row[j] = pg;
-    }
-    if (part == 0 && lane == 0) {
-      if (!served) atomicOr(s.err, kErrIndex);
-      s.lens[b] = served ? n : n & ~(page - 1);  // (no page for the last positions: they are left out)
-    }
+  const Found free = found(p.w.counts);
+  give_free(s, free, copies, tmp, [&](int rank, int pg) {
+    if (pg < 0) return;
+    const ForkItem q = item[of_rank[rank]];
+    s.table[q.dst * s.stride + (q.len >> s.page_shift)] = pg;
+    s.refs[pg] = 1;
+    p.w.jobs[rank] = make_int4(q.part, pg, q.len & (page - 1), 0);
   });
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.n; i += gridDim.x * kThreads) {
+    const ForkItem q = item[i];
+    if (q.dst < 0) continue;
+    const bool short_of = q.rank >= free.all;  // (no page for the last positions: they are left out)
+    s.lens[q.dst] = short_of ? q.len & ~(page - 1) : q.len;
+    if (short_of) {
+      atomicOr(s.err, kErrIndex);
+      s.table[q.dst * s.stride + (q.len >> s.page_shift)] = -1;
+      p.w.jobs[q.rank] = make_int4(0, 0, 0, 0);
+    }
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.w.copies = copies;
+  if (copies == 0) return;
+  cluster_sync();
+  for (int r = blockIdx.x * kThreads + threadIdx.x; r < copies; r += gridDim.x * kThreads) drop_ref(s, item[of_rank[r]].part);
 }
 
 // ---- compact ----------------------------------------------------------------------------------
@@ -435,35 +516,33 @@ struct CompactP {
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_constant__ CompactP p) {
   __shared__ int tmp[kWarps];
   const SeqsP& s = p.s;
-  const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" :::);  // (the copies: they wait for this grid's end)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 sh = page_share(s.n_pages);
   const int n = count_pages(s, sh.x, sh.y, tmp, [](int, int r) { return r > 0; });
   if (threadIdx.x == 0) p.w.counts[blockIdx.x] = n;
   cluster_sync();
-  int live = 0;
-  for (int c = 0; c < (int)gridDim.x; ++c) live += __ldcg(p.w.counts + c);
-  // holes before `live`, pages in use from it on: as many of the one as of the other
+  const Found in_use = found(p.w.counts);
+  const int live = in_use.all;
+  // holes before `live`, pages in use from it on: as many of the one as of the other.  The pages in
+  // use before `live` are those of the shares that lie before it, and of the part of the share that
+  // it lies in, which every CTA counts for itself.
   auto hole = [&](int pg, int r) { return pg < live && r <= 0; };
   auto far = [&](int pg, int r) { return pg >= live && r > 0; };
-  const int holes = sh.x >= live ? 0 : sh.y <= live ? sh.y - sh.x - n : count_pages(s, sh.x, sh.y, tmp, hole);
-  const int fars = sh.x >= live ? n : sh.y <= live ? 0 : n - (live - sh.x - holes);
-  if (threadIdx.x == 0) {
-    p.w.counts[kClusterMost + blockIdx.x] = holes;
-    p.w.totals[2 + blockIdx.x] = fars;
-  }
-  cluster_sync();
-  int h0 = 0, f0 = 0, moves = 0;
-  for (int c = 0; c < (int)gridDim.x; ++c) {
-    const int h = __ldcg(p.w.counts + kClusterMost + c), f = __ldcg(p.w.totals + 2 + c);
-    if (c < (int)blockIdx.x) {
-      h0 += h;
-      f0 += f;
-    }
-    moves += h;
-  }
-  if (holes > 0) list_pages(s, sh.x, sh.y, h0, moves, p.w.list, tmp, hole);
-  if (fars > 0) list_pages(s, sh.x, sh.y, f0, moves, p.w.list2, tmp, far);
+  const int each = max(4, (int)(((s.n_pages + 4 * (int64_t)gridDim.x - 1) / (4 * gridDim.x)) * 4)), mid = min(live / each, (int)gridDim.x - 1);
+  int near = count_pages(s, min(s.n_pages, mid * each), live, tmp, [](int, int r) { return r > 0; });
+  for (int c = 0; c < mid; ++c) near += __ldcg(p.w.counts + c);
+  const int moves = live - near;
+  // ranks of this share's first hole and first far page
+  const int h0 = sh.x < live ? sh.x - in_use.before : moves, f0 = sh.x < live ? 0 : in_use.before - near;
+  if (sh.x < live)
+    take_pages(s, sh.x, min(sh.y, live), h0, moves, tmp, hole, [&](int rank, int pg) {
+      if (pg >= 0) p.w.list[rank] = pg;
+    });
+  if (sh.y > live)
+    take_pages(s, sh.x, sh.y, f0, moves, tmp, far, [&](int rank, int pg) {
+      if (pg >= 0) p.w.list2[rank] = pg;
+    });
   for (int pg = sh.x + threadIdx.x; pg < sh.y; pg += kThreads)
     if (const int r = __ldcg(s.refs + pg); !far(pg, r)) p.new_ids[pg] = r > 0 ? pg : -1;
   cluster_sync();
@@ -475,18 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
     p.w.jobs[i] = make_int4(from, to, 1 << s.page_shift, 0);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.w.totals[1] = moves;
+    *p.w.copies = moves;
     p.live[0] = live;
   }
   cluster_sync();
   for_items(s.batch, [&](int b, int part, int parts) {
-    const int m = pages_of(s, seq_len(s, b));
     int32_t* row = s.table + b * s.stride;
-#pragma unroll 4
-    for (int j = part * 32 + lane; j < m; j += parts * 32) {
-      const int pg = row[j];
-      if (page_ok(s, pg)) row[j] = __ldcg(p.new_ids + pg);
-    }
+    for_entries(s, row, 0, pages_of(s, seq_len(s, b)), part, parts, [&](int j, int pg) { row[j] = __ldcg(p.new_ids + pg); });
   });
 }
 
@@ -559,7 +633,7 @@ struct Seqs {
 qps_status check_seqs(const qps_paged_seqs& a, const char* call, Seqs* out) {
   if (a.reserved0 != 0) return bad(call, "reserved fields must be 0");
   if (!a.caches || a.n_caches < 1 || a.n_caches > 65535) return bad(call, "caches is NULL, or n_caches not in [1, 65535]");
-  if (a.batch < 1 || a.batch > 65535) return bad(call, "batch must be in [1, 65535]");
+  if (a.batch < 1 || a.batch > kMostSeqs) return bad(call, "batch must be in [1, 4096]");
   if (!a.page_table || !a.kv_lens || !a.refs || !aligned_to(a.page_table, 4) || !aligned_to(a.kv_lens, 4) || !aligned_to(a.refs, 4))
     return bad(call, "page_table / kv_lens / refs are NULL or misaligned");
   SeqsP& p = out->p;
@@ -623,30 +697,28 @@ struct Cut {
     return r;
   }
 };
-size_t lay_out(PagesWs* w, void* base, int64_t items, int64_t list, int64_t list2, int64_t jobs, int64_t rows, int64_t batch) {
+size_t lay_out(PagesWs* w, void* base, int64_t list, int64_t rows, int64_t jobs) {
   Cut c{reinterpret_cast<char*>(base)};
-  w->counts = c.take<int>(2 * kClusterMost);
-  w->totals = c.take<int>(2 + kClusterMost);
+  w->counts = c.take<int>(kClusterMost);
+  w->copies = c.take<int>(1);
   w->list = c.take<int>(list);
-  w->list2 = c.take<int>(list2);
-  w->base = c.take<int>(items);
-  w->need = c.take<int>(items);
-  w->copy_rank = c.take<int>(items);
-  w->len = c.take<int>(items);
+  w->list2 = c.take<int>(list);
   w->rows = c.take<int>(rows);
-  w->owner = c.take<int>(batch);
   w->jobs = c.take<int4>(jobs);
   return c.bytes;
 }
 
 int pages_ctas(const SeqsP& s) { return s.n_pages > 4096 || s.batch > kWarps ? kClusterMost : 1; }
 
+// `smem`: bytes of the state.
 template <class P>
-qps_status launch_pages(void (*kernel)(P), const P& p, cudaStream_t s) {
+qps_status launch_pages(void (*kernel)(P), const P& p, size_t smem, cudaStream_t s) {
+  if (smem > 32 * 1024) QPS_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   cudaLaunchConfig_t cfg = {};
   const int ctas = pages_ctas(p.s);
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -677,7 +749,7 @@ qps_status launch_copies(const Seqs& q, const PagesWs& w, int64_t most, cudaStre
     p.page_shift = q.p.page_shift;
     p.n_pages = q.p.n_pages;
     p.jobs = w.jobs;
-    p.count = w.totals + 1;
+    p.count = w.copies;
     p.most = (int)most;
     p.err = q.p.err;
     cudaLaunchConfig_t cfg = {};
@@ -710,10 +782,8 @@ qps_status plan_extend(const qps_paged_extend_args* a, Seqs* q, PagesWs* w, size
   if (!a->n_new || !aligned_to(a->n_new, 4)) return bad(kExtend, "n_new is NULL or misaligned");
   if (a->window < 0 || a->sinks < 0) return bad(kExtend, "window and sinks must be >= 0");
   if (a->max_tokens < 0 || a->max_tokens >= (int64_t)1 << 31) return bad(kExtend, "max_tokens must be in [0, 2^31)");
-  // (a sequence's share of the tokens takes one page more than its full ones, and a copy)
-  const int64_t list = std::min<int64_t>(q->p.n_pages, (a->max_tokens >> q->p.page_shift) + 2 * (int64_t)a->seqs.batch);
   *jobs = std::min<int64_t>(a->seqs.batch, a->max_tokens);
-  *bytes = lay_out(w, a->workspace, a->seqs.batch, list, 0, *jobs, 0, 0);
+  *bytes = lay_out(w, a->workspace, 0, 0, *jobs);
   return QPS_OK;
 }
 
@@ -745,7 +815,7 @@ qps_status kv_extend_paged(const qps_paged_extend_args* a, cudaStream_t s) {
   p.starts = a->q_starts;
   p.slots = a->slots;
   p.positions = a->positions;
-  st = launch_pages(extend_kernel, p, s);
+  st = launch_pages(extend_kernel, p, p.s.batch * sizeof(ExtendSeq), s);
   return st != QPS_OK || jobs == 0 ? st : launch_copies(q, p.w, jobs, s);
 }
 
@@ -755,10 +825,10 @@ qps_status plan_fork(const qps_paged_fork_args* a, Seqs* q, PagesWs* w, size_t* 
   const qps_status st = check_seqs(a->seqs, kFork, q);
   if (st != QPS_OK) return st;
   if (a->reserved0 != 0) return bad(kFork, "reserved fields must be 0");
-  if (a->n < 0 || a->n > 65535) return bad(kFork, "n must be in [0, 65535]");
+  if (a->n < 0 || a->n > kMostSeqs) return bad(kFork, "n must be in [0, 4096]");
   if (a->n > 0 && (!a->src || !a->dst || !aligned_to(a->src, 4) || !aligned_to(a->dst, 4)))
     return bad(kFork, "src / dst are NULL or misaligned");
-  *bytes = lay_out(w, a->workspace, a->n, a->n, 0, a->n, (int64_t)a->n * a->seqs.table_width, a->seqs.batch);
+  *bytes = lay_out(w, a->workspace, 0, (int64_t)a->n * a->seqs.table_width, a->n);
   return QPS_OK;
 }
 
@@ -780,7 +850,7 @@ qps_status kv_fork_paged(const qps_paged_fork_args* a, cudaStream_t s) {
   p.src = a->src;
   p.dst = a->dst;
   p.n = a->n;
-  st = launch_pages(fork_kernel, p, s);
+  st = launch_pages(fork_kernel, p, p.n * (sizeof(ForkItem) + sizeof(int)) + p.s.batch * sizeof(int), s);
   return st != QPS_OK ? st : launch_copies(q, p.w, a->n, s);
 }
 
@@ -790,7 +860,7 @@ qps_status plan_compact(const qps_paged_compact_args* a, Seqs* q, PagesWs* w, si
   const qps_status st = check_seqs(a->seqs, kCompact, q);
   if (st != QPS_OK) return st;
   const int64_t moves = q->p.n_pages / 2;  // (a hole for each)
-  *bytes = lay_out(w, a->workspace, 0, moves, moves, moves, 0, 0);
+  *bytes = lay_out(w, a->workspace, moves, 0, moves);
   return QPS_OK;
 }
 
@@ -812,7 +882,7 @@ qps_status kv_compact_paged(const qps_paged_compact_args* a, cudaStream_t s) {
   p.s = q.p;
   p.new_ids = a->new_ids;
   p.live = a->live;
-  st = launch_pages(compact_kernel, p, s);
+  st = launch_pages(compact_kernel, p, 0, s);
   return st != QPS_OK ? st : launch_copies(q, p.w, q.p.n_pages / 2, s);
 }
 

@@ -101,7 +101,7 @@ def _page_calls(lib, caches=None, seqs=None, only=None, **kw):  # noqa: F811
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(n_caches=0), INVALID), (dict(caches=None), INVALID), (dict(batch=0), INVALID), (dict(batch=65536), INVALID),
+    (dict(n_caches=0), INVALID), (dict(caches=None), INVALID), (dict(batch=0), INVALID), (dict(batch=4097), INVALID),
     (dict(page_table=None), INVALID), (dict(page_table=0x20002), INVALID), (dict(kv_lens=None), INVALID), (dict(refs=0x31001), INVALID),
     (dict(table_width=0), INVALID), (dict(table_width=1 << 25, table_stride=1 << 25), INVALID), (dict(table_stride=15), INVALID),
     (dict(reserved0=1), INVALID)])
@@ -124,7 +124,7 @@ def test_caches_of_one_shape(lib):  # noqa: F811
 
 @pytest.mark.parametrize("name,change", [
     ("extend", dict(n_new=None)), ("extend", dict(n_new=0x32001)), ("extend", dict(window=-1)), ("extend", dict(sinks=-1)),
-    ("extend", dict(max_tokens=-1)), ("extend", dict(max_tokens=1 << 31)), ("fork", dict(n=-1)), ("fork", dict(n=65536)),
+    ("extend", dict(max_tokens=-1)), ("extend", dict(max_tokens=1 << 31)), ("fork", dict(n=-1)), ("fork", dict(n=4097)),
     ("fork", dict(src=None)), ("fork", dict(dst=0x37002)), ("fork", dict(reserved0=1))])
 def test_page_call_refusals(lib, name, change):  # noqa: F811
     assert _page_calls(lib, only=name, **change)[name] == (INVALID, INVALID)
