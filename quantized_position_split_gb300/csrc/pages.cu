@@ -46,7 +46,7 @@ struct PagesWs {
   int* list;     // (compact) free pages before the live count, in order
   int* list2;    // (compact) pages in use from it on, in order
   int* rows;     // (fork) [items][width] source rows as they were
-  int4* jobs;    // (from, to, rows, 0)
+  int4* jobs;    // (from, to, rows, whether `from` has a use less then)
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -152,14 +152,29 @@ __device__ __forceinline__ void drop_ref(const SeqsP& s, int pg) {
     atomicOr(s.err, kErrIndex);
   }
 }
-__device__ __forceinline__ bool is_free(int, int refs) { return refs == 0; }
-
-// Free pages: counted by every CTA (each its share) before a barrier; behind it, the first of them
-// given to take(rank, page), `most` in all.  Returns how many there are.
-__device__ __forceinline__ void count_free(const SeqsP& s, const PagesWs& w, int* tmp) {
-  const int2 sh = page_share(s.n_pages);
-  const int n = count_pages(s, sh.x, sh.y, tmp, is_free);
-  if (threadIdx.x == 0) w.counts[blockIdx.x] = n;
+// Free pages: counted by every CTA (each its share) before a barrier, the counts of the first pages
+// of the share kept in registers; behind it, the first of them given out in order, `most` in all.
+constexpr int kKept = 2;
+struct Share {
+  int2 at;
+  int4 kept[kKept];
+};
+__device__ __forceinline__ Share count_free(const SeqsP& s, const PagesWs& w, int* tmp) {
+  Share sh;
+  sh.at = page_share(s.n_pages);
+  auto free4 = [](int4 r) { return (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0); };
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) {
+    sh.kept[k] = refs4(s, sh.at.x + 4 * ((int)threadIdx.x + k * kThreads), sh.at.y);
+    n += free4(sh.kept[k]);
+  }
+#pragma unroll 4
+  for (int p = sh.at.x + 4 * ((int)threadIdx.x + kKept * kThreads); p < sh.at.y; p += 4 * kThreads) n += free4(refs4(s, p, sh.at.y));
+  int all;
+  block_scan(n, tmp, &all);
+  if (threadIdx.x == 0) w.counts[blockIdx.x] = all;
+  return sh;
 }
 struct Found {
   int before, all;  // by the CTAs before this one, by all
@@ -170,10 +185,31 @@ __device__ __forceinline__ Found found(const int* counts) {
   if (lane < (int)gridDim.x) n = __ldcg(counts + lane);
   return {__reduce_add_sync(0xffffffffu, lane < (int)blockIdx.x ? n : 0), __reduce_add_sync(0xffffffffu, n)};
 }
+// list[0 .. n) are pages in order, the first of rank `rank`: take(rank, list, n) is called by the whole
+// block, between barriers, for at most 4 kThreads pages at a time.
 template <class T>
-__device__ __forceinline__ void give_free(const SeqsP& s, Found n, int most, int* tmp, T take) {
-  const int2 sh = page_share(s.n_pages);
-  take_pages(s, sh.x, sh.y, n.before, min(most, n.all), tmp, is_free, take);
+__device__ __forceinline__ void give_free(const SeqsP& s, const Share& sh, Found n, int most, int* tmp, int* list, T take) {
+  int rank = n.before;
+  most = min(most, n.all);
+  int k = 0;
+  for (int at = sh.at.x; at < sh.at.y && rank < most; at += 4 * kThreads, ++k) {
+    const int p = at + 4 * (int)threadIdx.x;
+    const int4 r = k == 0 ? sh.kept[0] : k == 1 ? sh.kept[1] : refs4(s, p, sh.at.y);
+    const int is[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
+    const int mine = is[0] + is[1] + is[2] + is[3];
+    int all;
+    int to = block_scan(mine, tmp, &all) - mine;
+    const int got = min(all, most - rank);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (is[i] && to < got) list[to] = p + i;
+      to += is[i];
+    }
+    __syncthreads();
+    if (got > 0) take(rank, list, got);
+    __syncthreads();
+    rank += all;
+  }
 }
 
 // f(j, entry) for the entries [j0, j1) of a row, by the warps part, part + parts, ..: four neighbours
@@ -229,7 +265,7 @@ struct ExtendSeq {
   int grow;    // n_new
   int start;   // first row of its new tokens
   int base;    // rank of its first page
-  int part;    // the page that its first new position lies in, if the sequence holds one; else -1
+  int part;    // (growing) the page that its first new position lies in, if it holds one; else -1
   int rank;    // place of its copy, -1: none; -2: it does not fit its row or the rows of slots
 };
 
@@ -237,7 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int tmp[kWarps];
   __shared__ int64_t tmp64[kWarps];
-  ExtendSeq* const seq = reinterpret_cast<ExtendSeq*>(smem);
+  int4* const rows = reinterpret_cast<int4*>(smem);                 // [4 kThreads]
+  int* const list = reinterpret_cast<int*>(rows + 4 * kThreads);    // [4 kThreads]
+  ExtendSeq* const seq = reinterpret_cast<ExtendSeq*>(list + 4 * kThreads);
   const SeqsP& s = p.s;
   const int lane = threadIdx.x & 31, page = 1 << s.page_shift;
   const int64_t held = (int64_t)s.width << s.page_shift;
@@ -251,6 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
     if (b < s.batch) {
       q.grow = p.n_new[b];
       q.len = seq_len(s, b);
+      if (q.grow > 0 && (q.len & (page - 1))) {  // (no step of this call gives it back)
+        const int pg = __ldcg(s.table + b * s.stride + (q.len >> s.page_shift));
+        if (page_ok(s, pg)) q.part = pg;
+      }
     }
     const int64_t more = max(0, q.grow);
     int64_t all;
@@ -291,94 +333,78 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const __grid_consta
   }
   cluster_sync();
   // ---- free pages; what each sequence needs, in order ------------------------------------------
-  count_free(s, p.w, tmp);
+  const Share share = count_free(s, p.w, tmp);
   int need = 0, copies = 0;
   for (int b0 = 0; b0 < s.batch; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
     int n = 0, copy = 0;
     if (b < s.batch && seq[b].grow > 0 && seq[b].rank != -2) {
-      const int len = seq[b].len;
-      if (len & (page - 1)) {  // (a last page that others name too is copied before it is written)
-        const int pg = __ldcg(s.table + b * s.stride + (len >> s.page_shift));
-        if (page_ok(s, pg)) {
-          seq[b].part = pg;
-          copy = __ldcg(s.refs + pg) > 1;
-        }
-      }
-      n = pages_of(s, end_of(seq[b])) - pages_of(s, len) + copy;
+      // (a last page that others name too is copied before it is written)
+      copy = seq[b].part >= 0 && __ldcg(s.refs + seq[b].part) > 1;
+      n = pages_of(s, end_of(seq[b])) - pages_of(s, seq[b].len) + copy;
     }
-    int all, all_copies;
-    const int upto = need + block_scan(n, tmp, &all), upto_copies = copies + block_scan(copy, tmp, &all_copies);
-    need += all;
-    copies += all_copies;
+    int64_t all;  // (pages below, copies above)
+    const int64_t upto = block_scan((int64_t)copy << 32 | n, tmp64, &all);
     if (b < s.batch) {
-      seq[b].base = upto - n;
-      if (copy) seq[b].rank = upto_copies - 1;
+      seq[b].base = need + (int)(uint32_t)upto - n;
+      if (copy) seq[b].rank = copies + (int)(upto >> 32) - 1;
     }
+    need += (int)(uint32_t)all;
+    copies += (int)(all >> 32);
   }
   cluster_sync();
   // ---- a free page finds its entry by its rank ---------------------------------------------------
   const Found free = found(p.w.counts);
+  auto next_base = [&](int b) { return b + 1 < s.batch ? seq[b + 1].base : need; };
   // of a sequence that grows: whether it gets its pages
-  auto served = [&](int b) {
-    return seq[b].rank != -2 && (b + 1 < s.batch ? seq[b + 1].base : need) <= free.all;
-  };
-  // rows of the new positions [t0, t1) of sequence b, on page pg: by a warp
-  auto put_slots = [&](int b, int64_t t0, int64_t t1, int pg) {
-    const ExtendSeq& q = seq[b];
-    t0 = max(t0, (int64_t)q.len);
-    t1 = min(t1, end_of(q));
-    for (int64_t t = t0 + lane; t < t1; t += 32) p.slots[q.start + (t - q.len)] = pg < 0 ? -1 : (int64_t)pg * page + (t & (page - 1));
-  };
-  give_free(s, free, need, tmp, [&](int rank, int pg) {
-    int b = 0, j = 0;
-    if (pg >= 0) {
+  auto served = [&](int b) { return seq[b].rank != -2 && (next_base(b) <= free.all || next_base(b) == seq[b].base); };
+  give_free(s, share, free, need, tmp, list, [&](int rank0, const int* pages, int n) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int rank = rank0 + i, pg = pages[i];
       int lo = 0, hi = s.batch;  // the last sequence with base <= rank
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (seq[mid].base <= rank) lo = mid;
         else hi = mid;
       }
-      b = lo;
-      if (served(b)) {
-        const ExtendSeq& q = seq[b];
-        j = pages_of(s, q.len) + rank - q.base - (q.rank >= 0);  // (the copy first, in the place before)
-        if (q.rank >= 0 && rank == q.base) p.w.jobs[q.rank] = make_int4(q.part, pg, q.len & (page - 1), 0);
-        s.table[b * s.stride + j] = pg;
+      int4 r = make_int4(0, 0, 0, 0);  // the first row of slots on the page, how many, the first slot
+      if (served(lo)) {
+        const ExtendSeq& q = seq[lo];
+        const int j = pages_of(s, q.len) + rank - q.base - (q.rank >= 0);  // (the copy first, in the place before)
+        if (q.rank >= 0 && rank == q.base) p.w.jobs[q.rank] = make_int4(q.part, pg, q.len & (page - 1), 1);
+        s.table[lo * s.stride + j] = pg;
         s.refs[pg] = 1;
-      } else {
-        pg = -1;
+        const int64_t t0 = max((int64_t)j << s.page_shift, (int64_t)q.len), t1 = min((int64_t)(j + 1) << s.page_shift, end_of(q));
+        r = make_int4(q.start + (int)(t0 - q.len), (int)(t1 - t0), pg * page + (int)(t0 & (page - 1)), 0);
       }
+      rows[i] = r;
     }
-    for (unsigned left = __ballot_sync(0xffffffffu, pg >= 0); left; left &= left - 1) {
-      const int src = __ffs(left) - 1, bb = __shfl_sync(0xffffffffu, b, src);
-      const int64_t t = (int64_t)__shfl_sync(0xffffffffu, j, src) << s.page_shift;
-      put_slots(bb, t, t + page, __shfl_sync(0xffffffffu, pg, src));
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < n; i += kWarps) {
+      const int4 r = rows[i];
+      for (int t = lane; t < r.y; t += 32) p.slots[r.x + t] = r.z + t;
     }
   });
   for_items(s.batch, [&](int b, int part, int) {
     const ExtendSeq& q = seq[b];
     if (part != 0) return;
-    const bool ok = q.grow <= 0 || served(b) || (q.rank != -2 && (b + 1 < s.batch ? seq[b + 1].base : need) == q.base);
+    const bool ok = q.grow <= 0 || served(b);
     if (lane == 0) {
       if (!ok) atomicOr(s.err, kErrIndex);
       else s.lens[b] = (int32_t)end_of(q);
       if (q.rank >= 0 && !ok) p.w.jobs[q.rank] = make_int4(0, 0, 0, 0);
     }
     if (q.grow <= 0) return;
+    const int n = (b + 1 < s.batch ? seq[b + 1].start : total) - q.start;
     if (!ok) {  // (its rows as far as there are any)
-      const int n = (b + 1 < s.batch ? seq[b + 1].start : total) - q.start;
       for (int i = lane; i < n; i += 32) p.slots[q.start + i] = -1;
-    } else if ((q.len & (page - 1)) && q.rank < 0) {
-      put_slots(b, q.len, (int64_t)pages_of(s, q.len) << s.page_shift, q.part);
+    } else if ((q.len & (page - 1)) && q.rank < 0) {  // rows on the page that it has
+      const int m = min(n, page - (q.len & (page - 1)));
+      for (int i = lane; i < m; i += 32)
+        p.slots[q.start + i] = q.part < 0 ? -1 : (int64_t)q.part * page + (q.len & (page - 1)) + i;
     }
   });
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.w.copies = copies;
-  if (copies == 0) return;
-  // ---- what is copied has a use less (it was none of the free ones) ------------------------------
-  cluster_sync();
-  for (int b = blockIdx.x * kThreads + threadIdx.x; b < s.batch; b += gridDim.x * kThreads)
-    if (seq[b].rank >= 0 && served(b)) drop_ref(s, seq[b].part);
 }
 
 // ---- fork -------------------------------------------------------------------------------------
@@ -404,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   ForkItem* const item = reinterpret_cast<ForkItem*>(smem);
   int* const of_rank = reinterpret_cast<int*>(item + p.n);  // [n] the item of a copy
   int* const owner = of_rank + p.n;                          // [batch]
+  int* const list = owner + p.s.batch;                       // [4 kThreads]
   const SeqsP& s = p.s;
   const int lane = threadIdx.x & 31, page = 1 << s.page_shift;
   asm volatile("griddepcontrol.launch_dependents;" :::);  // (the copies: they wait for this grid's end)
@@ -467,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   });
   cluster_sync();
   // ---- free pages; the rows, but for the pages that are copied -----------------------------------
-  count_free(s, p.w, tmp);
+  const Share share = count_free(s, p.w, tmp);
   for_items(p.n, [&](int i, int part, int parts) {
     const ForkItem q = item[i];
     if (q.dst < 0) return;
@@ -481,12 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   cluster_sync();
   // ---- a page for each last one that is not full -------------------------------------------------
   const Found free = found(p.w.counts);
-  give_free(s, free, copies, tmp, [&](int rank, int pg) {
-    if (pg < 0) return;
-    const ForkItem q = item[of_rank[rank]];
-    s.table[q.dst * s.stride + (q.len >> s.page_shift)] = pg;
-    s.refs[pg] = 1;
-    p.w.jobs[rank] = make_int4(q.part, pg, q.len & (page - 1), 0);
+  give_free(s, share, free, copies, tmp, list, [&](int rank0, const int* pages, int n) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const ForkItem q = item[of_rank[rank0 + i]];
+      s.table[q.dst * s.stride + (q.len >> s.page_shift)] = pages[i];
+      s.refs[pages[i]] = 1;
+      p.w.jobs[rank0 + i] = make_int4(q.part, pages[i], q.len & (page - 1), 1);
+    }
   });
   for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.n; i += gridDim.x * kThreads) {
     const ForkItem q = item[i];
@@ -496,13 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     if (short_of) {
       atomicOr(s.err, kErrIndex);
       s.table[q.dst * s.stride + (q.len >> s.page_shift)] = -1;
-      p.w.jobs[q.rank] = make_int4(0, 0, 0, 0);
+      p.w.jobs[q.rank] = make_int4(q.part, 0, 0, 1);
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.w.copies = copies;
-  if (copies == 0) return;
-  cluster_sync();
-  for (int r = blockIdx.x * kThreads + threadIdx.x; r < copies; r += gridDim.x * kThreads) drop_ref(s, item[of_rank[r]].part);
 }
 
 // ---- compact ----------------------------------------------------------------------------------
@@ -575,16 +600,21 @@ struct Plane {
 struct CopyP {
   Plane planes[kMostPlanes];
   int first[kMostPlanes + 1];  // chunks of a page before the plane's
-  int n, page_shift, n_pages;
+  int n, drops;
   const int4* jobs;
   const int* count;
   int most;                    // jobs there can be
-  unsigned int* err;
+  SeqsP s;
 };
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyP p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int jobs = min(*p.count, p.most), chunks = p.first[p.n];
+  // (of the uses that the tables' kernel has left to drop: while it gave pages out, what is copied
+  // must not count as free, and here it need not wait for all of its CTAs once more)
+  if (p.drops)
+    for (int i = blockIdx.x * kCopyThreads + threadIdx.x; i < jobs; i += gridDim.x * kCopyThreads)
+      if (p.jobs[i].w) drop_ref(p.s, p.jobs[i].x);
   for (int64_t u = blockIdx.x; u < (int64_t)jobs * chunks; u += gridDim.x) {
     const int4 job = p.jobs[u / chunks];
     const int ch = (int)(u % chunks);
@@ -596,8 +626,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     }
     const Plane pl = p.planes[lo];
     const uint32_t at = (uint32_t)(ch - p.first[lo]) * kChunk, end = min(pl.bytes, at + kChunk);
-    const uint32_t used = (uint32_t)(((uint64_t)pl.head_bytes * job.z) >> p.page_shift);  // bytes of a head that are copied
-    if (used == 0 || !in_bounds((uint32_t)job.x < (uint32_t)p.n_pages && (uint32_t)job.y < (uint32_t)p.n_pages, p.err)) continue;
+    const uint32_t used = (uint32_t)(((uint64_t)pl.head_bytes * job.z) >> p.s.page_shift);  // bytes of a head that are copied
+    if (used == 0 || !in_bounds(page_ok(p.s, job.x) && page_ok(p.s, job.y), p.s.err)) continue;
     const uint8_t* src = pl.data + (int64_t)job.x * pl.bytes;
     uint8_t* dst = pl.data + (int64_t)job.y * pl.bytes;
     constexpr int U = kChunk / (16 * kCopyThreads);
@@ -746,12 +776,11 @@ qps_status launch_copies(const Seqs& q, const PagesWs& w, int64_t most, cudaStre
       chunks += (p.planes[i].bytes + kChunk - 1) / kChunk;
     }
     p.first[p.n] = (int)chunks;  // (96 planes of 2^31 bytes: below 2^24)
-    p.page_shift = q.p.page_shift;
-    p.n_pages = q.p.n_pages;
+    p.drops = at == 0;
     p.jobs = w.jobs;
     p.count = w.copies;
     p.most = (int)most;
-    p.err = q.p.err;
+    p.s = q.p;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(most * chunks, (int64_t)sms * 8)));
     cfg.blockDim = dim3(kCopyThreads);
@@ -815,7 +844,7 @@ qps_status kv_extend_paged(const qps_paged_extend_args* a, cudaStream_t s) {
   p.starts = a->q_starts;
   p.slots = a->slots;
   p.positions = a->positions;
-  st = launch_pages(extend_kernel, p, p.s.batch * sizeof(ExtendSeq), s);
+  st = launch_pages(extend_kernel, p, p.s.batch * sizeof(ExtendSeq) + 4 * kThreads * (sizeof(int) + sizeof(int4)), s);
   return st != QPS_OK || jobs == 0 ? st : launch_copies(q, p.w, jobs, s);
 }
 
@@ -850,7 +879,7 @@ qps_status kv_fork_paged(const qps_paged_fork_args* a, cudaStream_t s) {
   p.src = a->src;
   p.dst = a->dst;
   p.n = a->n;
-  st = launch_pages(fork_kernel, p, p.n * (sizeof(ForkItem) + sizeof(int)) + p.s.batch * sizeof(int), s);
+  st = launch_pages(fork_kernel, p, p.n * (sizeof(ForkItem) + sizeof(int)) + (p.s.batch + 4 * kThreads) * sizeof(int), s);
   return st != QPS_OK ? st : launch_copies(q, p.w, a->n, s);
 }
 
