@@ -405,6 +405,7 @@ qps_status plan_prompt(const qps_paged_prompt_args* a, Plan* out) {
     for (int i = 0; i < cb->n; ++i) p.tq_levels[i] = cb->levels[i];
   }
   // row tiles: full ones, and at most one that is not for each sequence
+  p.resident = sms;
   const int64_t rows = a->tokens * p.group;
   p.tiles = (int)std::min<int64_t>(rows / prompt_rows(kv.d) + std::min<int64_t>(a->batch, a->tokens), rows);
   // tiles of positions that a sequence's tokens see, at most
@@ -413,6 +414,13 @@ qps_status plan_prompt(const qps_paged_prompt_args* a, Plan* out) {
   // Row tiles that leave SMs without work share their positions among several CTAs.
   const int64_t ctas = std::max<int64_t>(1, (int64_t)p.tiles * kv.hkv * prompt_col_ctas(kv.d));
   p.n_split = (int)std::max<int64_t>(1, std::min<int64_t>(sms / ctas, most));
+  // A ragged batch of few tokens: cut finer, so that one long sequence is not a few CTAs' work (its
+  // tiles stay 16 to a part at least, beside a part's start and end of about 6), as long as the
+  // parts stay small.
+  const int64_t part = a->tokens * a->hq * kv.d * (int64_t)sizeof(float);
+  if (a->batch > 1) p.n_split = (int)std::max<int64_t>(p.n_split, std::min({4 * sms / ctas, most / 16, ((int64_t)32 << 20) / std::max<int64_t>(1, part)}));
+  // (a part's row is counted in 32 bits; tokens that fill the SMs are not split)
+  if (p.n_split * a->tokens * a->hq >= (int64_t)1 << 32) p.n_split = 1;
   if ((int64_t)p.tiles * p.n_split * prompt_col_ctas(kv.d) * kv.hkv >= (int64_t)1 << 31)
     return bad("too many row tiles", QPS_ERR_UNSUPPORTED);
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };

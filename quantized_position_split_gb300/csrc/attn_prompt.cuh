@@ -121,18 +121,21 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this CTA's rows and tiles -------------------------------------------------------------
-  int idx = blockIdx.x;
-  const int head = idx % p.hkv;
-  idx /= p.hkv;
-  const int half = idx % (D / G::VD);
-  idx /= D / G::VD;
-  const int split = idx % p.n_split;
-  idx /= p.n_split;
-  // row tile `idx`: sequences in order, the last rows of each first (they see the most)
-  PromptSeq sq = {0, 0, 0};
-  int bz = -1, row0 = 0, dense0 = 0;  // dense0: the sequence's first decoded tile
-  const bool decoded = p.dense_k || p.dense_v;
-  {
+  // CTA `idx` of the grid: KV head, half of O's columns, split, row tile (sequences in order, the last
+  // rows of each first: they see the most).  Sequence -1: there are fewer row tiles.
+  struct Work {
+    int head, half, split, bz, row0, dense0;  // dense0: the sequence's first decoded tile
+    PromptSeq sq;
+  };
+  auto find = [&](int idx) {
+    Work k = {};
+    k.head = idx % p.hkv;
+    idx /= p.hkv;
+    k.half = idx % (D / G::VD);
+    idx /= D / G::VD;
+    k.split = idx % p.n_split;
+    idx /= p.n_split;
+    k.bz = -1;
     int before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       PromptSeq mine = {0, 0, 0};
@@ -146,21 +149,25 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       }
       const unsigned hit = __ballot_sync(0xffffffffu, before + sum > idx);
       const int src = hit ? __ffs(hit) - 1 : 32;
-      if (decoded) {
+      if (p.dense_k || p.dense_v) {
         const int tiles = lane < src && mine.n > 0 ? prompt_tiles(p, mine.len - mine.n, mine.len - 1).count : 0;
-        dense0 += __reduce_add_sync(0xffffffffu, tiles);
+        k.dense0 += __reduce_add_sync(0xffffffffu, tiles);
       }
       if (hit) {
-        bz = b0 + src;
-        sq.first = __shfl_sync(0xffffffffu, mine.first, src);
-        sq.n = __shfl_sync(0xffffffffu, mine.n, src);
-        sq.len = __shfl_sync(0xffffffffu, mine.len, src);
-        row0 = (before + __shfl_sync(0xffffffffu, sum, src) - 1 - idx) * NQ * kRows;
+        k.bz = b0 + src;
+        k.sq.first = __shfl_sync(0xffffffffu, mine.first, src);
+        k.sq.n = __shfl_sync(0xffffffffu, mine.n, src);
+        k.sq.len = __shfl_sync(0xffffffffu, mine.len, src);
+        k.row0 = (before + __shfl_sync(0xffffffffu, sum, src) - 1 - idx) * NQ * kRows;
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-  }
+    return k;
+  };
+  const Work work = find(blockIdx.x);
+  const int head = work.head, half = work.half, split = work.split, bz = work.bz, row0 = work.row0, dense0 = work.dense0;
+  const PromptSeq sq = work.sq;
   fence_before();
   __syncthreads();
   fence_after();
@@ -255,13 +262,12 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       return true;
     };
     int page = entry(0), next = entry(1);
-    bool ok = true;
-    if constexpr (NQ == 1) ok = ntiles == 0 || put_k(0, page);
+    // (the first tile, then the queries: the whole ring before them kept them 1500 cycles longer)
+    bool ok = ntiles == 0 || (put_k(0, page) && (NQ == 1 || put_v(0, page)) && wait(q_full, 0, 0));
     for (int j = 0; j < ntiles && ok; ++j) {
       const int after = entry(j + 2);
-      if constexpr (NQ == 2) ok = put_k(j, page);
-      else ok = j + 1 >= ntiles || put_k(j + 1, next);
-      ok = ok && put_v(j, page);
+      if constexpr (NQ == 2) ok = j == 0 || (put_k(j, page) && put_v(j, page));
+      else ok = (j + 1 >= ntiles || put_k(j + 1, next)) && put_v(j, page);
       page = next;
       next = after;
     }
@@ -334,6 +340,19 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       if (i + 2 < steps) ok = qk(i + 2);
     }
     commit(all_done, one);  // completes when everything issued above has
+  } else if (warp == 3) {
+    // ---- the queries of the CTA that follows on this SM, about, into L2 (from HBM they took 5200
+    // cycles of a CTA's start) -------------------------------------------------------------------
+    const int next = blockIdx.x + p.resident;
+    const Work k = next < (int)gridDim.x ? find(next) : Work{0, 0, 0, -1, 0, 0, {0, 0, 0}};
+    if (k.bz >= 0) {
+      const int t0 = k.row0 / p.group, t1 = (int)min((int64_t)k.sq.n - 1, ((int64_t)k.row0 + NQ * kRows - 1) / p.group);
+      const int lines = (p.group * D * 2 + 127) / 128;
+      for (int i = lane; i < (t1 - t0 + 1) * lines; i += 32) {
+        const int64_t at = (int64_t)(k.sq.first + t0 + i / lines) * p.q_tok + (int64_t)k.head * p.group * D + min(i % lines * 64, p.group * D - 8);
+        if (in_bounds(k.sq.first + t0 + i / lines < p.tokens, p.err)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + at));
+      }
+    }
   }
   } else {
     if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::MANY));
@@ -495,9 +514,9 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       const float2 s2 = unpack2(add2(sum[0], sum[1]));
       l += s2.x + s2.y;
     }
-    // ---- the rows' output, or their part of it: a thread's row through shared memory (the ring, all
-    // of whose slots have been used) and out as one bulk copy (stores from the registers, 32 rows an
-    // instruction, took 7200 cycles) ----------------------------------------------------------------
+    // ---- the rows' output, or their part of it: through shared memory (the ring, all of whose slots
+    // have been used), each warp its own rows, and out as whole lines (from the registers, a row a lane,
+    // 7200 cycles; as a bulk copy a row 3900) ---------------------------------------------------------
     if (ok) ok = wait(all_done, 0, ntiles);
     fence_after();
     if (ok && !__any_sync(0xffffffffu, *abort_flag)) {
@@ -515,7 +534,6 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
       static_assert(NQ * kRows * (PC * 4 + 16) <= ST * G::SLOT, "the rows fit the ring");
 #pragma unroll 1
       for (int x = 0; x < G::VD; x += PC) {
-        if (x > 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 #pragma unroll
         for (int c = 0; c < PC / 32; ++c) {
           uint32_t v[32];
@@ -549,14 +567,19 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
             }
           }
         }
-        mma::fence_proxy_async();
-        if (store) {
-          uint8_t* dst = reinterpret_cast<uint8_t*>(whole ? p.out : p.part_o) + (to * D + half * G::VD + x) * (wide ? 4 : 2);
-          asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(row)), "r"(bytes) : "memory");
+        __syncwarp();
+        const uint32_t chunks = bytes / 16, to32 = (uint32_t)(store ? to : 0);
+        const uint8_t* rows32 = row - lane * (bytes + 16);
+        uint8_t* const out = reinterpret_cast<uint8_t*>(whole ? p.out : p.part_o) + (half * G::VD + x) * (wide ? 4 : 2);
+#pragma unroll 4
+        for (uint32_t k = 0; k < chunks; ++k) {
+          const uint32_t i = k * 32 + lane, rr = i / chunks, c = i % chunks;  // (a power of two)
+          const int64_t dst = __shfl_sync(0xffffffffu, to32, rr);
+          if (__shfl_sync(0xffffffffu, (int)store, rr))
+            *reinterpret_cast<uint4*>(out + dst * (D * (wide ? 4 : 2)) + 16 * c) = *reinterpret_cast<const uint4*>(rows32 + rr * (bytes + 16) + 16 * c);
         }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        __syncwarp();
       }
-      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     fence_before();
   }

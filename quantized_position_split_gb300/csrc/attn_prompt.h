@@ -22,6 +22,7 @@ struct PromptParams {
   float scale, softcap;
   int window, sinks;      // window 0: none
   int tiles;              // row tiles there can be
+  int resident;           // CTAs that run at once
   int n_split;            // parts a row tile's positions are cut into
   float* part_o;          // f32 [n_split][tokens * hq][D], [n_split][tokens * hq]
   float* part_lse;
