@@ -373,7 +373,7 @@ template <int D, int KF, int VF, int NTW, bool CAUSAL, class P>
 __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, NTW>::CTAS)
     attn_mma_kernel(const __grid_constant__ P p, const __grid_constant__ TmaSet maps) {
   using G = Geo<D, KF, VF, NTW>;
-  constexpr bool PAGED = std::is_same<P, PagedAttnParams>::value;
+  constexpr bool PAGED = std::is_base_of<PagedAttnParams, P>::value;
   constexpr int kWarps = G::NW;
   constexpr int ROWS = 8 * NTW;  // query rows per CTA
   constexpr int MT = D / 16;     // m-tiles of O^T, k-steps of S^T
@@ -616,9 +616,9 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
   };
   auto page_of = [&](int64_t t) -> int {
     if constexpr (PAGED) {
-      const int at = t < t1 ? paged_true(win, (int)t) >> p.page_shift : 0;
-      if (t >= t1 || paged_unseen(p, win, (int)t, min(1 << p.page_shift, TT)) || !entry_in_bounds(p, bz * p.table_stride + at))
-        return (int)p.n_pages;
+      if (t >= t1 || paged_unseen(p, win, (int)t, min(1 << p.page_shift, TT))) return (int)p.n_pages;
+      const int64_t at = paged_true(p, win, (int)t) >> p.page_shift;
+      if (!entry_in_bounds(p, bz * p.table_stride + at)) return (int)p.n_pages;
       const int pg = p.table[(int64_t)bz * p.table_stride + at];
       if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
       atomicOr(p.err, kErrIndex);
@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
     uint8_t* st = wpipe + (k % G::STAGES) * G::STAGE;
     const int64_t tb = tile0 + (int64_t)tile * TT;
     int tok = (int)tb;
-    if constexpr (PAGED) tok = paged_true(win, tok);
+    if constexpr (PAGED) tok = paged_true(p, win, tok);
     const uint32_t bar = bars + (k % G::STAGES) * 8;
     if (lane == 0) mbar_expect_tx(bar, G::TX);
     __syncwarp();
@@ -818,10 +818,10 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         const int e = (row0 + nt * 8 + 2 * c + u) / p.group;
         const int i = p.shared ? e % p.n_q : e, b = p.shared ? e / p.n_q : bz;
         int n = (int)t1;
-        if (p.shared || p.causal || p.window) {
+        if (p.shared || p.causal || has_window<P>) {
           n = b < p.batch ? paged_len(p, b) : 0;
           if (p.causal) n += i + 1 - p.n_q;
-          if (p.window == 0) n = min(n, (int)t1);  // (a window's start is counted from it; chunks end with tiles)
+          if constexpr (!has_window<P>) n = min(n, (int)t1);  // (a window's start is counted from it; chunks end with tiles)
         }
         lim[nt][u] = n;
       }
@@ -1098,7 +1098,7 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
         const __half* nrm = reinterpret_cast<const __half*>(st + G::NORM_OFF);
         n_g[sb] = __half2float(nrm[16 * sb + g]);
         n_g8[sb] = __half2float(nrm[16 * sb + g + 8]);
-        if constexpr (PAGED) {  // (a norm behind the window may be anything: 0 x NaN)
+        if constexpr (has_window<P>) {  // (a norm behind the window may be anything: 0 x NaN)
           if (t_g >= p.sinks && t_g < win.none_lo) n_g[sb] = 0.f;
           if (t_g + 8 >= p.sinks && t_g + 8 < win.none_lo) n_g8[sb] = 0.f;
         }
@@ -1158,12 +1158,14 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
           if (t >= lim[nt][1]) x[sb][1] = -INFINITY;
           if (t + 8 >= lim[nt][0]) x[sb][2] = -INFINITY;
           if (t + 8 >= lim[nt][1]) x[sb][3] = -INFINITY;
-          if ((int)tb < win.all_lo) {  // (uniform) the start of the window lies in the tile for some row
-            const int w0 = lim[nt][0] - p.window, w1 = lim[nt][1] - p.window;
-            if (t >= p.sinks && t < w0) x[sb][0] = -INFINITY;
-            if (t >= p.sinks && t < w1) x[sb][1] = -INFINITY;
-            if (t + 8 >= p.sinks && t + 8 < w0) x[sb][2] = -INFINITY;
-            if (t + 8 >= p.sinks && t + 8 < w1) x[sb][3] = -INFINITY;
+          if constexpr (has_window<P>) {
+            if ((int)tb < win.all_lo) {  // (uniform) the start of the window lies in the tile for some row
+              const int w0 = lim[nt][0] - p.window, w1 = lim[nt][1] - p.window;
+              if (t >= p.sinks && t < w0) x[sb][0] = -INFINITY;
+              if (t >= p.sinks && t < w1) x[sb][1] = -INFINITY;
+              if (t + 8 >= p.sinks && t + 8 < w0) x[sb][2] = -INFINITY;
+              if (t + 8 >= p.sinks && t + 8 < w1) x[sb][3] = -INFINITY;
+            }
           }
         } else {
           if (!in_g[sb]) x[sb][0] = x[sb][1] = -INFINITY;
@@ -1494,6 +1496,8 @@ __global__ void __launch_bounds__(Geo<D, KF, VF, NTW>::NW * 32, Geo<D, KF, VF, N
                 make_uint4(0, 0, 0, 0);
         __syncwarp();
       }
+    }
+    if constexpr (has_window<P>) {
       // The same for positions that no row's window reaches (TurboQuant norms: attend_tile).
       const int tb = (int)(tile0 + (int64_t)(warp + k * kWarps) * TT);
       if (tb < win.none_lo && tb + TT > p.sinks && !is_tq(VF)) {
@@ -1770,7 +1774,7 @@ qps_status launch_mma_t(const P& p, cudaStream_t s) {
   TmaSet maps;
   std::memset(&maps, 0, sizeof(maps));
   const int nb = p.shared ? 1 : p.batch;
-  constexpr bool PAGED = std::is_same<P, PagedAttnParams>::value;
+  constexpr bool PAGED = std::is_base_of<PagedAttnParams, P>::value;
   if constexpr (PAGED) {  // [row bytes][positions of a page][KV heads][pages]
     const int page = 1 << p.page_shift, rows = page < G::TT ? page : G::TT;
     auto map = [&](TensorMap* m, const void* base, int rb, int ib, int sw) {
@@ -1839,7 +1843,7 @@ qps_status launch_mma_t(const P& p, cudaStream_t s) {
 // than this to attn_tm.cuh or attn_tt.cuh, see attn_paged.cu).
 template <int D, int KF, int VF, class P>
 constexpr int most_ntw() {
-  if (std::is_same<P, PagedAttnParams>::value) {
+  if (std::is_base_of<PagedAttnParams, P>::value) {
     if (KF == QPS_FMT_F16 && VF == QPS_FMT_F16 && D <= 128) return D == 64 ? 2 : 1;
     if (D == 128 && !is_tq(VF)) return 2;
   }

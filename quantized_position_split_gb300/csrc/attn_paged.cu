@@ -151,6 +151,7 @@ qps_status launch_merge(const PagedAttnParams& p, int parts, cudaStream_t s) {
 // ---- plan -----------------------------------------------------------------------------------
 struct Plan {
   PagedAttnParams p;
+  int window, sinks, win_round;  // (see WindowAttnParams; window 0: none)
   PagedKernel prefix_kernel, own_kernel;
   int parts;   // most parts a row can have; one: no merge
   size_t off_pre_lse, off_own_o, off_own_lse, off_chunks, bytes;
@@ -275,13 +276,12 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
   p.out_dtype = a->o_dtype;
   // (a window that no sequence outgrows is none; one that they do leaves no common prefix)
   const int held = a->table_width << kv.page_shift;
-  p.window = a->window > 0 && a->window < held && a->sinks < held ? a->window : 0;
-  p.sinks = p.window ? a->sinks : 0;
-  p.win_round = 1;
+  out->window = a->window > 0 && a->window < held && a->sinks < held ? a->window : 0;
+  out->sinks = out->window ? a->sinks : 0;
 
   // the prefix: whole tiles of the shared positions (what is left of them is read through
   // each sequence's own entries, which name the same pages)
-  p.prefix_len = a->batch > 1 && p.window == 0 ? (int)(a->shared_len & ~(int64_t)31) : 0;
+  p.prefix_len = a->batch > 1 && out->window == 0 ? (int)(a->shared_len & ~(int64_t)31) : 0;
   if (p.prefix_len > 0) {
     const int all = a->batch * rows;
     const Shape sh = shape_for(kv, all, true);
@@ -304,10 +304,10 @@ qps_status plan_paged(const qps_paged_attn_args* a, Plan* out) {
     const int least = a->batch >= round ? kMinMany : kMinPositions;
     p.min_units = least / kPagedUnit;
     p.unit_round = sh.tile / kPagedUnit;
-    p.win_round = sh.tile;
+    out->win_round = sh.tile;
     // chunks of a sequence that fills its table (of what its window leaves), and of all of them
     int64_t most = ((int64_t)a->table_width << kv.page_shift) - p.prefix_len;
-    if (p.window) most = std::min<int64_t>(most, (int64_t)p.window + a->n_q + p.sinks + 2 * sh.tile);
+    if (out->window) most = std::min<int64_t>(most, (int64_t)out->window + a->n_q + out->sinks + 2 * sh.tile);
     const int64_t each = std::max<int64_t>(1, (most + least - 1) / least);
     p.max_chunks = (int)std::min<int64_t>((int64_t)p.target + a->batch, each * a->batch);
     out->parts = p.n_prefix + (int)std::min<int64_t>(each, p.target + 1);
@@ -331,6 +331,18 @@ qps_status launch_paged(const PagedAttnParams& p, cudaStream_t s) {
     case 128: return launch_paged_mma_d128(p, s);
     case 256: return launch_paged_mma_d256(p, s);
     default: return launch_paged_mma_d512(p, s);
+  }
+}
+
+qps_status launch_window(const WindowAttnParams& p, cudaStream_t s) {
+  if (p.kernel == kTm) return p.d == 64 ? launch_window_tm_d64(p, s) : launch_window_tm_d128(p, s);
+  if (p.kernel == kTt)
+    return p.d == 128 ? launch_window_tt_d128(p, s) : p.d == 256 ? launch_window_tt_d256(p, s) : launch_window_tt_d512(p, s);
+  switch (p.d) {
+    case 64: return launch_window_mma_d64(p, s);
+    case 128: return launch_window_mma_d128(p, s);
+    case 256: return launch_window_mma_d256(p, s);
+    default: return launch_window_mma_d512(p, s);
   }
 }
 
@@ -387,7 +399,16 @@ qps_status attn_decode_paged(const qps_paged_attn_args* a, cudaStream_t s) {
   p.kernel = pl.own_kernel;
   p.rows_per_cta = rows;
   p.chunk = 0;
-  st = launch_paged(p, s);
+  if (pl.window) {
+    WindowAttnParams w{};
+    static_cast<PagedAttnParams&>(w) = p;
+    w.window = pl.window;
+    w.sinks = pl.sinks;
+    w.win_round = pl.win_round;
+    st = launch_window(w, s);
+  } else {
+    st = launch_paged(p, s);
+  }
   if (st != QPS_OK || pl.parts <= 1) return st;
   switch (p.d) {
     case 64: return launch_merge<64>(p, pl.parts, s);

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   const uint32_t sbase = smem_addr(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- barriers, TMEM --------------------------------------------------------------------------
   const uint32_t bars = sbase + G::BAR;
   auto full = [&](int s) { return bars + 8 * s; };
@@ -119,7 +120,6 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
     *abort_flag = 0;
   }
   if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this CTA's rows and tiles -------------------------------------------------------------
   // CTA `idx` of the grid: KV head, half of O's columns, split, row tile (sequences in order, the last
   // rows of each first: they see the most).  Sequence -1: there are fewer row tiles.
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
     // ---- the queries of the CTA that follows on this SM, about, into L2 (from HBM they took 5200
     // cycles of a CTA's start) -------------------------------------------------------------------
     const int next = blockIdx.x + p.resident;
-    const Work k = next < (int)gridDim.x ? find(next) : Work{0, 0, 0, -1, 0, 0, {0, 0, 0}};
+    const Work k = next < (int)gridDim.x && p.group <= NQ * kRows ? find(next) : Work{0, 0, 0, -1, 0, 0, {0, 0, 0}};
     if (k.bz >= 0) {
       const int t0 = k.row0 / p.group, t1 = (int)min((int64_t)k.sq.n - 1, ((int64_t)k.row0 + NQ * kRows - 1) / p.group);
       const int lines = (p.group * D * 2 + 127) / 128;

@@ -177,9 +177,10 @@ static __device__ __noinline__ bool report_give_up(unsigned int* err, int word, 
 }
 
 // ---- the kernel ------------------------------------------------------------------------------
-template <int D>
+// P: PagedAttnParams, or WindowAttnParams.
+template <int D, class P>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tm_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ TmaSet maps) {
+    attn_tm_kernel(const __grid_constant__ P p, const __grid_constant__ TmaSet maps) {
   using G = Geo<D>;
   constexpr int ST = G::STAGES;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = t0 + j * kTok + r * br;
       return r < nb && t < t1 && !paged_unseen(p, win, t, br);
     };
-    auto at = [&](int j) { return paged_true(win, t0 + j * kTok + r * br); };
+    auto at = [&](int j) { return paged_true(p, win, t0 + j * kTok + r * br); };
     auto entry = [&](int j) {
       const int i = at(j) >> p.page_shift;
       return has(j) && entry_in_bounds(p, bz * p.table_stride + i) ? row[i] : 0;
@@ -359,15 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma::fence_proxy_async();
         __syncwarp();
       }
-      if (t0 + j * kTok < win.none_lo && t0 + (j + 1) * kTok > p.sinks) {  // nor do rows that no window reaches
+      if constexpr (has_window<P>) {
         const int tb = t0 + j * kTok;
-        for (int i = max(0, p.sinks - tb) * 8 + lane; i < min(kTok, win.none_lo - tb) * 8; i += 32)
+        if (tb < win.none_lo && tb + kTok > p.sinks) {  // nor do rows that no window reaches
+          for (int i = max(0, p.sinks - tb) * 8 + lane; i < min(kTok, win.none_lo - tb) * 8; i += 32)
 #pragma unroll
-          for (int cg = 0; cg < G::CG; ++cg)
-            if (in_bounds(cg * (kTok * 128) + i * 16 + 16 <= G::TILE, p.err))
-              *reinterpret_cast<uint4*>(smem + vb + cg * (kTok * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-        mma::fence_proxy_async();
-        __syncwarp();
+            for (int cg = 0; cg < G::CG; ++cg)
+              if (in_bounds(cg * (kTok * 128) + i * 16 + 16 <= G::TILE, p.err))
+                *reinterpret_cast<uint4*>(smem + vb + cg * (kTok * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          mma::fence_proxy_async();
+          __syncwarp();
+        }
       }
       if (!(ok = wait(p_ready(w), (j >> 1) & 1, j))) break;
       fence_after();
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
       lim = paged_len(p, b);
       if (p.causal) lim += qi + 1 - p.n_q;
-      if (p.window) low = lim - p.window;
+      if constexpr (has_window<P>) low = lim - p.window;
       lim = min(lim, t1);
     }
     constexpr float LOG2E = 1.4426950408889634f;
@@ -409,9 +412,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Whole tiles of plain logits, the common case, have a body of their own: maxima and
       // exponentials straight from S (a positive scale keeps the order), four chains each,
       // the next 32 columns read beside the present ones' arithmetic.
-      const bool fast = __all_sync(0xffffffffu, (first + kTok <= lim && first >= low) || rr >= p.rows_per_cta) &&
+      const bool fast = __all_sync(0xffffffffu, (first + kTok <= lim && (!has_window<P> || first >= low)) || rr >= p.rows_per_cta) &&
                         cap <= 0.f && qs >= 0.f;
-      auto hidden = [&](int t) { return t >= lim || (t < low && t >= p.sinks); };
+      auto hidden = [&](int t) {
+        if constexpr (has_window<P>)
+          if (t < low && t >= p.sinks) return true;
+        return t >= lim;
+      };
       uint32_t va[32], vb[32];
       float mx = -INFINITY;
       if (fast) {
@@ -641,8 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_free(tmem, 512);
 }
 
-template <int D>
-qps_status launch_tm(const PagedAttnParams& p, cudaStream_t s) {
+template <int D, class P>
+qps_status launch_tm(const P& p, cudaStream_t s) {
   using G = Geo<D>;
   static_assert(G::SMEM <= 227 * 1024, "the stages exceed the shared memory of one CTA");
   static_assert(G::O_COL + 2 * D <= 512, "S and O exceed TMEM");
@@ -653,7 +660,7 @@ qps_status launch_tm(const PagedAttnParams& p, cudaStream_t s) {
     if (!encode_plane_map(i ? &maps.v : &maps.k, i ? p.v.data : p.k.data, 2 * D, page, p.hkv, page, (int)p.n_pages,
                           (int64_t)p.hkv * page, 128, 128, rows))
       return QPS_ERR_CUDA;
-  auto kern = attn_tm_kernel<D>;
+  auto kern = attn_tm_kernel<D, P>;
   static std::atomic<uint64_t> sized{0};
   int dev = 0;
   QPS_CUDA_TRY(cudaGetDevice(&dev));

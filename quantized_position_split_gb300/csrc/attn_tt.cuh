@@ -83,9 +83,10 @@ struct GeoTt {
 // j, j + 4, j + 8, j + 12 of step j.
 __device__ __forceinline__ int tq_unswap(int pos) { return (pos >> 2) + 4 * (pos & 3); }
 
-template <int D, int KF, int VF>
+// P: PagedAttnParams, or WindowAttnParams.
+template <int D, int KF, int VF, class P>
 __global__ void __launch_bounds__(kThreadsTt, 1)
-    attn_tt_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ TmaSet maps) {
+    attn_tt_kernel(const __grid_constant__ P p, const __grid_constant__ TmaSet maps) {
   using G = GeoTt<D, KF, VF>;
   constexpr bool VDEC = VF != QPS_FMT_F16;  // V is decoded, or boxed into the slots
   constexpr float LOG2E = 1.4426950408889634f;
@@ -238,14 +239,16 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
               mma::fence_proxy_async();
               __syncwarp();
             }
-            const int tb = t0 + (j - 1) * kTile;
-            if (tb < win.none_lo && tb + kTile > p.sinks) {  // nor do rows that no window reaches
-              for (int i = max(0, p.sinks - tb) * 8 + lane; i < min(kTile, win.none_lo - tb) * 8; i += 32)
+            if constexpr (has_window<P>) {
+              const int tb = t0 + (j - 1) * kTile;
+              if (tb < win.none_lo && tb + kTile > p.sinks) {  // nor do rows that no window reaches
+                for (int i = max(0, p.sinks - tb) * 8 + lane; i < min(kTile, win.none_lo - tb) * 8; i += 32)
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-                  *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
-              mma::fence_proxy_async();
-              __syncwarp();
+                  for (int g = 0; g < 2; ++g)
+                    *reinterpret_cast<uint4*>(smem + G::RING + s * kSlot + g * (kSlot / 2) + i * 16) = make_uint4(0, 0, 0, 0);
+                mma::fence_proxy_async();
+                __syncwarp();
+              }
             }
           }
           const uint64_t a = smem_desc(sbase + G::RING + s * kSlot, kSlot / 2);
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
       return grp < groups && t < t1 && !paged_unseen(p, win, t, br);
     };
     auto entry = [&](int j) {
-      const int i = paged_true(win, t0 + j * kTile + r * br) >> p.page_shift;
+      const int i = paged_true(p, win, t0 + j * kTile + r * br) >> p.page_shift;
       return has(j) && entry_in_bounds(p, bz * p.table_stride + i) ? table[i] : 0;
     };
     int next = entry(0), page = 0;
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
           for (int i = 1; i < 4; ++i) arrive(bar);  // (a slot's barrier counts four)
       }
       __syncwarp();
-      const int y = paged_true(win, t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
+      const int y = paged_true(p, win, t0 + j * kTile + r * br) & ((1 << p.page_shift) - 1);
       // the box stays in its page and its stage (or slot), the stage in its ring
       const bool fits = in_bounds(
           grp >= groups || (y + br <= 1 << p.page_shift && page <= p.n_pages && head < p.hkv &&
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll
       for (int i = 0; i < W; ++i) w[i] = 0u;
       if (j >= ntiles || unseen(t0 + j * kTile + tok)) return;
-      const int at = paged_true(win, t0 + j * kTile + tok);
+      const int at = paged_true(p, win, t0 + j * kTile + tok);
       if (!entry_in_bounds(p, bz * p.table_stride + (at >> p.page_shift))) return;
       const int pg = table[at >> p.page_shift];
       if ((uint64_t)(int64_t)pg >= (uint64_t)p.n_pages) return;  // (reported by the boxes' warps)
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
         const int e = rr / p.group, b = p.shared ? e / p.n_q : bz, qi = p.shared ? e % p.n_q : e;
         n = paged_len(p, b);
         if (p.causal) n += qi + 1 - p.n_q;
-        if (p.window == 0) n = min(n, t1);  // (a window's start is counted from it; chunks end with tiles)
+        if constexpr (!has_window<P>) n = min(n, t1);  // (a window's start is counted from it; chunks end with tiles)
       }
       lim[tid] = n;
       mneg[tid] = kNone;
@@ -616,11 +619,11 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
     for (int j = 0; j < ntiles; ++j) {
       const int at = t0 + j * kTile + tl;
       // (uniform) some row does not see the whole tile
-      const bool cut = t0 + (j + 1) * kTile > least || t0 + j * kTile < win.all_lo;
+      const bool cut = t0 + (j + 1) * kTile > least || (has_window<P> && t0 + j * kTile < win.all_lo);
       float norm = 1.f;
       if constexpr (is_tq(VF)) {  // (0 behind the end and for a bad page: nothing there is read)
         norm = 0.f;
-        const int to = paged_true(win, at);
+        const int to = paged_true(p, win, at);
         if (!unseen(at) && entry_in_bounds(p, bz * p.table_stride + (to >> p.page_shift))) {
           const int pg = table[to >> p.page_shift];
           if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages &&
@@ -660,7 +663,9 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int n = lim[r0 + 16 * c + i];
-            if (at >= n || (p.window && at >= p.sinks && at < n - p.window)) x[i] = -INFINITY;
+            if (at >= n) x[i] = -INFINITY;
+            if constexpr (has_window<P>)
+              if (at >= p.sinks && at < n - p.window) x[i] = -INFINITY;
           }
         }
       };
@@ -903,8 +908,8 @@ __global__ void __launch_bounds__(kThreadsTt, 1)
   if (warp == 1) tmem_free(tmem, 512);
 }
 
-template <int D, int KF, int VF>
-qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
+template <int D, int KF, int VF, class P>
+qps_status launch_tt(const P& p, cudaStream_t s) {
   using G = GeoTt<D, KF, VF>;
   static_assert(G::SMEM <= 227 * 1024, "the slots exceed the shared memory of one CTA");
   static_assert((2 + G::VC) * kN + 128 <= 512, "S, K and O exceed TMEM");
@@ -921,7 +926,7 @@ qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
                              : map(&maps.v, p.v.data, D / 4, 32, 32)) ||
       (VF == QPS_FMT_TQ3 && !map(&maps.va, p.v.aux, D / 8, 16, 0)))
     return QPS_ERR_CUDA;
-  auto kern = attn_tt_kernel<D, KF, VF>;
+  auto kern = attn_tt_kernel<D, KF, VF, P>;
   static std::atomic<uint64_t> sized{0};
   int dev = 0;
   QPS_CUDA_TRY(cudaGetDevice(&dev));
@@ -947,8 +952,8 @@ qps_status launch_tt(const PagedAttnParams& p, cudaStream_t s) {
 }
 
 // The format pairings of one head_dim.
-template <int D>
-qps_status launch_tt_d(const PagedAttnParams& p, cudaStream_t s) {
+template <int D, class P>
+qps_status launch_tt_d(const P& p, cudaStream_t s) {
 #define QPS_TT_CASE(KF, VF) \
   if (p.kfmt == KF && p.vfmt == VF) return launch_tt<D, KF, VF>(p, s);
   if constexpr (D > 128) {  // (128: attn_tm.cuh)

@@ -2,6 +2,8 @@
 // the attention's parameters.
 #pragma once
 
+#include <type_traits>
+
 #include "internal.h"
 
 namespace qps {
@@ -27,8 +29,6 @@ struct PagedAttnParams : AttnParams {
   int64_t n_pages;
   int page_shift, table_width;
   int prefix_len;     // positions attended by the prefix launch (a multiple of 32)
-  int window, sinks;  // sliding window (0: none; then prefix_len is 0) and first positions that stay visible
-  int win_round;      // what the window leaves out is a multiple of this many positions (a power of two)
   int target;         // chunks per (KV head, row group) the sequences are cut into, about
   int min_units;      // smallest chunk, in units
   int unit_round;     // chunks are multiples of this many units (a power of two)
@@ -48,6 +48,15 @@ struct PagedAttnParams : AttnParams {
   int out_dtype;
 };
 
+// The same with a sliding window: instances of their own (in one instance with the plain attention,
+// whose window would be 0, that took 3 to 7% longer).
+struct WindowAttnParams : PagedAttnParams {
+  int window, sinks;  // positions of the window, first positions that stay visible (prefix_len is 0)
+  int win_round;      // what the window leaves out is a multiple of this many positions (a power of two)
+};
+template <class P>
+constexpr bool has_window = std::is_same<P, WindowAttnParams>::value;
+
 // The chunking of the sequences' own positions [prefix_len, len), the same in the
 // attention and in the merge: units of 32 positions, C units a chunk (a multiple of
 // unit_round), sequence b's chunks numbered behind those of the sequences before it.  C is
@@ -65,18 +74,19 @@ __device__ __forceinline__ int paged_true_len(const PagedAttnParams& p, int b) {
 // sinks and the first token's window is left out of the sequence: the kernels count positions
 // without that gap, as if the sequence were shorter, and add it where they look a page up.  The
 // gap starts and ends at multiples of win_round, so that no box or tile crosses it.
-__device__ __forceinline__ int paged_gap_from(const PagedAttnParams& p) {
+__device__ __forceinline__ int paged_gap_from(const WindowAttnParams& p) {
   return (p.sinks + p.win_round - 1) & ~(p.win_round - 1);
 }
-__device__ __forceinline__ int paged_gap(const PagedAttnParams& p, int n) {
-  if (p.window == 0) return 0;
+__device__ __forceinline__ int paged_gap(const WindowAttnParams& p, int n) {
   const int low = max(0, n - p.n_q + 1 - p.window);
   return max(0, (low & ~(p.win_round - 1)) - paged_gap_from(p));
 }
 // Positions of sequence b, without its gap.
-__device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
-  const int n = paged_true_len(p, b);
-  return n - paged_gap(p, n);
+template <class P>
+__device__ __forceinline__ int paged_len(const P& p, int b) {
+  int n = paged_true_len(p, b);
+  if constexpr (has_window<P>) n -= paged_gap(p, n);
+  return n;
 }
 // The window as a CTA of sequence b needs it (all in positions without the gap): row e of the
 // sequence does not see [sinks, lim(e) - window), lim(e) being the end of what it sees.
@@ -84,20 +94,28 @@ struct PagedWindow {
   int gap, from;        // position t is position t + gap of the sequence where t >= from
   int none_lo, all_lo;  // no row sees [sinks, none_lo); every row sees its window's part behind all_lo
 };
-__device__ __forceinline__ PagedWindow paged_window(const PagedAttnParams& p, int b) {
+template <class P>
+__device__ __forceinline__ PagedWindow paged_window(const P& p, int b) {
   PagedWindow w = {0, 0, 0, 0};
-  if (p.window == 0) return w;
-  const int n = paged_true_len(p, b);
-  w.gap = paged_gap(p, n);
-  w.from = paged_gap_from(p);
-  w.none_lo = max(0, n - p.n_q + 1 - p.window - w.gap);
-  w.all_lo = max(0, n - p.window - w.gap);
+  if constexpr (has_window<P>) {
+    const int n = paged_true_len(p, b);
+    w.gap = paged_gap(p, n);
+    w.from = paged_gap_from(p);
+    w.none_lo = max(0, n - p.n_q + 1 - p.window - w.gap);
+    w.all_lo = max(0, n - p.window - w.gap);
+  }
   return w;
 }
-__device__ __forceinline__ int paged_true(const PagedWindow& w, int t) { return t >= w.from ? t + w.gap : t; }
+template <class P>
+__device__ __forceinline__ int paged_true(const P&, const PagedWindow& w, int t) {
+  if constexpr (has_window<P>) return t >= w.from ? t + w.gap : t;
+  return t;
+}
 // Whether no row sees any of the positions [t, t + n): their page may have been given back.
-__device__ __forceinline__ bool paged_unseen(const PagedAttnParams& p, const PagedWindow& w, int t, int n) {
-  return t + n <= w.none_lo && t >= p.sinks;
+template <class P>
+__device__ __forceinline__ bool paged_unseen(const P& p, const PagedWindow& w, int t, int n) {
+  if constexpr (has_window<P>) return t + n <= w.none_lo && t >= p.sinks;
+  return false;
 }
 // What the checked build holds the paged kernels' accesses against: entry `at` of the page
 // tables, 16 bytes of the queries from element `at`, row `at` of the outputs or of a part
@@ -131,7 +149,8 @@ __device__ __forceinline__ int paged_chunks(const PagedAttnParams& p, int len, i
 struct PagedPrefix {
   int len, b;
 };
-__device__ __forceinline__ PagedPrefix paged_prefix(const PagedAttnParams& p, int lane) {
+template <class P>
+__device__ __forceinline__ PagedPrefix paged_prefix(const P& p, int lane) {
   int len = -1, first = 0;
 #pragma unroll 4
   for (int b = lane; b < p.batch; b += 32) {
@@ -154,7 +173,8 @@ struct PagedChunk {
   int b, t0, t1, count;
   bool first, whole;
 };
-__device__ __forceinline__ PagedChunk paged_find(const PagedAttnParams& p, int index, int lane) {
+template <class P>
+__device__ __forceinline__ PagedChunk paged_find(const P& p, int index, int lane) {
   // every CTA goes this way before its first load of a position: the first 128 lengths are
   // read together, once
   constexpr int R = 4;
@@ -215,6 +235,16 @@ qps_status launch_paged_tm_d128(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tt_d128(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tt_d256(const PagedAttnParams& p, cudaStream_t s);
 qps_status launch_paged_tt_d512(const PagedAttnParams& p, cudaStream_t s);
+// The instances with a window.
+qps_status launch_window_mma_d64(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_mma_d128(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_mma_d256(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_mma_d512(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_tm_d64(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_tm_d128(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_tt_d128(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_tt_d256(const WindowAttnParams& p, cudaStream_t s);
+qps_status launch_window_tt_d512(const WindowAttnParams& p, cudaStream_t s);
 
 // The softmax's reference is kept below the maximum, so that the largest operand of P V is
 // 2^kRefShift, 2^(kRefShift + kRefLazy) at most before the reference is raised: fp16 holds
