@@ -512,7 +512,8 @@ QPS_API qps_status qps_attn_prompt_plan(const qps_paged_prompt_args* a, size_t* 
  * reads as zero rows; entries of pages that no query token sees are not read.  Logits, softmax
  * sums and O are float32; the weights are rounded once to fp16, the operand type.  Compressed
  * rows are decoded once a call to two fp16 parts (logits and values as accurate as the decode
- * call's; for a bf16 output values are rounded to one), cut to fp16's range.  A NaN or
+ * call's; for a bf16 output values are rounded to one), cut to fp16's range and to its smallest
+ * step, 2^-24.  A NaN or
  * infinite value among positions that some tokens see may reach tokens before it (0 x NaN);
  * keys, and anything that no token of the sequence sees, reach no row.
  * tokens == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

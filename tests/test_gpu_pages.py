@@ -301,3 +301,13 @@ def test_large_pool(qps):  # noqa: F811
     ids, live = qps.kv_compact_paged(qps.paged_compact_args(seqs))
     used = pages - 15000 + need
     assert live.tolist() == [used] and int((ids >= 0).sum()) == used and torch.equal(ids[ids >= 0].sort().values.cpu(), torch.arange(used, dtype=torch.int32))
+
+
+def test_as_many_sequences_as_a_call_takes(qps):  # noqa: F811
+    """4096 sequences, each of them a fork of another."""
+    r = np.random.default_rng(1)
+    x = Pair(qps, 4096, 5, 14000, 16, hkv=1, seed=1)
+    for _ in range(2):
+        x.extend([int(n) for n in r.integers(-20, 40, 4096)], 30, 2)
+        x.fork([int(n) for n in r.integers(-1, 4096, 4096)], r.permutation(4096).tolist())
+    x.compact()
