@@ -23,8 +23,15 @@
 // the rescale of O is rare.  P is rounded once to fp16 (the operand type); sums, m and O are
 // float32.
 //
-// Roles: warp 0 brings the slots, warp 1 issues the products, warps 4.. are the streams' softmax.
-// Waits are bounded as in attn_tm.cuh.
+// Roles: warp 0 brings the slots, warp 1 issues the products, warp 3 asks for the next CTA's queries,
+// warps 4.. are the streams' softmax.  Waits are bounded as in attn_tm.cuh.
+//
+// Measured, 40 / 8 heads of 128, fp16: 16384 tokens 1757 us (1.56 PFLOP/s of useful products, 0.81 of
+// the measured rate), 4096 tokens 151 us, behind a window of 1024 93 us; 4096 tokens of heads of 64
+// 120 us, of 256 276 us; 2048 tokens behind 8192, 16 / 2 heads of 512 with keys and values in two
+// parts 1284 us.  A tile of two streams takes 2614 cycles where its products take 2048; a CTA's start
+// and end take 12000 to 13000.  Heads of 512: the products of queries and keys read 128 bytes a cycle
+// of shared memory, its rate, beside the boxes that are written.
 #pragma once
 
 #include <atomic>
@@ -76,13 +83,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
 template <int D, int KP, int VP>
 struct GeoP {
   static constexpr int NQ = D <= 128 ? 2 : 1;      // tiles of rows
-  static constexpr int SD = D < 128 ? D : 128;     // columns of a slot
+  // columns of a slot (512: three slots of 128 beside the queries, or six of 64; 2048 tokens behind 8192
+  // with keys in two parts 1331 us and 1284, 4096 tokens of fp16 344 and 356)
+  static constexpr int SD = D == 64 || (D == 512 && KP == 2) ? 64 : 128;
   static constexpr int VD = D <= 256 ? D : 256;    // columns of O
   static constexpr int CG = SD / 64;               // 128-byte column groups of a slot
   static constexpr int SLOT = kTok * SD * 2;
   static constexpr int KS = KP * D / SD, VC = VD / SD, VS = VP * VC;  // slots of a tile
   static constexpr int Q_TILE = kRows * D * 2;
-  static constexpr int STAGES = D == 64 ? 10 : D == 512 ? 3 : 5;
+  static constexpr int STAGES = D == 64 ? 10 : D == 512 ? 3 * (128 / SD) : 5;
   static constexpr int RING = NQ * Q_TILE;
   static constexpr int BAR = RING + STAGES * SLOT;
   static constexpr int SMEM = BAR + 256 + 1024;    // + slack for the 1024-byte base alignment
@@ -210,150 +219,150 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   auto v_at = [&](int j) { return NQ == 2 ? j * KV + G::KS : G::KS + j * KV + (j + 1 < ntiles ? G::KS : 0); };
 
   if (warp < 4) {
-  if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::FEW));
-  if (warp == 0) {
-    // ---- slots: boxes of min(page, 128) positions of one page and 64 columns, one a lane; a
-    // lane's page of the next tile is read a tile ahead.  Decoded rows: boxes of 128 positions. ----
-    const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
-    const int cg = lane % G::CG, r = lane / G::CG;
-    const int32_t* row = p.table + (int64_t)bz * p.table_stride;
-    const bool paged = !p.dense_k || !p.dense_v;
-    auto entry = [&](int j) -> int {  // the lane's page of tile j (n_pages: none, zeros)
-      if (!paged || j >= ntiles || r >= nb) return (int)p.n_pages;
-      const int t = first_of(j) + r * br;
-      if (t >= end || (t >= p.sinks && t + br <= none_lo)) return (int)p.n_pages;
-      const int at = t >> p.page_shift;
-      if (!in_bounds(at < p.table_width, p.err)) return (int)p.n_pages;
-      const int pg = row[at];
-      if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
-      atomicOr(p.err, kErrIndex);
-      return (int)p.n_pages;
-    };
-    int f = 0;
-    auto put = [&](const TensorMap* map, bool dec, int col, int j, int page) -> bool {
-      const int s = f % ST;
-      if (f >= ST && !wait(empty(s), ((f / ST) & 1) ^ 1, j)) return false;
-      __syncwarp();
-      if (lane == 0) mbar_expect_tx(full(s), G::SLOT);
-      __syncwarp();
-      const uint32_t dst = sbase + G::RING + s * G::SLOT + cg * (kTok * 128);
-      const int x = (col + cg * 64) * 2, t = first_of(j);
-      const bool drop = map == &maps.k && j == p.drop_tile;
-      if (dec) {  // (behind the room: zeros)
-        const int at = prompt_dense(dense, t / kPromptTile);
-        if (r == 0 && !drop && in_bounds(at >= 0 && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
-          tma_load_4d(dst, map, x, 0, head, min(dense0 + at, p.dense_tiles), full(s));
-      } else if (r < nb && !drop) {
-        const int y = (t + r * br) & ((1 << p.page_shift) - 1);
-        if (in_bounds(page <= p.n_pages && y + br <= 1 << p.page_shift && head < p.hkv && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
-          tma_load_4d(dst + r * br * 128, map, x, y, head, page, full(s));
-      }
-      issued = ++f;
-      return true;
-    };
-    auto put_k = [&](int j, int page) -> bool {
-      for (int s = 0; s < G::KS; ++s)
-        if (!put(&maps.k, p.dense_k != nullptr, s * G::SD, j, page)) return false;
-      return true;
-    };
-    auto put_v = [&](int j, int page) -> bool {
-      for (int s = 0; s < G::VS; ++s)
-        if (!put(&maps.v, p.dense_v != nullptr, s / G::VC * D + half * G::VD + s % G::VC * G::SD, j, page)) return false;
-      return true;
-    };
-    int page = entry(0), next = entry(1);
-    // (the first tile, then the queries: the whole ring before them kept them 1500 cycles longer)
-    bool ok = ntiles == 0 || (put_k(0, page) && (NQ == 1 || put_v(0, page)) && wait(q_full, 0, 0));
-    for (int j = 0; j < ntiles && ok; ++j) {
-      const int after = entry(j + 2);
-      if constexpr (NQ == 2) ok = j == 0 || (put_k(j, page) && put_v(j, page));
-      else ok = (j + 1 >= ntiles || put_k(j + 1, next)) && put_v(j, page);
-      page = next;
-      next = after;
-    }
-  } else if (warp == 1) {
-    // ---- products: step i is tile i / NQ of stream i % NQ, S(i) in buffer i % 2.  S(0), S(1),
-    // then O(i) and S(i + 2) in turn. ------------------------------------------------------------
-    constexpr uint32_t ID_S = instr_desc(kTok, 0), ID_O = instr_desc(G::SD, 1);
-    const uint32_t one = elect_lane();
-    const int steps = ntiles * NQ;
-    auto qk = [&](int i) -> bool {
-      const int j = i / NQ, w = i % NQ, at = k_at(j);
-      const uint32_t d = tmem + G::S_COL + (i & 1) * kTok;
-#pragma unroll 1
-      for (int s = 0; s < G::KS; ++s) {
-        const int st = (at + s) % ST;
-        if (w == 0 && !wait(full(st), ((at + s) / ST) & 1, j)) return false;
-        fence_after();
-        if (w < live) {
-          const uint64_t a = smem_desc(sbase + w * G::Q_TILE + (s * G::CG % (D / 64)) * (kRows * 128), 16);
-          const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, 16);
-#pragma unroll
-          for (int kk = 0; kk < G::SD / 16; ++kk) {
-            const uint64_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
-            mma_ss(d, a + off, b + off, ID_S, s > 0 || kk > 0, one);
-          }
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::FEW));
+    if (warp == 0) {
+      // ---- slots: boxes of min(page, 128) positions of one page and 64 columns, one a lane; a
+      // lane's page of the next tile is read a tile ahead.  Decoded rows: boxes of 128 positions. ----
+      const int br = min(1 << p.page_shift, kTok), nb = kTok / br;
+      const int cg = lane % G::CG, r = lane / G::CG;
+      const int32_t* row = p.table + (int64_t)bz * p.table_stride;
+      const bool paged = !p.dense_k || !p.dense_v;
+      auto entry = [&](int j) -> int {  // the lane's page of tile j (n_pages: none, zeros)
+        if (!paged || j >= ntiles || r >= nb) return (int)p.n_pages;
+        const int t = first_of(j) + r * br;
+        if (t >= end || (t >= p.sinks && t + br <= none_lo)) return (int)p.n_pages;
+        const int at = t >> p.page_shift;
+        if (!in_bounds(at < p.table_width, p.err)) return (int)p.n_pages;
+        const int pg = row[at];
+        if ((uint64_t)(int64_t)pg < (uint64_t)p.n_pages) return pg;
+        atomicOr(p.err, kErrIndex);
+        return (int)p.n_pages;
+      };
+      int f = 0;
+      auto put = [&](const TensorMap* map, bool dec, int col, int j, int page) -> bool {
+        const int s = f % ST;
+        if (f >= ST && !wait(empty(s), ((f / ST) & 1) ^ 1, j)) return false;
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(full(s), G::SLOT);
+        __syncwarp();
+        const uint32_t dst = sbase + G::RING + s * G::SLOT + cg * (kTok * 128);
+        const int x = (col + cg * 64) * 2, t = first_of(j);
+        const bool drop = map == &maps.k && j == p.drop_tile;
+        if (dec) {  // (behind the room: zeros)
+          const int at = prompt_dense(dense, t / kPromptTile);
+          if (r == 0 && !drop && in_bounds(at >= 0 && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
+            tma_load_4d(dst, map, x, 0, head, min(dense0 + at, p.dense_tiles), full(s));
+        } else if (r < nb && !drop) {
+          const int y = (t + r * br) & ((1 << p.page_shift) - 1);
+          if (in_bounds(page <= p.n_pages && y + br <= 1 << p.page_shift && head < p.hkv && G::RING + (s + 1) * G::SLOT <= G::BAR, p.err))
+            tma_load_4d(dst + r * br * 128, map, x, y, head, page, full(s));
         }
-        if (w == NQ - 1) commit(empty(st), one);
+        issued = ++f;
+        return true;
+      };
+      auto put_k = [&](int j, int page) -> bool {
+        for (int s = 0; s < G::KS; ++s)
+          if (!put(&maps.k, p.dense_k != nullptr, s * G::SD, j, page)) return false;
+        return true;
+      };
+      auto put_v = [&](int j, int page) -> bool {
+        for (int s = 0; s < G::VS; ++s)
+          if (!put(&maps.v, p.dense_v != nullptr, s / G::VC * D + half * G::VD + s % G::VC * G::SD, j, page)) return false;
+        return true;
+      };
+      int page = entry(0), next = entry(1);
+      // (the first tile, then the queries: the whole ring before them kept them 1500 cycles longer)
+      bool ok = ntiles == 0 || (put_k(0, page) && (NQ == 1 || put_v(0, page)) && wait(q_full, 0, 0));
+      for (int j = 0; j < ntiles && ok; ++j) {
+        const int after = entry(j + 2);
+        if constexpr (NQ == 2) ok = j == 0 || (put_k(j, page) && put_v(j, page));
+        else ok = (j + 1 >= ntiles || put_k(j + 1, next)) && put_v(j, page);
+        page = next;
+        next = after;
       }
-      commit(s_full(i & 1), one);
-      return true;
-    };
-    bool ok = steps == 0 || wait(q_full, 0, 0);
-    for (int i = 0; i < min(2, steps) && ok; ++i) ok = qk(i);
-    for (int i = 0; i < steps && ok; ++i) {
-      const int j = i / NQ, w = i % NQ, at = v_at(j);
-      // (rows that no query sees hold whatever was there, and 0 x NaN is NaN)
-      const int t = first_of(j), a0 = max(0, p.sinks - t), a1 = min(kTok, none_lo - t), b0 = end - t;
+    } else if (warp == 1) {
+      // ---- products: step i is tile i / NQ of stream i % NQ, S(i) in buffer i % 2.  S(0), S(1),
+      // then O(i) and S(i + 2) in turn. ------------------------------------------------------------
+      constexpr uint32_t ID_S = instr_desc(kTok, 0), ID_O = instr_desc(G::SD, 1);
+      const uint32_t one = elect_lane();
+      const int steps = ntiles * NQ;
+      auto qk = [&](int i) -> bool {
+        const int j = i / NQ, w = i % NQ, at = k_at(j);
+        const uint32_t d = tmem + G::S_COL + (i & 1) * kTok;
 #pragma unroll 1
-      for (int s = 0; s < G::VS && ok; ++s) {
-        const int st = (at + s) % ST;
-        if (w == 0) {
-          if (!(ok = wait(full(st), ((at + s) / ST) & 1, j))) break;
-          if (b0 < kTok || a0 < a1) {
-            for (int r = lane >> 3; r < kTok; r += 4)
-              if (r >= b0 || (r >= a0 && r < a1))
-#pragma unroll
-                for (int g = 0; g < G::CG; ++g)
-                  *reinterpret_cast<uint4*>(smem + G::RING + st * G::SLOT + g * (kTok * 128) + r * 128 + (lane & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
-            mma::fence_proxy_async();
-            __syncwarp();
-          }
-        }
-        const uint32_t d = tmem + G::O_COL + w * D + s % G::VC * G::SD, a = tmem + G::S_COL + (i & 1) * kTok;
-        const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, kTok * 128);
-        const uint32_t more = j > 0 || s >= G::VC;  // (0: a stream's first product starts its O)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (w >= live) continue;
-          if (s == 0 && !(ok = wait(p_ready(i & 1, h), NQ == 2 ? j & 1 : (j >> 1) & 1, j))) break;
+        for (int s = 0; s < G::KS; ++s) {
+          const int st = (at + s) % ST;
+          if (w == 0 && !wait(full(st), ((at + s) / ST) & 1, j)) return false;
           fence_after();
+          if (w < live) {
+            const uint64_t a = smem_desc(sbase + w * G::Q_TILE + (s * G::CG % (D / 64)) * (kRows * 128), 16);
+            const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, 16);
 #pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            mma_ts(d, a + kk * 8, b + (uint64_t)((kk * 2048) >> 4), ID_O, more | (kk > 0), one);
+            for (int kk = 0; kk < G::SD / 16; ++kk) {
+              const uint64_t off = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+              mma_ss(d, a + off, b + off, ID_S, s > 0 || kk > 0, one);
+            }
+          }
+          if (w == NQ - 1) commit(empty(st), one);
         }
-        if (ok && w == NQ - 1) commit(empty(st), one);
+        commit(s_full(i & 1), one);
+        return true;
+      };
+      bool ok = steps == 0 || wait(q_full, 0, 0);
+      for (int i = 0; i < min(2, steps) && ok; ++i) ok = qk(i);
+      for (int i = 0; i < steps && ok; ++i) {
+        const int j = i / NQ, w = i % NQ, at = v_at(j);
+        // (rows that no query sees hold whatever was there, and 0 x NaN is NaN)
+        const int t = first_of(j), a0 = max(0, p.sinks - t), a1 = min(kTok, none_lo - t), b0 = end - t;
+#pragma unroll 1
+        for (int s = 0; s < G::VS && ok; ++s) {
+          const int st = (at + s) % ST;
+          if (w == 0) {
+            if (!(ok = wait(full(st), ((at + s) / ST) & 1, j))) break;
+            if (b0 < kTok || a0 < a1) {
+              for (int r = lane >> 3; r < kTok; r += 4)
+                if (r >= b0 || (r >= a0 && r < a1))
+#pragma unroll
+                  for (int g = 0; g < G::CG; ++g)
+                    *reinterpret_cast<uint4*>(smem + G::RING + st * G::SLOT + g * (kTok * 128) + r * 128 + (lane & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+              mma::fence_proxy_async();
+              __syncwarp();
+            }
+          }
+          const uint32_t d = tmem + G::O_COL + w * D + s % G::VC * G::SD, a = tmem + G::S_COL + (i & 1) * kTok;
+          const uint64_t b = smem_desc(sbase + G::RING + st * G::SLOT, kTok * 128);
+          const uint32_t more = j > 0 || s >= G::VC;  // (0: a stream's first product starts its O)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (w >= live) continue;
+            if (s == 0 && !(ok = wait(p_ready(i & 1, h), NQ == 2 ? j & 1 : (j >> 1) & 1, j))) break;
+            fence_after();
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_ts(d, a + kk * 8, b + (uint64_t)((kk * 2048) >> 4), ID_O, more | (kk > 0), one);
+          }
+          if (ok && w == NQ - 1) commit(empty(st), one);
+        }
+        if (!ok) break;
+        if constexpr (NQ == 1) commit(pv_done, one);
+        if (i + 2 < steps) ok = qk(i + 2);
       }
-      if (!ok) break;
-      if constexpr (NQ == 1) commit(pv_done, one);
-      if (i + 2 < steps) ok = qk(i + 2);
-    }
-    commit(all_done, one);  // completes when everything issued above has
-  } else if (warp == 3) {
-    // ---- the queries of the CTA that follows on this SM, about, into L2 (from HBM they took 5200
-    // cycles of a CTA's start) -------------------------------------------------------------------
-    const int next = blockIdx.x + p.resident;
-    const Work k = next < (int)gridDim.x && p.group <= NQ * kRows ? find(next) : Work{0, 0, 0, -1, 0, 0, {0, 0, 0}};
-    if (k.bz >= 0) {
-      const int t0 = k.row0 / p.group, t1 = (int)min((int64_t)k.sq.n - 1, ((int64_t)k.row0 + NQ * kRows - 1) / p.group);
-      const int lines = (p.group * D * 2 + 127) / 128;
-      for (int i = lane; i < (t1 - t0 + 1) * lines; i += 32) {
-        const int64_t at = (int64_t)(k.sq.first + t0 + i / lines) * p.q_tok + (int64_t)k.head * p.group * D + min(i % lines * 64, p.group * D - 8);
-        if (in_bounds(k.sq.first + t0 + i / lines < p.tokens, p.err)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + at));
+      commit(all_done, one);  // completes when everything issued above has
+    } else if (warp == 3) {
+      // ---- the queries of the CTA that follows on this SM, about, into L2 (from HBM they took 5200
+      // cycles of a CTA's start) -------------------------------------------------------------------
+      const int next = blockIdx.x + p.resident;
+      const Work k = next < (int)gridDim.x && p.group <= NQ * kRows ? find(next) : Work{0, 0, 0, -1, 0, 0, {0, 0, 0}};
+      if (k.bz >= 0) {
+        const int t0 = k.row0 / p.group, t1 = (int)min((int64_t)k.sq.n - 1, ((int64_t)k.row0 + NQ * kRows - 1) / p.group);
+        const int lines = (p.group * D * 2 + 127) / 128;
+        for (int i = lane; i < (t1 - t0 + 1) * lines; i += 32) {
+          const int64_t at = (int64_t)(k.sq.first + t0 + i / lines) * p.q_tok + (int64_t)k.head * p.group * D + min(i % lines * 64, p.group * D - 8);
+          if (in_bounds(k.sq.first + t0 + i / lines < p.tokens, p.err)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + at));
+        }
       }
     }
-  }
   } else {
     if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::MANY));
     // ---- softmax: stream w, one row a thread --------------------------------------------------
@@ -631,6 +640,11 @@ qps_status launch_prompt(const PromptParams& p, cudaStream_t s) {
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!(sized.load(std::memory_order_relaxed) & bit) || !bit) {
     QPS_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM));
+    // (the split draws on the registers of the launch: with fewer, the softmax warps would wait for ever)
+    cudaFuncAttributes fa;
+    QPS_CUDA_TRY(cudaFuncGetAttributes(&fa, kern));
+    if (G::NQ == 2 && 3 * fa.numRegs < G::FEW + 2 * G::MANY)
+      return fail(QPS_ERR_INTERNAL, "attn_prompt_paged: the kernel was built with too few registers for its split");
     sized.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
