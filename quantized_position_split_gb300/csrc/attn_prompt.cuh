@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
   const uint32_t sbase = smem_addr(smem);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- barriers, TMEM --------------------------------------------------------------------------
   const uint32_t bars = sbase + G::BAR;
   auto full = [&](int s) { return bars + 8 * s; };
@@ -129,6 +128,9 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
     *abort_flag = 0;
   }
   if (warp == 2) tmem_alloc(smem_addr(tmem_word), 512);
+  // (Before the wait for the grid ahead: a CTA that starts early may hold TMEM, as a grid is let in only
+  // when every CTA ahead of it has started, and those that use TMEM let it in behind their allocation.)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- this CTA's rows and tiles -------------------------------------------------------------
   // CTA `idx` of the grid: KV head, half of O's columns, split, row tile (sequences in order, the last
   // rows of each first: they see the most).  Sequence -1: there are fewer row tiles.
@@ -577,16 +579,21 @@ __global__ void __launch_bounds__(GeoP<D, KP, VP>::THREADS, 1)
           }
         }
         __syncwarp();
-        const uint32_t chunks = bytes / 16, to32 = (uint32_t)(store ? to : 0);
+        const uint32_t to32 = (uint32_t)(store ? to : 0);
         const uint8_t* rows32 = row - lane * (bytes + 16);
-        uint8_t* const out = reinterpret_cast<uint8_t*>(whole ? p.out : p.part_o) + (half * G::VD + x) * (wide ? 4 : 2);
-#pragma unroll 4
-        for (uint32_t k = 0; k < chunks; ++k) {
-          const uint32_t i = k * 32 + lane, rr = i / chunks, c = i % chunks;  // (a power of two)
-          const int64_t dst = __shfl_sync(0xffffffffu, to32, rr);
-          if (__shfl_sync(0xffffffffu, (int)store, rr))
-            *reinterpret_cast<uint4*>(out + dst * (D * (wide ? 4 : 2)) + 16 * c) = *reinterpret_cast<const uint4*>(rows32 + rr * (bytes + 16) + 16 * c);
-        }
+        auto copy_out = [&](auto size) {  // 32 rows of PC values of `size` bytes
+          constexpr int S = decltype(size)::value, CHUNKS = PC * S / 16;
+          uint8_t* const out = reinterpret_cast<uint8_t*>(whole ? p.out : p.part_o) + (half * G::VD + x) * S;
+#pragma unroll 8
+          for (int k = 0; k < CHUNKS; ++k) {
+            const int i = k * 32 + lane, rr = i / CHUNKS, c = i % CHUNKS;
+            const int64_t dst = __shfl_sync(0xffffffffu, to32, rr);
+            if (__shfl_sync(0xffffffffu, (int)store, rr))
+              *reinterpret_cast<uint4*>(out + dst * (D * S) + 16 * c) = *reinterpret_cast<const uint4*>(rows32 + rr * (PC * S + 16) + 16 * c);
+          }
+        };
+        if (wide) copy_out(std::integral_constant<int, 4>{});
+        else copy_out(std::integral_constant<int, 2>{});
         __syncwarp();
       }
     }
