@@ -29,7 +29,7 @@
 // Measured, 40 / 8 heads of 128, fp16: 16384 tokens 1757 us (1.56 PFLOP/s of useful products, 0.81 of
 // the measured rate), 4096 tokens 151 us, behind a window of 1024 93 us; 4096 tokens of heads of 64
 // 120 us, of 256 276 us; 2048 tokens behind 8192, 16 / 2 heads of 512 with keys and values in two
-// parts 1284 us.  A tile of two streams takes 2614 cycles where its products take 2048; a CTA's start
+// parts 1337 us.  A tile of two streams takes 2614 cycles where its products take 2048; a CTA's start
 // and end take 12000 to 13000.  Heads of 512: the products of queries and keys read 128 bytes a cycle
 // of shared memory, its rate, beside the boxes that are written.
 #pragma once
@@ -83,15 +83,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
 template <int D, int KP, int VP>
 struct GeoP {
   static constexpr int NQ = D <= 128 ? 2 : 1;      // tiles of rows
-  // columns of a slot (512: three slots of 128 beside the queries, or six of 64; 2048 tokens behind 8192
-  // with keys in two parts 1331 us and 1284, 4096 tokens of fp16 344 and 356)
-  static constexpr int SD = D == 64 || (D == 512 && KP == 2) ? 64 : 128;
+  // columns of a slot (64 at head_dim 512 too, in twice as many slots: 4096 tokens of q8_0 554 us for
+  // 518, 2048 behind 8192 of q8_0 / tq3 1298 for 1337; at 256: 331 for 271)
+  static constexpr int SD = D < 128 ? D : 128;
   static constexpr int VD = D <= 256 ? D : 256;    // columns of O
   static constexpr int CG = SD / 64;               // 128-byte column groups of a slot
   static constexpr int SLOT = kTok * SD * 2;
   static constexpr int KS = KP * D / SD, VC = VD / SD, VS = VP * VC;  // slots of a tile
   static constexpr int Q_TILE = kRows * D * 2;
-  static constexpr int STAGES = D == 64 ? 10 : D == 512 ? 3 * (128 / SD) : 5;
+  static constexpr int STAGES = D == 64 ? 10 : D == 512 ? 3 : 5;
   static constexpr int RING = NQ * Q_TILE;
   static constexpr int BAR = RING + STAGES * SLOT;
   static constexpr int SMEM = BAR + 256 + 1024;    // + slack for the 1024-byte base alignment
