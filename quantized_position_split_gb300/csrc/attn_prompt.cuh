@@ -26,10 +26,10 @@
 // Roles: warp 0 brings the slots, warp 1 issues the products, warp 3 asks for the next CTA's queries,
 // warps 4.. are the streams' softmax.  Waits are bounded as in attn_tm.cuh.
 //
-// Measured, 40 / 8 heads of 128, fp16: 16384 tokens 1757 us (1.56 PFLOP/s of useful products, 0.81 of
-// the measured rate), 4096 tokens 151 us, behind a window of 1024 93 us; 4096 tokens of heads of 64
-// 120 us, of 256 276 us; 2048 tokens behind 8192, 16 / 2 heads of 512 with keys and values in two
-// parts 1337 us.  A tile of two streams takes 2614 cycles where its products take 2048; a CTA's start
+// Measured, 40 / 8 heads of 128, fp16: 16384 tokens 1757 to 1797 us by the device (1.53 to 1.56 PFLOP/s
+// of useful products, 0.79 to 0.81 of the measured rate), 4096 tokens 142 to 153 us, behind a window of
+// 1024 95 us; 4096 tokens of heads of 64 120 us, of 256 271 to 278 us; 2048 tokens behind 8192, 16 / 2
+// heads of 512 with keys and values in two parts 1333 to 1345 us.  A tile of two streams takes 2614 cycles where its products take 2048; a CTA's start
 // and end take 12000 to 13000.  Heads of 512: the products of queries and keys read 128 bytes a cycle
 // of shared memory, its rate, beside the boxes that are written.
 #pragma once
@@ -83,8 +83,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
 template <int D, int KP, int VP>
 struct GeoP {
   static constexpr int NQ = D <= 128 ? 2 : 1;      // tiles of rows
-  // columns of a slot (64 at head_dim 512 too, in twice as many slots: 4096 tokens of q8_0 554 us for
-  // 518, 2048 behind 8192 of q8_0 / tq3 1298 for 1337; at 256: 331 for 271)
+  // columns of a slot (64 at head_dim 512 too, in twice as many slots: 4096 tokens of q8_0 555 us for
+  // 520, 2048 behind 8192 of q8_0 / tq3 1298 for 1337, so they gain in the one and lose more in the
+  // other; at 256: 331 for 271; means of two runs a side)
   static constexpr int SD = D < 128 ? D : 128;
   static constexpr int VD = D <= 256 ? D : 256;    // columns of O
   static constexpr int CG = SD / 64;               // 128-byte column groups of a slot
